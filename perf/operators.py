@@ -171,9 +171,9 @@ def prepare(case, seed):
         s["do"] = randn(*rows, hv, dv).to(dt)
         s["dstate"] = randn(len(lens), hv, dk, dv) if case["state"] else None
     if own:
-        from fft_long_convolution_libhyena_amd import DeltaPlan
+        from fft_long_convolution_libhyena_amd import DeltaRule
 
-        s["plan"] = DeltaPlan(hk, hv, dk, dv, dtype=case["dtype"])
+        s["rule"] = DeltaRule(hk, hv, dk, dv, dtype=case["dtype"])
     return s
 
 
@@ -201,17 +201,17 @@ def run(s):
         return (dq, dk, dwq, dwk) if c["weights"] else (dq, dk)
     if c["op"] == "step":
         if own:
-            o = s["plan"].step(s["q"], s["k"], s["v"], s["g"], s["beta"], s["states"], slots=s["slots"],
+            o = s["rule"].step(s["q"], s["k"], s["v"], s["g"], s["beta"], s["states"], slots=s["slots"],
                                scale=s["scale"])
             return o, s["states"]
         return _step(s)
     if c["op"] == "forward":
         if own:
-            return s["plan"].forward(s["q"], s["k"], s["v"], s["g"], s["beta"], state=s["state"], scale=s["scale"],
+            return s["rule"].forward(s["q"], s["k"], s["v"], s["g"], s["beta"], state=s["state"], scale=s["scale"],
                                      seq_start=s["seq_start"])
         return _forward(s)
     if own:
-        out = s["plan"].backward(s["q"], s["k"], s["v"], s["g"], s["beta"], s["do"], state=s["state"],
+        out = s["rule"].backward(s["q"], s["k"], s["v"], s["g"], s["beta"], s["do"], state=s["state"],
                                  dstate_out=s["dstate"], scale=s["scale"], seq_start=s["seq_start"])
         return out if s["state"] is not None else out[:5]
     return _backward(s)
