@@ -35,7 +35,8 @@ EXPORTS = ("hyena_plan_create", "hyena_plan_create_path", "hyena_plan_create_ex"
            "hyena_spectrum3d_bytes", "hyena_workspace3d_bytes", "hyena_filter_spectrum3d", "hyena_conv3d_forward",
            "hyena_filter_spectrum2d_batched", "hyena_conv2d_forward_per_sample", "hyena_filter_spectrum3d_batched",
            "hyena_conv3d_forward_per_sample", "hyena_plan2d_create_ex", "hyena_plan3d_create_ex",
-           "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_status_string")
+           "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_delta_workspace_bytes",
+           "hyena_delta_forward", "hyena_delta_step", "hyena_status_string")
 
 
 class FilterMLPStruct(ctypes.Structure):
@@ -55,6 +56,18 @@ class SynthParamsStruct(ctypes.Structure):
                 ("channels", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in (
                     "w_first", "w_hidden", "b_layer", "omega", "film_g", "film_gb", "film_b", "film_bb", "w_out",
                     "b_out", "win_mu", "win_sigma")]
+
+
+class DeltaParamsStruct(ctypes.Structure):
+    """hyena_delta_params_t: heads, dims, dtype and query scale of the gated delta rule."""
+    _fields_ = [("heads_k", ctypes.c_int64), ("heads_v", ctypes.c_int64), ("dim_k", ctypes.c_int64),
+                ("dim_v", ctypes.c_int64), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class DeltaInputsStruct(ctypes.Structure):
+    """hyena_delta_inputs_t: device pointers of q, k, v (each with its token stride), g and beta."""
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64), ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
 
 
 class HyenaError(RuntimeError):
@@ -161,6 +174,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         getattr(lib, f"hyena_filter_spectrum{nd}_batched").restype = ci
         getattr(lib, f"hyena_conv{nd}_forward_per_sample").argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         getattr(lib, f"hyena_conv{nd}_forward_per_sample").restype = ci
+    dp, di = ctypes.POINTER(DeltaParamsStruct), ctypes.POINTER(DeltaInputsStruct)
+    lib.hyena_delta_workspace_bytes.argtypes = [dp, i64, i64, vp]
+    lib.hyena_delta_workspace_bytes.restype = sz
+    lib.hyena_delta_forward.argtypes = [dp, i64, i64, vp, di, vp, vp, vp, vp, sz, vp]
+    lib.hyena_delta_forward.restype = ci
+    lib.hyena_delta_step.argtypes = [dp, i64, i64, di, vp, i64, vp, vp, vp]
+    lib.hyena_delta_step.restype = ci
     lib.hyena_status_string.argtypes = [ci]
     lib.hyena_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -674,3 +694,139 @@ class Plan3D(_GridPlan):
     def __init__(self, A: int, H: int, W: int, D: int, dtype: str = "f32", circular: bool = False):
         self.A, self.H, self.W = int(A), int(H), int(W)
         super().__init__((A, H, W), D, dtype, circular)
+
+
+class DeltaRule:
+    """The gated delta rule (hyena_delta_forward / _step of include/hyena.h): fixed heads,
+    dims and dtype ("f32" or "bf16"). Tensors must be on one device and calls run there,
+    on its current stream; the object holds no device memory."""
+
+    def __init__(self, heads_k: int, heads_v: int, dim_k: int, dim_v: int, dtype: str = "bf16"):
+        import torch
+
+        self._torch = torch
+        self.lib = load_library()
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be one of {list(_DTYPES)}")
+        self.heads_k, self.heads_v, self.dim_k, self.dim_v = int(heads_k), int(heads_v), int(dim_k), int(dim_v)
+        self.dtype = dtype
+
+    @property
+    def io_dtype(self):
+        return self._torch.bfloat16 if self.dtype == "bf16" else self._torch.float32
+
+    def _params(self, scale):
+        return DeltaParamsStruct(self.heads_k, self.heads_v, self.dim_k, self.dim_v, _DTYPES[self.dtype],
+                                 self.dim_k ** -0.5 if scale is None else float(scale))
+
+    def state_shape(self, N: int):
+        return (int(N), self.heads_v, self.dim_k, self.dim_v)
+
+    def _need(self, t, name, shape, dtype, device):
+        if not isinstance(t, self._torch.Tensor) or t.device != device or device.type != "cuda":
+            raise ValueError(f"{name} must be a tensor on the GPU that holds q")
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+
+    def _rows(self, t, name, rows, heads, dim, device):
+        """The token stride of t [*rows, heads, dim]: dense heads, one stride over all tokens."""
+        if not isinstance(t, self._torch.Tensor) or t.device != device or device.type != "cuda":
+            raise ValueError(f"{name} must be a tensor on the GPU that holds q")
+        if tuple(t.shape) != (*rows, heads, dim) or t.dtype != self.io_dtype:
+            raise ValueError(f"{name} must be a {self.io_dtype} tensor of shape {(*rows, heads, dim)}, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+        width = heads * dim
+        if t.numel() == 0:
+            return width
+        ld = t.stride(-3) if rows[-1] > 1 else (t.stride(0) if len(rows) == 2 and rows[0] > 1 else width)
+        if ((dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim) or ld < width
+                or (len(rows) == 2 and rows[0] > 1 and t.stride(0) != rows[1] * ld)):
+            raise ValueError(f"{name} must have dense heads and one stride between tokens")
+        if ld * t.element_size() % 16 or t.data_ptr() % 16:
+            raise ValueError(f"{name}'s rows must start on 16 bytes")
+        return ld
+
+    def _inputs(self, q, k, v, g, beta, rows, device):
+        Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
+        ld = [self._rows(q, "q", rows, Hk, Dk, device), self._rows(k, "k", rows, Hk, Dk, device),
+              self._rows(v, "v", rows, Hv, Dv, device)]
+        self._need(g, "g", (*rows, Hv), self.io_dtype, device)
+        self._need(beta, "beta", (*rows, Hv), self.io_dtype, device)
+        return DeltaInputsStruct(q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2], g.data_ptr(),
+                                 beta.data_ptr())
+
+    def _sequences(self, q, seq_start):
+        """(rows, N, tokens, pointer of seq_start) of q [B, T, ...] or packed [tokens, ...]."""
+        if seq_start is None:
+            if q.dim() != 4:
+                raise ValueError("q must be [B, T, heads_k, dim_k], or [tokens, heads_k, dim_k] with seq_start")
+            B, T = int(q.shape[0]), int(q.shape[1])
+            return (B, T), B, B * T, None
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, heads_k, dim_k] with seq_start")
+        if seq_start.dim() != 1 or seq_start.numel() < 2:
+            raise ValueError("seq_start must hold N + 1 offsets")
+        N = int(seq_start.numel()) - 1
+        self._need(seq_start, "seq_start", (N + 1,), self._torch.int64, q.device)
+        return (int(q.shape[0]),), N, int(q.shape[0]), seq_start.data_ptr()
+
+    def workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
+        return int(self.lib.hyena_delta_workspace_bytes(ctypes.byref(self._params(None)), int(N), int(tokens),
+                                                        16 if packed else None))
+
+    def _workspace(self, workspace, need, device):
+        if workspace is None:
+            workspace = self._torch.empty(need, dtype=self._torch.uint8, device=device)
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the GPU that holds q")
+        return workspace, workspace.numel() * workspace.element_size()
+
+    def forward(self, q, k, v, g, beta, state=None, scale=None, seq_start=None, o=None, state_out=None,
+                workspace=None):
+        """hyena_delta_forward: q, k [B, T, heads_k, dim_k], v [B, T, heads_v, dim_v] (views with
+        one stride between tokens are taken as they are), g, beta [B, T, heads_v]; or all with
+        [tokens] in place of [B, T] and seq_start [N + 1] int64 offsets on the device. state
+        [N, heads_v, dim_k, dim_v] fp32 or None (zeros). Returns (o like v, the final states)."""
+        torch, dev = self._torch, q.device
+        rows, N, tokens, starts = self._sequences(q, seq_start)
+        inputs = self._inputs(q, k, v, g, beta, rows, dev)
+        if state is not None:
+            self._need(state, "state", self.state_shape(N), torch.float32, dev)
+        if o is None:
+            o = torch.empty((*rows, self.heads_v, self.dim_v), dtype=self.io_dtype, device=dev)
+        self._need(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
+        if state_out is None:
+            state_out = torch.empty(self.state_shape(N), dtype=torch.float32, device=dev)
+        self._need(state_out, "state_out", self.state_shape(N), torch.float32, dev)
+        ws, ws_bytes = self._workspace(workspace, self.workspace_bytes(N, tokens, starts is not None), dev)
+        with torch.cuda.device(dev):
+            _check("hyena_delta_forward",
+                   self.lib.hyena_delta_forward(ctypes.byref(self._params(scale)), N, tokens, starts,
+                                                ctypes.byref(inputs), state.data_ptr() if state is not None else None,
+                                                o.data_ptr(), state_out.data_ptr(), ws.data_ptr(), ws_bytes,
+                                                _stream_handle(torch, dev)))
+        return o, state_out
+
+    def step(self, q, k, v, g, beta, states, slots=None, scale=None, o=None):
+        """hyena_delta_step: T further tokens of B rows (q, k [B, T, heads_k, dim_k], v
+        [B, T, heads_v, dim_v], g, beta [B, T, heads_v]) against states [num, heads_v, dim_k,
+        dim_v] fp32, updated in place; slots [B] int32 names each row's state. Returns o like v."""
+        torch, dev = self._torch, q.device
+        rows, B, _, _ = self._sequences(q, None)
+        inputs = self._inputs(q, k, v, g, beta, rows, dev)
+        if states.dim() != 4:
+            raise ValueError("states must be [num_states, heads_v, dim_k, dim_v]")
+        num = int(states.shape[0])
+        self._need(states, "states", self.state_shape(num), torch.float32, dev)
+        if slots is not None:
+            self._need(slots, "slots", (B,), torch.int32, dev)
+        if o is None:
+            o = torch.empty((*rows, self.heads_v, self.dim_v), dtype=self.io_dtype, device=dev)
+        self._need(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
+        with torch.cuda.device(dev):
+            _check("hyena_delta_step",
+                   self.lib.hyena_delta_step(ctypes.byref(self._params(scale)), B, rows[1], ctypes.byref(inputs),
+                                             states.data_ptr(), num, slots.data_ptr() if slots is not None else None,
+                                             o.data_ptr(), _stream_handle(torch, dev)))
+        return o

@@ -1,0 +1,165 @@
+// Gated delta rule, forward over whole sequences (chunked): argument checks,
+// workspace layout and launches of the preparation and the state scan.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/hyena.h"
+#include "delta.hpp"
+#include "delta_prep.hpp"
+#include "delta_scan.hpp"
+#include "plan.hpp"
+
+namespace hy {
+
+using namespace delta;
+
+hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
+                           const hyena_delta_inputs_t* in, DeltaCall& c) {
+    const hyena_status_t st = delta_check_shape(p, c);
+    if (st != HYENA_OK) return st;
+    if (N < 1 || tokens < 0 || (!seq_start && tokens % N)) return HYENA_ERR_INVALID_ARG;
+    if (!(p->scale >= -3.402823466e38f && p->scale <= 3.402823466e38f)) return HYENA_ERR_INVALID_ARG;
+    if (((uintptr_t)seq_start & 7u) != 0) return HYENA_ERR_INVALID_ARG;
+    if (in) {
+        c.in = *in;
+        const void* rows[] = {in->q, in->k, in->v};
+        for (const void* x : rows)
+            if (tokens > 0 && (!x || !aligned16(x))) return HYENA_ERR_INVALID_ARG;
+        const void* gates[] = {in->g, in->beta};  // read one element at a time
+        for (const void* x : gates)
+            if (tokens > 0 && (!x || ((uintptr_t)x & (c.bf ? 1u : 3u)))) return HYENA_ERR_INVALID_ARG;
+        const int64_t v = c.bf ? 8 : 4;  // elements per 16 bytes: operand rows start on 16 bytes
+        const int64_t ld[] = {in->ldq, in->ldk, in->ldv};
+        const int64_t width[] = {p->heads_k * p->dim_k, p->heads_k * p->dim_k, p->heads_v * p->dim_v};
+        for (int i = 0; i < 3; ++i)
+            if (ld[i] < width[i] || ld[i] % v || ld[i] > (int64_t(1) << 31)) return HYENA_ERR_INVALID_ARG;
+        c.shape.ldq = in->ldq;
+        c.shape.ldk = in->ldk;
+        c.shape.ldv = in->ldv;
+    }
+    if (N > kMaxSeqs || tokens > kMaxTokens) return HYENA_ERR_UNSUPPORTED;
+    c.seqs.start = seq_start;
+    c.seqs.N = N;
+    c.seqs.tokens = tokens;
+    c.seqs.T = seq_start ? 0 : tokens / N;
+    c.seqs.cpt = (c.seqs.T + kC - 1) / kC;
+    c.slots = seq_start ? tokens / kC + N : N * c.seqs.cpt;
+    // one workgroup per (slot, value head) and per column block of a (sequence, value head)
+    if (c.slots * p->heads_v > (int64_t(1) << 30) || N * p->heads_v > (int64_t(1) << 26)) return HYENA_ERR_UNSUPPORTED;
+    return HYENA_OK;
+}
+
+size_t delta_prep_layout(const DeltaCall& c, bool bwd, unsigned char* base, Prep& o) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char* p = base ? base + at : nullptr;
+        at += (bytes + 255) & ~(size_t)255;
+        return (void*)p;
+    };
+    const size_t pv = (size_t)c.slots * c.shape.hv, pk = (size_t)c.slots * c.shape.hk;
+    const size_t ns = c.bf ? 2 : 3, np = c.bf ? 1 : 3;
+    const size_t rows = (size_t)(c.dkp / 16) * 1024 * (c.bf ? 2 : 4);
+    o = Prep{};
+    o.t = (__bf16*)take(pv * kTri * ns * kFragBytes);
+    if (!bwd) o.p = (__bf16*)take(pv * kTri * np * kFragBytes);
+    if (bwd) o.tt = (__bf16*)take(pv * kTri * ns * kFragBytes);
+    if (bwd) o.pt = (__bf16*)take(pv * kTri * ns * kFragBytes);
+    o.kt = take(pk * rows);
+    if (bwd) o.qt = take(pk * rows);
+    o.sc = (float*)take(pv * 3 * kC * sizeof(float));
+    return at;
+}
+
+namespace {
+
+template <bool BF, int DK, bool BWD>
+hipError_t launch_prep_t(const DeltaCall& c, const Prep& o, hipStream_t st) {
+    using L = PrepLds<BF, DK>;
+    PrepArgs a{c.seqs, c.shape, c.in.q, c.in.k, c.in.g, c.in.beta, o};
+    if (sizeof(L) > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute((const void*)k_delta_prep<BF, DK, BWD>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(L));
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((k_delta_prep<BF, DK, BWD>), dim3((unsigned)c.slots, (unsigned)c.shape.hv), dim3(kThreads),
+                       sizeof(L), st, a);
+    return hipGetLastError();
+}
+
+template <bool BF, int DK, int NT, int MODE>
+hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
+    using L = ScanLds<BF, DK, NT>;
+    a.nblk = (c.shape.dv + 16 * NT - 1) / (16 * NT);
+    const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
+    static_assert(sizeof(L) <= 64 * 1024, "LDS of a scan workgroup");
+    hipLaunchKernelGGL((k_delta_scan<BF, DK, NT, MODE>), dim3((unsigned)(pairs * a.nblk)), dim3(kThreads), sizeof(L),
+                       st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t delta_prep(const DeltaCall& c, bool bwd, const Prep& o, hipStream_t st) {
+    if (c.slots < 1 || c.seqs.tokens < 1) return hipSuccess;
+    if (c.bf) {
+        if (c.dkp == 64) return bwd ? launch_prep_t<true, 64, true>(c, o, st) : launch_prep_t<true, 64, false>(c, o, st);
+        return bwd ? launch_prep_t<true, 128, true>(c, o, st) : launch_prep_t<true, 128, false>(c, o, st);
+    }
+    if (c.dkp == 64) return bwd ? launch_prep_t<false, 64, true>(c, o, st) : launch_prep_t<false, 64, false>(c, o, st);
+    return bwd ? launch_prep_t<false, 128, true>(c, o, st) : launch_prep_t<false, 128, false>(c, o, st);
+}
+
+hipError_t delta_scan(const DeltaCall& c, bool keep, const ScanArgs& a, hipStream_t st) {
+    if (c.bf) {
+        if (c.dkp == 64)
+            return keep ? launch_scan_t<true, 64, 2, kScanKeep>(c, a, st) : launch_scan_t<true, 64, 2, kScanOut>(c, a, st);
+        return keep ? launch_scan_t<true, 128, 2, kScanKeep>(c, a, st) : launch_scan_t<true, 128, 2, kScanOut>(c, a, st);
+    }
+    if (c.dkp == 64)
+        return keep ? launch_scan_t<false, 64, 2, kScanKeep>(c, a, st) : launch_scan_t<false, 64, 2, kScanOut>(c, a, st);
+    return keep ? launch_scan_t<false, 128, 2, kScanKeep>(c, a, st) : launch_scan_t<false, 128, 2, kScanOut>(c, a, st);
+}
+
+}  // namespace hy
+
+extern "C" {
+
+size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                   const int64_t* seq_start) {
+    hy::DeltaCall c;
+    if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
+    hy::delta::Prep o;
+    return hy::delta_prep_layout(c, false, nullptr, o);
+}
+
+hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                   const int64_t* seq_start, const hyena_delta_inputs_t* in, const float* state_in,
+                                   void* o, float* state_out, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream) {
+    using hy::aligned16;
+    hy::DeltaCall c;
+    if (!in) return HYENA_ERR_INVALID_ARG;
+    const hyena_status_t st = hy::delta_check(params, N, tokens, seq_start, in, c);
+    if (st != HYENA_OK) return st;
+    if ((tokens > 0 && !o) || !aligned16(o) || !aligned16(state_in) || !aligned16(state_out))
+        return HYENA_ERR_INVALID_ARG;
+    hy::delta::ScanArgs a{};
+    const size_t need = hy::delta_prep_layout(c, false, (unsigned char*)workspace, a.prep);
+    if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
+    hipError_t e = hy::delta_prep(c, false, a.prep, stream);
+    if (e != hipSuccess) return HYENA_ERR_DEVICE;
+    a.seqs = c.seqs;
+    a.sh = c.shape;
+    a.q = in->q;
+    a.k = in->k;
+    a.v = in->v;
+    a.s_in = state_in;
+    a.s_out = state_out;
+    a.o = o;
+    e = hy::delta_scan(c, false, a, stream);
+    return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
+}
+
+}  // extern "C"

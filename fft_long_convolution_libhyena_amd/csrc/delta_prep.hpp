@@ -1,0 +1,223 @@
+// Chunk-parallel preparation of the gated delta rule: the decays, T = (I + A)^-1 and
+// P of every (chunk, value head), written as matrix-core fragments so that the scans
+// read them 16 bytes per lane without staging, and K^T (Q^T) of every (chunk, key
+// head) in the same form.
+#pragma once
+#include "delta.hpp"
+
+namespace hy {
+namespace delta {
+
+struct PrepArgs {
+    Seqs seqs;
+    Shape sh;
+    const void *q, *k, *g, *beta;
+    Prep out;
+};
+
+constexpr int kMP = 68;  // LDS pitch (floats) of a 64 x 64 matrix: rows 16-byte aligned, four banks apart
+
+template <bool BF, int DK>
+struct PrepLds {
+    using T = typename Io<BF>::T;
+    static constexpr int KP = DK + 16 / (int)sizeof(T);  // row pitch of the staged K (Q) tile
+    float a[kC][kMP];
+    float p[kC][kMP];
+    alignas(16) T rows[kC][KP];
+    double G[kC];
+    float beta[kC];
+};
+
+// column fragments of the staged rows: lane (row k of tile t, tokens 32 s + 8 g ..)
+template <bool BF, int DK>
+__device__ __forceinline__ void write_transposed(const PrepLds<BF, DK>& l, void* dst, int tid) {
+    using T = typename Io<BF>::T;
+    T* o = (T*)dst;
+    for (int e = tid; e < (DK / 16) * 2 * 64; e += kThreads) {
+        const int f = e >> 6, lane = e & 63;
+        const int k = 16 * (f >> 1) + (lane & 15), t0 = 32 * (f & 1) + 8 * (lane >> 4);
+        alignas(16) T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = l.rows[t0 + i][k];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            reinterpret_cast<f32x4*>(o + (int64_t)e * 8)[i] = reinterpret_cast<const f32x4*>(v)[i];
+    }
+}
+
+template <bool BF, int DK>
+__device__ __forceinline__ void stage_rows(PrepLds<BF, DK>& l, const typename Io<BF>::T* src, int64_t ld, int rows,
+                                           int dk, int tid) {
+    using T = typename Io<BF>::T;
+    constexpr int V = 16 / (int)sizeof(T);  // elements per 16 bytes
+    for (int e = tid; e < kC * (DK / V); e += kThreads) {
+        const int t = e / (DK / V), k = (e % (DK / V)) * V;
+        f32x4 v = {};
+        if (t < rows && k < dk) v = *reinterpret_cast<const f32x4*>(src + t * ld + k);
+        *reinterpret_cast<f32x4*>(&l.rows[t][k]) = v;
+    }
+}
+
+// a 64 x 64 matrix in LDS (or its transpose) as block-triangular A fragments of N parts
+template <int N, bool TRANS>
+__device__ __forceinline__ void write_tri(const float (*m)[kMP], __bf16* dst, int tid) {
+    for (int e = tid; e < kTri * 64; e += kThreads) {
+        const int f = e >> 6, lane = e & 63;
+        const int i = TRANS ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : 2 + ((f - 2) >> 1));
+        const int s = TRANS ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : (f - 2) & 1);
+        const int row = 16 * i + (lane & 15), c0 = 32 * s + 8 * (lane >> 4);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = TRANS ? m[c0 + j][row] : m[row][c0 + j];
+        const Frag<N> fr = split8<N>(x);
+#pragma unroll
+        for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(dst + ((int64_t)f * N + n) * 512 + lane * 8) = fr.p[n];
+    }
+}
+
+// One workgroup per (slot, value head). Tiles of K K^T and Q K^T by bf16 matrix
+// products; the 16 x 16 diagonal blocks of I + A inverted by forward substitution in
+// fp32 (one wave each), the blocks below by T_ij = -T_ii sum_k A_ik T_kj on the fp32
+// matrix instruction, one block diagonal at a time: nothing of T is rounded before
+// its parts are written.
+template <bool BF, int DK, bool BWD>
+__global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
+    using IO = Io<BF>;
+    using T = typename IO::T;
+    extern __shared__ __align__(16) unsigned char lds_raw[];
+    PrepLds<BF, DK>& l = *reinterpret_cast<PrepLds<BF, DK>*>(lds_raw);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = lane >> 4, col = lane & 15;
+    const int64_t slot = blockIdx.x;
+    const int h = blockIdx.y, hk = h / a.sh.group;
+    Range r;
+    int64_t c, n;
+    if (!find_chunk(a.seqs, slot, r, c, n)) return;
+    const int64_t tok = r.first + c * kC;
+    const int rows = (int)(r.len - c * kC < kC ? r.len - c * kC : kC);
+    const int64_t sh_idx = slot * a.sh.hv + h;
+    const T* kp = (const T*)a.k + tok * a.sh.ldk + (int64_t)hk * a.sh.dk;
+    const T* qp = (const T*)a.q + tok * a.sh.ldq + (int64_t)hk * a.sh.dk;
+
+    stage_rows<BF, DK>(l, kp, a.sh.ldk, rows, a.sh.dk, tid);
+    if (wave == 0) {
+        float gv = 0.f, bv = 0.f;
+        if (lane < rows) {
+            gv = (float)((const T*)a.g)[(tok + lane) * a.sh.hv + h];
+            bv = (float)((const T*)a.beta)[(tok + lane) * a.sh.hv + h];
+        }
+        double G = (double)gv < kMinLog ? kMinLog : (double)gv;  // a NaN stays one
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_up(G, d);
+            if (lane >= d) G += up;
+        }
+        const double last = __shfl(G, 63);
+        l.G[lane] = G;
+        l.beta[lane] = bv;
+        float* sc = a.out.sc + sh_idx * 3 * kC;
+        sc[lane] = expf((float)G);
+        sc[kC + lane] = expf((float)(last - G));
+        sc[2 * kC + lane] = bv;
+    }
+    __syncthreads();
+
+    // wave w: row tile w of A and P
+    {
+        f32x4 kk[4] = {}, qk[4] = {};
+        const int row = 16 * wave + col;
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s) {
+            const int k0 = 32 * s + 8 * g;
+            float x[8];
+            load8(&l.rows[row][k0], true, x);
+            const Frag<IO::NI> ka = split8<IO::NI>(x);
+            const Frag<IO::NI> qa = to_frag(load_raw(qp + row * a.sh.ldq + k0, row < rows && k0 < a.sh.dk));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= wave) {
+                    load8(&l.rows[16 * j + col][k0], true, x);
+                    const Frag<IO::NI> kb = split8<IO::NI>(x);
+                    kk[j] = mma(ka, kb, kk[j]);
+                    qk[j] = mma(qa, kb, qk[j]);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ti = 16 * wave + 4 * g + i, tj = 16 * j + col;
+                float av = 0.f, pv = 0.f;
+                if (tj <= ti) {
+                    const float d = expf((float)(l.G[ti] - l.G[tj]));
+                    pv = d * qk[j][i];
+                    if (tj < ti) av = l.beta[ti] * d * kk[j][i];
+                }
+                l.a[ti][tj] = av;
+                l.p[ti][tj] = pv;
+            }
+    }
+    __syncthreads();
+    if (!BWD)
+        write_tri<BF ? 1 : 3, false>(l.p, a.out.p + sh_idx * kTri * (BF ? 1 : 3) * 512, tid);
+    else
+        write_tri<IO::NS, true>(l.p, a.out.pt + sh_idx * kTri * IO::NS * 512, tid);
+    if (h == hk * a.sh.group)
+        write_transposed<BF, DK>(l, (T*)a.out.kt + (slot * a.sh.hk + hk) * (DK / 16) * 1024, tid);
+    __syncthreads();
+
+    // T over P. Diagonal block `wave`: column `col` of the inverse, x_i = e_i - sum_{j<i} A_ij x_j
+    {
+        const int b = 16 * wave;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == col ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v = fmaf(-l.a[b + i][b + j], x[j], v);
+            x[i] = v;
+        }
+        if (g == 0)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l.p[b + i][b + col] = x[i];
+        // the blocks above the diagonal are zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j > wave)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l.p[b + 4 * g + i][16 * j + col] = 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+        if (wave >= d) {
+            const int j = wave - d, b = 16 * wave;
+            f32x4 x = {};
+            for (int k = j; k < wave; ++k)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    x = __builtin_amdgcn_mfma_f32_16x16x4f32(l.a[b + col][16 * k + 4 * s + g],
+                                                             l.p[16 * k + 4 * s + g][16 * j + col], x, 0, 0, 0);
+            // rows 4g + s of x in this lane: contract over {4g + s : g} at each s
+            f32x4 y = {};
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                y = __builtin_amdgcn_mfma_f32_16x16x4f32(l.p[b + col][b + 4 * g + s], x[s], y, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l.p[b + 4 * g + i][16 * j + col] = -y[i];
+        }
+        __syncthreads();
+    }
+    write_tri<IO::NS, false>(l.p, a.out.t + sh_idx * kTri * IO::NS * 512, tid);
+    if (BWD) {
+        write_tri<IO::NS, true>(l.p, a.out.tt + sh_idx * kTri * IO::NS * 512, tid);
+        if (h == hk * a.sh.group) {
+            stage_rows<BF, DK>(l, qp, a.sh.ldq, rows, a.sh.dk, tid);
+            __syncthreads();
+            write_transposed<BF, DK>(l, (T*)a.out.qt + (slot * a.sh.hk + hk) * (DK / 16) * 1024, tid);
+        }
+    }
+}
+
+}  // namespace delta
+}  // namespace hy

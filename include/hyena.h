@@ -624,6 +624,94 @@ hyena_status_t hyena_conv3d_forward_per_sample(hyena_plan3d_t plan, int64_t B, c
                                                const void* x, const void* spec, const float* bias, void* y,
                                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: a causal mixer of linear cost beside the long convolutions
+ * above, with a state of constant size. Every sequence and value head has a
+ * state S [dim_k][dim_v]; for each token in order, with the log decay g (g <= 0
+ * forgets, 0 keeps) and the write strength beta,
+ *   S <- exp(g) S;   S <- S + beta k (v - S^T k)^T;   o = scale S^T q,
+ * so the state's answer to the key k moves from S^T k towards v. The value heads
+ * share query and key heads in groups: value head h uses query/key head
+ * h / (heads_v / heads_k). Keys should have at most unit length (hyena_qk_norm_*
+ * gives it): with beta in [0, 1] the update is then a contraction.
+ *
+ * The calls take no plan: they run on the current device, which must be the one
+ * that holds the buffers. States are fp32 [dim_k][dim_v], row-major. Tokens lie
+ * behind each other, either as N sequences of tokens / N each (seq_start NULL) or
+ * packed, sequence n being tokens seq_start[n] .. seq_start[n+1]-1 (N + 1 offsets
+ * in device memory, not decreasing, seq_start[N] <= tokens; sequences may be
+ * empty). Offsets are read on the device: ones that break this rule give undefined
+ * results but no access outside the buffers. Rows that belong to no sequence are
+ * neither read nor written.
+ * ------------------------------------------------------------------------ */
+typedef struct hyena_delta_params_s {
+    int64_t heads_k, heads_v; /* heads_v a multiple of heads_k */
+    int64_t dim_k, dim_v;     /* multiples of 8; dim_k <= 128, dim_v <= 256 */
+    hyena_dtype_t dtype;      /* of q, k, v, g, beta, o and their gradients */
+    float scale;              /* of the queries, usually dim_k^-1/2; finite */
+} hyena_delta_params_t;
+
+/* Device arrays of one call. Token t's heads lie behind each other at
+ *   q + t*ldq, k + t*ldk [heads_k][dim_k],   v + t*ldv [heads_v][dim_v]
+ * (elements; q, k and v may be column ranges of one projection's rows); ld* at
+ * least the heads' width, a multiple of 16 bytes and at most 2^31.
+ * g, beta [tokens][heads_v], dense, aligned to their elements. */
+typedef struct hyena_delta_inputs_s {
+    const void* q;
+    int64_t ldq;
+    const void* k;
+    int64_t ldk;
+    const void* v;
+    int64_t ldv;
+    const void* g;
+    const void* beta;
+} hyena_delta_inputs_t;
+
+/* Bytes of workspace hyena_delta_forward needs (chunks of 64 tokens: their
+ * triangular factors, decays and transposed keys). Returns 0 for arguments that
+ * the call would refuse, and where there are no tokens. seq_start is not read:
+ * only whether it is NULL matters. */
+size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                   const int64_t* seq_start);
+
+/* The gated delta rule over whole sequences, in chunks of 64 tokens on the matrix
+ * cores.
+ *   state_in  [N][heads_v][dim_k][dim_v] fp32, device, or NULL (zeros)
+ *   o         [tokens][heads_v][dim_v] of the dtype, device (output)
+ *   state_out [N][heads_v][dim_k][dim_v] fp32, device (output), or NULL; may be
+ *             state_in itself. An empty sequence passes its state on.
+ *   workspace at least hyena_delta_workspace_bytes(...) bytes, 16-byte aligned
+ * The state is held in fp32 from the first token to the last; bf16 outputs are
+ * rounded once from sums whose operands are bf16 or sums of two bf16 parts, fp32
+ * results have the accuracy of fp32 products. Decays below exp(-200) count as 0 and
+ * g = -inf resets the state. Results do not depend on the other sequences of the
+ * call, bit for bit when the sequence starts at the same offset within 64 tokens or
+ * not. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
+ * pointers, sizes below 1, tokens not a multiple of N without seq_start, heads_v not
+ * a multiple of heads_k, bad ld or scale), HYENA_ERR_UNSUPPORTED (dims outside the
+ * ranges above, heads_v > 65535, N > 2^24, tokens > 2^31, or more than 2^30 (chunk,
+ * head) or 2^26 (sequence, head) pairs), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                   const int64_t* seq_start, const hyena_delta_inputs_t* in, const float* state_in,
+                                   void* o, float* state_out, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* The recurrent form: T further tokens (one when answering token by token, a few
+ * drafted ones) of each of B rows, row b's tokens at b*T .. b*T + T - 1 of the
+ * inputs and of o [B*T][heads_v][dim_v].
+ *   states [num_states][heads_v][dim_k][dim_v] fp32, device: read and updated in
+ *          place, once each
+ *   slots  [B] int32, device: the state of every row, or NULL (row b has state b,
+ *          num_states >= B). Rows that name the same slot are taken in order, as
+ *          successive tokens of it. A row whose slot is outside [0, num_states) gives
+ *          zeros and touches no state (rows that pad a captured batch).
+ * All arithmetic is fp32. Enqueued on `stream`; no workspace. Errors as
+ * hyena_delta_forward, of N = B and tokens = B*T; HYENA_ERR_INVALID_ARG also for
+ * B, T or num_states below 1 and for NULL slots with num_states < B. */
+hyena_status_t hyena_delta_step(const hyena_delta_params_t* params, int64_t B, int64_t T,
+                                const hyena_delta_inputs_t* in, float* states, int64_t num_states,
+                                const int32_t* slots, void* o, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* hyena_status_string(hyena_status_t s);
 
