@@ -50,12 +50,16 @@ struct Io<true> {
     using T = __bf16;
     static constexpr int NI = 1;  // parts of an input operand (exact)
     static constexpr int NS = 2;  // parts of the state, T and the written values
+    static constexpr int NO = 2;  // parts of the state and of u against Q and P
+    static constexpr int NP = 1;  // parts of P
 };
 template <>
 struct Io<false> {
     using T = float;
     static constexpr int NI = 3;
     static constexpr int NS = 3;
+    static constexpr int NO = 3;
+    static constexpr int NP = 3;
 };
 
 template <int N>
@@ -93,6 +97,30 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
             if (j >= 0 && j < NB) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
         }
     return c;
+}
+
+// the same for J right-hand operands, products of one part pair next to each other so
+// that consecutive instructions do not wait for each other's sums
+template <int NA, int NB, int J>
+__device__ __forceinline__ void mma_each(const Frag<NA>& a, const Frag<NB> (&b)[J], f32x4 (&c)[J]) {
+    constexpr int M = NA > NB ? NA : NB;
+#pragma unroll
+    for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int k = s - i;
+            if (k >= 0 && k < NB)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[j].p[k], c[j], 0, 0, 0);
+        }
+}
+template <int N, int M>
+__device__ __forceinline__ Frag<N> first_parts(const Frag<M>& f) {
+    Frag<N> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n) r.p[n] = f.p[n];
+    return r;
 }
 
 // eight consecutive elements as fp32 / as an operand; zeros where !ok
@@ -141,6 +169,71 @@ __device__ __forceinline__ Frag<3> to_frag(const Raw32& r) {
 }
 template <bool BF>
 using Raw = decltype(load_raw((const typename Io<BF>::T*)nullptr, true));
+
+// Rows of a chunk as a buffer resource: `rows` (0 or less: none) rows of `width` bytes,
+// `ld` bytes apart. Loads outside give zeros and stores outside are dropped by the
+// hardware's range check, so ragged chunks and padded columns need no branches (whose
+// merges would make every wait a full one). Offset kNoElem is outside any of them.
+constexpr uint32_t kNoElem = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t RowBuf;
+__device__ __forceinline__ RowBuf row_buf(const void* base, int64_t rows, uint32_t ld, uint32_t width) {
+    const int n = rows > kC ? kC : (int)rows;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n > 0 ? (int)((n - 1) * ld + width) : 0,
+                                             0x00020000);
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void buf_raw(RowBuf b, uint32_t off, Raw16& r) {
+    r.v = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+}
+__device__ __forceinline__ void buf_raw(RowBuf b, uint32_t off, Raw32& r) {
+    r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
+    r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off + 16, 0, 0));
+}
+// N (1 or 2) consecutive elements: raw registers, their values, and back
+template <bool BF, int N>
+struct Cols {
+    uint32_t w[BF ? 1 : N];
+};
+template <bool BF, int N>
+__device__ __forceinline__ void buf_cols(RowBuf b, uint32_t off, Cols<BF, N>& c) {
+    if constexpr (BF && N == 1)
+        c.w[0] = __builtin_amdgcn_raw_buffer_load_b16(b, (int)off, 0, 0);
+    else if constexpr (!BF && N == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0));
+        c.w[0] = v[0];
+        c.w[1] = v[1];
+    } else
+        c.w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
+}
+template <bool BF, int N>
+__device__ __forceinline__ float col_value(const Cols<BF, N>& c, int j) {
+    if constexpr (BF) return __uint_as_float(j == 0 ? c.w[0] << 16 : c.w[0] & 0xffff0000u);
+    return __uint_as_float(c.w[BF ? 0 : j]);
+}
+template <bool BF, int N>
+__device__ __forceinline__ void buf_store(RowBuf b, uint32_t off, const float (&x)[N]) {
+    if constexpr (BF) {
+        typedef __bf16 bf16xn __attribute__((ext_vector_type(N)));
+        bf16xn v;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = (__bf16)x[j];
+        if constexpr (N == 2)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, (int)off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), b, (int)off, 0, 0);
+    } else if constexpr (N == 2) {
+        const u32x2 v = {__float_as_uint(x[0]), __float_as_uint(x[1])};
+        __builtin_amdgcn_raw_buffer_store_b64(v, b, (int)off, 0, 0);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), b, (int)off, 0, 0);
+    }
+}
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 
 // N (1 or 2) consecutive elements
 template <int N>
@@ -289,6 +382,7 @@ struct Prep {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxSeqs = int64_t(1) << 24;
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // elements: 64 rows stay below 2^31 bytes
 
 struct PrepArgs;
 struct ScanArgs;

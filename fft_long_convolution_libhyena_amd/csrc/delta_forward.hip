@@ -33,12 +33,13 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
         const int64_t ld[] = {in->ldq, in->ldk, in->ldv};
         const int64_t width[] = {p->heads_k * p->dim_k, p->heads_k * p->dim_k, p->heads_v * p->dim_v};
         for (int i = 0; i < 3; ++i)
-            if (ld[i] < width[i] || ld[i] % v || ld[i] > (int64_t(1) << 31)) return HYENA_ERR_INVALID_ARG;
+            if (ld[i] < width[i] || ld[i] % v || ld[i] > kMaxLd) return HYENA_ERR_INVALID_ARG;
         c.shape.ldq = in->ldq;
         c.shape.ldk = in->ldk;
         c.shape.ldv = in->ldv;
     }
-    if (N > kMaxSeqs || tokens > kMaxTokens) return HYENA_ERR_UNSUPPORTED;
+    if (N > kMaxSeqs || tokens > kMaxTokens || p->heads_v * p->dim_v > kMaxLd || p->heads_k * p->dim_k > kMaxLd)
+        return HYENA_ERR_UNSUPPORTED;
     c.seqs.start = seq_start;
     c.seqs.N = N;
     c.seqs.tokens = tokens;

@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     }
     __syncthreads();
     if (!BWD)
-        write_tri<BF ? 1 : 3, false>(l.p, a.out.p + sh_idx * kTri * (BF ? 1 : 3) * 512, tid);
+        write_tri<IO::NP, false>(l.p, a.out.p + sh_idx * kTri * IO::NP * 512, tid);
     else
         write_tri<IO::NS, true>(l.p, a.out.pt + sh_idx * kTri * IO::NS * 512, tid);
     if (h == hk * a.sh.group)

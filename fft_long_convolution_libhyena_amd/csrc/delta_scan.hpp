@@ -7,7 +7,7 @@
 // registers; the right-hand operands (the state's parts, the residual e, the written
 // values u) pass between the waves through LDS as fragments, with three barriers a
 // chunk. The next chunk's left operands are loaded as soon as this chunk's are used;
-// the barriers leave those loads in flight.
+// the barriers leave those loads in flight, and no load is conditional.
 #pragma once
 #include "delta.hpp"
 
@@ -32,23 +32,22 @@ enum { kScanOut = 0, kScanKeep = 1 };
 template <bool BF, int DK, int NT>
 struct ScanLds {
     using IO = Io<BF>;
-    static constexpr int KS = DK / 32;
-    static constexpr int NU = BF ? 1 : 3;  // parts of u against P: o is rounded to bf16 right after
-    alignas(16) __bf16 s[KS][NT][IO::NS][512];
+    alignas(16) __bf16 s[DK / 32][NT][IO::NS][512];
     alignas(16) __bf16 e[2][NT][IO::NS][512];
-    alignas(16) __bf16 u[2][NT][NU][512];
+    alignas(16) __bf16 u[2][NT][IO::NO][512];
     alignas(16) __bf16 ku[2][NT][IO::NS][512];
 };
 
 template <bool BF, int DK, int NT, int MODE>
-__global__ __launch_bounds__(kThreads) void k_delta_scan(ScanArgs a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_delta_scan(ScanArgs a) {
     using IO = Io<BF>;
     using T = typename IO::T;
     constexpr int KS = DK / 32, MT = DK / 64;
-    constexpr int NS = IO::NS, NP = BF ? 1 : 3;
+    constexpr int NS = IO::NS, NP = IO::NP, NO = IO::NO;
+    constexpr uint32_t E = sizeof(T);
     extern __shared__ __align__(16) unsigned char lds_raw[];
     ScanLds<BF, DK, NT>& l = *reinterpret_cast<ScanLds<BF, DK, NT>*>(lds_raw);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, col = lane & 15;
     // column blocks of one head sit 8 workgroups apart, so that they land on one XCD
     // and share its L2 for the head's operands
@@ -59,8 +58,9 @@ __global__ __launch_bounds__(kThreads) void k_delta_scan(ScanArgs a) {
     if (pair >= a.seqs.N * hv) return;
     const int64_t n = pair / hv;
     const int h = (int)(pair % hv), hk = h / a.sh.group;
-    const Range r = seq_range(a.seqs, n);
-    const int64_t nch = (r.len + kC - 1) / kC;
+    const Range rr = seq_range(a.seqs, n);
+    const int64_t first = uniform64(rr.first), len = uniform64(rr.len), slot0 = uniform64(rr.slot0);
+    const int64_t nch = (len + kC - 1) / kC;
     const int dk = a.sh.dk, dv = a.sh.dv;
     const int c0 = blk * 16 * NT + NT * col;  // this lane's first column
     const bool cok = c0 < dv;
@@ -77,54 +77,77 @@ __global__ __launch_bounds__(kThreads) void k_delta_scan(ScanArgs a) {
             for (int j = 0; j < NT; ++j) S[m][j][i] = x[j];
         }
 
-    const int64_t row = 16 * wave + col;   // token of this lane's operand rows
-    const int64_t drow = 16 * wave + 4 * g;  // first of this lane's four result rows
-    const T* kp = (const T*)a.k + (r.first + row) * a.sh.ldk + (int64_t)hk * dk + 8 * g;
-    const T* qp = (const T*)a.q + (r.first + row) * a.sh.ldq + (int64_t)hk * dk + 8 * g;
-    const T* vp = (const T*)a.v + (r.first + drow) * a.sh.ldv + (int64_t)h * dv + c0;
-    T* op = (T*)(MODE == kScanOut ? a.o : a.u) + ((r.first + drow) * hv + h) * (int64_t)dv + c0;
+    const int row = 16 * wave + col;     // token of this lane's operand rows
+    const int drow = 16 * wave + 4 * g;  // first of this lane's four result rows
+    const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E, ldv = (uint32_t)a.sh.ldv * E;
+    const uint32_t ldo = (uint32_t)(hv * dv) * E;
+    uint32_t koff[KS], qoff[KS], voff[4], ooff[4], soff[MT][4];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const uint32_t k = 32 * s + 8 * g;
+        koff[s] = (int)k < dk ? row * ldk + k * E : kNoElem;
+        qoff[s] = (int)k < dk ? row * ldq + k * E : kNoElem;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        voff[i] = cok ? (drow + i) * ldv + c0 * E : kNoElem;
+        ooff[i] = cok ? (drow + i) * ldo + c0 * E : kNoElem;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 16 * (wave * MT + m) + 4 * g + i;
+            soff[m][i] = cok && k < dk ? (uint32_t)(k * dv + c0) * E : kNoElem;
+        }
+    const T* kbase = (const T*)a.k + first * a.sh.ldk + (int64_t)hk * dk;
+    const T* qbase = (const T*)a.q + first * a.sh.ldq + (int64_t)hk * dk;
+    const T* vbase = (const T*)a.v + first * a.sh.ldv + (int64_t)h * dv;
+    T* obase = (T*)(MODE == kScanOut ? a.o : a.u) + (first * hv + h) * (int64_t)dv;
 
     Raw<BF> K[KS], Q[KS], KT[MT][2];
     Frag<NS> Tf[2];
     Frag<NP> Pf[2];
-    float V[4][NT];
+    Cols<BF, NT> V[4];
     f32x4 gam, kap, bet;
     float glast = 0.f;
     auto load_k = [&](int64_t c) {
-        const bool ok = c * kC + row < r.len;
+        const RowBuf b = row_buf(kbase + c * kC * a.sh.ldk, len - c * kC, ldk, dk * E);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) K[s] = load_raw(kp + c * kC * a.sh.ldk + 32 * s, ok && 32 * s + 8 * g < dk);
+        for (int s = 0; s < KS; ++s) buf_raw(b, koff[s], K[s]);
     };
     auto load_q = [&](int64_t c) {
-        const bool ok = c * kC + row < r.len;
+        const RowBuf b = row_buf(qbase + c * kC * a.sh.ldq, len - c * kC, ldq, dk * E);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) Q[s] = load_raw(qp + c * kC * a.sh.ldq + 32 * s, ok && 32 * s + 8 * g < dk);
+        for (int s = 0; s < KS; ++s) buf_raw(b, qoff[s], Q[s]);
     };
     auto load_v = [&](int64_t c) {
+        const RowBuf b = row_buf(vbase + c * kC * a.sh.ldv, len - c * kC, ldv, dv * E);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_cols<NT>(vp + (c * kC + i) * a.sh.ldv, cok && c * kC + drow + i < r.len, V[i]);
+        for (int i = 0; i < 4; ++i) buf_cols<BF, NT>(b, voff[i], V[i]);
     };
     auto load_sc = [&](int64_t c) {
-        const float* sc = a.prep.sc + ((r.slot0 + c) * hv + h) * 3 * kC;
+        const float* sc = a.prep.sc + ((slot0 + c) * hv + h) * 3 * kC;
         gam = *reinterpret_cast<const f32x4*>(sc + drow);
         kap = *reinterpret_cast<const f32x4*>(sc + kC + drow);
         bet = *reinterpret_cast<const f32x4*>(sc + 2 * kC + drow);
         glast = sc[kC - 1];
     };
-    // every fragment of row tile `wave`: one step for tiles 0 and 1, two below
+    // every fragment of row tile `wave`: one step for tiles 0 and 1 (read twice, so
+    // that no load is conditional), two below
+    const int f0 = lower_frag(wave, 0), f1 = lower_frag(wave, wave >= 2 ? 1 : 0);
     auto load_t = [&](int64_t c) {
-        const __bf16* p = a.prep.t + ((r.slot0 + c) * hv + h) * kTri * NS * 512;
-        Tf[0] = get_frag<NS>(p + lower_frag(wave, 0) * NS * 512, 512, lane);
-        if (wave >= 2) Tf[1] = get_frag<NS>(p + lower_frag(wave, 1) * NS * 512, 512, lane);
+        const __bf16* p = a.prep.t + ((slot0 + c) * hv + h) * kTri * NS * 512;
+        Tf[0] = get_frag<NS>(p + f0 * NS * 512, 512, lane);
+        Tf[1] = get_frag<NS>(p + f1 * NS * 512, 512, lane);
     };
     auto load_p = [&](int64_t c) {
-        const __bf16* p = a.prep.p + ((r.slot0 + c) * hv + h) * kTri * NP * 512;
-        Pf[0] = get_frag<NP>(p + lower_frag(wave, 0) * NP * 512, 512, lane);
-        if (wave >= 2) Pf[1] = get_frag<NP>(p + lower_frag(wave, 1) * NP * 512, 512, lane);
+        const __bf16* p = a.prep.p + ((slot0 + c) * hv + h) * kTri * NP * 512;
+        Pf[0] = get_frag<NP>(p + f0 * NP * 512, 512, lane);
+        Pf[1] = get_frag<NP>(p + f1 * NP * 512, 512, lane);
     };
     auto load_kt = [&](int64_t c) {
-        const T* p = (const T*)a.prep.kt + ((r.slot0 + c) * a.sh.hk + hk) * (DK / 16) * 1024 + lane * 8;
+        const T* p = (const T*)a.prep.kt + ((slot0 + c) * a.sh.hk + hk) * (DK / 16) * 1024 + lane * 8;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -140,126 +163,148 @@ __global__ __launch_bounds__(kThreads) void k_delta_scan(ScanArgs a) {
                 put_rows<NS>(&l.s[t >> 1][j][0][0], 512, t & 1, lane, x);
             }
     };
+    // outputs of chunk c from Q S and the fragments of u, one chunk late: these
+    // products run while the next chunk's first fragments come from LDS
+    f32x4 qs[NT];
+    Frag<NO> uf[2][NT];
+    auto finish = [&](int64_t c) {
+        f32x4 o1[NT] = {};
+        mma_each(Pf[0], uf[0], qs);
+        if (wave >= 2) mma_each(Pf[1], uf[1], o1);
+        const RowBuf b = row_buf(obase + c * kC * hv * (int64_t)dv, len - c * kC, ldo, dv * E);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[j] = a.sh.scale * (qs[j][i] + o1[j][i]);
+            buf_store<BF, NT>(b, ooff[i], x);
+        }
+    };
     if (nch > 0) {
         load_k(0);
-        load_sc(0);
         load_v(0);
+        load_sc(0);
         if (MODE == kScanOut) load_q(0);
         load_t(0);
-        if (MODE == kScanOut) load_p(0);
         load_kt(0);
+        if (MODE == kScanOut) load_p(0);
         put_state();
     }
     for (int64_t c = 0; c < nch; ++c) {
         const int64_t nx = c + 1 < nch ? c + 1 : c;  // the last chunk loads itself again
         if (MODE == kScanKeep) {
-            T* sp = (T*)a.s0 + ((r.slot0 + c) * hv + h) * (int64_t)dk * dv + c0;
+            const RowBuf b = __builtin_amdgcn_make_buffer_rsrc(
+                (T*)a.s0 + ((slot0 + c) * hv + h) * (int64_t)dk * dv, 0, (int)(dk * dv * E), 0x00020000);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int k = 16 * (wave * MT + m) + 4 * g + i;
                     float x[NT];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) x[j] = S[m][j][i];
-                    if (cok && k < dk) store_cols<NT>(sp + (int64_t)k * dv, x);
+                    buf_store<BF, NT>(b, soff[m][i], x);
                 }
         }
         lds_barrier();  // the state's fragments are in place
-        f32x4 ks[NT] = {}, qs[NT] = {};
+        Frag<NS> sf[KS][NT];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const Frag<IO::NI> ka = to_frag(K[s]);
-            Frag<IO::NI> qa;
-            if (MODE == kScanOut) qa = to_frag(Q[s]);
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const Frag<NS> sf = get_frag<NS>(&l.s[s][j][0][0], 512, lane);
-                ks[j] = mma(ka, sf, ks[j]);
-                if (MODE == kScanOut) {
-                    Frag<NP> s1;  // one part of the state against bf16 outputs
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) s1.p[i] = sf.p[i];
-                    qs[j] = mma(qa, s1, qs[j]);
-                }
-            }
+            for (int j = 0; j < NT; ++j) sf[s][j] = get_frag<NS>(&l.s[s][j][0][0], 512, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if (MODE == kScanOut && c > 0) {
+            finish(c - 1);
+            load_p(c);
         }
+        f32x4 ks[NT] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) mma_each(to_frag(K[s]), sf[s], ks);
         load_k(nx);
-        if (MODE == kScanOut) load_q(nx);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = bet[i] * (V[i][j] - gam[i] * ks[j][i]);
+            for (int i = 0; i < 4; ++i) x[i] = bet[i] * (col_value(V[i], j) - gam[i] * ks[j][i]);
             put_rows<NS>(&l.e[wave >> 1][j][0][0], 512, wave & 1, lane, x);
         }
         load_v(nx);
         lds_barrier();  // e
-        f32x4 u[NT] = {};
+        Frag<NS> ef[2][NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            u[j] = mma(Tf[0], get_frag<NS>(&l.e[0][j][0][0], 512, lane), u[j]);
-            if (wave >= 2) u[j] = mma(Tf[1], get_frag<NS>(&l.e[1][j][0][0], 512, lane), u[j]);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ef[s][j] = get_frag<NS>(&l.e[s][j][0][0], 512, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if (MODE == kScanOut) {  // while e's fragments arrive
+#pragma unroll
+            for (int j = 0; j < NT; ++j) qs[j] = f32x4{};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Frag<NO> so[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) so[j] = first_parts<NO>(sf[s][j]);
+                mma_each(to_frag(Q[s]), so, qs);
+            }
+            load_q(nx);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qs[j][i] *= gam[i];
         }
+        f32x4 u[NT] = {}, u1[NT] = {};
+        mma_each(Tf[0], ef[0], u);
+        if (wave >= 2) mma_each(Tf[1], ef[1], u1);
         load_t(nx);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             float x[4], y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = u[j][i];
-                y[i] = kap[i] * u[j][i];
+                x[i] = u[j][i] + u1[j][i];
+                y[i] = kap[i] * x[i];
+                u[j][i] = x[i];
             }
-            if (MODE == kScanOut) put_rows<NP>(&l.u[wave >> 1][j][0][0], 512, wave & 1, lane, x);
+            if (MODE == kScanOut) put_rows<NO>(&l.u[wave >> 1][j][0][0], 512, wave & 1, lane, x);
             put_rows<NS>(&l.ku[wave >> 1][j][0][0], 512, wave & 1, lane, y);
         }
-        if (MODE == kScanKeep)
+        if (MODE == kScanKeep) {
+            const RowBuf b = row_buf(obase + c * kC * hv * (int64_t)dv, len - c * kC, ldo, dv * E);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (cok && c * kC + drow + i < r.len) {
-                    float x[NT];
+            for (int i = 0; i < 4; ++i) {
+                float x[NT];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j] = u[j][i];
-                    store_cols<NT>(op + (c * kC + i) * hv * (int64_t)dv, x);
-                }
+                for (int j = 0; j < NT; ++j) x[j] = u[j][i];
+                buf_store<BF, NT>(b, ooff[i], x);
+            }
+        }
+        const float gl = glast;
+        load_sc(nx);
         lds_barrier();  // u
+        Frag<NS> kf[2][NT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) kf[s][j] = get_frag<NS>(&l.ku[s][j][0][0], 512, lane);
+        if (MODE == kScanOut)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) uf[s][j] = get_frag<NO>(&l.u[s][j][0][0], 512, lane);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][j][i] *= glast;
+                for (int i = 0; i < 4; ++i) S[m][j][i] *= gl;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const Frag<NS> uf = get_frag<NS>(&l.ku[s][j][0][0], 512, lane);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) S[m][j] = mma(to_frag(KT[m][s]), uf, S[m][j]);
-            }
+            for (int m = 0; m < MT; ++m) mma_each(to_frag(KT[m][s]), kf[s], S[m]);
         load_kt(nx);
         put_state();
-        if (MODE == kScanOut) {
-            f32x4 o[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[j][i] = gam[i] * qs[j][i];
-                o[j] = mma(Pf[0], get_frag<NP>(&l.u[0][j][0][0], 512, lane), o[j]);
-                if (wave >= 2) o[j] = mma(Pf[1], get_frag<NP>(&l.u[1][j][0][0], 512, lane), o[j]);
-            }
-            load_p(nx);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (cok && c * kC + drow + i < r.len) {
-                    float x[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j] = a.sh.scale * o[j][i];
-                    store_cols<NT>(op + (c * kC + i) * hv * (int64_t)dv, x);
-                }
-        }
-        load_sc(nx);
     }
+    if (MODE == kScanOut && nch > 0) finish(nch - 1);
     if (a.s_out)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
