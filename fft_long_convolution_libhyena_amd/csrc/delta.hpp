@@ -62,25 +62,44 @@ struct Io<false> {
     static constexpr int NP = 3;
 };
 
+// Row r of row tile t as the scans number them: the pair of tiles 2s, 2s + 1 covers
+// rows 32 s .. 32 s + 31 such that the result rows that one lane holds in both (4 g + i
+// of each) are rows 32 s + 8 g .. + 7 in order, which is what the same lane must hold
+// of a right-hand operand. Results become operands without leaving their lane.
+__device__ __forceinline__ constexpr int tile_row(int t, int r) {
+    return 32 * (t >> 1) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+}
 template <int N>
 struct Frag {
     bf16x8 p[N];
 };
 
+// two values rounded to bf16 in one instruction; and back
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+}
 template <int N>
 __device__ __forceinline__ Frag<N> split8(const float (&x)[8]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     Frag<N> f;
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = x[i];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
+        u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __bf16 h = (__bf16)r[i];
-            f.p[n][i] = h;
-            if (n + 1 < N) r[i] -= (float)h;
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack2(r[2 * i], r[2 * i + 1]);
+            if (n + 1 < N) {
+                r[2 * i] -= __uint_as_float(w[i] << 16);
+                r[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
         }
+        f.p[n] = __builtin_bit_cast(bf16x8, w);
+    }
     return f;
 }
 
@@ -99,10 +118,10 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
     return c;
 }
 
-// the same for J right-hand operands, products of one part pair next to each other so
-// that consecutive instructions do not wait for each other's sums
+// the same for J row tiles, products of one part pair next to each other so that
+// consecutive instructions do not wait for each other's sums
 template <int NA, int NB, int J>
-__device__ __forceinline__ void mma_each(const Frag<NA>& a, const Frag<NB> (&b)[J], f32x4 (&c)[J]) {
+__device__ __forceinline__ void mma_tiles(const Frag<NA> (&a)[J], const Frag<NB>& b, f32x4* c) {
     constexpr int M = NA > NB ? NA : NB;
 #pragma unroll
     for (int s = M - 1; s >= 0; --s)
@@ -112,7 +131,7 @@ __device__ __forceinline__ void mma_each(const Frag<NA>& a, const Frag<NB> (&b)[
             if (k >= 0 && k < NB)
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b[j].p[k], c[j], 0, 0, 0);
+                    c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j].p[i], b.p[k], c[j], 0, 0, 0);
         }
 }
 template <int N, int M>
@@ -168,7 +187,15 @@ __device__ __forceinline__ Frag<3> to_frag(const Raw32& r) {
     return split8<3>(x);
 }
 template <bool BF>
-using Raw = decltype(load_raw((const typename Io<BF>::T*)nullptr, true));
+struct RawOf {
+    using type = Raw16;
+};
+template <>
+struct RawOf<false> {
+    using type = Raw32;
+};
+template <bool BF>
+using Raw = typename RawOf<BF>::type;
 
 // Rows of a chunk as a buffer resource: `rows` (0 or less: none) rows of `width` bytes,
 // `ld` bytes apart. Loads outside give zeros and stores outside are dropped by the
@@ -181,6 +208,9 @@ __device__ __forceinline__ RowBuf row_buf(const void* base, int64_t rows, uint32
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n > 0 ? (int)((n - 1) * ld + width) : 0,
                                              0x00020000);
 }
+__device__ __forceinline__ RowBuf plain_buf(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void buf_raw(RowBuf b, uint32_t off, Raw16& r) {
@@ -190,6 +220,112 @@ __device__ __forceinline__ void buf_raw(RowBuf b, uint32_t off, Raw32& r) {
     r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 0));
     r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off + 16, 0, 0));
 }
+__device__ __forceinline__ f32x4 buf_f4(RowBuf b, uint32_t off, int soff) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, soff, 0));
+}
+// 64 rows of DK elements in LDS as bf16 parts, read as operands along the rows (K S, Q S)
+// or across them (K^T u, by the transposing LDS read). Rows are 64 bytes longer than
+// their data, and eight rows shift by 16 bytes: both reads then spread over all banks.
+template <int NI, int DK>
+struct Tile {
+    static constexpr int pitch = 2 * DK + 64;
+    alignas(16) unsigned char b[NI][kC * pitch];
+    __device__ static constexpr int at(int row, int k) { return row * pitch + ((row >> 3) & 3) * 16 + 2 * k; }
+    // row tile t, elements 32 s ..: lane (row tile_row(t, col), elements 32 s + 8 g ..)
+    __device__ __forceinline__ Frag<NI> rows(int lane, int t, int s) const {
+        const int col = lane & 15, g = lane >> 4;
+        Frag<NI> f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            f.p[n] = *reinterpret_cast<const bf16x8*>(b[n] + at(tile_row(0, col), 8 * g) +
+                                                      (4 * (t & 1) + 32 * (t >> 1)) * pitch + 64 * s);
+        return f;
+    }
+    // column tile m, rows 32 s ..: lane (element tile_row(m, col), rows 32 s + 8 g ..). The
+    // transposing read gives lane i of 16 element i % 4 of the four 8-byte pieces that
+    // lanes i/4, i/4 + 4, i/4 + 8 and i/4 + 12 address: one column, four rows.
+    __device__ __forceinline__ Frag<NI> cols(int lane, int m, int s) const {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* Lds4;
+        const int r = lane & 15, g = lane >> 4;
+        Frag<NI> f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const unsigned char* p = b[n] + at(8 * g + (r >> 2), 8 * (r & 3)) + 32 * s * pitch + 64 * (m >> 1) + 8 * (m & 1);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(p + 4 * pitch));
+            typedef short s16x8 __attribute__((ext_vector_type(8)));
+            f.p[n] = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        return f;
+    }
+};
+
+// 64 rows of CB columns of v in LDS (bf16), read as results lie: lane (column, four rows)
+template <int CB>
+struct ColTile {
+    static constexpr int pitch = 2 * CB + 16;
+    alignas(16) unsigned char b[kC * pitch];
+    // rows 32 (t / 2) + 8 g + 4 (t % 2) .. + 3 of column c0 + lane % 16, by the transposing read
+    __device__ __forceinline__ u32x2 rows4(int lane, int t, int c0) const {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* Lds4;
+        const int r = lane & 15, g = lane >> 4;
+        const unsigned char* p = b + (8 * g + (r >> 2)) * pitch + 8 * (r & 3) + (32 * (t >> 1) + 4 * (t & 1)) * pitch + 2 * c0;
+        return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)p));
+    }
+};
+
+// One wave moves the tiles: 16 bytes a lane, 1 KiB an instruction, whole rows.
+template <bool BF, int DK>
+struct Stage {
+    static constexpr int EPL = BF ? 8 : 4, LR = DK / EPL, RI = 64 / LR, N = LR;
+    u32x4 r[N];
+    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int dk, int lane) {
+        const uint32_t k = (lane % LR) * EPL, E = BF ? 2 : 4;
+        const uint32_t off = (int)k < dk ? (lane / LR) * ld + k * E : kNoElem;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + i * RI * ld), 0, 0));
+    }
+    __device__ __forceinline__ void store(Tile<BF ? 1 : 3, DK>& t, int lane) const {
+        using TL = Tile<BF ? 1 : 3, DK>;
+        const int at = (lane / LR) * TL::pitch + 2 * (lane % LR) * EPL;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int o = at + i * RI * TL::pitch + ((i * RI >> 3) & 3) * 16;
+            if constexpr (BF) {
+                *reinterpret_cast<u32x4*>(t.b[0] + o) = r[i];
+            } else {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(r[i][j]);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    u32x2 w;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        w[j] = pack2(x[2 * j], x[2 * j + 1]);
+                        x[2 * j] -= __uint_as_float(w[j] << 16);
+                        x[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                    *reinterpret_cast<u32x2*>(t.b[n] + o) = w;
+                }
+            }
+        }
+    }
+};
+
+// part n of fragment f at byte `at` of a record
+template <int N>
+__device__ __forceinline__ Frag<N> buf_frag(RowBuf b, int at, int f, int lane) {
+    Frag<N> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        r.p[n] = __builtin_bit_cast(bf16x8, buf_f4(b, lane * 16, at + (f * N + n) * kFragBytes));
+    return r;
+}
+
 // N (1 or 2) consecutive elements: raw registers, their values, and back
 template <bool BF, int N>
 struct Cols {
@@ -276,30 +412,25 @@ __device__ __forceinline__ void store_cols(float* p, const float (&x)[N]) {
         p[0] = x[0];
 }
 
-// Four values of a D tile (rows 4g..4g+3 of 16-row tile `half` of a 32-row block)
-// into part n of the block's B fragment.
-template <int N>
-__device__ __forceinline__ void put_rows(__bf16* frag, int part_stride, int half, int lane, const float (&x)[4]) {
-    const int g = lane >> 4, col = lane & 15;
-    __bf16* p = frag + ((2 * half + (g >> 1)) * 16 + col) * 8 + (g & 1) * 4;
-    float r[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        bf16x4 h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = (__bf16)r[i];
-            if (n + 1 < N) r[i] -= (float)h[i];
-        }
-        *reinterpret_cast<bf16x4*>(p + n * part_stride) = h;
-    }
-}
 template <int N>
 __device__ __forceinline__ Frag<N> get_frag(const __bf16* frag, int part_stride, int lane) {
     Frag<N> f;
 #pragma unroll
     for (int n = 0; n < N; ++n) f.p[n] = *reinterpret_cast<const bf16x8*>(frag + n * part_stride + lane * 8);
     return f;
+}
+
+// Instruction order of the region before it: N times one matrix instruction followed by
+// V vector instructions and by M loads (a lone wave overlaps them only if they alternate).
+template <int N, int V, int M>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (V) __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+        if (M) __builtin_amdgcn_sched_group_barrier(0x020, M, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // LDS traffic of the workgroup is complete and every wave is here; loads from
@@ -369,15 +500,21 @@ struct Shape {
     float scale;
 };
 
-// Workspace of the chunk-parallel part, per (slot, value head) unless noted.
+// What the preparation leaves for every (slot, value head), one record of `rec` bytes:
+// fragments of T diag(beta) (and, for the forward, P; for the backward's second scan, T^T
+// and P^T in records of their own), then exp(G) [64], exp(G_last - G) [64], beta [64].
+template <bool BF>
+struct Rec {
+    static constexpr int t = 0;                                        // lower, NS parts
+    static constexpr int p = kTri * Io<BF>::NS * kFragBytes;           // lower, NP parts
+    static constexpr int sc = p + kTri * Io<BF>::NP * kFragBytes;
+    static constexpr int bytes = sc + 1024;
+    static constexpr int pt = kTri * Io<BF>::NS * kFragBytes;          // backward: T^T at 0, P^T here
+    static constexpr int back = 2 * kTri * Io<BF>::NS * kFragBytes;
+};
 struct Prep {
-    __bf16* t;    // T, lower fragments, NS parts
-    __bf16* p;    // P, lower fragments (forward)
-    __bf16* tt;   // T^T and P^T, upper fragments, NS parts (backward)
-    __bf16* pt;
-    void* kt;     // K^T fragments per (slot, key head): dk/16 row tiles x 2 steps
-    void* qt;     // Q^T likewise (backward)
-    float* sc;    // exp(G) [64], exp(G_last - G) [64], beta [64]
+    unsigned char* rec;   // [slot][value head]
+    unsigned char* back;  // [slot][value head] T^T and P^T, upper fragments (backward)
 };
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;

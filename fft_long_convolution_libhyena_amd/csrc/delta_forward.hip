@@ -56,19 +56,12 @@ size_t delta_prep_layout(const DeltaCall& c, bool bwd, unsigned char* base, Prep
     auto take = [&](size_t bytes) {
         unsigned char* p = base ? base + at : nullptr;
         at += (bytes + 255) & ~(size_t)255;
-        return (void*)p;
+        return p;
     };
-    const size_t pv = (size_t)c.slots * c.shape.hv, pk = (size_t)c.slots * c.shape.hk;
-    const size_t ns = c.bf ? 2 : 3, np = c.bf ? 1 : 3;
-    const size_t rows = (size_t)(c.dkp / 16) * 1024 * (c.bf ? 2 : 4);
+    const size_t pv = (size_t)c.slots * c.shape.hv;
     o = Prep{};
-    o.t = (__bf16*)take(pv * kTri * ns * kFragBytes);
-    if (!bwd) o.p = (__bf16*)take(pv * kTri * np * kFragBytes);
-    if (bwd) o.tt = (__bf16*)take(pv * kTri * ns * kFragBytes);
-    if (bwd) o.pt = (__bf16*)take(pv * kTri * ns * kFragBytes);
-    o.kt = take(pk * rows);
-    if (bwd) o.qt = take(pk * rows);
-    o.sc = (float*)take(pv * 3 * kC * sizeof(float));
+    o.rec = take(pv * (c.bf ? Rec<true>::bytes : Rec<false>::bytes));
+    if (bwd) o.back = take(pv * (c.bf ? Rec<true>::back : Rec<false>::back));
     return at;
 }
 
@@ -88,14 +81,16 @@ hipError_t launch_prep_t(const DeltaCall& c, const Prep& o, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <bool BF, int DK, int NT, int MODE>
+template <bool BF, int DK, int MODE>
 hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
-    using L = ScanLds<BF, DK, NT>;
-    a.nblk = (c.shape.dv + 16 * NT - 1) / (16 * NT);
+    using Cfg = ScanCfg<BF, DK, MODE>;
+    constexpr int lds = (int)sizeof(typename Cfg::Lds);
+    a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
     const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
-    static_assert(sizeof(L) <= 64 * 1024, "LDS of a scan workgroup");
-    hipLaunchKernelGGL((k_delta_scan<BF, DK, NT, MODE>), dim3((unsigned)(pairs * a.nblk)), dim3(kThreads), sizeof(L),
-                       st, a);
+    const hipError_t e = hipFuncSetAttribute((const void*)k_delta_scan<BF, DK, MODE>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_delta_scan<BF, DK, MODE>), dim3((unsigned)(pairs * a.nblk)), dim3(Cfg::threads), lds, st, a);
     return hipGetLastError();
 }
 
@@ -114,12 +109,12 @@ hipError_t delta_prep(const DeltaCall& c, bool bwd, const Prep& o, hipStream_t s
 hipError_t delta_scan(const DeltaCall& c, bool keep, const ScanArgs& a, hipStream_t st) {
     if (c.bf) {
         if (c.dkp == 64)
-            return keep ? launch_scan_t<true, 64, 2, kScanKeep>(c, a, st) : launch_scan_t<true, 64, 2, kScanOut>(c, a, st);
-        return keep ? launch_scan_t<true, 128, 2, kScanKeep>(c, a, st) : launch_scan_t<true, 128, 2, kScanOut>(c, a, st);
+            return keep ? launch_scan_t<true, 64, kScanKeep>(c, a, st) : launch_scan_t<true, 64, kScanOut>(c, a, st);
+        return keep ? launch_scan_t<true, 128, kScanKeep>(c, a, st) : launch_scan_t<true, 128, kScanOut>(c, a, st);
     }
     if (c.dkp == 64)
-        return keep ? launch_scan_t<false, 64, 2, kScanKeep>(c, a, st) : launch_scan_t<false, 64, 2, kScanOut>(c, a, st);
-    return keep ? launch_scan_t<false, 128, 2, kScanKeep>(c, a, st) : launch_scan_t<false, 128, 2, kScanOut>(c, a, st);
+        return keep ? launch_scan_t<false, 64, kScanKeep>(c, a, st) : launch_scan_t<false, 64, kScanOut>(c, a, st);
+    return keep ? launch_scan_t<false, 128, kScanKeep>(c, a, st) : launch_scan_t<false, 128, kScanOut>(c, a, st);
 }
 
 }  // namespace hy

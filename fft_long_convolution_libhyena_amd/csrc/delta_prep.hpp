@@ -1,7 +1,6 @@
 // Chunk-parallel preparation of the gated delta rule: the decays, T = (I + A)^-1 and
 // P of every (chunk, value head), written as matrix-core fragments so that the scans
-// read them 16 bytes per lane without staging, and K^T (Q^T) of every (chunk, key
-// head) in the same form.
+// read them 16 bytes per lane without staging.
 #pragma once
 #include "delta.hpp"
 
@@ -28,23 +27,6 @@ struct PrepLds {
     float beta[kC];
 };
 
-// column fragments of the staged rows: lane (row k of tile t, tokens 32 s + 8 g ..)
-template <bool BF, int DK>
-__device__ __forceinline__ void write_transposed(const PrepLds<BF, DK>& l, void* dst, int tid) {
-    using T = typename Io<BF>::T;
-    T* o = (T*)dst;
-    for (int e = tid; e < (DK / 16) * 2 * 64; e += kThreads) {
-        const int f = e >> 6, lane = e & 63;
-        const int k = 16 * (f >> 1) + (lane & 15), t0 = 32 * (f & 1) + 8 * (lane >> 4);
-        alignas(16) T v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = l.rows[t0 + i][k];
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<f32x4*>(o + (int64_t)e * 8)[i] = reinterpret_cast<const f32x4*>(v)[i];
-    }
-}
-
 template <bool BF, int DK>
 __device__ __forceinline__ void stage_rows(PrepLds<BF, DK>& l, const typename Io<BF>::T* src, int64_t ld, int rows,
                                            int dk, int tid) {
@@ -58,17 +40,18 @@ __device__ __forceinline__ void stage_rows(PrepLds<BF, DK>& l, const typename Io
     }
 }
 
-// a 64 x 64 matrix in LDS (or its transpose) as block-triangular A fragments of N parts
+// a 64 x 64 matrix in LDS (or its transpose; or with column c scaled by scale[c]) as
+// block-triangular A fragments of N parts
 template <int N, bool TRANS>
-__device__ __forceinline__ void write_tri(const float (*m)[kMP], __bf16* dst, int tid) {
+__device__ __forceinline__ void write_tri(const float (*m)[kMP], const float* scale, __bf16* dst, int tid) {
     for (int e = tid; e < kTri * 64; e += kThreads) {
         const int f = e >> 6, lane = e & 63;
         const int i = TRANS ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : 2 + ((f - 2) >> 1));
         const int s = TRANS ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : (f - 2) & 1);
-        const int row = 16 * i + (lane & 15), c0 = 32 * s + 8 * (lane >> 4);
+        const int row = tile_row(i, lane & 15), c0 = 32 * s + 8 * (lane >> 4);
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = TRANS ? m[c0 + j][row] : m[row][c0 + j];
+        for (int j = 0; j < 8; ++j) x[j] = (TRANS ? m[c0 + j][row] : m[row][c0 + j]) * (scale ? scale[c0 + j] : 1.f);
         const Frag<N> fr = split8<N>(x);
 #pragma unroll
         for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(dst + ((int64_t)f * N + n) * 512 + lane * 8) = fr.p[n];
@@ -115,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
         const double last = __shfl(G, 63);
         l.G[lane] = G;
         l.beta[lane] = bv;
-        float* sc = a.out.sc + sh_idx * 3 * kC;
+        float* sc = reinterpret_cast<float*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::sc);
         sc[lane] = expf((float)G);
         sc[kC + lane] = expf((float)(last - G));
         sc[2 * kC + lane] = bv;
@@ -159,11 +142,9 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     }
     __syncthreads();
     if (!BWD)
-        write_tri<IO::NP, false>(l.p, a.out.p + sh_idx * kTri * IO::NP * 512, tid);
+        write_tri<IO::NP, false>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::p), tid);
     else
-        write_tri<IO::NS, true>(l.p, a.out.pt + sh_idx * kTri * IO::NS * 512, tid);
-    if (h == hk * a.sh.group)
-        write_transposed<BF, DK>(l, (T*)a.out.kt + (slot * a.sh.hk + hk) * (DK / 16) * 1024, tid);
+        write_tri<IO::NS, true>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.back + sh_idx * Rec<BF>::back + Rec<BF>::pt), tid);
     __syncthreads();
 
     // T over P. Diagonal block `wave`: column `col` of the inverse, x_i = e_i - sum_{j<i} A_ij x_j
@@ -208,15 +189,9 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
         }
         __syncthreads();
     }
-    write_tri<IO::NS, false>(l.p, a.out.t + sh_idx * kTri * IO::NS * 512, tid);
-    if (BWD) {
-        write_tri<IO::NS, true>(l.p, a.out.tt + sh_idx * kTri * IO::NS * 512, tid);
-        if (h == hk * a.sh.group) {
-            stage_rows<BF, DK>(l, qp, a.sh.ldq, rows, a.sh.dk, tid);
-            __syncthreads();
-            write_transposed<BF, DK>(l, (T*)a.out.qt + (slot * a.sh.hk + hk) * (DK / 16) * 1024, tid);
-        }
-    }
+    write_tri<IO::NS, false>(l.p, l.beta, reinterpret_cast<__bf16*>(a.out.rec + sh_idx * Rec<BF>::bytes), tid);
+    if (BWD)
+        write_tri<IO::NS, true>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.back + sh_idx * Rec<BF>::back), tid);
 }
 
 }  // namespace delta

@@ -1,14 +1,27 @@
-// The state scan of the gated delta rule: one workgroup of four waves carries 16 NT
-// columns of one (sequence, value head)'s state through its chunks.
+// The state scan of the gated delta rule. A workgroup carries NB blocks of 16 columns of
+// one (sequence, value head)'s state through its chunks; three kinds of waves share it:
+//   state     one wave a block: e, u and the new state, all in its registers
+//   outputs   one wave a block, a chunk behind: o = scale (exp(G) Q S + P u)
+//   staging   brings K, Q (and bf16 v) of the next chunks into LDS: the two outputs'
+//             waves beside their work (bf16), or a wave of its own
+// The state is fp32 with its bf16 parts beside it as right-hand operands. With rows
+// numbered as in tile_row, every result of a chunk (the residual e, the written values u,
+// the new state) becomes the next product's operand in the lane that holds it: nothing on
+// the way from one state to the next passes through LDS or another wave. The outputs
+// are off that way; their wave takes the parts of the state and u from LDS. T, P and the
+// decays come as the preparation laid them out, 1 KiB a load, a chunk ahead. One barrier a
+// chunk (two where LDS holds one buffer of K and Q only: fp32, three parts).
 //
-// Wave w owns tokens 16w .. 16w+15 of a chunk (K S, Q S, T e, P u) and rows
-// DK/4 w .. of the state, which stay in its registers in fp32. Every operand element
-// on the left of a product is thus read by exactly one wave, straight from memory into
-// registers; the right-hand operands (the state's parts, the residual e, the written
-// values u) pass between the waves through LDS as fragments, with three barriers a
-// chunk. The next chunk's left operands are loaded as soon as this chunk's are used;
-// the barriers leave those loads in flight, and no load is conditional.
+// What bounds it: a state wave is alone on its SIMD, so its instructions (82 matrix, about
+// 300 vector for a chunk of a 128 x 16 block) run in order, matrix and vector ones
+// alternating; the chain over the chunks is sequential. Measured on the way, one chunk of
+// 64 tokens, 128 x 128 heads, bf16: tokens and state rows split over four waves, operands
+// exchanged in LDS with three barriers, 2.3 us for 32 columns; each wave loading K, Q and
+// K^T for itself, 2.0 us for 16 columns (a load of 16 rows of 64 bytes costs 60 clocks,
+// one of 1 KiB in a row 16).
 #pragma once
+#include <type_traits>
+
 #include "delta.hpp"
 
 namespace hy {
@@ -29,292 +42,424 @@ struct ScanArgs {
 
 enum { kScanOut = 0, kScanKeep = 1 };
 
-template <bool BF, int DK, int NT>
-struct ScanLds {
-    using IO = Io<BF>;
-    alignas(16) __bf16 s[DK / 32][NT][IO::NS][512];
-    alignas(16) __bf16 e[2][NT][IO::NS][512];
-    alignas(16) __bf16 u[2][NT][IO::NO][512];
-    alignas(16) __bf16 ku[2][NT][IO::NS][512];
+// eight rows of one column from a pair of result tiles, as an operand
+template <int N>
+__device__ __forceinline__ Frag<N> pair_frag(const f32x4& a, const f32x4& b) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split8<N>(x);
+}
+
+template <bool BF, int DK>
+struct Exchange {  // the operands of one chunk's outputs
+    alignas(16) __bf16 s[DK / 32][Io<BF>::NO][512];
+    alignas(16) f32x4 u[4][64];  // as computed: the outputs' wave has time to split it
+};
+template <bool BF, int DK, int MODE>
+struct ScanCfg {
+    static constexpr int NB = BF ? 2 : 1;   // column blocks
+    static constexpr int BUF = BF ? 2 : 1;  // buffers of K and of Q
+    static constexpr bool OUT = MODE == kScanOut;
+    static constexpr bool STAGER = !(OUT && BF);  // a wave that only stages
+    static constexpr int threads = 64 * ((OUT ? 2 : 1) * NB + (STAGER ? 1 : 0));
+    struct None {};
+    struct LdsOut {
+        Tile<Io<BF>::NI, DK> k[BUF], q[BUF];
+        Exchange<BF, DK> x[NB][2];
+    };
+    struct LdsKeep {
+        Tile<Io<BF>::NI, DK> k[BUF];
+    };
+    struct LdsV {
+        ColTile<16 * NB> v[BUF];
+    };
+    struct Lds : std::conditional<OUT, LdsOut, LdsKeep>::type, std::conditional<BF, LdsV, None>::type {};
+};
+// v of a chunk, 32 columns: 16 rows of 64 bytes an instruction
+struct StageV {
+    u32x4 r[4];
+    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int col0, int dv, int lane) {
+        const int c = col0 + 8 * (lane & 3);
+        const uint32_t off = c < dv ? (lane >> 2) * ld + c * 2 : kNoElem;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + i * 16 * ld), 0, 0));
+    }
+    __device__ __forceinline__ void store(ColTile<32>& t, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x4*>(t.b + (16 * i + (lane >> 2)) * ColTile<32>::pitch + 16 * (lane & 3)) = r[i];
+    }
 };
 
-template <bool BF, int DK, int NT, int MODE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_delta_scan(ScanArgs a) {
+template <class Cfg>
+__device__ __forceinline__ constexpr int waves_of() {
+    return Cfg::threads / 64;
+}
+
+template <bool BF, int DK, int MODE>
+__global__ __launch_bounds__((ScanCfg<BF, DK, MODE>::threads)) __attribute__((amdgpu_waves_per_eu((ScanCfg<BF, DK, MODE>::threads > 256 ? 2 : 1))))
+void k_delta_scan(ScanArgs a) {
     using IO = Io<BF>;
     using T = typename IO::T;
-    constexpr int KS = DK / 32, MT = DK / 64;
-    constexpr int NS = IO::NS, NP = IO::NP, NO = IO::NO;
+    using Cfg = ScanCfg<BF, DK, MODE>;
+    constexpr bool OUT = Cfg::OUT;
+    constexpr int KS = DK / 32, MT = DK / 16, NB = Cfg::NB, BUF = Cfg::BUF;
+    constexpr int NI = IO::NI, NS = IO::NS, NP = IO::NP, NO = IO::NO;
     constexpr uint32_t E = sizeof(T);
     extern __shared__ __align__(16) unsigned char lds_raw[];
-    ScanLds<BF, DK, NT>& l = *reinterpret_cast<ScanLds<BF, DK, NT>*>(lds_raw);
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    typename Cfg::Lds& l = *reinterpret_cast<typename Cfg::Lds*>(lds_raw);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, col = lane & 15;
     // column blocks of one head sit 8 workgroups apart, so that they land on one XCD
     // and share its L2 for the head's operands
     const int64_t bid = blockIdx.x;
     const int64_t pair = bid / (8 * a.nblk) * 8 + (bid & 7);
-    const int blk = (int)(bid / 8 % a.nblk);
     const int hv = a.sh.hv;
     if (pair >= a.seqs.N * hv) return;
     const int64_t n = pair / hv;
     const int h = (int)(pair % hv), hk = h / a.sh.group;
     const Range rr = seq_range(a.seqs, n);
     const int64_t first = uniform64(rr.first), len = uniform64(rr.len), slot0 = uniform64(rr.slot0);
-    const int64_t nch = (len + kC - 1) / kC;
+    const int nch = (int)((len + kC - 1) / kC);
+    const int tail = (int)(len - (int64_t)(nch - 1) * kC);  // rows of the last chunk
     const int dk = a.sh.dk, dv = a.sh.dv;
-    const int c0 = blk * 16 * NT + NT * col;  // this lane's first column
-    const bool cok = c0 < dv;
+    const int64_t recstep = (int64_t)hv * Rec<BF>::bytes;
+    const unsigned char* rec = a.prep.rec + (slot0 * hv + h) * Rec<BF>::bytes;
 
-    f32x4 S[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = 16 * (wave * MT + m) + 4 * g + i;
-            float x[NT];
-            load_cols<NT>(a.s_in + ((n * hv + h) * dk + k) * dv + c0, a.s_in && k < dk && cok, x);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) S[m][j][i] = x[j];
-        }
-
-    const int row = 16 * wave + col;     // token of this lane's operand rows
-    const int drow = 16 * wave + 4 * g;  // first of this lane's four result rows
-    const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E, ldv = (uint32_t)a.sh.ldv * E;
-    const uint32_t ldo = (uint32_t)(hv * dv) * E;
-    uint32_t koff[KS], qoff[KS], voff[4], ooff[4], soff[MT][4];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        const uint32_t k = 32 * s + 8 * g;
-        koff[s] = (int)k < dk ? row * ldk + k * E : kNoElem;
-        qoff[s] = (int)k < dk ? row * ldq + k * E : kNoElem;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        voff[i] = cok ? (drow + i) * ldv + c0 * E : kNoElem;
-        ooff[i] = cok ? (drow + i) * ldo + c0 * E : kNoElem;
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = 16 * (wave * MT + m) + 4 * g + i;
-            soff[m][i] = cok && k < dk ? (uint32_t)(k * dv + c0) * E : kNoElem;
-        }
-    const T* kbase = (const T*)a.k + first * a.sh.ldk + (int64_t)hk * dk;
-    const T* qbase = (const T*)a.q + first * a.sh.ldq + (int64_t)hk * dk;
-    const T* vbase = (const T*)a.v + first * a.sh.ldv + (int64_t)h * dv;
-    T* obase = (T*)(MODE == kScanOut ? a.o : a.u) + (first * hv + h) * (int64_t)dv;
-
-    Raw<BF> K[KS], Q[KS], KT[MT][2];
-    Frag<NS> Tf[2];
-    Frag<NP> Pf[2];
-    Cols<BF, NT> V[4];
-    f32x4 gam, kap, bet;
-    float glast = 0.f;
-    auto load_k = [&](int64_t c) {
-        const RowBuf b = row_buf(kbase + c * kC * a.sh.ldk, len - c * kC, ldk, dk * E);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) buf_raw(b, koff[s], K[s]);
+    // what a staging wave does for K, Q or v: chunk c stored, chunk c + 1 on its way
+    const int64_t krow = (int64_t)kC * a.sh.ldk * E, qrow = (int64_t)kC * a.sh.ldq * E, vrow = (int64_t)kC * a.sh.ldv * E;
+    const unsigned char* kbase = (const unsigned char*)((const T*)a.k + first * a.sh.ldk + (int64_t)hk * dk);
+    const unsigned char* qbase = OUT ? (const unsigned char*)((const T*)a.q + first * a.sh.ldq + (int64_t)hk * dk) : nullptr;
+    const unsigned char* vbase = (const unsigned char*)((const T*)a.v + first * a.sh.ldv + (int64_t)h * dv);
+    const int wgcol = (int)(bid / 8 % a.nblk) * NB * 16;
+    auto rows_in = [&](int c) { return c + 1 < nch ? kC : tail; };
+    auto load_tile = [&](Stage<BF, DK>& r, const unsigned char* base, int64_t step, int64_t ld, int c) {
+        r.load(plain_buf(base + c * step, (rows_in(c) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk, lane);
     };
-    auto load_q = [&](int64_t c) {
-        const RowBuf b = row_buf(qbase + c * kC * a.sh.ldq, len - c * kC, ldq, dk * E);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) buf_raw(b, qoff[s], Q[s]);
+    auto load_vt = [&](StageV& r, int c) {
+        r.load(plain_buf(vbase + c * vrow, (rows_in(c) - 1) * (uint32_t)(a.sh.ldv * E) + dv * E), (uint32_t)(a.sh.ldv * E), wgcol,
+               dv, lane);
     };
-    auto load_v = [&](int64_t c) {
-        const RowBuf b = row_buf(vbase + c * kC * a.sh.ldv, len - c * kC, ldv, dv * E);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) buf_cols<BF, NT>(b, voff[i], V[i]);
-    };
-    auto load_sc = [&](int64_t c) {
-        const float* sc = a.prep.sc + ((slot0 + c) * hv + h) * 3 * kC;
-        gam = *reinterpret_cast<const f32x4*>(sc + drow);
-        kap = *reinterpret_cast<const f32x4*>(sc + kC + drow);
-        bet = *reinterpret_cast<const f32x4*>(sc + 2 * kC + drow);
-        glast = sc[kC - 1];
-    };
-    // every fragment of row tile `wave`: one step for tiles 0 and 1 (read twice, so
-    // that no load is conditional), two below
-    const int f0 = lower_frag(wave, 0), f1 = lower_frag(wave, wave >= 2 ? 1 : 0);
-    auto load_t = [&](int64_t c) {
-        const __bf16* p = a.prep.t + ((slot0 + c) * hv + h) * kTri * NS * 512;
-        Tf[0] = get_frag<NS>(p + f0 * NS * 512, 512, lane);
-        Tf[1] = get_frag<NS>(p + f1 * NS * 512, 512, lane);
-    };
-    auto load_p = [&](int64_t c) {
-        const __bf16* p = a.prep.p + ((slot0 + c) * hv + h) * kTri * NP * 512;
-        Pf[0] = get_frag<NP>(p + f0 * NP * 512, 512, lane);
-        Pf[1] = get_frag<NP>(p + f1 * NP * 512, 512, lane);
-    };
-    auto load_kt = [&](int64_t c) {
-        const T* p = (const T*)a.prep.kt + ((slot0 + c) * a.sh.hk + hk) * (DK / 16) * 1024 + lane * 8;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) KT[m][s] = load_raw(p + ((wave * MT + m) * 2 + s) * 512, true);
-    };
-    auto put_state = [&]() {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int t = wave * MT + m;
-                const float x[4] = {S[m][j][0], S[m][j][1], S[m][j][2], S[m][j][3]};
-                put_rows<NS>(&l.s[t >> 1][j][0][0], 512, t & 1, lane, x);
+    if constexpr (Cfg::STAGER)
+        if (wave == waves_of<Cfg>() - 1) {
+            Stage<BF, DK> rk, rq;
+            StageV rv;
+            if (nch > 0) {
+                load_tile(rk, kbase, krow, a.sh.ldk, 0);
+                if constexpr (BF) load_vt(rv, 0);
+                rk.store(l.k[0], lane);
+                if constexpr (BF) rv.store(l.v[0], lane);
+                if (nch > 1) {
+                    load_tile(rk, kbase, krow, a.sh.ldk, 1);
+                    if constexpr (BF) load_vt(rv, 1);
+                }
+                if constexpr (OUT) load_tile(rq, qbase, qrow, a.sh.ldq, 0);
+                lds_barrier();
             }
+            for (int c = 0; c < nch; ++c) {
+                if (BUF == 1) lds_barrier();  // K of chunk c and Q of chunk c - 1 have been read
+                if (c + 1 < nch) {
+                    rk.store(l.k[(c + 1) & (BUF - 1)], lane);
+                    if constexpr (BF) rv.store(l.v[(c + 1) & (BUF - 1)], lane);
+                }
+                if constexpr (OUT) rq.store(l.q[c & (BUF - 1)], lane);
+                if (c + 2 < nch) {
+                    load_tile(rk, kbase, krow, a.sh.ldk, c + 2);
+                    if constexpr (BF) load_vt(rv, c + 2);
+                }
+                if constexpr (OUT)
+                    if (c + 1 < nch) load_tile(rq, qbase, qrow, a.sh.ldq, c + 1);
+                lds_barrier();
+            }
+            return;
+        }
+
+    const int blk = (int)(bid / 8 % a.nblk) * NB + wave % NB;
+    const int c0 = blk * 16 + col;  // this lane's column
+    const bool cok = c0 < dv;
+    const uint32_t ldo = (uint32_t)(hv * dv) * E;
+    unsigned char* op = (unsigned char*)((T*)(OUT ? a.o : a.u) + (first * hv + h) * (int64_t)dv);
+    // row i of this lane's results in tile t
+    auto drow = [&](int t, int i) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + i; };
+    const uint32_t ooff = cok ? drow(0, 0) * ldo + c0 * E : kNoElem;
+    const uint32_t ofull = (kC - 1) * ldo + dv * E, olast = (tail - 1) * ldo + dv * E;
+    auto store_rows = [&](const f32x4(&y)[4], int c) {
+        const RowBuf b = plain_buf(op, c + 1 < nch ? ofull : olast);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x[1] = {y[t][i]};
+                buf_store<BF, 1>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + i) * ldo, x);
+            }
+        op += (int64_t)kC * ldo;
     };
-    // outputs of chunk c from Q S and the fragments of u, one chunk late: these
-    // products run while the next chunk's first fragments come from LDS
-    f32x4 qs[NT];
-    Frag<NO> uf[2][NT];
-    auto finish = [&](int64_t c) {
-        f32x4 o1[NT] = {};
-        mma_each(Pf[0], uf[0], qs);
-        if (wave >= 2) mma_each(Pf[1], uf[1], o1);
-        const RowBuf b = row_buf(obase + c * kC * hv * (int64_t)dv, len - c * kC, ldo, dv * E);
+
+    if constexpr (OUT)
+        if (wave >= NB) {
+            Frag<NP> Pf[kTri];
+            f32x4 gam[4];
+            auto load = [&]() {
+                const RowBuf rb = plain_buf(rec, Rec<BF>::bytes);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) gam[t] = buf_f4(rb, drow(t, 0) * 4, Rec<BF>::sc);
+#pragma unroll
+                for (int f = 0; f < kTri; ++f) Pf[f] = buf_frag<NP>(rb, Rec<BF>::p, f, lane);
+            };
+            auto outputs = [&](int c) {
+                const Exchange<BF, DK>& in = l.x[wave - NB][c & 1];
+                const Tile<NI, DK>& q = l.q[c & (BUF - 1)];
+                f32x4 y[4] = {};
+                Frag<NI> qa[2][4];
+                Frag<NO> sp[2];
+                auto read = [&](int s) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) qa[s & 1][t] = q.rows(lane, t, s);
+                    sp[s & 1] = get_frag<NO>(&in.s[s][0][0], 512, lane);
+                };
+                read(0);
+                read(1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    mma_tiles(qa[s & 1], sp[s & 1], y);
+                    if (s + 2 < KS) read(s + 2);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                f32x4 u[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) u[t] = in.u[t][lane];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] *= gam[t];
+                const Frag<NO> u0 = pair_frag<NO>(u[0], u[1]), u1 = pair_frag<NO>(u[2], u[3]);
+                const Frag<NP> p0[4] = {Pf[0], Pf[1], Pf[2], Pf[4]}, p1[2] = {Pf[3], Pf[5]};
+                mma_tiles(p0, u0, y);
+                mma_tiles(p1, u1, y + 2);
+                __builtin_amdgcn_sched_barrier(0);
+                if (c + 1 < nch) rec += recstep;
+                load();
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] *= a.sh.scale;
+                store_rows(y, c);
+            };
+            if (nch > 0) load();
+            if constexpr (Cfg::STAGER) {
+                if (nch > 0) lds_barrier();
+                for (int c = 0; c < nch; ++c) {
+                    lds_barrier();
+                    lds_barrier();
+                    outputs(c);
+                }
+            } else {
+                // the first outputs' wave also stages K and v (chunk c + 1 while the state is at
+                // c), the second Q (chunk c)
+                Stage<BF, DK> rt;
+                StageV rv;
+                const int lead = wave == NB ? 1 : 0;
+                const unsigned char* base = lead ? kbase : qbase;
+                const int64_t step = lead ? krow : qrow, ld = lead ? a.sh.ldk : a.sh.ldq;
+                Tile<NI, DK>* tile = lead ? l.k : l.q;
+                if (nch > 0) {
+                    load_tile(rt, base, step, ld, 0);
+                    if (lead) {
+                        load_vt(rv, 0);
+                        rt.store(tile[0], lane);
+                        rv.store(l.v[0], lane);
+                        if (nch > 1) {
+                            load_tile(rt, base, step, ld, 1);
+                            load_vt(rv, 1);
+                        }
+                    }
+                    lds_barrier();
+                }
+                for (int c = 0; c < nch; ++c) {
+                    const int m = c + lead;
+                    if (m < nch) {
+                        rt.store(tile[m & 1], lane);
+                        if (lead) rv.store(l.v[m & 1], lane);
+                    }
+                    if (m + 1 < nch) {
+                        load_tile(rt, base, step, ld, m + 1);
+                        if (lead) load_vt(rv, m + 1);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (c > 0) outputs(c - 1);
+                    lds_barrier();
+                }
+                if (nch > 0) outputs(nch - 1);
+            }
+            return;
+        }
+
+    f32x4 S[MT];
+    Frag<NS> sf[KS];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float x[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) x[j] = a.sh.scale * (qs[j][i] + o1[j][i]);
-            buf_store<BF, NT>(b, ooff[i], x);
+            const int k = drow(t, i);
+            S[t][i] = a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
         }
-    };
-    if (nch > 0) {
-        load_k(0);
-        load_v(0);
-        load_sc(0);
-        if (MODE == kScanOut) load_q(0);
-        load_t(0);
-        load_kt(0);
-        if (MODE == kScanOut) load_p(0);
-        put_state();
-    }
-    for (int64_t c = 0; c < nch; ++c) {
-        const int64_t nx = c + 1 < nch ? c + 1 : c;  // the last chunk loads itself again
-        if (MODE == kScanKeep) {
-            const RowBuf b = __builtin_amdgcn_make_buffer_rsrc(
-                (T*)a.s0 + ((slot0 + c) * hv + h) * (int64_t)dk * dv, 0, (int)(dk * dv * E), 0x00020000);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+    for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1]);
+
+    const uint32_t ldv = (uint32_t)a.sh.ldv * E;
+    const uint32_t voff = cok ? drow(0, 0) * ldv + c0 * E : kNoElem;
+    auto vbuf = [&](int c) { return plain_buf(vbase + c * vrow, (rows_in(c) - 1) * ldv + dv * E); };
+    Frag<NS> Tf[kTri];
+    uint32_t V[4][4];  // fp32 only, a chunk ahead; bf16 v comes through LDS
+    f32x4 gam[4], kap[4];
+    float glast = 0.f;
+    auto load_v = [&](const RowBuf& b, int t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            V[t][i] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)(voff + (32 * (t >> 1) + 4 * (t & 1) + i) * ldv), 0, 0);
+    };
+    auto load_gam = [&](const RowBuf& b, int t) { gam[t] = buf_f4(b, drow(t, 0) * 4, Rec<BF>::sc); };
+    auto load_kap = [&](const RowBuf& b, int t) { kap[t] = buf_f4(b, drow(t, 0) * 4, Rec<BF>::sc + kC * 4); };
+    auto load_last = [&](const RowBuf& b) {
+        glast = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, 0, Rec<BF>::sc + (kC - 1) * 4, 0));
+    };
+    auto load_t = [&](const RowBuf& b, int f) { Tf[f] = buf_frag<NS>(b, Rec<BF>::t, f, lane); };
+    if (nch > 0) {
+        const RowBuf vb = vbuf(0), rb = plain_buf(rec, Rec<BF>::bytes);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (!BF) load_v(vb, t);
+            load_gam(rb, t);
+            load_kap(rb, t);
+        }
+        load_last(rb);
+#pragma unroll
+        for (int f = 0; f < kTri; ++f) load_t(rb, f);
+        lds_barrier();  // K of the first chunk is in LDS
+    }
+    unsigned char* s0p = OUT ? nullptr : (unsigned char*)a.s0 + (slot0 * hv + h) * (int64_t)dk * dv * E;
+    constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;  // matrix instructions per product
+    for (int c = 0; c < nch; ++c) {
+        if (c + 1 < nch) rec += recstep;  // loaded for the next chunk; the last one reads itself again
+        const RowBuf vb = vbuf(c + 1 < nch ? c + 1 : c), rb = plain_buf(rec, Rec<BF>::bytes);
+        const Tile<NI, DK>& K = l.k[c & (BUF - 1)];
+        if constexpr (!OUT) {
+            const RowBuf b = plain_buf(s0p, dk * dv * E);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float x[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j] = S[m][j][i];
-                    buf_store<BF, NT>(b, soff[m][i], x);
+                    const float x[1] = {S[t][i]};
+                    buf_store<BF, 1>(b, cok && drow(t, i) < dk ? (uint32_t)(drow(t, i) * dv + c0) * E : kNoElem, x);
                 }
+            s0p += (int64_t)hv * dk * dv * E;
         }
-        lds_barrier();  // the state's fragments are in place
-        Frag<NS> sf[KS][NT];
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) sf[s][j] = get_frag<NS>(&l.s[s][j][0][0], 512, lane);
         __builtin_amdgcn_sched_barrier(0);
-        if (MODE == kScanOut && c > 0) {
-            finish(c - 1);
-            load_p(c);
+        // e = V - exp(G) K S; LDS reads two steps ahead of their products
+        f32x4 x[4] = {};
+        Frag<NI> ka[2][4];
+        auto read_rows = [&](int s) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ka[s & 1][t] = K.rows(lane, t, s);
+        };
+        read_rows(0);
+        read_rows(1);
+        u32x2 v4[4];
+        if constexpr (BF) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v4[t] = l.v[c & (BUF - 1)].rows4(lane, t, 16 * wave);
         }
-        f32x4 ks[NT] = {};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) mma_each(to_frag(K[s]), sf[s], ks);
-        load_k(nx);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = bet[i] * (col_value(V[i], j) - gam[i] * ks[j][i]);
-            put_rows<NS>(&l.e[wave >> 1][j][0][0], 512, wave & 1, lane, x);
-        }
-        load_v(nx);
-        lds_barrier();  // e
-        Frag<NS> ef[2][NT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) ef[s][j] = get_frag<NS>(&l.e[s][j][0][0], 512, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        if (MODE == kScanOut) {  // while e's fragments arrive
-#pragma unroll
-            for (int j = 0; j < NT; ++j) qs[j] = f32x4{};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                Frag<NO> so[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) so[j] = first_parts<NO>(sf[s][j]);
-                mma_each(to_frag(Q[s]), so, qs);
-            }
-            load_q(nx);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qs[j][i] *= gam[i];
-        }
-        f32x4 u[NT] = {}, u1[NT] = {};
-        mma_each(Tf[0], ef[0], u);
-        if (wave >= 2) mma_each(Tf[1], ef[1], u1);
-        load_t(nx);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            float x[4], y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = u[j][i] + u1[j][i];
-                y[i] = kap[i] * x[i];
-                u[j][i] = x[i];
-            }
-            if (MODE == kScanOut) put_rows<NO>(&l.u[wave >> 1][j][0][0], 512, wave & 1, lane, x);
-            put_rows<NS>(&l.ku[wave >> 1][j][0][0], 512, wave & 1, lane, y);
-        }
-        if (MODE == kScanKeep) {
-            const RowBuf b = row_buf(obase + c * kC * hv * (int64_t)dv, len - c * kC, ldo, dv * E);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) x[j] = u[j][i];
-                buf_store<BF, NT>(b, ooff[i], x);
-            }
-        }
-        const float gl = glast;
-        load_sc(nx);
-        lds_barrier();  // u
-        Frag<NS> kf[2][NT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) kf[s][j] = get_frag<NS>(&l.ku[s][j][0][0], 512, lane);
-        if (MODE == kScanOut)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) uf[s][j] = get_frag<NO>(&l.u[s][j][0][0], 512, lane);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int s = 0; s < KS; ++s) {
+            mma_tiles(ka[s & 1], sf[s], x);
+            if constexpr (OUT) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+                for (int p = 0; p < NO; ++p) *reinterpret_cast<bf16x8*>(&l.x[wave][c & 1].s[s][p][lane * 8]) = sf[s].p[p];
+            }
+            if (s + 2 < KS) read_rows(s + 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        Frag<NI> kt[2][MT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][j][i] *= gl;
+        for (int m = 0; m < MT; ++m) kt[0][m] = K.cols(lane, m, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        Frag<NS> ef[2];
+        auto residual = [&](int p) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int t = 2 * p; t < 2 * p + 2; ++t) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma_each(to_frag(KT[m][s]), kf[s], S[m]);
-        load_kt(nx);
-        put_state();
+                for (int i = 0; i < 4; ++i) {
+                    float v;
+                    if constexpr (BF)
+                        v = __uint_as_float(i & 1 ? v4[t][i >> 1] & 0xffff0000u : v4[t][i >> 1] << 16);
+                    else
+                        v = __uint_as_float(V[t][i]);
+                    x[t][i] = fmaf(-gam[t][i], x[t][i], v);
+                }
+                if (!BF) load_v(vb, t);
+                load_gam(rb, t);
+            }
+            ef[p] = pair_frag<NS>(x[2 * p], x[2 * p + 1]);
+        };
+        residual(0);
+        __builtin_amdgcn_sched_barrier(0);
+        // u = T diag(beta) e, the second half of e split meanwhile
+        f32x4 u[4] = {};
+        const Frag<NS> t0[4] = {Tf[0], Tf[1], Tf[2], Tf[4]};
+        mma_tiles(t0, ef[0], u);
+        residual(1);
+        interleave<4 * X3, 4, 1>();
+        const Frag<NS> t1[2] = {Tf[3], Tf[5]};
+        mma_tiles(t1, ef[1], u + 2);
+        Frag<NS> kf[2];
+        kf[0] = pair_frag<NS>(kap[0] * u[0], kap[1] * u[1]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) S[m] *= glast;
+#pragma unroll
+        for (int f = 0; f < kTri; ++f) load_t(rb, f);
+        load_kap(rb, 0);
+        load_kap(rb, 1);
+        load_last(rb);
+        interleave<2 * X3, 12, 2>();
+#pragma unroll
+        for (int m = 0; m < MT; ++m) kt[1][m] = K.cols(lane, m, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        // S = exp(G_last) S + K^T diag(exp(G_last - G)) u: the second half of u is split
+        // during the first products, and the new state's parts two tiles at a time
+        auto update = [&](int s, int p) {
+            const Frag<NI> w[2] = {kt[s][2 * p], kt[s][2 * p + 1]};
+            mma_tiles(w, kf[s], S + 2 * p);
+        };
+        auto parts = [&](int p) { sf[p] = pair_frag<NS>(S[2 * p], S[2 * p + 1]); };
+#pragma unroll
+        for (int p = 0; p < KS; ++p) update(0, p);
+        kf[1] = pair_frag<NS>(kap[2] * u[2], kap[3] * u[3]);
+        load_kap(rb, 2);
+        load_kap(rb, 3);
+        interleave<MT * X2, 5, 1>();
+        if constexpr (OUT) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) l.x[wave][c & 1].u[t][lane] = u[t];
+        } else {
+            store_rows(u, c);
+        }
+        update(1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int p = 1; p < KS; ++p) {
+            update(1, p);
+            parts(p - 1);
+            interleave<2 * X2, 6, 0>();
+        }
+        parts(KS - 1);
+        if (BUF == 1) lds_barrier();  // K may be replaced
+        lds_barrier();                // chunk c's operands and the next K are in LDS
     }
-    if (MODE == kScanOut && nch > 0) finish(nch - 1);
     if (a.s_out)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int k = 16 * (wave * MT + m) + 4 * g + i;
-                float x[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) x[j] = S[m][j][i];
-                if (cok && k < dk) store_cols<NT>(a.s_out + ((n * hv + h) * dk + k) * dv + c0, x);
+                const int k = drow(t, i);
+                if (cok && k < dk) a.s_out[((n * hv + h) * dk + k) * dv + c0] = S[t][i];
             }
 }
 
