@@ -42,11 +42,34 @@ struct ScanArgs {
 
 enum { kScanOut = 0, kScanKeep = 1 };
 
-// eight rows of one column from a pair of result tiles, as an operand
+// Minus the identity, as left operands that take rows of a 32-row operand back to the
+// result tile (t even or odd) they came from.
+struct MinusOne {
+    bf16x8 a[2];
+    __device__ __forceinline__ explicit MinusOne(int lane) {
+        const int col = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[t][j] = (__bf16)(g == col >> 2 && j == 4 * t + (col & 3) ? -1.f : 0.f);
+    }
+};
+// Eight rows of one column from a pair of result tiles, as an operand. What a part
+// leaves of the values (exact in fp32) is a matrix product too, x + (-1) h: two
+// instructions on the matrix cores in place of sixteen vector ones.
 template <int N>
-__device__ __forceinline__ Frag<N> pair_frag(const f32x4& a, const f32x4& b) {
-    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    return split8<N>(x);
+__device__ __forceinline__ Frag<N> pair_frag(f32x4 a, f32x4 b, const MinusOne& minus) {
+    Frag<N> f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const u32x4 w = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
+        f.p[n] = __builtin_bit_cast(bf16x8, w);
+        if (n + 1 < N) {
+            a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus.a[0], f.p[n], a, 0, 0, 0);
+            b = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus.a[1], f.p[n], b, 0, 0, 0);
+        }
+    }
+    return f;
 }
 
 template <bool BF, int DK>
@@ -174,6 +197,7 @@ void k_delta_scan(ScanArgs a) {
             return;
         }
 
+    const MinusOne minus(lane);
     const int blk = (int)(bid / 8 % a.nblk) * NB + wave % NB;
     const int c0 = blk * 16 + col;  // this lane's column
     const bool cok = c0 < dv;
@@ -231,7 +255,7 @@ void k_delta_scan(ScanArgs a) {
                 for (int t = 0; t < 4; ++t) u[t] = in.u[t][lane];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) y[t] *= gam[t];
-                const Frag<NO> u0 = pair_frag<NO>(u[0], u[1]), u1 = pair_frag<NO>(u[2], u[3]);
+                const Frag<NO> u0 = pair_frag<NO>(u[0], u[1], minus), u1 = pair_frag<NO>(u[2], u[3], minus);
                 const Frag<NP> p0[4] = {Pf[0], Pf[1], Pf[2], Pf[4]}, p1[2] = {Pf[3], Pf[5]};
                 mma_tiles(p0, u0, y);
                 mma_tiles(p1, u1, y + 2);
@@ -291,6 +315,7 @@ void k_delta_scan(ScanArgs a) {
             return;
         }
 
+    __builtin_amdgcn_s_setprio(3);  // the sequential part goes first
     f32x4 S[MT];
     Frag<NS> sf[KS];
 #pragma unroll
@@ -301,7 +326,7 @@ void k_delta_scan(ScanArgs a) {
             S[t][i] = a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
         }
 #pragma unroll
-    for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1]);
+    for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1], minus);
 
     const uint32_t ldv = (uint32_t)a.sh.ldv * E;
     const uint32_t voff = cok ? drow(0, 0) * ldv + c0 * E : kNoElem;
@@ -397,7 +422,7 @@ void k_delta_scan(ScanArgs a) {
                 if (!BF) load_v(vb, t);
                 load_gam(rb, t);
             }
-            ef[p] = pair_frag<NS>(x[2 * p], x[2 * p + 1]);
+            ef[p] = pair_frag<NS>(x[2 * p], x[2 * p + 1], minus);
         };
         residual(0);
         __builtin_amdgcn_sched_barrier(0);
@@ -410,7 +435,7 @@ void k_delta_scan(ScanArgs a) {
         const Frag<NS> t1[2] = {Tf[3], Tf[5]};
         mma_tiles(t1, ef[1], u + 2);
         Frag<NS> kf[2];
-        kf[0] = pair_frag<NS>(kap[0] * u[0], kap[1] * u[1]);
+        kf[0] = pair_frag<NS>(kap[0] * u[0], kap[1] * u[1], minus);
 #pragma unroll
         for (int m = 0; m < MT; ++m) S[m] *= glast;
 #pragma unroll
@@ -428,10 +453,10 @@ void k_delta_scan(ScanArgs a) {
             const Frag<NI> w[2] = {kt[s][2 * p], kt[s][2 * p + 1]};
             mma_tiles(w, kf[s], S + 2 * p);
         };
-        auto parts = [&](int p) { sf[p] = pair_frag<NS>(S[2 * p], S[2 * p + 1]); };
+        auto parts = [&](int p) { sf[p] = pair_frag<NS>(S[2 * p], S[2 * p + 1], minus); };
 #pragma unroll
         for (int p = 0; p < KS; ++p) update(0, p);
-        kf[1] = pair_frag<NS>(kap[2] * u[2], kap[3] * u[3]);
+        kf[1] = pair_frag<NS>(kap[2] * u[2], kap[3] * u[3], minus);
         load_kap(rb, 2);
         load_kap(rb, 3);
         interleave<MT * X2, 5, 1>();
