@@ -36,7 +36,8 @@ EXPORTS = ("hyena_plan_create", "hyena_plan_create_path", "hyena_plan_create_ex"
            "hyena_filter_spectrum2d_batched", "hyena_conv2d_forward_per_sample", "hyena_filter_spectrum3d_batched",
            "hyena_conv3d_forward_per_sample", "hyena_plan2d_create_ex", "hyena_plan3d_create_ex",
            "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_delta_workspace_bytes",
-           "hyena_delta_forward", "hyena_delta_step", "hyena_status_string")
+           "hyena_delta_forward", "hyena_delta_backward_workspace_bytes", "hyena_delta_backward", "hyena_delta_step",
+           "hyena_status_string")
 
 
 class FilterMLPStruct(ctypes.Structure):
@@ -179,6 +180,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.hyena_delta_workspace_bytes.restype = sz
     lib.hyena_delta_forward.argtypes = [dp, i64, i64, vp, di, vp, vp, vp, vp, sz, vp]
     lib.hyena_delta_forward.restype = ci
+    lib.hyena_delta_backward_workspace_bytes.argtypes = [dp, i64, i64, vp]
+    lib.hyena_delta_backward_workspace_bytes.restype = sz
+    lib.hyena_delta_backward.argtypes = [dp, i64, i64, vp, di] + [vp] * 10 + [sz, vp]
+    lib.hyena_delta_backward.restype = ci
     lib.hyena_delta_step.argtypes = [dp, i64, i64, di, vp, i64, vp, vp, vp]
     lib.hyena_delta_step.restype = ci
     lib.hyena_status_string.argtypes = [ci]
@@ -807,6 +812,36 @@ class DeltaRule:
                                                 o.data_ptr(), state_out.data_ptr(), ws.data_ptr(), ws_bytes,
                                                 _stream_handle(torch, dev)))
         return o, state_out
+
+    def backward_workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
+        return int(self.lib.hyena_delta_backward_workspace_bytes(ctypes.byref(self._params(None)), int(N), int(tokens),
+                                                                 16 if packed else None))
+
+    def backward(self, q, k, v, g, beta, do, state=None, dstate_out=None, scale=None, seq_start=None, workspace=None):
+        """hyena_delta_backward: the gradients (dq, dk, dv, dg, dbeta, dstate) of the forward's
+        inputs (dense, in the dtype; dstate fp32) for the gradient do [like o] of its outputs and,
+        unless None, dstate_out [N, heads_v, dim_k, dim_v] fp32 of its final states."""
+        torch, dev = self._torch, q.device
+        rows, N, tokens, starts = self._sequences(q, seq_start)
+        inputs = self._inputs(q, k, v, g, beta, rows, dev)
+        Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
+        self._need(do, "do", (*rows, Hv, Dv), self.io_dtype, dev)
+        for name, t in (("state", state), ("dstate_out", dstate_out)):
+            if t is not None:
+                self._need(t, name, self.state_shape(N), torch.float32, dev)
+        out = [torch.empty((*rows, *shape), dtype=self.io_dtype, device=dev)
+               for shape in ((Hk, Dk), (Hk, Dk), (Hv, Dv), (Hv,), (Hv,))]
+        dstate = torch.empty(self.state_shape(N), dtype=torch.float32, device=dev)
+        ws, ws_bytes = self._workspace(workspace, self.backward_workspace_bytes(N, tokens, starts is not None), dev)
+        with torch.cuda.device(dev):
+            _check("hyena_delta_backward",
+                   self.lib.hyena_delta_backward(ctypes.byref(self._params(scale)), N, tokens, starts,
+                                                 ctypes.byref(inputs), state.data_ptr() if state is not None else None,
+                                                 do.data_ptr(),
+                                                 dstate_out.data_ptr() if dstate_out is not None else None,
+                                                 *(t.data_ptr() for t in out), dstate.data_ptr(), ws.data_ptr(),
+                                                 ws_bytes, _stream_handle(torch, dev)))
+        return (*out, dstate)
 
     def step(self, q, k, v, g, beta, states, slots=None, scale=None, o=None):
         """hyena_delta_step: T further tokens of B rows (q, k [B, T, heads_k, dim_k], v

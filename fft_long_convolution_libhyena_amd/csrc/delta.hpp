@@ -494,6 +494,18 @@ __device__ __forceinline__ bool find_chunk(const Seqs& s, int64_t slot, Range& r
     return c >= 0 && c * kC < r.len;
 }
 
+// The running sum of the log decays over a chunk's 64 lanes, in 64 bits: differences of
+// it stay exact to fp32 however strong single decays are.
+__device__ __forceinline__ double chunk_decay(float g, int lane) {
+    double G = (double)g < kMinLog ? kMinLog : (double)g;  // a NaN stays one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double up = __shfl_up(G, d);
+        if (lane >= d) G += up;
+    }
+    return G;
+}
+
 struct Shape {
     int hk, hv, group, dk, dv;
     int64_t ldq, ldk, ldv;

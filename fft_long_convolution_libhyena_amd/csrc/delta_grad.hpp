@@ -1,0 +1,370 @@
+// The backward's chunk-parallel part: with the state S0 before and its gradient dS1
+// behind every chunk, the written values u and the residuals' gradients r, the gradients
+// of q, k, g and beta. Per chunk and value head, with D_ij = exp(G_i - G_j),
+// W_ij = scale D_ij (dO_i . u_j) for j <= i, M_ij = -beta_i D_ij (r_i . u_j) for j < i:
+//   dQ = scale diag(exp G) dO S0^T + W K
+//   dK = -diag(exp(G) beta) r S0^T + diag(exp(G_last - G)) u dS1^T + W^T Q + (M + M^T) K
+//   dbeta_i = r_i . v_i - exp(G_i) k_i . (r S0^T)_i - sum_j D_ij (k_i . k_j) (r_i . u_j)
+//   dG_i = scale exp(G_i) q_i . (dO S0^T)_i - beta_i exp(G_i) k_i . (r S0^T)_i
+//          + sum_j X_ij - sum_j X_ji - exp(G_last - G_i) k_i . (u dS1^T)_i,
+//   X_ij = W_ij q_i . k_j + M_ij k_i . k_j,
+//   dG_last += sum_i exp(G_last - G_i) k_i . (u dS1^T)_i + exp(G_last) <dS1, S0>,
+// and dg_t is the sum of dG_i over i >= t. (dbeta uses r itself, not beta r, so beta = 0
+// has its gradient.)
+#pragma once
+#include "delta.hpp"
+
+namespace hy {
+namespace delta {
+
+struct GradArgs {
+    Seqs seqs;
+    Shape sh;
+    const void *q, *k, *v, *g, *beta, *dout;
+    const void *s0, *ds1, *u, *r;
+    void *dq, *dk;       // [tokens][hk][dk]
+    void *dg, *dbeta;    // [tokens][hv]
+};
+
+// R rows of W elements in LDS, natural order; fp32 is split when read
+template <bool BF, int R, int W>
+struct GradTile;
+template <int R, int W>
+struct GradTile<true, R, W> {
+    using T = __bf16;
+    static constexpr int pitch = 2 * W + 16;
+    alignas(16) unsigned char b[R * pitch];
+    __device__ __forceinline__ u32x4* at16(int row, int e) { return reinterpret_cast<u32x4*>(b + row * pitch + 2 * e); }
+    __device__ __forceinline__ float get(int row, int e) const {
+        return (float)*reinterpret_cast<const __bf16*>(b + row * pitch + 2 * e);
+    }
+    __device__ __forceinline__ void put(int row, int e, float x) { *reinterpret_cast<__bf16*>(b + row * pitch + 2 * e) = (__bf16)x; }
+    __device__ __forceinline__ Frag<1> rows(int lane, int t, int s) const {
+        return Frag<1>{{*reinterpret_cast<const bf16x8*>(b + (16 * t + (lane & 15)) * pitch + 64 * s + 16 * (lane >> 4))}};
+    }
+    __device__ __forceinline__ Frag<1> cols(int lane, int m, int s) const {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        typedef __attribute__((address_space(3))) s16x4* Lds4;
+        const unsigned char* p = b + (32 * s + 8 * (lane >> 4) + ((lane & 15) >> 2)) * pitch + 32 * m + 8 * (lane & 3);
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(p + 4 * pitch));
+        return Frag<1>{{__builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))}};
+    }
+};
+template <int R, int W>
+struct GradTile<false, R, W> {
+    using T = float;
+    static constexpr int pitch = 4 * W + 16;
+    alignas(16) unsigned char b[R * pitch];
+    __device__ __forceinline__ u32x4* at16(int row, int e) { return reinterpret_cast<u32x4*>(b + row * pitch + 4 * e); }
+    __device__ __forceinline__ float get(int row, int e) const { return *reinterpret_cast<const float*>(b + row * pitch + 4 * e); }
+    __device__ __forceinline__ void put(int row, int e, float x) { *reinterpret_cast<float*>(b + row * pitch + 4 * e) = x; }
+    __device__ __forceinline__ Frag<3> rows(int lane, int t, int s) const {
+        float x[8];
+        load8(reinterpret_cast<const float*>(b + (16 * t + (lane & 15)) * pitch + 128 * s + 32 * (lane >> 4)), true, x);
+        return split8<3>(x);
+    }
+    __device__ __forceinline__ Frag<3> cols(int lane, int m, int s) const {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = get(32 * s + 8 * (lane >> 4) + i, 16 * m + (lane & 15));
+        return split8<3>(x);
+    }
+};
+
+template <bool BF, int DK>
+struct GradLds {
+    GradTile<BF, kC, DK> k, q;
+    struct Steps {
+        GradTile<BF, kC, 32> o, u, r;
+        GradTile<BF, DK, 32> s, d;
+    };
+    struct Mats {
+        GradTile<BF, kC, kC> w, n;
+    };
+    union {
+        Steps step;  // 32 columns of v's width
+        Mats mat;    // after the last of them
+    };
+    double G[kC];
+    float gam[kC], kap[kC], bet[kC], rv[kC], row[kC], krs[kC], kus[kC], dbz[kC];
+    float cs[4][kC];
+    float red[4];
+};
+
+template <bool BF, int DK, bool SHARED>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu((BF && !SHARED ? 2 : 1))))
+void k_delta_grad(GradArgs a) {
+    using T = typename Io<BF>::T;
+    constexpr int MT = DK / 16, KS = DK / 32;
+    constexpr uint32_t E = sizeof(T);
+    constexpr int V = 16 / (int)E, LPR = 32 / V;  // elements of 16 bytes; lanes of a 32-element row
+    constexpr int RPP = kThreads / LPR;           // rows one pass of the workgroup stages
+    constexpr int NR = kC / RPP, NSr = DK / RPP;  // passes for 64 rows, for DK rows
+    extern __shared__ __align__(16) unsigned char lds_raw[];
+    GradLds<BF, DK>& l = *reinterpret_cast<GradLds<BF, DK>*>(lds_raw);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, col = lane & 15;
+    const int64_t slot = blockIdx.x;
+    const int hk = blockIdx.y;
+    Range rg;
+    int64_t c, n;
+    if (!find_chunk(a.seqs, slot, rg, c, n)) return;
+    const int64_t tok = uniform64(rg.first + c * kC);
+    const int rows = __builtin_amdgcn_readfirstlane((int)(rg.len - c * kC < kC ? rg.len - c * kC : kC));
+    const int hv = a.sh.hv, dk = a.sh.dk, dv = a.sh.dv;
+    const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E, ldv = (uint32_t)a.sh.ldv * E,
+                   ldo = (uint32_t)(hv * dv) * E;
+
+    {  // K and Q
+        const RowBuf kb = row_buf((const T*)a.k + tok * a.sh.ldk + (int64_t)hk * dk, rows, ldk, dk * E);
+        const RowBuf qb = row_buf((const T*)a.q + tok * a.sh.ldq + (int64_t)hk * dk, rows, ldq, dk * E);
+#pragma unroll
+        for (int e = 0; e < kC * (DK / V) / kThreads; ++e) {
+            const int x = e * kThreads + tid, t = x / (DK / V), k = x % (DK / V) * V;
+            *l.k.at16(t, k) = __builtin_bit_cast(u32x4, buf_f4(kb, k < dk ? t * ldk + k * E : kNoElem, 0));
+            *l.q.at16(t, k) = __builtin_bit_cast(u32x4, buf_f4(qb, k < dk ? t * ldq + k * E : kNoElem, 0));
+        }
+    }
+    f32x4 dq[MT] = {}, dkk[MT] = {};
+    const int srow = tid / LPR, scol = tid % LPR * V;
+    for (int hh = 0; hh < (SHARED ? a.sh.group : 1); ++hh) {
+        const int h = hk * a.sh.group + hh;
+        const int64_t sidx = (slot * hv + h) * (int64_t)dk * dv;
+        const int64_t obase = (tok * hv + h) * (int64_t)dv;
+        const RowBuf ob = row_buf((const T*)a.dout + obase, rows, ldo, dv * E), ub = row_buf((const T*)a.u + obase, rows, ldo, dv * E);
+        const RowBuf rb = row_buf((const T*)a.r + obase, rows, ldo, dv * E);
+        const RowBuf vb = row_buf((const T*)a.v + tok * a.sh.ldv + (int64_t)h * dv, rows, ldv, dv * E);
+        const RowBuf sb = plain_buf((const T*)a.s0 + sidx, dk * dv * E), db = plain_buf((const T*)a.ds1 + sidx, dk * dv * E);
+        u32x4 po[NR], pu[NR], pr[NR], pv[NR], ps[NSr], pd[NSr];
+        auto fetch = [&](int c0) {
+            const bool ok = c0 + scol < dv;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const uint32_t off = ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem;
+                po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, off, 0));
+                pu[i] = __builtin_bit_cast(u32x4, buf_f4(ub, off, 0));
+                pr[i] = __builtin_bit_cast(u32x4, buf_f4(rb, off, 0));
+                pv[i] = __builtin_bit_cast(u32x4, buf_f4(vb, ok ? (i * RPP + srow) * ldv + (c0 + scol) * E : kNoElem, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < NSr; ++i) {
+                const int k = i * RPP + srow;
+                const uint32_t off = ok && k < dk ? (uint32_t)(k * dv + c0 + scol) * E : kNoElem;
+                ps[i] = __builtin_bit_cast(u32x4, buf_f4(sb, off, 0));
+                pd[i] = __builtin_bit_cast(u32x4, buf_f4(db, off, 0));
+            }
+        };
+        auto dot16 = [&](const u32x4& x, const u32x4& y) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF) {
+                    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+                    s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
+                } else {
+                    s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
+                }
+            }
+            return s;
+        };
+        fetch(0);
+        if (w == 0) {
+            float gv = 0.f, bv = 0.f;
+            if (lane < rows) {
+                gv = (float)((const T*)a.g)[(tok + lane) * hv + h];
+                bv = (float)((const T*)a.beta)[(tok + lane) * hv + h];
+            }
+            const double G = chunk_decay(gv, lane);
+            const double last = __shfl(G, 63);
+            l.G[lane] = G;
+            l.gam[lane] = expf((float)G);
+            l.kap[lane] = expf((float)(last - G));
+            l.bet[lane] = bv;
+        }
+        f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
+        float rv[NR] = {}, sd = 0.f;
+        for (int c0 = 0; c0 < dv; c0 += 32) {
+            __syncthreads();  // the step before (or the head before) has read its tiles
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                *l.step.o.at16(i * RPP + srow, scol) = po[i];
+                *l.step.u.at16(i * RPP + srow, scol) = pu[i];
+                *l.step.r.at16(i * RPP + srow, scol) = pr[i];
+                rv[i] += dot16(pr[i], pv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NSr; ++i) {
+                *l.step.s.at16(i * RPP + srow, scol) = ps[i];
+                *l.step.d.at16(i * RPP + srow, scol) = pd[i];
+                sd += dot16(ps[i], pd[i]);
+            }
+            if (c0 + 32 < dv) fetch(c0 + 32);
+            lds_barrier();
+            const auto ao = l.step.o.rows(lane, w, 0), ar = l.step.r.rows(lane, w, 0), au = l.step.u.rows(lane, w, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const auto b = l.step.u.rows(lane, j, 0);
+                    dp[j] = mma(ao, b, dp[j]);
+                    z[j] = mma(ar, b, z[j]);
+                }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const auto b = l.step.s.rows(lane, m, 0);
+                qs[m] = mma(ao, b, qs[m]);
+                rs[m] = mma(ar, b, rs[m]);
+                us[m] = mma(au, l.step.d.rows(lane, m, 0), us[m]);
+            }
+        }
+        // k_i . k_j and q_i . k_j
+        f32x4 kk[4] = {}, qk[4] = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const auto ka = l.k.rows(lane, w, s), qa = l.q.rows(lane, w, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const auto b = l.k.rows(lane, j, s);
+                    kk[j] = mma(ka, b, kk[j]);
+                    qk[j] = mma(qa, b, qk[j]);
+                }
+        }
+        // sums along rows over the sixteen lanes of a row
+        auto row_sum = [&](f32x4 x) {
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] += __shfl_xor(x[i], d);
+            return x;
+        };
+        f32x4 qqs = {}, krs = {}, kus = {}, rx = {}, dbz = {};
+        const int ti = 16 * w + 4 * g;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float kv = l.k.get(ti + i, 16 * m + col);
+                qqs[i] = fmaf(l.q.get(ti + i, 16 * m + col), qs[m][i], qqs[i]);
+                krs[i] = fmaf(kv, rs[m][i], krs[i]);
+                kus[i] = fmaf(kv, us[m][i], kus[i]);
+            }
+        const f32x4 gam = *reinterpret_cast<const f32x4*>(l.gam + ti), kap = *reinterpret_cast<const f32x4*>(l.kap + ti);
+        const f32x4 bet = *reinterpret_cast<const f32x4*>(l.bet + ti);
+        float cx[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tj = 16 * j + col;
+                float wv = 0.f, mv = 0.f;
+                if (j <= w && tj <= ti + i) {
+                    const float d = expf((float)(l.G[ti + i] - l.G[tj]));
+                    wv = a.sh.scale * d * dp[j][i];
+                    float x = wv * qk[j][i];
+                    if (tj < ti + i) {
+                        const float dz = d * z[j][i];
+                        mv = -bet[i] * dz;
+                        dbz[i] = fmaf(-dz, kk[j][i], dbz[i]);
+                        x = fmaf(mv, kk[j][i], x);
+                    }
+                    rx[i] += x;
+                    cx[j] += x;
+                }
+                dp[j][i] = wv;
+                z[j][i] = mv;
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            cx[j] += __shfl_xor(cx[j], 16);
+            cx[j] += __shfl_xor(cx[j], 32);
+            if (g == 0) l.cs[w][16 * j + col] = cx[j];
+        }
+        qqs = row_sum(qqs);
+        krs = row_sum(krs);
+        kus = row_sum(kus);
+        rx = row_sum(rx);
+        dbz = row_sum(dbz);
+        if (col == 0) {
+            *reinterpret_cast<f32x4*>(l.row + ti) = a.sh.scale * gam * qqs - bet * gam * krs + rx;
+            *reinterpret_cast<f32x4*>(l.krs + ti) = gam * krs;
+            *reinterpret_cast<f32x4*>(l.kus + ti) = kap * kus;
+            *reinterpret_cast<f32x4*>(l.dbz + ti) = dbz;
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+#pragma unroll
+            for (int d = 1; d < LPR; d <<= 1) rv[i] += __shfl_xor(rv[i], d);
+            if (tid % LPR == 0) l.rv[i * RPP + srow] = rv[i];
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sd += __shfl_xor(sd, d);
+        if (lane == 0) l.red[w] = sd;
+        __syncthreads();  // the last step's tiles have been read: W and M take their place
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tj = 16 * j + col;
+                l.mat.w.put(ti + i, tj, dp[j][i]);
+                if (tj < ti + i) {
+                    l.mat.n.put(ti + i, tj, z[j][i]);
+                    l.mat.n.put(tj, ti + i, z[j][i]);
+                } else if (tj == ti + i) {
+                    l.mat.n.put(tj, tj, 0.f);
+                }
+            }
+        __syncthreads();
+        if (w == 0) {
+            double d = (double)l.row[lane] - l.cs[0][lane] - l.cs[1][lane] - l.cs[2][lane] - l.cs[3][lane] - l.kus[lane];
+            double ku = l.kus[lane];
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) ku += __shfl_xor(ku, s);
+            if (lane == 63) d += ku + (double)l.gam[63] * ((double)l.red[0] + l.red[1] + l.red[2] + l.red[3]);
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) {
+                const double up = __shfl_down(d, s);
+                if (lane + s < 64) d += up;
+            }
+            if (lane < rows) {
+                ((T*)a.dg)[(tok + lane) * hv + h] = (T)(float)d;
+                ((T*)a.dbeta)[(tok + lane) * hv + h] = (T)(l.rv[lane] - l.krs[lane] + l.dbz[lane]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            dq[m] += a.sh.scale * gam * qs[m];
+            dkk[m] += kap * us[m] - gam * bet * rs[m];
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const auto na = l.mat.n.rows(lane, w, s);
+            const auto wa = l.mat.w.rows(lane, w, s);
+            const auto wt = l.mat.w.cols(lane, w, s);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const auto kc = l.k.cols(lane, m, s);
+                if (2 * s <= w) dq[m] = mma(wa, kc, dq[m]);
+                dkk[m] = mma(na, kc, dkk[m]);
+                if (2 * s + 1 >= w) dkk[m] = mma(wt, l.q.cols(lane, m, s), dkk[m]);
+            }
+        }
+    }
+    const uint32_t ldd = (uint32_t)(a.sh.hk * dk) * E;
+    const RowBuf qo = row_buf((T*)a.dq + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
+    const RowBuf ko = row_buf((T*)a.dk + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 16 * m + col;
+            const uint32_t off = k < dk ? (16 * w + 4 * g + i) * ldd + k * E : kNoElem;
+            const float x[1] = {dq[m][i]}, y[1] = {dkk[m][i]};
+            buf_store<BF, 1>(qo, off, x);
+            buf_store<BF, 1>(ko, off, y);
+        }
+}
+
+}  // namespace delta
+}  // namespace hy

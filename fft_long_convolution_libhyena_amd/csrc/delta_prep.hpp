@@ -89,12 +89,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
             gv = (float)((const T*)a.g)[(tok + lane) * a.sh.hv + h];
             bv = (float)((const T*)a.beta)[(tok + lane) * a.sh.hv + h];
         }
-        double G = (double)gv < kMinLog ? kMinLog : (double)gv;  // a NaN stays one
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double up = __shfl_up(G, d);
-            if (lane >= d) G += up;
-        }
+        const double G = chunk_decay(gv, lane);
         const double last = __shfl(G, 63);
         l.G[lane] = G;
         l.beta[lane] = bv;

@@ -696,6 +696,32 @@ hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N
                                    void* o, float* state_out, void* workspace, size_t workspace_bytes,
                                    hipStream_t stream);
 
+/* Bytes of workspace hyena_delta_backward needs: the forward's, the states before and
+ * the state gradients behind every chunk of 64 tokens, and two arrays like o. Returns 0
+ * as hyena_delta_workspace_bytes. */
+size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                            const int64_t* seq_start);
+
+/* Backward of hyena_delta_forward: with the forward's inputs and the gradients
+ *   dout       [tokens][heads_v][dim_v] of the dtype, of o
+ *   dstate_out [N][heads_v][dim_k][dim_v] fp32, of the final states, or NULL (zeros)
+ * of one scalar, its gradients with respect to every input (outputs, dense):
+ *   dq, dk [tokens][heads_k][dim_k], dv [tokens][heads_v][dim_v], dg, dbeta
+ *   [tokens][heads_v] of the dtype, rounded once from fp32 sums (over the value heads
+ *   that share a key head, too); dstate_in [N][heads_v][dim_k][dim_v] fp32, or NULL.
+ * The states are computed again from the inputs; nothing of the forward call is kept.
+ * bf16 calls round the operands of the chunk-parallel products (the states and their
+ * gradients at chunk borders, u, r) to bf16, the states themselves stay fp32 along
+ * both scans. Every sum has a fixed order: results are bitwise reproducible. Rows
+ * that belong to no sequence are left as they were. Arguments, workspace (of at least
+ * hyena_delta_backward_workspace_bytes) and errors otherwise as in
+ * hyena_delta_forward. Outputs must not alias inputs or each other. */
+hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
+                                    const int64_t* seq_start, const hyena_delta_inputs_t* in, const float* state_in,
+                                    const void* dout, const float* dstate_out, void* dq, void* dk, void* dv, void* dg,
+                                    void* dbeta, float* dstate_in, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
 /* The recurrent form: T further tokens (one when answering token by token, a few
  * drafted ones) of each of B rows, row b's tokens at b*T .. b*T + T - 1 of the
  * inputs and of o [B*T][heads_v][dim_v].

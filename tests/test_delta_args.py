@@ -79,6 +79,31 @@ def test_workspace(lib):
     assert lib.hyena_delta_workspace_bytes(None, 2, 128, None) == 0
 
 
+def backward(lib, p=None, N=2, tokens=128, start=None, i=None, ws=P, ws_bytes=1 << 40, **kw):
+    a = dict(s_in=None, dout=P, ds_out=None, dq=P, dk=P, dv=P, dg=P, dbeta=P, ds_in=None)
+    a.update(kw)
+    p, i = p or params(), i or inputs()
+    return lib.hyena_delta_backward(ctypes.byref(p), N, tokens, start, ctypes.byref(i), a["s_in"], a["dout"], a["ds_out"],
+                                    a["dq"], a["dk"], a["dv"], a["dg"], a["dbeta"], a["ds_in"], ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [dict(N=0), dict(tokens=129), dict(dout=None), dict(dq=None), dict(dk=None), dict(dv=None),
+                                dict(dg=None), dict(dbeta=None), dict(dq=P + 8), dict(s_in=P + 4), dict(ds_out=P + 4),
+                                dict(ds_in=P + 4), dict(ws=P + 8), dict(i=inputs(ldq=120))])
+def test_backward_arguments(lib, kw):
+    assert backward(lib, **kw) == INVALID
+
+
+def test_backward_workspace(lib):
+    need = lib.hyena_delta_backward_workspace_bytes(ctypes.byref(params()), 2, 128, None)
+    assert need > lib.hyena_delta_workspace_bytes(ctypes.byref(params()), 2, 128, None) > 0
+    assert backward(lib, ws_bytes=need - 1) == WORKSPACE
+    assert backward(lib, ws=None) == WORKSPACE
+    assert backward(lib, params(dim_k=136), i=inputs(ldq=1 << 20, ldk=1 << 20)) == UNSUPPORTED
+    assert lib.hyena_delta_backward_workspace_bytes(None, 2, 128, None) == 0
+    assert lib.hyena_delta_backward_workspace_bytes(ctypes.byref(params()), 2, 127, None) == 0
+
+
 def test_null_structs(lib):
     assert lib.hyena_delta_forward(None, 2, 128, None, ctypes.byref(inputs()), None, P, P, P, 1 << 40, None) == INVALID
     assert lib.hyena_delta_forward(ctypes.byref(params()), 2, 128, None, None, None, P, P, P, 1 << 40, None) == INVALID
