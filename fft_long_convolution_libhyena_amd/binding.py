@@ -20,6 +20,7 @@ STATUS = {0: "HYENA_OK", 1: "HYENA_ERR_INVALID_ARG", 2: "HYENA_ERR_UNSUPPORTED",
           3: "HYENA_ERR_WORKSPACE", 4: "HYENA_ERR_DEVICE"}
 _PATHS = {"auto": PATH_AUTO, "lds": PATH_LDS, "fourstep": PATH_FOURSTEP, "partitioned": PATH_PARTITIONED}
 _DTYPES = {"f32": HYENA_F32, "bf16": HYENA_BF16}
+_NORMS = {"rms": 0, "l2": 1}  # HYENA_NORM_RMS, HYENA_NORM_L2
 
 # every symbol include/hyena.h declares
 FLAG_CIRCULAR = 1  # HYENA_FLAG_CIRCULAR
@@ -37,6 +38,7 @@ EXPORTS = ("hyena_plan_create", "hyena_plan_create_path", "hyena_plan_create_ex"
            "hyena_conv3d_forward_per_sample", "hyena_plan2d_create_ex", "hyena_plan3d_create_ex",
            "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_delta_workspace_bytes",
            "hyena_delta_forward", "hyena_delta_backward_workspace_bytes", "hyena_delta_backward", "hyena_delta_step",
+           "hyena_qk_norm_forward", "hyena_qk_norm_backward_workspace_bytes", "hyena_qk_norm_backward",
            "hyena_status_string")
 
 
@@ -69,6 +71,13 @@ class DeltaInputsStruct(ctypes.Structure):
     """hyena_delta_inputs_t: device pointers of q, k, v (each with its token stride), g and beta."""
     _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
                 ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64), ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
+class QKNormParamsStruct(ctypes.Structure):
+    """hyena_qk_norm_params_t: sizes, kinds and device pointers of the head norm."""
+    _fields_ = [("heads_q", ctypes.c_int64), ("heads_k", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("rot", ctypes.c_int64), ("kind", ctypes.c_int), ("layout", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("freq", ctypes.c_void_p)]
 
 
 class HyenaError(RuntimeError):
@@ -186,6 +195,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.hyena_delta_backward.restype = ci
     lib.hyena_delta_step.argtypes = [dp, i64, i64, di, vp, i64, vp, vp, vp]
     lib.hyena_delta_step.restype = ci
+    qp = ctypes.POINTER(QKNormParamsStruct)
+    lib.hyena_qk_norm_forward.argtypes = [qp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.hyena_qk_norm_forward.restype = ci
+    lib.hyena_qk_norm_backward_workspace_bytes.argtypes = [qp, i64]
+    lib.hyena_qk_norm_backward_workspace_bytes.restype = sz
+    lib.hyena_qk_norm_backward.argtypes = [qp, i64, vp, i64, vp, i64] + [vp] * 8 + [sz, vp]
+    lib.hyena_qk_norm_backward.restype = ci
     lib.hyena_status_string.argtypes = [ci]
     lib.hyena_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -701,6 +717,130 @@ class Plan3D(_GridPlan):
         super().__init__((A, H, W), D, dtype, circular)
 
 
+def _token_rows(torch, t, name, rows, heads, dim, dtype, device):
+    """The token stride of t [*rows, heads, dim] (rows: (tokens,) or (B, T)): dense heads,
+    one stride over all tokens, rows that start on 16 bytes."""
+    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be a tensor on the GPU that holds q")
+    if tuple(t.shape) != (*rows, heads, dim) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(*rows, heads, dim)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    width = heads * dim
+    if t.numel() == 0:
+        return width
+    ld = t.stride(-3) if rows[-1] > 1 else (t.stride(0) if len(rows) == 2 and rows[0] > 1 else width)
+    if ((dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim) or ld < width
+            or (len(rows) == 2 and rows[0] > 1 and t.stride(0) != rows[1] * ld)):
+        raise ValueError(f"{name} must have dense heads and one stride between tokens")
+    if ld * t.element_size() % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s rows must start on 16 bytes")
+    return ld
+
+
+class QKNorm:
+    """Norms of queries and keys for each head with the position rotation (hyena_qk_norm_* of
+    include/hyena.h): kind "rms" or "l2"; w_q, w_k [dim] fp32 weights or None; freq [F] fp32
+    radians per position of the F rotated pairs, or None; pairs: neighbours (2i, 2i+1) are
+    rotated instead of the halves (i, i + F). The tensors given here are used by every call."""
+
+    def __init__(self, heads_q: int, heads_k: int, dim: int, dtype: str = "bf16", kind: str = "rms", eps: float = 1e-6,
+                 w_q=None, w_k=None, freq=None, pairs: bool = False):
+        import torch
+
+        self._torch = torch
+        self.lib = load_library()
+        if dtype not in _DTYPES or kind not in _NORMS:
+            raise ValueError(f"dtype must be one of {list(_DTYPES)}, kind one of {list(_NORMS)}")
+        self.heads_q, self.heads_k, self.dim, self.dtype = int(heads_q), int(heads_k), int(dim), dtype
+        self.kind, self.eps, self.pairs = kind, float(eps), bool(pairs)
+        self.w_q, self.w_k, self.freq = w_q, w_k, freq
+        for name, t, n in (("w_q", w_q, self.dim), ("w_k", w_k, self.dim), ("freq", freq, None)):
+            if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()
+                                  or (n is not None and t.numel() != n)):
+                raise ValueError(f"{name} must be a contiguous fp32 vector" + (f" of {n}" if n else ""))
+
+    @property
+    def io_dtype(self):
+        return self._torch.bfloat16 if self.dtype == "bf16" else self._torch.float32
+
+    def _params(self, device):
+        for name in ("w_q", "w_k", "freq"):
+            t = getattr(self, name)
+            if t is not None and t.device != device:
+                raise ValueError(f"{name} must be on the GPU that holds q")
+        ptr = lambda t: t.data_ptr() if t is not None and t.numel() else None  # noqa: E731
+        return QKNormParamsStruct(self.heads_q, self.heads_k, self.dim, self.freq.numel() if self.freq is not None else 0,
+                                  _NORMS[self.kind], 1 if self.pairs else 0, _DTYPES[self.dtype], self.eps,
+                                  ptr(self.w_q), ptr(self.w_k), ptr(self.freq))
+
+    def _args(self, q, k, positions):
+        torch, dev = self._torch, q.device
+        if q.dim() not in (3, 4):
+            raise ValueError("q must be [tokens, heads_q, dim] or [B, T, heads_q, dim]")
+        rows = tuple(int(n) for n in q.shape[:-2])
+        tokens = 1
+        for n in rows:
+            tokens *= n
+        ldq = _token_rows(torch, q, "q", rows, self.heads_q, self.dim, self.io_dtype, dev)
+        ldk = _token_rows(torch, k, "k", rows, self.heads_k, self.dim, self.io_dtype, dev)
+        if positions is None:
+            if self.freq is not None and self.freq.numel():
+                raise ValueError("positions are needed for the rotation")
+        elif (positions.device != dev or positions.dtype != torch.int64 or tuple(positions.shape) != rows
+              or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int64 tensor of shape {rows} on the GPU that holds q")
+        return rows, tokens, ldq, ldk, positions.data_ptr() if positions is not None else None
+
+    def _dense(self, t, name, rows, heads, device):
+        if t is None:
+            return self._torch.empty((*rows, heads, self.dim), dtype=self.io_dtype, device=device)
+        if (not isinstance(t, self._torch.Tensor) or t.device != device or t.dtype != self.io_dtype
+                or tuple(t.shape) != (*rows, heads, self.dim) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {self.io_dtype} tensor of shape {(*rows, heads, self.dim)}")
+        return t
+
+    def forward(self, q, k, positions=None, q_out=None, k_out=None):
+        """hyena_qk_norm_forward: q [tokens or B, T, heads_q, dim], k [.., heads_k, dim] (one stride
+        between tokens), positions int64 of the tokens' shape -> (q_out, k_out), dense."""
+        torch, dev = self._torch, q.device
+        rows, tokens, ldq, ldk, pos = self._args(q, k, positions)
+        q_out = self._dense(q_out, "q_out", rows, self.heads_q, dev)
+        k_out = self._dense(k_out, "k_out", rows, self.heads_k, dev)
+        with torch.cuda.device(dev):
+            _check("hyena_qk_norm_forward",
+                   self.lib.hyena_qk_norm_forward(ctypes.byref(self._params(dev)), tokens, q.data_ptr(), ldq,
+                                                  k.data_ptr(), ldk, pos, q_out.data_ptr(), k_out.data_ptr(),
+                                                  _stream_handle(torch, dev)))
+        return q_out, k_out
+
+    def backward_workspace_bytes(self, tokens: int, device) -> int:
+        return int(self.lib.hyena_qk_norm_backward_workspace_bytes(ctypes.byref(self._params(device)), int(tokens)))
+
+    def backward(self, q, k, dq_out, dk_out, positions=None, workspace=None):
+        """hyena_qk_norm_backward: (dq, dk, dw_q, dw_k) for the gradients of the forward's outputs;
+        the weights' gradients are None where there is no weight."""
+        torch, dev = self._torch, q.device
+        rows, tokens, ldq, ldk, pos = self._args(q, k, positions)
+        for name, t, h in (("dq_out", dq_out, self.heads_q), ("dk_out", dk_out, self.heads_k)):
+            if t is None:
+                raise ValueError(f"{name} is needed")
+            self._dense(t, name, rows, h, dev)
+        dq, dk = self._dense(None, "dq", rows, self.heads_q, dev), self._dense(None, "dk", rows, self.heads_k, dev)
+        dw_q, dw_k = (torch.empty(self.dim, dtype=torch.float32, device=dev) if w is not None else None
+                      for w in (self.w_q, self.w_k))
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        if workspace is None and (dw_q is not None or dw_k is not None):
+            workspace = torch.empty(self.backward_workspace_bytes(tokens, dev), dtype=torch.uint8, device=dev)
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        with torch.cuda.device(dev):
+            _check("hyena_qk_norm_backward",
+                   self.lib.hyena_qk_norm_backward(ctypes.byref(self._params(dev)), tokens, q.data_ptr(), ldq,
+                                                   k.data_ptr(), ldk, pos, dq_out.data_ptr(), dk_out.data_ptr(),
+                                                   dq.data_ptr(), dk.data_ptr(), ptr(dw_q), ptr(dw_k), ptr(workspace),
+                                                   ws_bytes, _stream_handle(torch, dev)))
+        return dq, dk, dw_q, dw_k
+
+
 class DeltaRule:
     """The gated delta rule (hyena_delta_forward / _step of include/hyena.h): fixed heads,
     dims and dtype ("f32" or "bf16"). Tensors must be on one device and calls run there,
@@ -734,28 +874,10 @@ class DeltaRule:
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                              f"got {t.dtype} {tuple(t.shape)}")
 
-    def _rows(self, t, name, rows, heads, dim, device):
-        """The token stride of t [*rows, heads, dim]: dense heads, one stride over all tokens."""
-        if not isinstance(t, self._torch.Tensor) or t.device != device or device.type != "cuda":
-            raise ValueError(f"{name} must be a tensor on the GPU that holds q")
-        if tuple(t.shape) != (*rows, heads, dim) or t.dtype != self.io_dtype:
-            raise ValueError(f"{name} must be a {self.io_dtype} tensor of shape {(*rows, heads, dim)}, "
-                             f"got {t.dtype} {tuple(t.shape)}")
-        width = heads * dim
-        if t.numel() == 0:
-            return width
-        ld = t.stride(-3) if rows[-1] > 1 else (t.stride(0) if len(rows) == 2 and rows[0] > 1 else width)
-        if ((dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim) or ld < width
-                or (len(rows) == 2 and rows[0] > 1 and t.stride(0) != rows[1] * ld)):
-            raise ValueError(f"{name} must have dense heads and one stride between tokens")
-        if ld * t.element_size() % 16 or t.data_ptr() % 16:
-            raise ValueError(f"{name}'s rows must start on 16 bytes")
-        return ld
-
     def _inputs(self, q, k, v, g, beta, rows, device):
         Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
-        ld = [self._rows(q, "q", rows, Hk, Dk, device), self._rows(k, "k", rows, Hk, Dk, device),
-              self._rows(v, "v", rows, Hv, Dv, device)]
+        ld = [_token_rows(self._torch, t, name, rows, heads, dim, self.io_dtype, device)
+              for t, name, heads, dim in ((q, "q", Hk, Dk), (k, "k", Hk, Dk), (v, "v", Hv, Dv))]
         self._need(g, "g", (*rows, Hv), self.io_dtype, device)
         self._need(beta, "beta", (*rows, Hv), self.io_dtype, device)
         return DeltaInputsStruct(q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2], g.data_ptr(),

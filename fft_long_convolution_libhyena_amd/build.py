@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhyena.so")
 SOURCES = ["hyena_api.hip", "hyena_backward.hip", "hyena_operator.hip", "fourstep.hip", "fourstep_backward.hip", "implicit_filter.hip", "kernel_synthesis.hip", "inproj.hip", "outproj.hip", "conv2d.hip", "conv3d.hip", "partitioned.hip", "lds_path_a.hip", "lds_path_b.hip", "lds_path_c.hip",
            "lds_path_d.hip", "lds_backward_a.hip", "lds_backward_b.hip", "lds_backward_c.hip", "lds_backward_d.hip",
-           "lds_backward_e.hip", "lds_backward_f.hip", "delta_forward.hip", "delta_backward.hip", "delta_step.hip"]
+           "lds_backward_e.hip", "lds_backward_f.hip", "delta_forward.hip", "delta_backward.hip", "delta_step.hip", "qk_norm.hip"]
 HEADERS = ["fft_core.hpp", "kernels.hpp", "pair.hpp", "plan.hpp", "tables.hpp", "conv_nd.hpp", "lds_path.hpp", "fourstep.hpp", "backward.hpp",
            "lds_backward.hpp", "outproj.hpp", "delta.hpp", "delta_prep.hpp", "delta_scan.hpp", "delta_rev.hpp",
            "delta_grad.hpp"]

@@ -738,6 +738,60 @@ hyena_status_t hyena_delta_step(const hyena_delta_params_t* params, int64_t B, i
                                 const hyena_delta_inputs_t* in, float* states, int64_t num_states,
                                 const int32_t* slots, void* o, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys for each head, with the position rotation in the same
+ * pass. For the vector x [dim] of one head of one token, weight w and F = rot pairs:
+ *   n = x / sqrt(mean(x^2) + eps)  (HYENA_NORM_RMS)
+ *   n = x / sqrt(sum(x^2) + eps)   (HYENA_NORM_L2: unit length, what the gated delta
+ *                                   rule wants of its keys)
+ *   y = n * w, then for i < F the pair (y[i], y[i+F]) (HYENA_ROT_HALVES) or
+ *   (y[2i], y[2i+1]) (HYENA_ROT_PAIRS) turned by the angle position * freq[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos).
+ * Angles are formed and reduced in fp64, everything else is fp32 and rounded once.
+ * ------------------------------------------------------------------------ */
+typedef enum { HYENA_NORM_RMS = 0, HYENA_NORM_L2 = 1 } hyena_norm_t;
+typedef enum { HYENA_ROT_HALVES = 0, HYENA_ROT_PAIRS = 1 } hyena_rot_t;
+
+typedef struct hyena_qk_norm_params_s {
+    int64_t heads_q, heads_k;
+    int64_t dim;         /* a multiple of 8, at most 256 */
+    int64_t rot;         /* F: rotated pairs, a multiple of 4, 2 F <= dim; 0 for none */
+    hyena_norm_t kind;
+    hyena_rot_t layout;
+    hyena_dtype_t dtype; /* of q, k, their outputs and gradients */
+    float eps;           /* above 0, finite */
+    const float* w_q;    /* [dim] fp32, device, shared by the heads, or NULL (ones) */
+    const float* w_k;
+    const float* freq;   /* [F] fp32, device: radians per position; NULL if F = 0 */
+} hyena_qk_norm_params_t;
+
+/* q [tokens][heads_q][dim] with ldq elements between tokens (at least the heads'
+ * width, a multiple of 16 bytes, at most 2^31; a column range of a projection's rows
+ * may be given as it lies), k likewise; positions [tokens] int64, device (NULL if
+ * F = 0); q_out, k_out dense (outputs). Runs on the current device, no plan.
+ * Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned pointers,
+ * bad sizes, ld, eps, kind or layout), HYENA_ERR_UNSUPPORTED (dim or rot outside the
+ * ranges above, more than 65535 heads in all, tokens > 2^31), HYENA_ERR_DEVICE. */
+hyena_status_t hyena_qk_norm_forward(const hyena_qk_norm_params_t* params, int64_t tokens, const void* q, int64_t ldq,
+                                     const void* k, int64_t ldk, const int64_t* positions, void* q_out, void* k_out,
+                                     hipStream_t stream);
+
+/* Bytes of workspace hyena_qk_norm_backward needs where it sums weight gradients
+ * (partial sums of at most 1024 workgroups, or one a head where there are more).
+ * Returns 0 for arguments that the call would refuse and for tokens = 0. */
+size_t hyena_qk_norm_backward_workspace_bytes(const hyena_qk_norm_params_t* params, int64_t tokens);
+
+/* Backward: the gradients dq, dk (dense, outputs) of q and k, and dw_q, dw_k [dim] fp32
+ * of the weights (outputs; NULL where not wanted; of the ones, where the weight is
+ * NULL), for the gradients dq_out, dk_out (dense) of the forward's outputs. Weight
+ * gradients are complete sums over tokens and heads in a fixed order. workspace: as
+ * above, 16-byte aligned; ignored where neither weight gradient is asked for. Errors
+ * as the forward's, and HYENA_ERR_WORKSPACE. Outputs must not alias inputs. */
+hyena_status_t hyena_qk_norm_backward(const hyena_qk_norm_params_t* params, int64_t tokens, const void* q, int64_t ldq,
+                                      const void* k, int64_t ldk, const int64_t* positions, const void* dq_out,
+                                      const void* dk_out, void* dq, void* dk, float* dw_q, float* dw_k, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* hyena_status_string(hyena_status_t s);
 

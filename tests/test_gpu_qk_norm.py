@@ -1,0 +1,191 @@
+"""Head norm with rotation on the GPU against its plain form in 64 bits.
+
+Tolerances (relative 2-norm): bf16 outputs are rounded once from fp32, half a step 2^-8.
+fp32: a value passes a sum of up to 256 squares (its root halves the relative error), the
+reciprocal root, two products and a rotation of four more operations: at most
+(256 / 2 + 16) * 2^-24. The backward has a second sum of 256 and up to 16 operations more:
+(256 + 256 / 2 + 32) * 2^-24. Weight gradients are sums of n terms of either error in fp32
+by lanes, groups and workgroups (at most 8192 additions each way here): n is bounded by
+the longest chain, 512 * 2^-24, on terms off by the backward's bound.
+"""
+import pytest
+import torch
+
+import _delta as D
+
+pytestmark = pytest.mark.gpu
+
+FWD = {"bf16": 2.0 ** -8, "f32": (256 / 2 + 16) * 2.0 ** -24}
+BWD = {"bf16": 2.0 ** -8 + 416 * 2.0 ** -24, "f32": 416 * 2.0 ** -24}
+DW = (512 + 416) * 2.0 ** -24
+
+
+def reference(x, w, pos, freq, kind, pairs, eps):
+    """64-bit y of x [tokens, heads, dim]; differentiable."""
+    n = x.shape[-1]
+    size = x.square().sum(-1, keepdim=True) / (n if kind == "rms" else 1) + eps
+    y = x / size.sqrt()
+    if w is not None:
+        y = y * w
+    f = 0 if freq is None else freq.numel()
+    if f == 0:
+        return y
+    ang = pos.double()[:, None, None] * freq.double()
+    c, s = ang.cos(), ang.sin()
+    a, b = (y[..., 0:2 * f:2], y[..., 1:2 * f:2]) if pairs else (y[..., :f], y[..., f:2 * f])
+    u, v = a * c - b * s, a * s + b * c
+    head = torch.stack([u, v], -1).flatten(-2) if pairs else torch.cat([u, v], -1)
+    return torch.cat([head, y[..., 2 * f:]], -1)
+
+
+def make(tokens, hq, hk, dim, rot, dtype, seed, far=0, weights=True):
+    gen = torch.Generator().manual_seed(seed)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rn = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    return dict(q=rn(tokens, hq, dim).to(dt), k=(3 * rn(tokens, hk, dim)).to(dt), dq_out=rn(tokens, hq, dim).to(dt),
+                dk_out=rn(tokens, hk, dim).to(dt), w_q=1 + 0.3 * rn(dim) if weights else None,
+                w_k=1 + 0.3 * rn(dim) if weights else None,
+                freq=10000.0 ** (-torch.arange(rot).float() / max(rot, 1)) if rot else None,
+                pos=torch.randint(0, far + 50, (tokens,), generator=gen))
+
+
+def gpu(x):
+    return None if x is None else x.cuda()
+
+
+def norm(d, hq, hk, dim, dtype, kind, pairs, eps=1e-6):
+    from fft_long_convolution_libhyena_amd import QKNorm
+
+    return QKNorm(hq, hk, dim, dtype=dtype, kind=kind, eps=eps, w_q=gpu(d["w_q"]), w_k=gpu(d["w_k"]), freq=gpu(d["freq"]),
+                  pairs=pairs)
+
+
+CASES = [
+    # tokens, heads_q, heads_k, dim, F, far, weights
+    (1, 1, 1, 8, 0, 0, True),
+    (5, 6, 6, 128, 64, 1000000, True),
+    (37, 3, 1, 72, 12, 0, False),
+    (130, 12, 4, 64, 16, 100000, True),
+    (9, 2, 7, 256, 128, 0, False),
+    (64, 5, 2, 96, 24, 10, True),
+    (3000, 2, 1, 16, 8, 0, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind,pairs", [("rms", False), ("l2", True), ("l2", False), ("rms", True)])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rot,far,weights", CASES)
+def test_forward_and_backward(tokens, hq, hk, dim, rot, far, weights, kind, pairs, dtype):
+    d = make(tokens, hq, hk, dim, rot, dtype, tokens + dim, far, weights)
+    m = norm(d, hq, hk, dim, dtype, kind, pairs)
+    pos = gpu(d["pos"])
+    out = m.forward(d["q"].cuda(), d["k"].cuda(), pos)
+    got = m.backward(d["q"].cuda(), d["k"].cuda(), d["dq_out"].cuda(), d["dk_out"].cuda(), pos)
+    for i, n in enumerate("qk"):
+        x = d[n].double().requires_grad_()
+        w = d["w_" + n].double().requires_grad_() if weights else None
+        y = reference(x, w, d["pos"], d["freq"], kind, pairs, 1e-6)
+        assert D.rel(out[i], y) <= FWD[dtype]
+        grads = torch.autograd.grad((y * d[f"d{n}_out"].double()).sum(), [x] + ([w] if weights else []))
+        assert D.rel(got[i], grads[0]) <= BWD[dtype]
+        if weights:
+            assert D.rel(got[2 + i], grads[1]) <= DW
+        else:
+            assert got[2 + i] is None
+
+
+def test_views_of_a_projection_and_batch_shape():
+    hq, hk, dim, B, T = 4, 2, 64, 2, 33
+    d = make(B * T, hq, hk, dim, 32, "bf16", 3)
+    rows = torch.cat([d["q"].flatten(1), d["k"].flatten(1), torch.zeros(B * T, 8).bfloat16()], 1).cuda()
+    q = rows[:, :hq * dim].unflatten(1, (hq, dim)).unflatten(0, (B, T))
+    k = rows[:, hq * dim:(hq + hk) * dim].unflatten(1, (hk, dim)).unflatten(0, (B, T))
+    m = norm(d, hq, hk, dim, "bf16", "rms", False)
+    pos = d["pos"].cuda().unflatten(0, (B, T))
+    a = m.forward(q, k, pos)
+    b = m.forward(d["q"].cuda(), d["k"].cuda(), d["pos"].cuda())
+    for x, y in zip(a, b):
+        assert x.shape[:2] == (B, T) and torch.equal(x.flatten(0, 1), y)
+
+
+def test_zero_vectors_infinities_and_nan():
+    """A zero head gives zeros (eps holds the root up); what is not finite stays in its head."""
+    d = make(6, 2, 1, 64, 16, "f32", 4)
+    d["q"][1, 0] = 0
+    d["q"][2, 1, 5] = float("nan")
+    d["q"][3, 0, 7] = float("inf")
+    m = norm(d, 2, 1, 64, "f32", "l2", False)
+    q, k = m.forward(d["q"].cuda(), d["k"].cuda(), d["pos"].cuda())
+    assert bool((q[1, 0] == 0).all())
+    bad = ~torch.isfinite(q)
+    assert bool(bad[2, 1].any()) and bool(bad[3, 0].any())
+    bad[2, 1] = False
+    bad[3, 0] = False
+    assert not bool(bad.any()) and bool(torch.isfinite(k).all())
+
+
+def test_no_tokens():
+    d = make(0, 2, 1, 64, 16, "bf16", 5)
+    m = norm(d, 2, 1, 64, "bf16", "rms", False)
+    q, k = m.forward(d["q"].cuda(), d["k"].cuda(), d["pos"].cuda())
+    assert q.shape == (0, 2, 64) and k.shape == (0, 1, 64)
+    out = m.backward(d["q"].cuda(), d["k"].cuda(), d["dq_out"].cuda(), d["dk_out"].cuda(), d["pos"].cuda())
+    assert bool((out[2] == 0).all()) and bool((out[3] == 0).all())
+
+
+def test_repeatable_and_captured():
+    d = make(500, 6, 6, 128, 64, "bf16", 6)
+    m = norm(d, 6, 6, 128, "bf16", "rms", False)
+    x = {n: d[n].cuda() for n in ("q", "k", "dq_out", "dk_out", "pos")}
+    call = lambda: (*m.forward(x["q"], x["k"], x["pos"]),  # noqa: E731
+                    *m.backward(x["q"], x["k"], x["dq_out"], x["dk_out"], x["pos"]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    for i in range(3):
+        x["q"].mul_(0.5 + i)
+        x["pos"].add_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, call()):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_then_delta_rule_then_backward(dtype):
+    """The layer's path: projection rows -> normed queries and keys -> delta rule, and its
+    gradients back through both, against the same chain in 64 bits."""
+    from fft_long_convolution_libhyena_amd import DeltaRule, QKNorm
+
+    hk, hv, dim, B, T = 2, 4, 64, 2, 70
+    gen = torch.Generator().manual_seed(11)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k = (torch.randn(B * T, hk, dim, generator=gen).to(dt) for _ in range(2))
+    d = D.make([T] * B, hk, hv, dim, dim, dtype, seed=12)
+    freq = 10000.0 ** (-torch.arange(16).float() / 16)
+    pos = torch.arange(T).repeat(B)
+    m = QKNorm(hk, hk, dim, dtype=dtype, kind="l2", freq=freq.cuda())
+    rule = DeltaRule(hk, hv, dim, dim, dtype)
+    rows = lambda t: t.cuda().unflatten(0, (B, T))  # noqa: E731
+    qn, kn = m.forward(rows(q), rows(k), rows(pos))
+    rest = [rows(d[n]) for n in ("v", "g", "beta")]
+    o, _ = rule.forward(qn, kn, *rest)
+    dqn, dkn, dv, dg, db, _ = rule.backward(qn, kn, *rest, rows(d["do"]))
+    dq, dk, _, _ = m.backward(rows(q), rows(k), dqn, dkn, rows(pos))
+    leaves = [x.double().requires_grad_() for x in (q, k, d["v"], d["g"], d["beta"])]
+    y = [reference(x, None, pos, freq, "l2", False, 1e-6) for x in leaves[:2]]
+    zero = torch.zeros(hv, dim, dim, dtype=torch.float64)
+    ref = torch.cat([D.recurrence(*(x[i * T:(i + 1) * T] for x in (*y, *leaves[2:])), zero, dim ** -0.5)[0] for i in range(B)])
+    want = torch.autograd.grad((ref * d["do"].double()).sum(), leaves)
+    # bf16: what the parts' own tests allow, and one more rounding of the normed vectors
+    # (and of their gradients) on the way; they add in squares
+    tol = 2.0 ** -8 * (4 + 1) ** 0.5 if dtype == "bf16" else 2 * 416 * 2.0 ** -24
+    tol_grad = 2.0 ** -8 * (4 * 7 + 2) ** 0.5 if dtype == "bf16" else 4 * 416 * 2.0 ** -24
+    assert D.rel(o.flatten(0, 1), ref) <= tol
+    for got, exact in zip((dq, dk, dv, dg, db), want):
+        assert D.rel(got.flatten(0, 1), exact) <= tol_grad
