@@ -42,6 +42,13 @@ struct ScanArgs {
 
 enum { kScanOut = 0, kScanKeep = 1 };
 
+// The outputs' waves rest for this many 64-clock units after a barrier, while the state
+// waves read K: both at once would halve the state's LDS rate where it waits for it.
+#ifndef HY_SLEEP
+#define HY_SLEEP 8
+#endif
+constexpr int kOutSleep = HY_SLEEP;
+
 // Minus the identity, as left operands that take rows of a 32-row operand back to the
 // result tile (t even or odd) they came from.
 struct MinusOne {
@@ -298,6 +305,7 @@ void k_delta_scan(ScanArgs a) {
                 }
                 for (int c = 0; c < nch; ++c) {
                     const int m = c + lead;
+                    __builtin_amdgcn_s_sleep(kOutSleep);
                     if (m < nch) {
                         rt.store(tile[m & 1], lane);
                         if (lead) rv.store(l.v[m & 1], lane);
@@ -331,7 +339,7 @@ void k_delta_scan(ScanArgs a) {
     const uint32_t ldv = (uint32_t)a.sh.ldv * E;
     const uint32_t voff = cok ? drow(0, 0) * ldv + c0 * E : kNoElem;
     auto vbuf = [&](int c) { return plain_buf(vbase + c * vrow, (rows_in(c) - 1) * ldv + dv * E); };
-    Frag<NS> Tf[kTri];
+    Frag<NS> Tab[BF ? 2 : 1][kTri];  // fp32 has no room for two
     uint32_t V[4][4];  // fp32 only, a chunk ahead; bf16 v comes through LDS
     f32x4 gam[4], kap[4];
     float glast = 0.f;
@@ -345,7 +353,7 @@ void k_delta_scan(ScanArgs a) {
     auto load_last = [&](const RowBuf& b) {
         glast = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, 0, Rec<BF>::sc + (kC - 1) * 4, 0));
     };
-    auto load_t = [&](const RowBuf& b, int f) { Tf[f] = buf_frag<NS>(b, Rec<BF>::t, f, lane); };
+    auto load_t = [&](Frag<NS>(&to)[kTri], const RowBuf& b, int f) { to[f] = buf_frag<NS>(b, Rec<BF>::t, f, lane); };
     if (nch > 0) {
         const RowBuf vb = vbuf(0), rb = plain_buf(rec, Rec<BF>::bytes);
 #pragma unroll
@@ -356,12 +364,13 @@ void k_delta_scan(ScanArgs a) {
         }
         load_last(rb);
 #pragma unroll
-        for (int f = 0; f < kTri; ++f) load_t(rb, f);
+        for (int f = 0; f < kTri; ++f) load_t(Tab[0], rb, f);
         lds_barrier();  // K of the first chunk is in LDS
     }
     unsigned char* s0p = OUT ? nullptr : (unsigned char*)a.s0 + (slot0 * hv + h) * (int64_t)dk * dv * E;
     constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;  // matrix instructions per product
-    for (int c = 0; c < nch; ++c) {
+    // one chunk; T alternates between two sets of registers
+    auto chunk = [&](int c, Frag<NS>(&Tf)[kTri], Frag<NS>(&Tn)[kTri]) {
         if (c + 1 < nch) rec += recstep;  // loaded for the next chunk; the last one reads itself again
         const RowBuf vb = vbuf(c + 1 < nch ? c + 1 : c), rb = plain_buf(rec, Rec<BF>::bytes);
         const Tile<NI, DK>& K = l.k[c & (BUF - 1)];
@@ -400,6 +409,10 @@ void k_delta_scan(ScanArgs a) {
                 for (int p = 0; p < NO; ++p) *reinterpret_cast<bf16x8*>(&l.x[wave][c & 1].s[s][p][lane * 8]) = sf[s].p[p];
             }
             if (s + 2 < KS) read_rows(s + 2);
+            if constexpr (BF) {
+#pragma unroll
+                for (int f = s * kTri / KS; f < (s + 1) * kTri / KS; ++f) load_t(Tn, rb, f);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         Frag<NI> kt[2][MT];
@@ -438,12 +451,14 @@ void k_delta_scan(ScanArgs a) {
         kf[0] = pair_frag<NS>(kap[0] * u[0], kap[1] * u[1], minus);
 #pragma unroll
         for (int m = 0; m < MT; ++m) S[m] *= glast;
+        interleave<2 * X3, 12, 0>();
+        if constexpr (!BF) {
 #pragma unroll
-        for (int f = 0; f < kTri; ++f) load_t(rb, f);
+            for (int f = 0; f < kTri; ++f) load_t(Tn, rb, f);
+        }
         load_kap(rb, 0);
         load_kap(rb, 1);
         load_last(rb);
-        interleave<2 * X3, 12, 2>();
 #pragma unroll
         for (int m = 0; m < MT; ++m) kt[1][m] = K.cols(lane, m, 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -453,7 +468,26 @@ void k_delta_scan(ScanArgs a) {
             const Frag<NI> w[2] = {kt[s][2 * p], kt[s][2 * p + 1]};
             mma_tiles(w, kf[s], S + 2 * p);
         };
-        auto parts = [&](int p) { sf[p] = pair_frag<NS>(S[2 * p], S[2 * p + 1], minus); };
+        f32x4 rest[MT];
+        auto next_part = [&](int p, int n) {
+            const f32x4 &a = rest[2 * p], &b = rest[2 * p + 1];
+            const u32x4 w = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
+            sf[p].p[n] = __builtin_bit_cast(bf16x8, w);
+            if (n + 1 < NS) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    rest[2 * p + t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus.a[t], sf[p].p[n], rest[2 * p + t], 0, 0, 0);
+            }
+        };
+        auto first_part = [&](int p) {
+            rest[2 * p] = S[2 * p];
+            rest[2 * p + 1] = S[2 * p + 1];
+            next_part(p, 0);
+        };
+        auto last_parts = [&](int p) {
+#pragma unroll
+            for (int n = 1; n < NS; ++n) next_part(p, n);
+        };
 #pragma unroll
         for (int p = 0; p < KS; ++p) update(0, p);
         kf[1] = pair_frag<NS>(kap[2] * u[2], kap[3] * u[3], minus);
@@ -466,18 +500,24 @@ void k_delta_scan(ScanArgs a) {
         } else {
             store_rows(u, c);
         }
-        update(1, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        // the new state's parts, two tiles at a time: first part a step behind the products,
+        // its remainder and second part another step, so that none waits for a result
 #pragma unroll
-        for (int p = 1; p < KS; ++p) {
-            update(1, p);
-            parts(p - 1);
-            interleave<2 * X2, 6, 0>();
+        for (int p = 0; p < KS + 2; ++p) {
+            if (p < KS) update(1, p);
+            if (p >= 1 && p <= KS) first_part(p - 1);
+            if (p >= 2) last_parts(p - 2);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        parts(KS - 1);
         if (BUF == 1) lds_barrier();  // K may be replaced
         lds_barrier();                // chunk c's operands and the next K are in LDS
+    };
+    int c = 0;
+    for (; c + 1 < nch; c += 2) {
+        chunk(c, Tab[0], Tab[BF ? 1 : 0]);
+        chunk(c + 1, Tab[BF ? 1 : 0], Tab[0]);
     }
+    if (c < nch) chunk(c, Tab[0], Tab[BF ? 1 : 0]);
     if (a.s_out)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
