@@ -19,26 +19,15 @@ constexpr int kMP = 68;  // LDS pitch (floats) of a 64 x 64 matrix: rows 16-byte
 template <bool BF, int DK>
 struct PrepLds {
     using T = typename Io<BF>::T;
-    static constexpr int KP = DK + 16 / (int)sizeof(T);  // row pitch of the staged K (Q) tile
+    static constexpr int KP = DK + 16 / (int)sizeof(T);  // row pitch of the staged K tile
     float a[kC][kMP];
-    float p[kC][kMP];
-    alignas(16) T rows[kC][KP];
+    union {
+        alignas(16) T rows[kC][KP];  // K, until its products are made
+        float p[kC][kMP];            // then P, then T
+    };
     double G[kC];
     float beta[kC];
 };
-
-template <bool BF, int DK>
-__device__ __forceinline__ void stage_rows(PrepLds<BF, DK>& l, const typename Io<BF>::T* src, int64_t ld, int rows,
-                                           int dk, int tid) {
-    using T = typename Io<BF>::T;
-    constexpr int V = 16 / (int)sizeof(T);  // elements per 16 bytes
-    for (int e = tid; e < kC * (DK / V); e += kThreads) {
-        const int t = e / (DK / V), k = (e % (DK / V)) * V;
-        f32x4 v = {};
-        if (t < rows && k < dk) v = *reinterpret_cast<const f32x4*>(src + t * ld + k);
-        *reinterpret_cast<f32x4*>(&l.rows[t][k]) = v;
-    }
-}
 
 // a 64 x 64 matrix in LDS (or its transpose; or with column c scaled by scale[c]) as
 // block-triangular A fragments of N parts
@@ -76,27 +65,48 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     Range r;
     int64_t c, n;
     if (!find_chunk(a.seqs, slot, r, c, n)) return;
-    const int64_t tok = r.first + c * kC;
-    const int rows = (int)(r.len - c * kC < kC ? r.len - c * kC : kC);
+    const int64_t tok = uniform64(r.first + c * kC);
+    const int rows = __builtin_amdgcn_readfirstlane((int)(r.len - c * kC < kC ? r.len - c * kC : kC));
     const int64_t sh_idx = slot * a.sh.hv + h;
     const T* kp = (const T*)a.k + tok * a.sh.ldk + (int64_t)hk * a.sh.dk;
     const T* qp = (const T*)a.q + tok * a.sh.ldq + (int64_t)hk * a.sh.dk;
 
-    stage_rows<BF, DK>(l, kp, a.sh.ldk, rows, a.sh.dk, tid);
+    // the loads of K and Q are on their way while every wave sums the decays for itself
+    constexpr int V = 16 / (int)sizeof(T), NL = kC * (DK / V) / kThreads;
+    const uint32_t E = sizeof(T), ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E;
+    const RowBuf kb = row_buf(kp, rows, ldk, a.sh.dk * E), qb = row_buf(qp, rows, ldq, a.sh.dk * E);
+    f32x4 kr[NL];
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+        const int t = (e * kThreads + tid) / (DK / V), k = (e * kThreads + tid) % (DK / V) * V;
+        kr[e] = buf_f4(kb, k < a.sh.dk ? t * ldk + k * E : kNoElem, 0);
+    }
+    Raw<BF> qr[DK / 32];
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+        const int k0 = 32 * s + 8 * g;
+        buf_raw(qb, k0 < a.sh.dk ? (16 * wave + col) * ldq + k0 * E : kNoElem, qr[s]);
+    }
+    float gv = 0.f, bv = 0.f;
+    if (lane < rows) {
+        gv = (float)((const T*)a.g)[(tok + lane) * a.sh.hv + h];
+        bv = (float)((const T*)a.beta)[(tok + lane) * a.sh.hv + h];
+    }
+    const double G = chunk_decay(gv, lane);
     if (wave == 0) {
-        float gv = 0.f, bv = 0.f;
-        if (lane < rows) {
-            gv = (float)((const T*)a.g)[(tok + lane) * a.sh.hv + h];
-            bv = (float)((const T*)a.beta)[(tok + lane) * a.sh.hv + h];
-        }
-        const double G = chunk_decay(gv, lane);
-        const double last = __shfl(G, 63);
         l.G[lane] = G;
         l.beta[lane] = bv;
+    } else if (wave == 1) {
+        const double last = __shfl(G, 63);
         float* sc = reinterpret_cast<float*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::sc);
         sc[lane] = expf((float)G);
         sc[kC + lane] = expf((float)(last - G));
         sc[2 * kC + lane] = bv;
+    }
+#pragma unroll
+    for (int e = 0; e < NL; ++e) {
+        const int t = (e * kThreads + tid) / (DK / V), k = (e * kThreads + tid) % (DK / V) * V;
+        *reinterpret_cast<f32x4*>(&l.rows[t][k]) = kr[e];
     }
     __syncthreads();
 
@@ -110,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
             float x[8];
             load8(&l.rows[row][k0], true, x);
             const Frag<IO::NI> ka = split8<IO::NI>(x);
-            const Frag<IO::NI> qa = to_frag(load_raw(qp + row * a.sh.ldq + k0, row < rows && k0 < a.sh.dk));
+            const Frag<IO::NI> qa = to_frag(qr[s]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= wave) {
@@ -120,6 +130,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
                     qk[j] = mma(qa, kb, qk[j]);
                 }
         }
+        __syncthreads();  // K has been read: P takes its place
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll

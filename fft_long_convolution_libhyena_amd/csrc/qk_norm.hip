@@ -234,20 +234,32 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
         }
 }
 
-// sums of the workgroups' partial gradients: 32 columns x 8 rows of threads
-__global__ __launch_bounds__(256) void k_qk_norm_dw(const float* part, int64_t n, int dim, float* dwq, float* dwk) {
-    __shared__ double red[8][33];
+// sums of the workgroups' partial gradients: 32 columns x 32 rows of threads, each row's
+// partials four at a time (with 8 rows one at a time, 1024 partials took 32 us)
+__global__ __launch_bounds__(1024) void k_qk_norm_dw(const float* part, int64_t n, int dim, float* dwq, float* dwk) {
+    __shared__ double red[32][33];
     const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + c;
     double s = 0;
-    if (e < 2 * dim)
-        for (int64_t i = r; i < n; i += 8) s += (double)part[i * 2 * dim + e];
+    if (e < 2 * dim) {
+        int64_t i = r;
+        for (; i + 96 < n; i += 128) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = part[(i + 32 * j) * 2 * dim + e];
+            s += ((double)x[0] + x[1]) + ((double)x[2] + x[3]);
+        }
+        for (; i < n; i += 32) s += (double)part[i * 2 * dim + e];
+    }
     red[r][c] = s;
     __syncthreads();
+    for (int d = 16; d > 0; d >>= 1) {
+        if (r < d) red[r][c] += red[r + d][c];
+        __syncthreads();
+    }
     if (r == 0 && e < 2 * dim) {
-        for (int i = 1; i < 8; ++i) s += red[i][c];
         float* o = e < dim ? dwq : dwk;
-        if (o) o[e % dim] = (float)s;
+        if (o) o[e % dim] = (float)red[0][c];
     }
 }
 
@@ -403,7 +415,7 @@ hyena_status_t hyena_qk_norm_backward(const hyena_qk_norm_params_t* params, int6
     }
     if (e == hipSuccess && sums) {  // without tokens: zeros
         const int64_t n = tokens > 0 ? (int64_t)g.x * g.y : 0;
-        hipLaunchKernelGGL(hy::k_qk_norm_dw, dim3((unsigned)((2 * params->dim + 31) / 32)), dim3(256), 0, stream,
+        hipLaunchKernelGGL(hy::k_qk_norm_dw, dim3((unsigned)((2 * params->dim + 31) / 32)), dim3(1024), 0, stream,
                            (const float*)workspace, n, (int)params->dim, dw_q, dw_k);
         e = hipGetLastError();
     }
