@@ -494,10 +494,11 @@ __device__ __forceinline__ bool find_chunk(const Seqs& s, int64_t slot, Range& r
     return c >= 0 && c * kC < r.len;
 }
 
-// The running sum of the log decays over a chunk's 64 lanes, in 64 bits: differences of
-// it stay exact to fp32 however strong single decays are.
+// The running sum of the log decays over a chunk's 64 lanes, in 64 bits and to base 2:
+// differences of it stay exact to fp32 however strong single decays are, and a decay is one
+// hardware exp2 of such a difference (accurate to its last bit or two, as an expf would be).
 __device__ __forceinline__ double chunk_decay(float g, int lane) {
-    double G = (double)g < kMinLog ? kMinLog : (double)g;  // a NaN stays one
+    double G = ((double)g < kMinLog ? kMinLog : (double)g) * 1.4426950408889634074;  // a NaN stays one
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const double up = __shfl_up(G, d);
@@ -505,6 +506,8 @@ __device__ __forceinline__ double chunk_decay(float g, int lane) {
     }
     return G;
 }
+
+__device__ __forceinline__ float decay(double d) { return __builtin_amdgcn_exp2f((float)d); }
 
 struct Shape {
     int hk, hv, group, dk, dv;

@@ -179,8 +179,8 @@ void k_delta_grad(GradArgs a) {
             const double G = chunk_decay(gv, lane);
             const double last = __shfl(G, 63);
             l.G[lane] = G;
-            l.gam[lane] = expf((float)G);
-            l.kap[lane] = expf((float)(last - G));
+            l.gam[lane] = decay(G);
+            l.kap[lane] = decay(last - G);
             l.bet[lane] = bv;
         }
         f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
@@ -260,7 +260,7 @@ void k_delta_grad(GradArgs a) {
                 const int tj = 16 * j + col;
                 float wv = 0.f, mv = 0.f;
                 if (j <= w && tj <= ti + i) {
-                    const float d = expf((float)(l.G[ti + i] - l.G[tj]));
+                    const float d = decay(l.G[ti + i] - l.G[tj]);
                     wv = a.sh.scale * d * dp[j][i];
                     float x = wv * qk[j][i];
                     if (tj < ti + i) {

@@ -99,8 +99,8 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     } else if (wave == 1) {
         const double last = __shfl(G, 63);
         float* sc = reinterpret_cast<float*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::sc);
-        sc[lane] = expf((float)G);
-        sc[kC + lane] = expf((float)(last - G));
+        sc[lane] = decay(G);
+        sc[kC + lane] = decay(last - G);
         sc[2 * kC + lane] = bv;
     }
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
                 const int ti = 16 * wave + 4 * g + i, tj = 16 * j + col;
                 float av = 0.f, pv = 0.f;
                 if (tj <= ti) {
-                    const float d = expf((float)(l.G[ti] - l.G[tj]));
+                    const float d = decay(l.G[ti] - l.G[tj]);
                     pv = d * qk[j][i];
                     if (tj < ti) av = l.beta[ti] * d * kk[j][i];
                 }
@@ -161,7 +161,12 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
         for (int i = 0; i < 16; ++i) {
             float v = i == col ? 1.f : 0.f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) v = fmaf(-l.a[b + i][b + j], x[j], v);
+            for (int j = 0; j < i; j += 4) {  // A is zero on and above the diagonal
+                const f32x4 row = *reinterpret_cast<const f32x4*>(&l.a[b + i][b + j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < i) v = fmaf(-row[e], x[j + e], v);
+            }
             x[i] = v;
         }
         if (g == 0)
