@@ -532,6 +532,22 @@ struct Prep {
     unsigned char* back;  // [slot][value head] T^T and P^T, upper fragments (backward)
 };
 
+// What the backward's scans leave for the chunk-parallel part: per (slot, value head) and
+// block of 16 columns, the state (its gradient) as KS, a 64-token array as two operand
+// fragments in the element type, 16 or 32 bytes a lane: lane l has column l % 16 of the
+// block, elements 8 (l / 16) .. + 7 of 32. One contiguous store of 1 KiB in place of
+// sixteen of 32-byte pieces.
+template <bool BF>
+__device__ __forceinline__ void store_frag(unsigned char* p, int lane, const f32x4& a, const f32x4& b) {
+    if constexpr (BF) {
+        const u32x4 w = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
+        *reinterpret_cast<u32x4*>(p + lane * 16) = w;
+    } else {
+        *reinterpret_cast<f32x4*>(p + lane * 32) = a;
+        *reinterpret_cast<f32x4*>(p + lane * 32 + 16) = b;
+    }
+}
+
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxSeqs = int64_t(1) << 24;
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // elements: 64 rows stay below 2^31 bytes

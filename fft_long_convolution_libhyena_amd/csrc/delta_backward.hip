@@ -31,8 +31,8 @@ BackLayout back_layout(const DeltaCall& c, unsigned char* base) {
         return p;
     };
     const size_t e = c.bf ? 2 : 4;
-    const size_t states = (size_t)c.slots * c.shape.hv * c.shape.dk * c.shape.dv * e;
-    const size_t rows = (size_t)c.seqs.tokens * c.shape.hv * c.shape.dv * e;
+    const size_t cols = (size_t)c.slots * c.shape.hv * ((c.shape.dv + 15) / 16 * 16) * e;  // of every slot and head
+    const size_t states = cols * c.dkp, rows = cols * kC;
     b.s0 = take(states);
     b.ds1 = take(states);
     b.u = take(rows);
@@ -47,6 +47,7 @@ hipError_t launch_rev_t(const DeltaCall& c, RevArgs a, hipStream_t st) {
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
+    a.nb16 = (c.shape.dv + 15) / 16;
     const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
     const hipError_t e =
         hipFuncSetAttribute((const void*)k_delta_rev<BF, DK>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -116,7 +117,7 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
         f.u = b.u;
         if (hy::delta_scan(c, true, f, stream) != hipSuccess) return HYENA_ERR_DEVICE;
     }
-    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, 0};
+    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, 0, 0};
     hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->v, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, dq, dk, dg, dbeta};
     hipError_t e;
     if (c.bf)

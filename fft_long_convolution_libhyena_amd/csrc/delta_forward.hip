@@ -86,6 +86,7 @@ hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
     using Cfg = ScanCfg<BF, DK, MODE>;
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
     a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
+    a.nb16 = (c.shape.dv + 15) / 16;
     const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
     const hipError_t e = hipFuncSetAttribute((const void*)k_delta_scan<BF, DK, MODE>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);

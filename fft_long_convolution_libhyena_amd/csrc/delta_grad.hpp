@@ -21,7 +21,7 @@ struct GradArgs {
     Seqs seqs;
     Shape sh;
     const void *q, *k, *v, *g, *beta, *dout;
-    const void *s0, *ds1, *u, *r;
+    const void *s0, *ds1, *u, *r;  // the scans' fragments
     void *dq, *dk;       // [tokens][hk][dk]
     void *dg, *dbeta;    // [tokens][hv]
 };
@@ -73,12 +73,32 @@ struct GradTile<false, R, W> {
     }
 };
 
+// W rows (state rows or tokens) of 32 columns out of the scans' fragments, read as an
+// operand whose contraction runs over the columns: bf16 stays column by column and is read
+// across; fp32 is turned when it is stored.
+template <bool BF, int W>
+struct StepTile;
+template <int W>
+struct StepTile<true, W> : GradTile<true, 32, W> {
+    __device__ __forceinline__ void put8(int c, int e, const u32x4 (&x)[1]) { *this->at16(c, e) = x[0]; }
+    __device__ __forceinline__ Frag<1> op(int lane, int m) const { return this->cols(lane, m, 0); }
+};
+template <int W>
+struct StepTile<false, W> : GradTile<false, W, 32> {
+    __device__ __forceinline__ void put8(int c, int e, const u32x4 (&x)[2]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) this->put(e + i, c, __uint_as_float(x[i >> 2][i & 3]));
+    }
+    __device__ __forceinline__ Frag<3> op(int lane, int m) const { return this->rows(lane, m, 0); }
+};
+
 template <bool BF, int DK>
 struct GradLds {
     GradTile<BF, kC, DK> k, q;
     struct Steps {
-        GradTile<BF, kC, 32> o, u, r;
-        GradTile<BF, DK, 32> s, d;
+        GradTile<BF, kC, 32> o, v;
+        StepTile<BF, kC> u, r;
+        StepTile<BF, DK> s, d;
     };
     struct Mats {
         GradTile<BF, kC, kC> w, n;
@@ -101,7 +121,9 @@ void k_delta_grad(GradArgs a) {
     constexpr uint32_t E = sizeof(T);
     constexpr int V = 16 / (int)E, LPR = 32 / V;  // elements of 16 bytes; lanes of a 32-element row
     constexpr int RPP = kThreads / LPR;           // rows one pass of the workgroup stages
-    constexpr int NR = kC / RPP, NSr = DK / RPP;  // passes for 64 rows, for DK rows
+    constexpr int NR = kC / RPP;                  // passes for 64 rows
+    constexpr int NV = (int)E / 2;                // 16-byte pieces of a lane's part of a fragment
+    constexpr int NF = DK / 64;                   // state fragments a wave stages (of 2 KS)
     extern __shared__ __align__(16) unsigned char lds_raw[];
     GradLds<BF, DK>& l = *reinterpret_cast<GradLds<BF, DK>*>(lds_raw);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -131,30 +153,38 @@ void k_delta_grad(GradArgs a) {
     const int srow = tid / LPR, scol = tid % LPR * V;
     for (int hh = 0; hh < (SHARED ? a.sh.group : 1); ++hh) {
         const int h = hk * a.sh.group + hh;
-        const int64_t sidx = (slot * hv + h) * (int64_t)dk * dv;
         const int64_t obase = (tok * hv + h) * (int64_t)dv;
-        const RowBuf ob = row_buf((const T*)a.dout + obase, rows, ldo, dv * E), ub = row_buf((const T*)a.u + obase, rows, ldo, dv * E);
-        const RowBuf rb = row_buf((const T*)a.r + obase, rows, ldo, dv * E);
+        const int nb16 = (dv + 15) / 16;
+        const int64_t fidx = (slot * hv + h) * nb16;  // first block's fragments
+        const RowBuf ob = row_buf((const T*)a.dout + obase, rows, ldo, dv * E);
         const RowBuf vb = row_buf((const T*)a.v + tok * a.sh.ldv + (int64_t)h * dv, rows, ldv, dv * E);
-        const RowBuf sb = plain_buf((const T*)a.s0 + sidx, dk * dv * E), db = plain_buf((const T*)a.ds1 + sidx, dk * dv * E);
-        u32x4 po[NR], pu[NR], pr[NR], pv[NR], ps[NSr], pd[NSr];
+        const RowBuf ub = plain_buf((const T*)a.u + fidx * 1024, nb16 * 1024 * E), rb = plain_buf((const T*)a.r + fidx * 1024, nb16 * 1024 * E);
+        const RowBuf sb = plain_buf((const T*)a.s0 + fidx * KS * 512, nb16 * KS * 512 * E);
+        const RowBuf db = plain_buf((const T*)a.ds1 + fidx * KS * 512, nb16 * KS * 512 * E);
+        // a step's 2 blocks: wave w stages fragment w of the four of u and r and fragments
+        // NF w .. of the 2 KS of the states; blocks past the last read zeros
+        u32x4 po[NR], pv[NR], pu[NV], pr[NV], ps[NF][NV], pd[NF][NV];
         auto fetch = [&](int c0) {
             const bool ok = c0 + scol < dv;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                const uint32_t off = ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem;
-                po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, off, 0));
-                pu[i] = __builtin_bit_cast(u32x4, buf_f4(ub, off, 0));
-                pr[i] = __builtin_bit_cast(u32x4, buf_f4(rb, off, 0));
+                po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem, 0));
                 pv[i] = __builtin_bit_cast(u32x4, buf_f4(vb, ok ? (i * RPP + srow) * ldv + (c0 + scol) * E : kNoElem, 0));
             }
+            const uint32_t b0 = (c0 / 16) * 1024 * E + w * 512 * E + lane * 8 * E;
+            const uint32_t s0 = (c0 / 16) * (KS * 512) * E + NF * w * 512 * E + lane * 8 * E;
 #pragma unroll
-            for (int i = 0; i < NSr; ++i) {
-                const int k = i * RPP + srow;
-                const uint32_t off = ok && k < dk ? (uint32_t)(k * dv + c0 + scol) * E : kNoElem;
-                ps[i] = __builtin_bit_cast(u32x4, buf_f4(sb, off, 0));
-                pd[i] = __builtin_bit_cast(u32x4, buf_f4(db, off, 0));
+            for (int j = 0; j < NV; ++j) {
+                pu[j] = __builtin_bit_cast(u32x4, buf_f4(ub, b0 + 16 * j, 0));
+                pr[j] = __builtin_bit_cast(u32x4, buf_f4(rb, b0 + 16 * j, 0));
             }
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    ps[f][j] = __builtin_bit_cast(u32x4, buf_f4(sb, s0 + f * 512 * E + 16 * j, 0));
+                    pd[f][j] = __builtin_bit_cast(u32x4, buf_f4(db, s0 + f * 512 * E + 16 * j, 0));
+                }
         };
         auto dot16 = [&](const u32x4& x, const u32x4& y) {
             float s = 0.f;
@@ -184,38 +214,42 @@ void k_delta_grad(GradArgs a) {
             l.bet[lane] = bv;
         }
         f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
-        float rv[NR] = {}, sd = 0.f;
+        f32x4 rvt = {};
+        float sd = 0.f;
         for (int c0 = 0; c0 < dv; c0 += 32) {
             __syncthreads();  // the step before (or the head before) has read its tiles
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 *l.step.o.at16(i * RPP + srow, scol) = po[i];
-                *l.step.u.at16(i * RPP + srow, scol) = pu[i];
-                *l.step.r.at16(i * RPP + srow, scol) = pr[i];
-                rv[i] += dot16(pr[i], pv[i]);
+                *l.step.v.at16(i * RPP + srow, scol) = pv[i];
             }
+            l.step.u.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pu);
+            l.step.r.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pr);
 #pragma unroll
-            for (int i = 0; i < NSr; ++i) {
-                *l.step.s.at16(i * RPP + srow, scol) = ps[i];
-                *l.step.d.at16(i * RPP + srow, scol) = pd[i];
-                sd += dot16(ps[i], pd[i]);
+            for (int f = 0; f < NF; ++f) {
+                const int x = NF * w + f;  // block x / KS, step x % KS
+                l.step.s.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, ps[f]);
+                l.step.d.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, pd[f]);
+#pragma unroll
+                for (int j = 0; j < NV; ++j) sd += dot16(ps[f][j], pd[f][j]);
             }
             if (c0 + 32 < dv) fetch(c0 + 32);
             lds_barrier();
-            const auto ao = l.step.o.rows(lane, w, 0), ar = l.step.r.rows(lane, w, 0), au = l.step.u.rows(lane, w, 0);
+            const auto ao = l.step.o.rows(lane, w, 0), ar = l.step.r.op(lane, w), au = l.step.u.op(lane, w);
+            rvt = mma(ar, l.step.v.rows(lane, w, 0), rvt);  // its diagonal is r . v
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= w) {
-                    const auto b = l.step.u.rows(lane, j, 0);
+                    const auto b = l.step.u.op(lane, j);
                     dp[j] = mma(ao, b, dp[j]);
                     z[j] = mma(ar, b, z[j]);
                 }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const auto b = l.step.s.rows(lane, m, 0);
+                const auto b = l.step.s.op(lane, m);
                 qs[m] = mma(ao, b, qs[m]);
                 rs[m] = mma(ar, b, rs[m]);
-                us[m] = mma(au, l.step.d.rows(lane, m, 0), us[m]);
+                us[m] = mma(au, l.step.d.op(lane, m), us[m]);
             }
         }
         // k_i . k_j and q_i . k_j
@@ -292,11 +326,10 @@ void k_delta_grad(GradArgs a) {
             *reinterpret_cast<f32x4*>(l.kus + ti) = kap * kus;
             *reinterpret_cast<f32x4*>(l.dbz + ti) = dbz;
         }
+        if (col >> 2 == g) {
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-#pragma unroll
-            for (int d = 1; d < LPR; d <<= 1) rv[i] += __shfl_xor(rv[i], d);
-            if (tid % LPR == 0) l.rv[i * RPP + srow] = rv[i];
+            for (int i = 0; i < 4; ++i)
+                if ((col & 3) == i) l.rv[16 * w + col] = rvt[i];
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sd += __shfl_xor(sd, d);

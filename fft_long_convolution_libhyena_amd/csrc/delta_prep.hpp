@@ -19,7 +19,7 @@ constexpr int kMP = 68;  // LDS pitch (floats) of a 64 x 64 matrix: rows 16-byte
 template <bool BF, int DK>
 struct PrepLds {
     using T = typename Io<BF>::T;
-    static constexpr int KP = DK + 16 / (int)sizeof(T);  // row pitch of the staged K tile
+    static constexpr int KP = DK + 32 / (int)sizeof(T);  // row pitch of the staged K tile: 32 bytes over spread its reads
     float a[kC][kMP];
     union {
         alignas(16) T rows[kC][KP];  // K, until its products are made

@@ -23,10 +23,10 @@ struct RevArgs {
     const void* dout;      // [tokens][hv][dv]
     const float* ds_out;   // [N][hv][dk][dv] gradient of the final states, or null
     float* ds_in;          // likewise of the initial states (output), or null
-    void* ds1;             // [slot][hv][dk][dv] dS behind every chunk
-    void* r;               // [tokens][hv][dv]
+    void* ds1;             // dS behind every chunk, as fragments
+    void* r;               // as fragments
     void* dv;              // [tokens][hv][dv] (output)
-    int nblk;
+    int nblk, nb16;
 };
 
 template <int DK>
@@ -315,16 +315,11 @@ void k_delta_rev(RevArgs a) {
         const int nx = i + 1 < nch ? i + 1 : i;
         const Tile<NI, DK>& K = l.k[i & (BUF - 1)];
         const RevInputs<DK>& in = l.x[wave][i & 1];
-        {
-            const RowBuf b = plain_buf((T*)a.ds1 + ((slot0 + nch - 1 - i) * hv + h) * (int64_t)dk * dv, dk * dv * E);
+        const int64_t fr = ((slot0 + nch - 1 - i) * hv + h) * a.nb16 + blk;  // this block's fragments
+        if (blk < a.nb16)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x[1] = {S[t][j]};
-                    buf_store<BF, 1>(b, cok && drow(t, j) < dk ? (uint32_t)(drow(t, j) * dv + c0) * E : kNoElem, x);
-                }
-        }
+            for (int s = 0; s < KS; ++s)
+                store_frag<BF>((unsigned char*)a.ds1 + (fr * KS + s) * (512 * E), lane, S[2 * s], S[2 * s + 1]);
         // dU = P^T dO + diag(exp(G_last - G)) K dS
         f32x4 x[4] = {};
         Frag<NI> ka[2][4];
@@ -385,7 +380,10 @@ void k_delta_rev(RevArgs a) {
         for (int p = 0; p < KS; ++p) update(1, p);
         rpart(0);
         interleave<MT * X2, 5, 0>();
-        store_rows(a.r, r, i);
+        if (blk < a.nb16)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                store_frag<BF>((unsigned char*)a.r + (fr * 2 + s) * (512 * E), lane, r[2 * s], r[2 * s + 1]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) r[t] *= bet[t];
         store_rows(a.dv, r, i);

@@ -35,9 +35,10 @@ struct ScanArgs {
     const float* s_in;  // [N][hv][dk][dv] or null (zeros)
     float* s_out;       // likewise, or null
     void* o;            // [tokens][hv][dv] (outputs)
-    void* s0;           // [slot][hv][dk][dv] state before every chunk (for the backward)
-    void* u;            // [tokens][hv][dv] written values (for the backward)
-    int nblk;           // column blocks per head
+    void* s0;           // state before every chunk, as fragments (for the backward)
+    void* u;            // written values, as fragments (for the backward)
+    int nblk;           // workgroups per head
+    int nb16;           // blocks of 16 columns per head
 };
 
 enum { kScanOut = 0, kScanKeep = 1 };
@@ -209,7 +210,7 @@ void k_delta_scan(ScanArgs a) {
     const int c0 = blk * 16 + col;  // this lane's column
     const bool cok = c0 < dv;
     const uint32_t ldo = (uint32_t)(hv * dv) * E;
-    unsigned char* op = (unsigned char*)((T*)(OUT ? a.o : a.u) + (first * hv + h) * (int64_t)dv);
+    unsigned char* op = OUT ? (unsigned char*)((T*)a.o + (first * hv + h) * (int64_t)dv) : nullptr;
     // row i of this lane's results in tile t
     auto drow = [&](int t, int i) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1) + i; };
     const uint32_t ooff = cok ? drow(0, 0) * ldo + c0 * E : kNoElem;
@@ -367,7 +368,10 @@ void k_delta_scan(ScanArgs a) {
         for (int f = 0; f < kTri; ++f) load_t(Tab[0], rb, f);
         lds_barrier();  // K of the first chunk is in LDS
     }
-    unsigned char* s0p = OUT ? nullptr : (unsigned char*)a.s0 + (slot0 * hv + h) * (int64_t)dk * dv * E;
+    // this block's fragments of the backward, one chunk's behind another's
+    const bool kept = !OUT && blk < a.nb16;
+    unsigned char* s0p = OUT ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
+    unsigned char* up = OUT ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
     constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;  // matrix instructions per product
     // one chunk; T alternates between two sets of registers
     auto chunk = [&](int c, Frag<NS>(&Tf)[kTri], Frag<NS>(&Tn)[kTri]) {
@@ -375,15 +379,10 @@ void k_delta_scan(ScanArgs a) {
         const RowBuf vb = vbuf(c + 1 < nch ? c + 1 : c), rb = plain_buf(rec, Rec<BF>::bytes);
         const Tile<NI, DK>& K = l.k[c & (BUF - 1)];
         if constexpr (!OUT) {
-            const RowBuf b = plain_buf(s0p, dk * dv * E);
+            if (kept)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x[1] = {S[t][i]};
-                    buf_store<BF, 1>(b, cok && drow(t, i) < dk ? (uint32_t)(drow(t, i) * dv + c0) * E : kNoElem, x);
-                }
-            s0p += (int64_t)hv * dk * dv * E;
+                for (int s = 0; s < KS; ++s) store_frag<BF>(s0p + s * 512 * E, lane, S[2 * s], S[2 * s + 1]);
+            s0p += (int64_t)hv * a.nb16 * (KS * 512 * E);
         }
         __builtin_amdgcn_sched_barrier(0);
         // e = V - exp(G) K S; LDS reads two steps ahead of their products
@@ -498,7 +497,10 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) l.x[wave][c & 1].u[t][lane] = u[t];
         } else {
-            store_rows(u, c);
+            if (kept)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) store_frag<BF>(up + s * 512 * E, lane, u[2 * s], u[2 * s + 1]);
+            up += (int64_t)hv * a.nb16 * (1024 * E);
         }
         // the new state's parts, two tiles at a time: first part a step behind the products,
         // its remainder and second part another step, so that none waits for a result
