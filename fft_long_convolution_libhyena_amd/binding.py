@@ -227,7 +227,37 @@ def _check(call: str, st: int) -> None:
 
 
 def _stream_handle(torch, device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle of the current stream, without the Stream object around it (2 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _launch(torch, name, fn, device, *args) -> None:
+    """Run a plan-less call on `device`, on its current stream. The calls of a serving loop
+    take a few microseconds on the GPU, so the host's part is kept as short."""
+    if torch.cuda.current_device() == device.index:
+        _check(name, fn(*args, _stream_handle(torch, device)))
+    else:
+        with torch.cuda.device(device):
+            _check(name, fn(*args, _stream_handle(torch, device)))
+
+
+def _gpu_of(t, name):
+    """The device of a call, that of its first tensor."""
+    device = getattr(t, "device", None)
+    if device is None or device.type != "cuda":
+        raise ValueError(f"{name} must be a tensor on a GPU")
+    return device
+
+
+def _dense(t, name, shape, dtype, device) -> int:
+    """The address of a contiguous tensor of this shape and dtype on the call's device."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+        got = f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+    except AttributeError:
+        got = f"got {type(t).__name__}"
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, {got}")
 
 
 def kernel_synthesis(params, z, out=None):
@@ -717,24 +747,26 @@ class Plan3D(_GridPlan):
         super().__init__((A, H, W), D, dtype, circular)
 
 
-def _token_rows(torch, t, name, rows, heads, dim, dtype, device):
-    """The token stride of t [*rows, heads, dim] (rows: (tokens,) or (B, T)): dense heads,
-    one stride over all tokens, rows that start on 16 bytes."""
-    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be a tensor on the GPU that holds q")
-    if tuple(t.shape) != (*rows, heads, dim) or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(*rows, heads, dim)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    width = heads * dim
-    if t.numel() == 0:
-        return width
-    ld = t.stride(-3) if rows[-1] > 1 else (t.stride(0) if len(rows) == 2 and rows[0] > 1 else width)
-    if ((dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim) or ld < width
-            or (len(rows) == 2 and rows[0] > 1 and t.stride(0) != rows[1] * ld)):
-        raise ValueError(f"{name} must have dense heads and one stride between tokens")
-    if ld * t.element_size() % 16 or t.data_ptr() % 16:
+def _token_rows(t, name, rows, heads, dim, dtype, device):
+    """Address and token stride of t [*rows, heads, dim] (rows: (tokens,) or (B, T)): dense
+    heads, one stride over all tokens, rows that start on 16 bytes."""
+    shape, width = (*rows, heads, dim), heads * dim
+    try:
+        if t.shape != shape or t.dtype is not dtype or t.device != device:
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor, got {type(t).__name__}") from None
+    ld, at = width, t.data_ptr()
+    if not t.is_contiguous() and t.numel():
+        st = t.stride()
+        ld = st[-3] if rows[-1] > 1 else (st[0] if len(rows) == 2 and rows[0] > 1 else width)
+        if ((dim > 1 and st[-1] != 1) or (heads > 1 and st[-2] != dim) or ld < width
+                or (len(rows) == 2 and rows[0] > 1 and st[0] != rows[1] * ld)):
+            raise ValueError(f"{name} must have dense heads and one stride between tokens")
+    if (ld * dtype.itemsize | at) & 15 and t.numel():
         raise ValueError(f"{name}'s rows must start on 16 bytes")
-    return ld
+    return at, ld
 
 
 class QKNorm:
@@ -753,64 +785,52 @@ class QKNorm:
             raise ValueError(f"dtype must be one of {list(_DTYPES)}, kind one of {list(_NORMS)}")
         self.heads_q, self.heads_k, self.dim, self.dtype = int(heads_q), int(heads_k), int(dim), dtype
         self.kind, self.eps, self.pairs = kind, float(eps), bool(pairs)
+        self.io_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self.w_q, self.w_k, self.freq = w_q, w_k, freq
         for name, t, n in (("w_q", w_q, self.dim), ("w_k", w_k, self.dim), ("freq", freq, None)):
             if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()
                                   or (n is not None and t.numel() != n)):
                 raise ValueError(f"{name} must be a contiguous fp32 vector" + (f" of {n}" if n else ""))
 
-    @property
-    def io_dtype(self):
-        return self._torch.bfloat16 if self.dtype == "bf16" else self._torch.float32
-
     def _params(self, device):
+        ptr = []
         for name in ("w_q", "w_k", "freq"):
             t = getattr(self, name)
             if t is not None and t.device != device:
                 raise ValueError(f"{name} must be on the GPU that holds q")
-        ptr = lambda t: t.data_ptr() if t is not None and t.numel() else None  # noqa: E731
+            ptr.append(t.data_ptr() if t is not None and t.numel() else None)
         return QKNormParamsStruct(self.heads_q, self.heads_k, self.dim, self.freq.numel() if self.freq is not None else 0,
-                                  _NORMS[self.kind], 1 if self.pairs else 0, _DTYPES[self.dtype], self.eps,
-                                  ptr(self.w_q), ptr(self.w_k), ptr(self.freq))
+                                  _NORMS[self.kind], 1 if self.pairs else 0, _DTYPES[self.dtype], self.eps, *ptr)
 
     def _args(self, q, k, positions):
-        torch, dev = self._torch, q.device
-        if q.dim() not in (3, 4):
+        dev = _gpu_of(q, "q")
+        rows = tuple(q.shape[:-2])
+        if len(rows) not in (1, 2):
             raise ValueError("q must be [tokens, heads_q, dim] or [B, T, heads_q, dim]")
-        rows = tuple(int(n) for n in q.shape[:-2])
-        tokens = 1
-        for n in rows:
-            tokens *= n
-        ldq = _token_rows(torch, q, "q", rows, self.heads_q, self.dim, self.io_dtype, dev)
-        ldk = _token_rows(torch, k, "k", rows, self.heads_k, self.dim, self.io_dtype, dev)
-        if positions is None:
-            if self.freq is not None and self.freq.numel():
-                raise ValueError("positions are needed for the rotation")
-        elif (positions.device != dev or positions.dtype != torch.int64 or tuple(positions.shape) != rows
-              or not positions.is_contiguous()):
-            raise ValueError(f"positions must be a contiguous int64 tensor of shape {rows} on the GPU that holds q")
-        return rows, tokens, ldq, ldk, positions.data_ptr() if positions is not None else None
+        tokens = rows[0] if len(rows) == 1 else rows[0] * rows[1]
+        qp, ldq = _token_rows(q, "q", rows, self.heads_q, self.dim, self.io_dtype, dev)
+        kp, ldk = _token_rows(k, "k", rows, self.heads_k, self.dim, self.io_dtype, dev)
+        pos = None
+        if positions is not None:
+            pos = _dense(positions, "positions", rows, self._torch.int64, dev)
+        elif self.freq is not None and self.freq.numel():
+            raise ValueError("positions are needed for the rotation")
+        return dev, rows, (ctypes.byref(self._params(dev)), tokens, qp, ldq, kp, ldk, pos)
 
-    def _dense(self, t, name, rows, heads, device):
+    def _out(self, t, name, rows, heads, device):
+        shape = (*rows, heads, self.dim)
         if t is None:
-            return self._torch.empty((*rows, heads, self.dim), dtype=self.io_dtype, device=device)
-        if (not isinstance(t, self._torch.Tensor) or t.device != device or t.dtype != self.io_dtype
-                or tuple(t.shape) != (*rows, heads, self.dim) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {self.io_dtype} tensor of shape {(*rows, heads, self.dim)}")
-        return t
+            t = self._torch.empty(shape, dtype=self.io_dtype, device=device)
+            return t, t.data_ptr()
+        return t, _dense(t, name, shape, self.io_dtype, device)
 
     def forward(self, q, k, positions=None, q_out=None, k_out=None):
         """hyena_qk_norm_forward: q [tokens or B, T, heads_q, dim], k [.., heads_k, dim] (one stride
         between tokens), positions int64 of the tokens' shape -> (q_out, k_out), dense."""
-        torch, dev = self._torch, q.device
-        rows, tokens, ldq, ldk, pos = self._args(q, k, positions)
-        q_out = self._dense(q_out, "q_out", rows, self.heads_q, dev)
-        k_out = self._dense(k_out, "k_out", rows, self.heads_k, dev)
-        with torch.cuda.device(dev):
-            _check("hyena_qk_norm_forward",
-                   self.lib.hyena_qk_norm_forward(ctypes.byref(self._params(dev)), tokens, q.data_ptr(), ldq,
-                                                  k.data_ptr(), ldk, pos, q_out.data_ptr(), k_out.data_ptr(),
-                                                  _stream_handle(torch, dev)))
+        dev, rows, args = self._args(q, k, positions)
+        q_out, qp = self._out(q_out, "q_out", rows, self.heads_q, dev)
+        k_out, kp = self._out(k_out, "k_out", rows, self.heads_k, dev)
+        _launch(self._torch, "hyena_qk_norm_forward", self.lib.hyena_qk_norm_forward, dev, *args, qp, kp)
         return q_out, k_out
 
     def backward_workspace_bytes(self, tokens: int, device) -> int:
@@ -819,25 +839,19 @@ class QKNorm:
     def backward(self, q, k, dq_out, dk_out, positions=None, workspace=None):
         """hyena_qk_norm_backward: (dq, dk, dw_q, dw_k) for the gradients of the forward's outputs;
         the weights' gradients are None where there is no weight."""
-        torch, dev = self._torch, q.device
-        rows, tokens, ldq, ldk, pos = self._args(q, k, positions)
-        for name, t, h in (("dq_out", dq_out, self.heads_q), ("dk_out", dk_out, self.heads_k)):
-            if t is None:
-                raise ValueError(f"{name} is needed")
-            self._dense(t, name, rows, h, dev)
-        dq, dk = self._dense(None, "dq", rows, self.heads_q, dev), self._dense(None, "dk", rows, self.heads_k, dev)
+        torch = self._torch
+        dev, rows, args = self._args(q, k, positions)
+        up = [_dense(t, name, (*rows, h, self.dim), self.io_dtype, dev)
+              for name, t, h in (("dq_out", dq_out, self.heads_q), ("dk_out", dk_out, self.heads_k))]
+        (dq, dqp), (dk, dkp) = self._out(None, "dq", rows, self.heads_q, dev), self._out(None, "dk", rows, self.heads_k, dev)
         dw_q, dw_k = (torch.empty(self.dim, dtype=torch.float32, device=dev) if w is not None else None
                       for w in (self.w_q, self.w_k))
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
         if workspace is None and (dw_q is not None or dw_k is not None):
-            workspace = torch.empty(self.backward_workspace_bytes(tokens, dev), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(self.backward_workspace_bytes(args[1], dev), dtype=torch.uint8, device=dev)
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        with torch.cuda.device(dev):
-            _check("hyena_qk_norm_backward",
-                   self.lib.hyena_qk_norm_backward(ctypes.byref(self._params(dev)), tokens, q.data_ptr(), ldq,
-                                                   k.data_ptr(), ldk, pos, dq_out.data_ptr(), dk_out.data_ptr(),
-                                                   dq.data_ptr(), dk.data_ptr(), ptr(dw_q), ptr(dw_k), ptr(workspace),
-                                                   ws_bytes, _stream_handle(torch, dev)))
+        _launch(torch, "hyena_qk_norm_backward", self.lib.hyena_qk_norm_backward, dev, *args, *up, dqp, dkp, ptr(dw_q),
+                ptr(dw_k), ptr(workspace), ws_bytes)
         return dq, dk, dw_q, dw_k
 
 
@@ -855,59 +869,57 @@ class DeltaRule:
             raise ValueError(f"dtype must be one of {list(_DTYPES)}")
         self.heads_k, self.heads_v, self.dim_k, self.dim_v = int(heads_k), int(heads_v), int(dim_k), int(dim_v)
         self.dtype = dtype
-
-    @property
-    def io_dtype(self):
-        return self._torch.bfloat16 if self.dtype == "bf16" else self._torch.float32
+        self.io_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
 
     def _params(self, scale):
-        return DeltaParamsStruct(self.heads_k, self.heads_v, self.dim_k, self.dim_v, _DTYPES[self.dtype],
-                                 self.dim_k ** -0.5 if scale is None else float(scale))
+        return ctypes.byref(DeltaParamsStruct(self.heads_k, self.heads_v, self.dim_k, self.dim_v, _DTYPES[self.dtype],
+                                              self.dim_k ** -0.5 if scale is None else scale))
 
     def state_shape(self, N: int):
         return (int(N), self.heads_v, self.dim_k, self.dim_v)
 
-    def _need(self, t, name, shape, dtype, device):
-        if not isinstance(t, self._torch.Tensor) or t.device != device or device.type != "cuda":
-            raise ValueError(f"{name} must be a tensor on the GPU that holds q")
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                             f"got {t.dtype} {tuple(t.shape)}")
-
     def _inputs(self, q, k, v, g, beta, rows, device):
-        Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
-        ld = [_token_rows(self._torch, t, name, rows, heads, dim, self.io_dtype, device)
-              for t, name, heads, dim in ((q, "q", Hk, Dk), (k, "k", Hk, Dk), (v, "v", Hv, Dv))]
-        self._need(g, "g", (*rows, Hv), self.io_dtype, device)
-        self._need(beta, "beta", (*rows, Hv), self.io_dtype, device)
-        return DeltaInputsStruct(q.data_ptr(), ld[0], k.data_ptr(), ld[1], v.data_ptr(), ld[2], g.data_ptr(),
-                                 beta.data_ptr())
+        Hk, Hv, Dk, Dv, dt = self.heads_k, self.heads_v, self.dim_k, self.dim_v, self.io_dtype
+        return ctypes.byref(DeltaInputsStruct(
+            *_token_rows(q, "q", rows, Hk, Dk, dt, device), *_token_rows(k, "k", rows, Hk, Dk, dt, device),
+            *_token_rows(v, "v", rows, Hv, Dv, dt, device), _dense(g, "g", (*rows, Hv), dt, device),
+            _dense(beta, "beta", (*rows, Hv), dt, device)))
 
     def _sequences(self, q, seq_start):
-        """(rows, N, tokens, pointer of seq_start) of q [B, T, ...] or packed [tokens, ...]."""
+        """(device, rows, N, tokens, address of seq_start) of q [B, T, ...] or packed [tokens, ...]."""
+        dev = _gpu_of(q, "q")
+        rows = tuple(q.shape[:-2])
         if seq_start is None:
-            if q.dim() != 4:
+            if len(rows) != 2:
                 raise ValueError("q must be [B, T, heads_k, dim_k], or [tokens, heads_k, dim_k] with seq_start")
-            B, T = int(q.shape[0]), int(q.shape[1])
-            return (B, T), B, B * T, None
-        if q.dim() != 3:
+            return dev, rows, rows[0], rows[0] * rows[1], None
+        if len(rows) != 1:
             raise ValueError("q must be [tokens, heads_k, dim_k] with seq_start")
         if seq_start.dim() != 1 or seq_start.numel() < 2:
             raise ValueError("seq_start must hold N + 1 offsets")
         N = int(seq_start.numel()) - 1
-        self._need(seq_start, "seq_start", (N + 1,), self._torch.int64, q.device)
-        return (int(q.shape[0]),), N, int(q.shape[0]), seq_start.data_ptr()
+        return dev, rows, N, rows[0], _dense(seq_start, "seq_start", (N + 1,), self._torch.int64, dev)
 
     def workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
-        return int(self.lib.hyena_delta_workspace_bytes(ctypes.byref(self._params(None)), int(N), int(tokens),
-                                                        16 if packed else None))
+        return int(self.lib.hyena_delta_workspace_bytes(self._params(None), int(N), int(tokens), 16 if packed else None))
+
+    def backward_workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
+        return int(self.lib.hyena_delta_backward_workspace_bytes(self._params(None), int(N), int(tokens),
+                                                                 16 if packed else None))
 
     def _workspace(self, workspace, need, device):
         if workspace is None:
             workspace = self._torch.empty(need, dtype=self._torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
+            return workspace, workspace.data_ptr(), need
+        if workspace.device != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the GPU that holds q")
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+    def _out(self, t, name, shape, dtype, device):
+        if t is None:
+            t = self._torch.empty(shape, dtype=dtype, device=device)
+            return t, t.data_ptr()
+        return t, _dense(t, name, shape, dtype, device)
 
     def forward(self, q, k, v, g, beta, state=None, scale=None, seq_start=None, o=None, state_out=None,
                 workspace=None):
@@ -915,75 +927,52 @@ class DeltaRule:
         one stride between tokens are taken as they are), g, beta [B, T, heads_v]; or all with
         [tokens] in place of [B, T] and seq_start [N + 1] int64 offsets on the device. state
         [N, heads_v, dim_k, dim_v] fp32 or None (zeros). Returns (o like v, the final states)."""
-        torch, dev = self._torch, q.device
-        rows, N, tokens, starts = self._sequences(q, seq_start)
+        torch = self._torch
+        dev, rows, N, tokens, starts = self._sequences(q, seq_start)
         inputs = self._inputs(q, k, v, g, beta, rows, dev)
-        if state is not None:
-            self._need(state, "state", self.state_shape(N), torch.float32, dev)
-        if o is None:
-            o = torch.empty((*rows, self.heads_v, self.dim_v), dtype=self.io_dtype, device=dev)
-        self._need(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
-        if state_out is None:
-            state_out = torch.empty(self.state_shape(N), dtype=torch.float32, device=dev)
-        self._need(state_out, "state_out", self.state_shape(N), torch.float32, dev)
-        ws, ws_bytes = self._workspace(workspace, self.workspace_bytes(N, tokens, starts is not None), dev)
-        with torch.cuda.device(dev):
-            _check("hyena_delta_forward",
-                   self.lib.hyena_delta_forward(ctypes.byref(self._params(scale)), N, tokens, starts,
-                                                ctypes.byref(inputs), state.data_ptr() if state is not None else None,
-                                                o.data_ptr(), state_out.data_ptr(), ws.data_ptr(), ws_bytes,
-                                                _stream_handle(torch, dev)))
+        states = self.state_shape(N)
+        sp = _dense(state, "state", states, torch.float32, dev) if state is not None else None
+        o, op = self._out(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
+        state_out, fp = self._out(state_out, "state_out", states, torch.float32, dev)
+        params = self._params(scale)
+        need = self.lib.hyena_delta_workspace_bytes(params, N, tokens, starts)
+        workspace, ws, ws_bytes = self._workspace(workspace, need, dev)
+        _launch(torch, "hyena_delta_forward", self.lib.hyena_delta_forward, dev, params, N, tokens, starts, inputs, sp, op,
+                fp, ws, ws_bytes)
         return o, state_out
-
-    def backward_workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
-        return int(self.lib.hyena_delta_backward_workspace_bytes(ctypes.byref(self._params(None)), int(N), int(tokens),
-                                                                 16 if packed else None))
 
     def backward(self, q, k, v, g, beta, do, state=None, dstate_out=None, scale=None, seq_start=None, workspace=None):
         """hyena_delta_backward: the gradients (dq, dk, dv, dg, dbeta, dstate) of the forward's
         inputs (dense, in the dtype; dstate fp32) for the gradient do [like o] of its outputs and,
         unless None, dstate_out [N, heads_v, dim_k, dim_v] fp32 of its final states."""
-        torch, dev = self._torch, q.device
-        rows, N, tokens, starts = self._sequences(q, seq_start)
+        torch = self._torch
+        dev, rows, N, tokens, starts = self._sequences(q, seq_start)
         inputs = self._inputs(q, k, v, g, beta, rows, dev)
-        Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
-        self._need(do, "do", (*rows, Hv, Dv), self.io_dtype, dev)
-        for name, t in (("state", state), ("dstate_out", dstate_out)):
-            if t is not None:
-                self._need(t, name, self.state_shape(N), torch.float32, dev)
+        Hk, Hv, Dk, Dv, states = self.heads_k, self.heads_v, self.dim_k, self.dim_v, self.state_shape(N)
+        dop = _dense(do, "do", (*rows, Hv, Dv), self.io_dtype, dev)
+        sp, dsp = (_dense(t, name, states, torch.float32, dev) if t is not None else None
+                   for name, t in (("state", state), ("dstate_out", dstate_out)))
         out = [torch.empty((*rows, *shape), dtype=self.io_dtype, device=dev)
                for shape in ((Hk, Dk), (Hk, Dk), (Hv, Dv), (Hv,), (Hv,))]
-        dstate = torch.empty(self.state_shape(N), dtype=torch.float32, device=dev)
-        ws, ws_bytes = self._workspace(workspace, self.backward_workspace_bytes(N, tokens, starts is not None), dev)
-        with torch.cuda.device(dev):
-            _check("hyena_delta_backward",
-                   self.lib.hyena_delta_backward(ctypes.byref(self._params(scale)), N, tokens, starts,
-                                                 ctypes.byref(inputs), state.data_ptr() if state is not None else None,
-                                                 do.data_ptr(),
-                                                 dstate_out.data_ptr() if dstate_out is not None else None,
-                                                 *(t.data_ptr() for t in out), dstate.data_ptr(), ws.data_ptr(),
-                                                 ws_bytes, _stream_handle(torch, dev)))
-        return (*out, dstate)
+        out.append(torch.empty(states, dtype=torch.float32, device=dev))
+        params = self._params(scale)
+        need = self.lib.hyena_delta_backward_workspace_bytes(params, N, tokens, starts)
+        workspace, ws, ws_bytes = self._workspace(workspace, need, dev)
+        _launch(torch, "hyena_delta_backward", self.lib.hyena_delta_backward, dev, params, N, tokens, starts, inputs, sp,
+                dop, dsp, *(t.data_ptr() for t in out), ws, ws_bytes)
+        return tuple(out)
 
     def step(self, q, k, v, g, beta, states, slots=None, scale=None, o=None):
         """hyena_delta_step: T further tokens of B rows (q, k [B, T, heads_k, dim_k], v
         [B, T, heads_v, dim_v], g, beta [B, T, heads_v]) against states [num, heads_v, dim_k,
         dim_v] fp32, updated in place; slots [B] int32 names each row's state. Returns o like v."""
-        torch, dev = self._torch, q.device
-        rows, B, _, _ = self._sequences(q, None)
+        torch = self._torch
+        dev, rows, B, _, _ = self._sequences(q, None)
         inputs = self._inputs(q, k, v, g, beta, rows, dev)
-        if states.dim() != 4:
-            raise ValueError("states must be [num_states, heads_v, dim_k, dim_v]")
-        num = int(states.shape[0])
-        self._need(states, "states", self.state_shape(num), torch.float32, dev)
-        if slots is not None:
-            self._need(slots, "slots", (B,), torch.int32, dev)
-        if o is None:
-            o = torch.empty((*rows, self.heads_v, self.dim_v), dtype=self.io_dtype, device=dev)
-        self._need(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
-        with torch.cuda.device(dev):
-            _check("hyena_delta_step",
-                   self.lib.hyena_delta_step(ctypes.byref(self._params(scale)), B, rows[1], ctypes.byref(inputs),
-                                             states.data_ptr(), num, slots.data_ptr() if slots is not None else None,
-                                             o.data_ptr(), _stream_handle(torch, dev)))
+        num = states.shape[0] if states.dim() == 4 else 0
+        stp = _dense(states, "states", (num, self.heads_v, self.dim_k, self.dim_v), torch.float32, dev)
+        slp = _dense(slots, "slots", (B,), torch.int32, dev) if slots is not None else None
+        o, op = self._out(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
+        _launch(torch, "hyena_delta_step", self.lib.hyena_delta_step, dev, self._params(scale), B, rows[1], inputs, stp, num,
+                slp, op)
         return o

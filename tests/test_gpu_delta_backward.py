@@ -112,8 +112,6 @@ def test_rows_outside_sequences_stay():
     """Gradients of rows that belong to no sequence are not written."""
     dims = (1, 1, 64, 64)
     d = D.make([50, 40], *dims, "bf16", seed=8)
-    import ctypes
-
     from fft_long_convolution_libhyena_amd import DeltaRule
 
     r = DeltaRule(*dims)
@@ -126,7 +124,7 @@ def test_rows_outside_sequences_stay():
     inputs = r._inputs(x["q"], x["k"], x["v"], x["g"], x["beta"], (140,), x["q"].device)
     outs = [torch.full_like(x[n], 7.0) for n in ("q", "k", "v", "g", "beta")]
     ws = torch.empty(r.backward_workspace_bytes(2, 140, True), dtype=torch.uint8, device="cuda")
-    st = r.lib.hyena_delta_backward(ctypes.byref(r._params(None)), 2, 140, start.data_ptr(), ctypes.byref(inputs), None,
+    st = r.lib.hyena_delta_backward(r._params(None), 2, 140, start.data_ptr(), inputs, None,
                                     x["do"].data_ptr(), None, *(o.data_ptr() for o in outs), None, ws.data_ptr(), ws.numel(),
                                     torch.cuda.current_stream().cuda_stream)
     assert st == 0
