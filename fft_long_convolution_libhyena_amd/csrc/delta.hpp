@@ -276,21 +276,23 @@ struct ColTile {
     }
 };
 
-// One wave moves the tiles: 16 bytes a lane, 1 KiB an instruction, whole rows.
-template <bool BF, int DK>
+// A wave moves the tiles (or W waves a share each, rows 64 / W of them): 16 bytes a
+// lane, 1 KiB an instruction, whole rows.
+template <bool BF, int DK, int W = 1>
 struct Stage {
-    static constexpr int EPL = BF ? 8 : 4, LR = DK / EPL, RI = 64 / LR, N = LR;
+    static constexpr int EPL = BF ? 8 : 4, LR = DK / EPL, RI = 64 / LR, N = LR / W;
+    static_assert(W == 1 || W == 4, "shares of 16 rows: their 16-byte shifts add up");
     u32x4 r[N];
-    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int dk, int lane) {
+    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int dk, int lane, int w = 0) {
         const uint32_t k = (lane % LR) * EPL, E = BF ? 2 : 4;
-        const uint32_t off = (int)k < dk ? (lane / LR) * ld + k * E : kNoElem;
+        const uint32_t off = (int)k < dk ? (lane / LR + w * (kC / W)) * ld + k * E : kNoElem;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + i * RI * ld), 0, 0));
     }
-    __device__ __forceinline__ void store(Tile<BF ? 1 : 3, DK>& t, int lane) const {
+    __device__ __forceinline__ void store(Tile<BF ? 1 : 3, DK>& t, int lane, int w = 0) const {
         using TL = Tile<BF ? 1 : 3, DK>;
-        const int at = (lane / LR) * TL::pitch + 2 * (lane % LR) * EPL;
+        const int at = (lane / LR) * TL::pitch + 2 * (lane % LR) * EPL + TL::at(w * (kC / W), 0);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int o = at + i * RI * TL::pitch + ((i * RI >> 3) & 3) * 16;
@@ -494,6 +496,68 @@ __device__ __forceinline__ bool find_chunk(const Seqs& s, int64_t slot, Range& r
     return c >= 0 && c * kC < r.len;
 }
 
+// Where few sequences would leave most of the card idle, long ones are cut into pieces of
+// `len` chunks that are scanned side by side: a first scan takes every piece but the last
+// from a zero state (its end B) and from the identity (its end M: the state behind a piece
+// is M S + B), and each piece's own scan begins by carrying the state through the pieces
+// before it. That is twice the scan's work and a third of its time from three pieces on,
+// so a sequence of up to three pieces' length stays whole.
+struct Pieces {
+    int64_t len;    // chunks a piece; 0: every sequence whole
+    int64_t per;    // piece slots a sequence, where all are of one length
+    int64_t slots;  // of the call; sequence n's start at start[n] / (64 len) + n, as chunks do
+    float* b;       // [slot][value head][16-column block][tile][lane][4] the ends B
+    unsigned char* m;   // [slot][value head] the ends M, as left operands of state tiles in parts
+    unsigned char* mt;  // their transposes (backward), or null
+};
+struct Piece {
+    Range r;        // its tokens; chunk c of it is workspace slot r.slot0 + c
+    int64_t n;      // sequence
+    int64_t first;  // piece slot of the sequence's first piece
+    int s, count;   // number in the sequence, pieces of the sequence
+};
+__device__ __forceinline__ bool find_piece(const Seqs& q, const Pieces& ps, int64_t slot, Piece& p) {
+    if (!ps.len) {
+        p.n = p.first = slot;
+        p.r = seq_range(q, slot);
+        p.s = 0;
+        p.count = 1;
+        return true;
+    }
+    if (!q.start) {
+        p.n = slot / ps.per;
+        p.first = p.n * ps.per;
+    } else {
+        const int64_t unit = kC * ps.len;
+        auto start = [&](int64_t n) {
+            const int64_t b = q.start[n];
+            return b < 0 ? 0 : (b > q.tokens ? q.tokens : b);
+        };
+        int64_t lo = 0, hi = q.N - 1;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (start(mid) / unit + mid <= slot)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        p.n = lo;
+        p.first = start(lo) / unit + lo;
+    }
+    p.r = seq_range(q, p.n);
+    p.s = (int)(slot - p.first);
+    const int64_t chunks = (p.r.len + kC - 1) / kC;
+    p.count = chunks > 3 * ps.len ? (int)((chunks + ps.len - 1) / ps.len) : 1;
+    if (p.s < 0 || p.s >= p.count) return false;
+    if (p.count > 1) {
+        const int64_t c0 = p.s * ps.len, left = p.r.len - c0 * kC;
+        p.r.first += c0 * kC;
+        p.r.slot0 += c0;
+        p.r.len = left < ps.len * kC ? left : ps.len * kC;
+    }
+    return true;
+}
+
 // The running sum of the log decays over a chunk's 64 lanes, in 64 bits and to base 2:
 // differences of it stay exact to fp32 however strong single decays are, and a decay is one
 // hardware exp2 of such a difference (accurate to its last bit or two, as an expf would be).
@@ -552,6 +616,11 @@ constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxSeqs = int64_t(1) << 24;
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // elements: 64 rows stay below 2^31 bytes
 
+constexpr int kCus = 256;
+// A piece below this many chunks gains nothing: the ends' launch and a carry (2 us a piece)
+// cost what the shorter scan saves.
+constexpr int64_t kMinPiece = 16;
+
 struct PrepArgs;
 struct ScanArgs;
 
@@ -574,7 +643,11 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
 // bytes of the preparation's workspace; pointers from base
 size_t delta_prep_layout(const DeltaCall& c, bool bwd, unsigned char* base, delta::Prep& o);
 hipError_t delta_prep(const DeltaCall& c, bool bwd, const delta::Prep& o, hipStream_t st);
-// the state scan: outputs, or (keep) states and written values for the backward
+// how (and whether) the call's long sequences are cut; bytes of the pieces' workspace
+delta::Pieces delta_pieces(const DeltaCall& c);
+size_t delta_pieces_layout(const DeltaCall& c, bool bwd, unsigned char* base, delta::Pieces& o);
+// the state scan: outputs, or (keep) states and written values for the backward; the
+// pieces' ends first where sequences are cut
 hipError_t delta_scan(const DeltaCall& c, bool keep, const delta::ScanArgs& a, hipStream_t st);
 
 }  // namespace hy

@@ -115,6 +115,7 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
         f.s_in = state_in;
         f.s0 = b.s0;
         f.u = b.u;
+        f.pieces.slots = c.seqs.N;
         if (hy::delta_scan(c, true, f, stream) != hipSuccess) return HYENA_ERR_DEVICE;
     }
     hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, 0, 0};

@@ -85,9 +85,11 @@ template <bool BF, int DK, int MODE>
 hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
     using Cfg = ScanCfg<BF, DK, MODE>;
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
-    a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
+    const int w = 16 * Cfg::NB;
+    a.nbv = (c.shape.dv + w - 1) / w;
+    a.nblk = a.nbv + (Cfg::ENDS ? (DK + w - 1) / w : 0);
     a.nb16 = (c.shape.dv + 15) / 16;
-    const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
+    const int64_t pairs = (a.pieces.slots * c.shape.hv + 7) / 8 * 8;
     const hipError_t e = hipFuncSetAttribute((const void*)k_delta_scan<BF, DK, MODE>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
@@ -95,7 +97,54 @@ hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <bool BF, int DK>
+hipError_t launch_scans_t(const DeltaCall& c, bool keep, const ScanArgs& a, hipStream_t st) {
+    if (a.pieces.len) {
+        const hipError_t e = launch_scan_t<BF, DK, kScanEnds>(c, a, st);
+        if (e != hipSuccess) return e;
+    }
+    return keep ? launch_scan_t<BF, DK, kScanKeep>(c, a, st) : launch_scan_t<BF, DK, kScanOut>(c, a, st);
+}
+
 }  // namespace
+
+Pieces delta_pieces(const DeltaCall& c) {
+    Pieces p{};
+    p.slots = c.seqs.N;
+    // piece slots whose workgroups, of the scan or of the ends, all run at once (one a CU)
+    const int64_t wn = c.bf ? 32 : 16, we = c.bf ? 64 : 48, dv = c.shape.dv;
+    const int64_t scan = (dv + wn - 1) / wn, ends = (dv + we - 1) / we + (c.dkp + we - 1) / we;
+    const int64_t room = kCus / (c.shape.hv * (scan > ends ? scan : ends)), N = c.seqs.N;
+    if (room < 3 * N) return p;
+    const int64_t chunks = c.seqs.start ? (c.seqs.tokens + kC - 1) / kC : c.seqs.cpt;  // of one sequence at most
+    const int64_t fit = c.seqs.start ? room - N + (N == 1) : room / N;
+    const int64_t len = (chunks + fit - 1) / fit;
+    p.len = len < kMinPiece ? kMinPiece : len;
+    if (chunks <= 3 * p.len) {
+        p.len = 0;
+        return p;
+    }
+    p.per = (chunks + p.len - 1) / p.len;
+    p.slots = c.seqs.start ? c.seqs.tokens / (kC * p.len) + N : N * p.per;
+    return p;
+}
+
+size_t delta_pieces_layout(const DeltaCall& c, bool bwd, unsigned char* base, Pieces& o) {
+    o = delta_pieces(c);
+    if (!o.len) return 0;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char* p = base ? base + at : nullptr;
+        at += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    const size_t heads = (size_t)o.slots * c.shape.hv;
+    const size_t m = heads * c.dkp * c.dkp * 2 * (c.bf ? Io<true>::NS : Io<false>::NS);
+    o.b = (float*)take(heads * ((c.shape.dv + 15) / 16 * 16) * c.dkp * sizeof(float));
+    o.m = take(m);
+    if (bwd) o.mt = take(m);
+    return at;
+}
 
 hipError_t delta_prep(const DeltaCall& c, bool bwd, const Prep& o, hipStream_t st) {
     if (c.slots < 1 || c.seqs.tokens < 1) return hipSuccess;
@@ -108,14 +157,8 @@ hipError_t delta_prep(const DeltaCall& c, bool bwd, const Prep& o, hipStream_t s
 }
 
 hipError_t delta_scan(const DeltaCall& c, bool keep, const ScanArgs& a, hipStream_t st) {
-    if (c.bf) {
-        if (c.dkp == 64)
-            return keep ? launch_scan_t<true, 64, kScanKeep>(c, a, st) : launch_scan_t<true, 64, kScanOut>(c, a, st);
-        return keep ? launch_scan_t<true, 128, kScanKeep>(c, a, st) : launch_scan_t<true, 128, kScanOut>(c, a, st);
-    }
-    if (c.dkp == 64)
-        return keep ? launch_scan_t<false, 64, kScanKeep>(c, a, st) : launch_scan_t<false, 64, kScanOut>(c, a, st);
-    return keep ? launch_scan_t<false, 128, kScanKeep>(c, a, st) : launch_scan_t<false, 128, kScanOut>(c, a, st);
+    if (c.bf) return c.dkp == 64 ? launch_scans_t<true, 64>(c, keep, a, st) : launch_scans_t<true, 128>(c, keep, a, st);
+    return c.dkp == 64 ? launch_scans_t<false, 64>(c, keep, a, st) : launch_scans_t<false, 128>(c, keep, a, st);
 }
 
 }  // namespace hy
@@ -127,7 +170,8 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
     hy::DeltaCall c;
     if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
     hy::delta::Prep o;
-    return hy::delta_prep_layout(c, false, nullptr, o);
+    hy::delta::Pieces p;
+    return hy::delta_prep_layout(c, false, nullptr, o) + hy::delta_pieces_layout(c, false, nullptr, p);
 }
 
 hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
@@ -142,7 +186,9 @@ hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N
     if ((tokens > 0 && !o) || !aligned16(o) || !aligned16(state_in) || !aligned16(state_out))
         return HYENA_ERR_INVALID_ARG;
     hy::delta::ScanArgs a{};
-    const size_t need = hy::delta_prep_layout(c, false, (unsigned char*)workspace, a.prep);
+    const size_t prep = hy::delta_prep_layout(c, false, (unsigned char*)workspace, a.prep);
+    const size_t need =
+        prep + hy::delta_pieces_layout(c, false, workspace ? (unsigned char*)workspace + prep : nullptr, a.pieces);
     if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     hipError_t e = hy::delta_prep(c, false, a.prep, stream);

@@ -37,11 +37,14 @@ struct ScanArgs {
     void* o;            // [tokens][hv][dv] (outputs)
     void* s0;           // state before every chunk, as fragments (for the backward)
     void* u;            // written values, as fragments (for the backward)
+    Pieces pieces;
     int nblk;           // workgroups per head
+    int nbv;            // of them, those on columns of v; the others on M's (ends)
     int nb16;           // blocks of 16 columns per head
 };
 
-enum { kScanOut = 0, kScanKeep = 1 };
+// outputs; states and written values kept; the ends of pieces
+enum { kScanOut = 0, kScanKeep = 1, kScanEnds = 2 };
 
 // The outputs' waves rest for this many 64-clock units after a barrier, while the state
 // waves read K: both at once would halve the state's LDS rate where it waits for it.
@@ -87,10 +90,12 @@ struct Exchange {  // the operands of one chunk's outputs
 };
 template <bool BF, int DK, int MODE>
 struct ScanCfg {
-    static constexpr int NB = BF ? 2 : 1;   // column blocks
-    static constexpr int BUF = BF ? 2 : 1;  // buffers of K and of Q
-    static constexpr bool OUT = MODE == kScanOut;
-    static constexpr bool STAGER = !(OUT && BF);  // a wave that only stages
+    static constexpr bool OUT = MODE == kScanOut, ENDS = MODE == kScanEnds;
+    // column blocks; without outputs to make, the ends' state waves have the CU to themselves
+    static constexpr int NB = ENDS ? (BF ? 4 : 3) : BF ? 2 : 1;
+    static constexpr int BUF = BF ? 2 : 1;                        // buffers of K and of Q
+    static constexpr bool STAGER = !(BF && (OUT || ENDS));       // a wave that only stages
+    static constexpr bool SELF = BF && ENDS;                      // the state waves stage
     static constexpr int threads = 64 * ((OUT ? 2 : 1) * NB + (STAGER ? 1 : 0));
     struct None {};
     struct LdsOut {
@@ -122,6 +127,91 @@ struct StageV {
     }
 };
 
+// likewise 64 columns by four waves, 16 rows each: 8 rows of 128 bytes an instruction
+struct StageV4 {
+    u32x4 r[2];
+    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int col0, int dv, int lane, int w) {
+        const int c = col0 + 8 * (lane & 7);
+        const uint32_t off = c < dv ? (16 * w + (lane >> 3)) * ld + c * 2 : kNoElem;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + i * 8 * ld), 0, 0));
+    }
+    __device__ __forceinline__ void store(ColTile<64>& t, int lane, int w) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x4*>(t.b + (16 * w + 8 * i + (lane >> 3)) * ColTile<64>::pitch + 16 * (lane & 7)) = r[i];
+    }
+};
+
+// The state in front of a piece: the end of the sequence's first piece, carried through
+// `steps` more, S = M S + B. b and m point at the first and step from piece to piece
+// (the reverse scan goes the other way, with the transposes). M does not depend on the
+// state, so its fragments are under way a step (fp32: half a step) ahead.
+template <int NS, int DK>
+__device__ __forceinline__ void carry(f32x4 (&S)[DK / 16], const float* b, int64_t bstep, const unsigned char* m, int64_t mstep,
+                                      int steps, int lane, const MinusOne& minus) {
+    constexpr int KS = DK / 32, MT = DK / 16, P = MT / 2, R = NS == 2 ? P : P / 2;
+    auto end = [&](const float* p, int t) { return *reinterpret_cast<const f32x4*>(p + (t * 64 + lane) * 4); };
+#pragma unroll
+    for (int t = 0; t < MT; ++t) S[t] = end(b, t);
+    if (steps < 1) return;
+    Frag<NS> a[R][2][KS];
+    auto load = [&](const unsigned char* p, int i) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                a[i % R][t][s] = get_frag<NS>(reinterpret_cast<const __bf16*>(p) + ((2 * i + t) * KS + s) * NS * 512, 512, lane);
+    };
+    m += mstep;
+#pragma unroll
+    for (int i = 0; i < R; ++i) load(m, i);
+    for (int k = 0; k < steps; ++k) {
+        b += bstep;
+        Frag<NS> f[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) f[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1], minus);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) S[t] = end(b, t);
+        const unsigned char* next = k + 1 < steps ? m + mstep : m;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Frag<NS> w[2] = {a[i % R][0][s], a[i % R][1][s]};
+                mma_tiles(w, f[s], S + 2 * i);
+            }
+            load(i + R < P ? m : next, (i + R) % P);
+        }
+        m = next;
+    }
+}
+// a column of M, as a state wave holds it, to where carry takes it: element j of lane
+// (row of the tile, eight columns) of fragment (row tile, 32 columns)
+template <int NS, int DK>
+__device__ __forceinline__ void store_end(unsigned char* m, unsigned char* mt, const f32x4 (&S)[DK / 16], int c0, int lane) {
+    constexpr int KS = DK / 32, MT = DK / 16;
+    const int g = lane >> 4;
+    // the row of M^T that this column is: tile and row in it, inverting tile_row
+    const int tm = 2 * (c0 >> 5) + (c0 >> 2 & 1), tr = 4 * (c0 >> 3 & 3) + (c0 & 3);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const f32x4 &x = S[2 * s], &y = S[2 * s + 1];
+        const Frag<NS> f = split8<NS>({x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tile = 2 * s + (j >> 2), l = 16 * (c0 >> 3 & 3) + 4 * g + (j & 3);
+                reinterpret_cast<__bf16*>(m)[((tile * KS + (c0 >> 5)) * NS + n) * 512 + l * 8 + (c0 & 7)] = f.p[n][j];
+            }
+            if (mt) *reinterpret_cast<bf16x8*>(mt + (((tm * KS + s) * NS + n) * 512 + (16 * g + tr) * 8) * 2) = f.p[n];
+        }
+    }
+    static_assert(MT == 2 * KS, "pairs of tiles");
+}
+
 template <class Cfg>
 __device__ __forceinline__ constexpr int waves_of() {
     return Cfg::threads / 64;
@@ -133,7 +223,7 @@ void k_delta_scan(ScanArgs a) {
     using IO = Io<BF>;
     using T = typename IO::T;
     using Cfg = ScanCfg<BF, DK, MODE>;
-    constexpr bool OUT = Cfg::OUT;
+    constexpr bool OUT = Cfg::OUT, ENDS = Cfg::ENDS;
     constexpr int KS = DK / 32, MT = DK / 16, NB = Cfg::NB, BUF = Cfg::BUF;
     constexpr int NI = IO::NI, NS = IO::NS, NP = IO::NP, NO = IO::NO;
     constexpr uint32_t E = sizeof(T);
@@ -146,11 +236,18 @@ void k_delta_scan(ScanArgs a) {
     const int64_t bid = blockIdx.x;
     const int64_t pair = bid / (8 * a.nblk) * 8 + (bid & 7);
     const int hv = a.sh.hv;
-    if (pair >= a.seqs.N * hv) return;
-    const int64_t n = pair / hv;
+    if (pair >= a.pieces.slots * hv) return;
+    Piece pc;
+    if (!find_piece(a.seqs, a.pieces, pair / hv, pc)) return;
+    const int64_t n = pc.n;
     const int h = (int)(pair % hv), hk = h / a.sh.group;
-    const Range rr = seq_range(a.seqs, n);
-    const int64_t first = uniform64(rr.first), len = uniform64(rr.len), slot0 = uniform64(rr.slot0);
+    const int64_t first = uniform64(pc.r.first), len = uniform64(pc.r.len), slot0 = uniform64(pc.r.slot0);
+    const int64_t pslot = uniform64(pc.first);
+    const int ps = __builtin_amdgcn_readfirstlane(pc.s);
+    const bool last = pc.s + 1 == pc.count;
+    const int wg = (int)(bid / 8 % a.nblk);
+    const bool onm = ENDS && wg >= a.nbv;  // columns of M
+    if (ENDS && (last || (onm && ps == 0))) return;
     const int nch = (int)((len + kC - 1) / kC);
     const int tail = (int)(len - (int64_t)(nch - 1) * kC);  // rows of the last chunk
     const int dk = a.sh.dk, dv = a.sh.dv;
@@ -162,7 +259,7 @@ void k_delta_scan(ScanArgs a) {
     const unsigned char* kbase = (const unsigned char*)((const T*)a.k + first * a.sh.ldk + (int64_t)hk * dk);
     const unsigned char* qbase = OUT ? (const unsigned char*)((const T*)a.q + first * a.sh.ldq + (int64_t)hk * dk) : nullptr;
     const unsigned char* vbase = (const unsigned char*)((const T*)a.v + first * a.sh.ldv + (int64_t)h * dv);
-    const int wgcol = (int)(bid / 8 % a.nblk) * NB * 16;
+    const int wgcol = (onm ? wg - a.nbv : wg) * NB * 16;
     auto rows_in = [&](int c) { return c + 1 < nch ? kC : tail; };
     auto load_tile = [&](Stage<BF, DK>& r, const unsigned char* base, int64_t step, int64_t ld, int c) {
         r.load(plain_buf(base + c * step, (rows_in(c) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk, lane);
@@ -206,9 +303,9 @@ void k_delta_scan(ScanArgs a) {
         }
 
     const MinusOne minus(lane);
-    const int blk = (int)(bid / 8 % a.nblk) * NB + wave % NB;
+    const int blk = wgcol / 16 + wave % NB;
     const int c0 = blk * 16 + col;  // this lane's column
-    const bool cok = c0 < dv;
+    const bool cok = !onm && c0 < dv;
     const uint32_t ldo = (uint32_t)(hv * dv) * E;
     unsigned char* op = OUT ? (unsigned char*)((T*)a.o + (first * hv + h) * (int64_t)dv) : nullptr;
     // row i of this lane's results in tile t
@@ -332,8 +429,14 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = drow(t, i);
-            S[t][i] = a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
+            S[t][i] = ps == 0 && a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
+            if (onm) S[t][i] = k == c0 ? 1.f : 0.f;
         }
+    // ends of the piece in front: [slot][head] sized records
+    const int64_t bsize = (int64_t)a.nb16 * MT * 256, msize = DK * DK * NS * 2;
+    if (!ENDS && ps > 0 && blk < a.nb16)
+        carry<NS, DK>(S, a.pieces.b + (pslot * hv + h) * bsize + blk * (MT * 256), hv * bsize, a.pieces.m + (pslot * hv + h) * msize,
+                      hv * msize, ps - 1, lane, minus);
 #pragma unroll
     for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1], minus);
 
@@ -355,7 +458,25 @@ void k_delta_scan(ScanArgs a) {
         glast = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, 0, Rec<BF>::sc + (kC - 1) * 4, 0));
     };
     auto load_t = [&](Frag<NS>(&to)[kTri], const RowBuf& b, int f) { to[f] = buf_frag<NS>(b, Rec<BF>::t, f, lane); };
+    Stage<BF, DK, Cfg::SELF ? 4 : 1> rk;
+    StageV4 rv;
+    auto self_load = [&](int c) {
+        rk.load(plain_buf(kbase + c * krow, (rows_in(c) - 1) * (uint32_t)(a.sh.ldk * E) + dk * E), (uint32_t)(a.sh.ldk * E), dk,
+                lane, wave);
+        rv.load(vbuf(c), ldv, wgcol, onm ? 0 : dv, lane, wave);
+    };
+    auto self_store = [&](int c) {
+        if constexpr (Cfg::SELF) {
+            rk.store(l.k[c & 1], lane, wave);
+            rv.store(l.v[c & 1], lane, wave);
+        }
+    };
     if (nch > 0) {
+        if constexpr (Cfg::SELF) {
+            self_load(0);
+            self_store(0);
+            self_load(nch > 1 ? 1 : 0);
+        }
         const RowBuf vb = vbuf(0), rb = plain_buf(rec, Rec<BF>::bytes);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -369,16 +490,16 @@ void k_delta_scan(ScanArgs a) {
         lds_barrier();  // K of the first chunk is in LDS
     }
     // this block's fragments of the backward, one chunk's behind another's
-    const bool kept = !OUT && blk < a.nb16;
-    unsigned char* s0p = OUT ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
-    unsigned char* up = OUT ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
+    const bool kept = MODE == kScanKeep && blk < a.nb16;
+    unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
+    unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
     constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;  // matrix instructions per product
     // one chunk; T alternates between two sets of registers
     auto chunk = [&](int c, Frag<NS>(&Tf)[kTri], Frag<NS>(&Tn)[kTri]) {
         if (c + 1 < nch) rec += recstep;  // loaded for the next chunk; the last one reads itself again
         const RowBuf vb = vbuf(c + 1 < nch ? c + 1 : c), rb = plain_buf(rec, Rec<BF>::bytes);
         const Tile<NI, DK>& K = l.k[c & (BUF - 1)];
-        if constexpr (!OUT) {
+        if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
                 for (int s = 0; s < KS; ++s) store_frag<BF>(s0p + s * 512 * E, lane, S[2 * s], S[2 * s + 1]);
@@ -412,6 +533,11 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
                 for (int f = s * kTri / KS; f < (s + 1) * kTri / KS; ++f) load_t(Tn, rb, f);
             }
+            if constexpr (Cfg::SELF)
+                if (s == KS - 1) {  // no branches: the last chunks store and load one that is not read
+                    self_store(c + 1);
+                    self_load(c + 2 < nch ? c + 2 : nch - 1);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
         Frag<NI> kt[2][MT];
@@ -496,7 +622,7 @@ void k_delta_scan(ScanArgs a) {
         if constexpr (OUT) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) l.x[wave][c & 1].u[t][lane] = u[t];
-        } else {
+        } else if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) store_frag<BF>(up + s * 512 * E, lane, u[2 * s], u[2 * s + 1]);
@@ -520,7 +646,19 @@ void k_delta_scan(ScanArgs a) {
         chunk(c + 1, Tab[BF ? 1 : 0], Tab[0]);
     }
     if (c < nch) chunk(c, Tab[0], Tab[BF ? 1 : 0]);
-    if (a.s_out)
+    if constexpr (ENDS) {
+        const int64_t at = (pslot + ps) * hv + h;
+        if (!onm) {
+            if (blk < a.nb16)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    *reinterpret_cast<f32x4*>(a.pieces.b + at * bsize + blk * (MT * 256) + (t * 64 + lane) * 4) = S[t];
+        } else if (c0 < DK) {
+            store_end<NS, DK>(a.pieces.m + at * msize, a.pieces.mt ? a.pieces.mt + at * msize : nullptr, S, c0, lane);
+        }
+        return;
+    }
+    if (a.s_out && last)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll

@@ -53,6 +53,37 @@ def test_forward_packed(lens, hk, hv, dk, dv, dtype):
     assert o.dtype == d["q"].dtype and s.dtype == torch.float32
 
 
+# Sequences long enough to be cut into pieces, slow decays and weak writes so that the state
+# in front of a piece reaches far into it. Cutting adds, per carry, the roundings of M's and
+# S's operands (two of 2^-16) or sums of 128 terms more; fp32 states also sum over ~55 chunks.
+TOL_LONG = {"bf16": math.sqrt(5 + 2 * 2) * 2.0 ** -16, "f32": (192 + 2 * 128 + 55) * 2.0 ** -24}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,packed,hk,hv,dk,dv", [
+    ([3500], False, 1, 1, 64, 64),
+    ([3500, 3500], False, 1, 2, 40, 72),
+    ([4100], True, 2, 2, 128, 96),
+    ([3201, 0, 70], True, 1, 2, 128, 40),
+    ([1, 3300, 3137], True, 1, 1, 72, 128),
+])
+def test_forward_cut_into_pieces(lens, packed, hk, hv, dk, dv, dtype):
+    d = D.make(lens, hk, hv, dk, dv, dtype, seed=sum(lens), decay=1e-3)
+    d["beta"] = d["beta"] * 0.0625
+    g = on_gpu(d)
+    r = rule(d, hk, hv, dk, dv, dtype)
+    if packed:
+        args, start = [g[n] for n in ("q", "k", "v", "g", "beta")], D.starts(lens, "cuda")
+    else:
+        args, start = [g[n].unflatten(0, (len(lens), lens[0])) for n in ("q", "k", "v", "g", "beta")], None
+    o, s = r.forward(*args, state=g["state"], seq_start=start)
+    o2, s2 = r.forward(*args, state=g["state"], seq_start=start)
+    ro, rs = D.forward(d, dk ** -0.5)
+    assert D.rel(s, rs) <= TOL_LONG[dtype]
+    assert D.rel(o.reshape(ro.shape), ro) <= max(TOL_O[dtype], TOL_LONG[dtype])
+    assert bool((o == o2).all()) and bool((s == s2).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T", [(1, 1), (2, 100), (3, 257), (2, 0)])
 def test_forward_batch_without_state(B, T, dtype):
