@@ -18,6 +18,7 @@ namespace {
 
 struct BackLayout {
     Prep prep;
+    Pieces pieces;
     void *s0, *ds1, *u, *r;
     size_t bytes;
 };
@@ -37,22 +38,22 @@ BackLayout back_layout(const DeltaCall& c, unsigned char* base) {
     b.ds1 = take(states);
     b.u = take(rows);
     b.r = take(rows);
-    b.bytes = at;
+    b.bytes = at + delta_pieces_layout(c, true, base ? base + at : nullptr, b.pieces);
     return b;
 }
 
-template <bool BF, int DK>
+template <bool BF, int DK, bool ENDS>
 hipError_t launch_rev_t(const DeltaCall& c, RevArgs a, hipStream_t st) {
     using Cfg = RevCfg<BF, DK>;
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
     a.nb16 = (c.shape.dv + 15) / 16;
-    const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
+    const int64_t pairs = (a.pieces.slots * c.shape.hv + 7) / 8 * 8;
     const hipError_t e =
-        hipFuncSetAttribute((const void*)k_delta_rev<BF, DK>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        hipFuncSetAttribute((const void*)k_delta_rev<BF, DK, ENDS>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_delta_rev<BF, DK>), dim3((unsigned)(pairs * a.nblk)), dim3(Cfg::threads), lds, st, a);
+    hipLaunchKernelGGL((k_delta_rev<BF, DK, ENDS>), dim3((unsigned)(pairs * a.nblk)), dim3(Cfg::threads), lds, st, a);
     return hipGetLastError();
 }
 
@@ -70,7 +71,9 @@ hipError_t launch_grad_t(const DeltaCall& c, const GradArgs& a, hipStream_t st) 
 
 template <bool BF, int DK>
 hipError_t launch_back_t(const DeltaCall& c, const RevArgs& r, const GradArgs& g, hipStream_t st) {
-    const hipError_t e = launch_rev_t<BF, DK>(c, r, st);
+    hipError_t e = hipSuccess;
+    if (r.pieces.len) e = launch_rev_t<BF, DK, true>(c, r, st);
+    if (e == hipSuccess) e = launch_rev_t<BF, DK, false>(c, r, st);
     if (e != hipSuccess || c.seqs.tokens < 1) return e;
     return c.shape.group > 1 ? launch_grad_t<BF, DK, true>(c, g, st) : launch_grad_t<BF, DK, false>(c, g, st);
 }
@@ -115,10 +118,10 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
         f.s_in = state_in;
         f.s0 = b.s0;
         f.u = b.u;
-        f.pieces.slots = c.seqs.N;
+        f.pieces = b.pieces;
         if (hy::delta_scan(c, true, f, stream) != hipSuccess) return HYENA_ERR_DEVICE;
     }
-    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, 0, 0};
+    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, b.pieces, 0, 0};
     hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->v, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, dq, dk, dg, dbeta};
     hipError_t e;
     if (c.bf)

@@ -26,6 +26,7 @@ struct RevArgs {
     void* ds1;             // dS behind every chunk, as fragments
     void* r;               // as fragments
     void* dv;              // [tokens][hv][dv] (output)
+    Pieces pieces;
     int nblk, nb16;
 };
 
@@ -51,7 +52,9 @@ struct RevCfg {
     struct Lds : LdsT, std::conditional<BF, LdsV, None>::type {};
 };
 
-template <bool BF, int DK>
+// ENDS: only dS in front of a piece that starts from zero (the last from ds_out), for
+// the pieces before it to carry
+template <bool BF, int DK, bool ENDS>
 __global__ __launch_bounds__((RevCfg<BF, DK>::threads)) __attribute__((amdgpu_waves_per_eu(1)))
 void k_delta_rev(RevArgs a) {
     using IO = Io<BF>;
@@ -67,11 +70,13 @@ void k_delta_rev(RevArgs a) {
     const int64_t bid = blockIdx.x;
     const int64_t pair = bid / (8 * a.nblk) * 8 + (bid & 7);
     const int hv = a.sh.hv;
-    if (pair >= a.seqs.N * hv) return;
-    const int64_t n = pair / hv;
+    if (pair >= a.pieces.slots * hv) return;
+    Piece pc;
+    if (!find_piece(a.seqs, a.pieces, pair / hv, pc) || (ENDS && pc.s == 0)) return;
+    const int64_t n = pc.n;
     const int h = (int)(pair % hv), hk = h / a.sh.group;
-    const Range rr = seq_range(a.seqs, n);
-    const int64_t first = uniform64(rr.first), len = uniform64(rr.len), slot0 = uniform64(rr.slot0);
+    const int64_t first = uniform64(pc.r.first), len = uniform64(pc.r.len), slot0 = uniform64(pc.r.slot0);
+    const int behind = __builtin_amdgcn_readfirstlane(pc.count - 1 - pc.s);  // pieces behind this one
     const int nch = (int)((len + kC - 1) / kC);
     const int tail = (int)(len - (int64_t)(nch - 1) * kC);
     const int dk = a.sh.dk, dv = a.sh.dv;
@@ -269,8 +274,14 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = drow(t, i);
-            S[t][i] = a.ds_out && k < dk && cok ? a.ds_out[((n * hv + h) * dk + k) * dv + c0] : 0.f;
+            S[t][i] = behind == 0 && a.ds_out && k < dk && cok ? a.ds_out[((n * hv + h) * dk + k) * dv + c0] : 0.f;
         }
+    const int64_t bsize = (int64_t)a.nb16 * MT * 256, msize = DK * DK * NS * 2;
+    if (!ENDS && behind > 0 && blk < a.nb16) {
+        const int64_t at = (uniform64(pc.first) + pc.count - 1) * hv + h;  // the last piece
+        carry<NS, DK>(S, a.pieces.b + at * bsize + blk * (MT * 256), -hv * bsize, a.pieces.mt + at * msize, -hv * msize, behind - 1,
+                      lane, minus);
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1], minus);
 
@@ -316,7 +327,7 @@ void k_delta_rev(RevArgs a) {
         const Tile<NI, DK>& K = l.k[i & (BUF - 1)];
         const RevInputs<DK>& in = l.x[wave][i & 1];
         const int64_t fr = ((slot0 + nch - 1 - i) * hv + h) * a.nb16 + blk;  // this block's fragments
-        if (blk < a.nb16)
+        if (!ENDS && blk < a.nb16)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
                 store_frag<BF>((unsigned char*)a.ds1 + (fr * KS + s) * (512 * E), lane, S[2 * s], S[2 * s + 1]);
@@ -380,13 +391,15 @@ void k_delta_rev(RevArgs a) {
         for (int p = 0; p < KS; ++p) update(1, p);
         rpart(0);
         interleave<MT * X2, 5, 0>();
-        if (blk < a.nb16)
+        if (!ENDS && blk < a.nb16)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 store_frag<BF>((unsigned char*)a.r + (fr * 2 + s) * (512 * E), lane, r[2 * s], r[2 * s + 1]);
+        if constexpr (!ENDS) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) r[t] *= bet[t];
-        store_rows(a.dv, r, i);
+            for (int t = 0; t < 4; ++t) r[t] *= bet[t];
+            store_rows(a.dv, r, i);
+        }
         load_sc(nx);
         __builtin_amdgcn_sched_barrier(0);
         update(0, 0);
@@ -401,7 +414,15 @@ void k_delta_rev(RevArgs a) {
         if (BUF == 1) lds_barrier();
         lds_barrier();
     }
-    if (a.ds_in)
+    if constexpr (ENDS) {
+        if (blk < a.nb16)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                *reinterpret_cast<f32x4*>(a.pieces.b + ((uniform64(pc.first) + pc.s) * hv + h) * bsize + blk * (MT * 256) +
+                                          (t * 64 + lane) * 4) = S[t];
+        return;
+    }
+    if (a.ds_in && pc.s == 0)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll

@@ -62,6 +62,29 @@ def test_gradients(lens, hk, hv, dk, dv, dtype):
     check(run(d, dtype, (hk, hv, dk, dv)), D.backward(d, dk ** -0.5), dtype)
 
 
+# Long enough to be cut into pieces, with slow decays and weak writes so that states and their
+# gradients reach far. Each carry adds the roundings of two operands (2^-16) or sums of 128
+# terms, in the state's scan and in its gradient's; fp32 states also sum over ~55 chunks.
+LONG = {"bf16": dict(TOL["bf16"], dstate=math.sqrt(7 + 2 * 2) * 2 ** -16),
+        "f32": {n: 2 * (192 + 2 * 128 + 55) * 2.0 ** -24 for n in NAMES}}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [
+    ([3500], 1, 2, 64, 72),
+    ([2050], 1, 1, 128, 128),
+    ([1700, 0, 33], 1, 1, 40, 96),
+    ([70, 2500, 1999], 2, 2, 128, 40),
+])
+def test_gradients_cut_into_pieces(lens, hk, hv, dk, dv, dtype):
+    d = D.make(lens, hk, hv, dk, dv, dtype, seed=sum(lens), decay=1e-3)
+    d["beta"] = d["beta"] * 0.0625
+    got, again = (run(d, dtype, (hk, hv, dk, dv)) for _ in range(2))
+    for name, x, y, z in zip(NAMES, got, D.backward(d, dk ** -0.5), again):
+        assert D.rel(x, y) <= LONG[dtype][name], (name, D.rel(x, y))
+        assert bool((x == z).all()), name
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("use_state,use_dstate", [(False, False), (False, True), (True, False)])
 def test_without_states(dtype, use_state, use_dstate):
