@@ -281,7 +281,7 @@ struct ColTile {
 template <bool BF, int DK, int W = 1>
 struct Stage {
     static constexpr int EPL = BF ? 8 : 4, LR = DK / EPL, RI = 64 / LR, N = LR / W;
-    static_assert(W == 1 || W == 4, "shares of 16 rows: their 16-byte shifts add up");
+    static_assert(W <= 4, "shares of 16 rows or more: their 16-byte shifts add up");
     u32x4 r[N];
     __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int dk, int lane, int w = 0) {
         const uint32_t k = (lane % LR) * EPL, E = BF ? 2 : 4;

@@ -88,12 +88,15 @@ void k_delta_rev(RevArgs a) {
     const unsigned char* obase = (const unsigned char*)((const T*)a.dout + (first * hv + h) * (int64_t)dv);
     // chunks are numbered in the order they are taken: number i is chunk nch - 1 - i
     auto rows_in = [&](int i) { return i == 0 ? tail : kC; };
-    auto load_tile = [&](Stage<BF, DK>& r, const unsigned char* base, int64_t step, int64_t ld, int i) {
-        r.load(plain_buf(base + (nch - 1 - i) * step, (rows_in(i) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk,
-               lane);
+    // (numbers behind the last: the last again, staged and never read)
+    auto load_tile = [&](auto& r, const unsigned char* base, int64_t step, int64_t ld, int i, int w = 0) {
+        i = i < nch ? i : nch - 1;
+        r.load(plain_buf(base + (nch - 1 - i) * step, (rows_in(i) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk, lane,
+               w);
     };
-    auto load_o = [&](StageV& r, int i) {
-        r.load(plain_buf(obase + (nch - 1 - i) * orow, (rows_in(i) - 1) * ldo + dv * E), ldo, wgcol, dv, lane);
+    auto load_o = [&](auto& r, int i, int w) {
+        i = i < nch ? i : nch - 1;
+        r.load(plain_buf(obase + (nch - 1 - i) * orow, (rows_in(i) - 1) * ldo + dv * E), ldo, wgcol, dv, lane, w);
     };
 
     if constexpr (Cfg::STAGER)
@@ -105,20 +108,20 @@ void k_delta_rev(RevArgs a) {
                 load_tile(rk, kbase, krow, a.sh.ldk, 0);
                 rq.store(l.q[0], lane);
                 rk.store(l.k[0], lane);
-                if (nch > 1) load_tile(rq, qbase, qrow, a.sh.ldq, 1);
+                load_tile(rq, qbase, qrow, a.sh.ldq, 1);
                 lds_barrier();
                 lds_barrier();  // the first inputs are made
-                if (nch > 1) rq.store(l.q[0], lane);
-                if (nch > 1) load_tile(rk, kbase, krow, a.sh.ldk, 1);
-                if (nch > 2) load_tile(rq, qbase, qrow, a.sh.ldq, 2);
+                rq.store(l.q[0], lane);
+                load_tile(rk, kbase, krow, a.sh.ldk, 1);
+                load_tile(rq, qbase, qrow, a.sh.ldq, 2);
                 lds_barrier();
             }
             for (int i = 0; i < nch; ++i) {
                 lds_barrier();  // K of number i and Q of number i + 1 have been read
-                if (i + 1 < nch) rk.store(l.k[0], lane);
-                if (i + 2 < nch) rq.store(l.q[0], lane);
-                if (i + 2 < nch) load_tile(rk, kbase, krow, a.sh.ldk, i + 2);
-                if (i + 3 < nch) load_tile(rq, qbase, qrow, a.sh.ldq, i + 3);
+                rk.store(l.k[0], lane);
+                rq.store(l.q[0], lane);
+                load_tile(rk, kbase, krow, a.sh.ldk, i + 2);
+                load_tile(rq, qbase, qrow, a.sh.ldq, i + 3);
                 lds_barrier();
             }
             return;
@@ -192,7 +195,7 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 gf[s] = pair_frag<NS>(a.sh.scale * gam[2 * s] * o[2 * s], a.sh.scale * gam[2 * s + 1] * o[2 * s + 1], minus);
-            if (i + 1 < nch) load(i + 1);
+            load(i + 1 < nch ? i + 1 : nch - 1);
 #pragma unroll
             for (int m = 0; m < MT; m += 2) {
                 f32x4 y[2] = {};
@@ -214,52 +217,42 @@ void k_delta_rev(RevArgs a) {
                 lds_barrier();
             }
             for (int i = 0; i < nch; ++i) {
-                if (i + 1 < nch) inputs(i + 1);
+                inputs(i + 1);
                 lds_barrier();
                 lds_barrier();
             }
         } else {
-            // the first input wave also stages K (number i + 1 while the state is at i), the
-            // second Q and dO (number i + 2)
-            Stage<BF, DK> rt;
-            StageV ro;
-            const int lead = wave == NB ? 1 : 2;
-            const unsigned char* base = lead == 1 ? kbase : qbase;
-            const int64_t step = lead == 1 ? krow : qrow, ld = lead == 1 ? a.sh.ldk : a.sh.ldq;
-            Tile<NI, DK>* tile = lead == 1 ? l.k : l.q;
+            // each also stages its half of the rows: K of number i + 1 while the state is at i,
+            // Q and dO of number i + 2
+            Stage<BF, DK, NB> rk, rq;
+            StageV<NB> ro;
+            const int w = wave - NB;
+            auto stage_q = [&](int i) {
+                rq.store(l.q[i & 1], lane, w);
+                ro.store(l.o[i & 1], lane, w);
+                load_tile(rq, qbase, qrow, a.sh.ldq, i + 1, w);
+                load_o(ro, i + 1, w);
+            };
+            auto stage_k = [&](int i) {
+                rk.store(l.k[i & 1], lane, w);
+                load_tile(rk, kbase, krow, a.sh.ldk, i + 1, w);
+            };
             if (nch > 0) {
-                load_tile(rt, base, step, ld, 0);
-                if (lead == 2) load_o(ro, 0);
-                rt.store(tile[0], lane);
-                if (lead == 2) ro.store(l.o[0], lane);
-                if (nch > 1) {
-                    load_tile(rt, base, step, ld, 1);
-                    if (lead == 2) load_o(ro, 1);
-                }
+                load_tile(rq, qbase, qrow, a.sh.ldq, 0, w);
+                load_o(ro, 0, w);
+                load_tile(rk, kbase, krow, a.sh.ldk, 0, w);
+                stage_q(0);
+                stage_k(0);
                 lds_barrier();
+                stage_q(1);
                 inputs(0);
-                if (lead == 2 && nch > 1) {
-                    rt.store(tile[1], lane);
-                    ro.store(l.o[1], lane);
-                    if (nch > 2) {
-                        load_tile(rt, base, step, ld, 2);
-                        load_o(ro, 2);
-                    }
-                }
                 lds_barrier();
             }
             for (int i = 0; i < nch; ++i) {
-                const int m = i + lead;
-                if (m < nch) {
-                    rt.store(tile[m & 1], lane);
-                    if (lead == 2) ro.store(l.o[m & 1], lane);
-                }
-                if (m + 1 < nch) {
-                    load_tile(rt, base, step, ld, m + 1);
-                    if (lead == 2) load_o(ro, m + 1);
-                }
+                stage_k(i + 1);
+                stage_q(i + 2);
                 __builtin_amdgcn_sched_barrier(0);
-                if (i + 1 < nch) inputs(i + 1);
+                inputs(i + 1);
                 lds_barrier();
             }
         }

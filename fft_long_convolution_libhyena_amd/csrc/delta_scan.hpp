@@ -110,20 +110,21 @@ struct ScanCfg {
     };
     struct Lds : std::conditional<OUT, LdsOut, LdsKeep>::type, std::conditional<BF, LdsV, None>::type {};
 };
-// v of a chunk, 32 columns: 16 rows of 64 bytes an instruction
+// v of a chunk, 32 columns, by W waves: 16 rows of 64 bytes an instruction
+template <int W>
 struct StageV {
-    u32x4 r[4];
-    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int col0, int dv, int lane) {
+    u32x4 r[4 / W];
+    __device__ __forceinline__ void load(RowBuf b, uint32_t ld, int col0, int dv, int lane, int w = 0) {
         const int c = col0 + 8 * (lane & 3);
-        const uint32_t off = c < dv ? (lane >> 2) * ld + c * 2 : kNoElem;
+        const uint32_t off = c < dv ? (w * (64 / W) + (lane >> 2)) * ld + c * 2 : kNoElem;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4 / W; ++i)
             r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)(off + i * 16 * ld), 0, 0));
     }
-    __device__ __forceinline__ void store(ColTile<32>& t, int lane) const {
+    __device__ __forceinline__ void store(ColTile<32>& t, int lane, int w = 0) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x4*>(t.b + (16 * i + (lane >> 2)) * ColTile<32>::pitch + 16 * (lane & 3)) = r[i];
+        for (int i = 0; i < 4 / W; ++i)
+            *reinterpret_cast<u32x4*>(t.b + (w * (64 / W) + 16 * i + (lane >> 2)) * ColTile<32>::pitch + 16 * (lane & 3)) = r[i];
     }
 };
 
@@ -261,42 +262,39 @@ void k_delta_scan(ScanArgs a) {
     const unsigned char* vbase = (const unsigned char*)((const T*)a.v + first * a.sh.ldv + (int64_t)h * dv);
     const int wgcol = (onm ? wg - a.nbv : wg) * NB * 16;
     auto rows_in = [&](int c) { return c + 1 < nch ? kC : tail; };
-    auto load_tile = [&](Stage<BF, DK>& r, const unsigned char* base, int64_t step, int64_t ld, int c) {
-        r.load(plain_buf(base + c * step, (rows_in(c) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk, lane);
+    // (chunks behind the last: the last again, staged and never read, so that the waves that
+    // load have no branches, behind which every wait would be one for all loads)
+    auto load_tile = [&](auto& r, const unsigned char* base, int64_t step, int64_t ld, int c, int w = 0) {
+        c = c < nch ? c : nch - 1;
+        r.load(plain_buf(base + c * step, (rows_in(c) - 1) * (uint32_t)(ld * E) + dk * E), (uint32_t)(ld * E), dk, lane, w);
     };
-    auto load_vt = [&](StageV& r, int c) {
+    auto load_vt = [&](auto& r, int c, int w = 0) {
+        c = c < nch ? c : nch - 1;
         r.load(plain_buf(vbase + c * vrow, (rows_in(c) - 1) * (uint32_t)(a.sh.ldv * E) + dv * E), (uint32_t)(a.sh.ldv * E), wgcol,
-               dv, lane);
+               onm ? 0 : dv, lane, w);
     };
     if constexpr (Cfg::STAGER)
         if (wave == waves_of<Cfg>() - 1) {
             Stage<BF, DK> rk, rq;
-            StageV rv;
+            StageV<1> rv;
             if (nch > 0) {
                 load_tile(rk, kbase, krow, a.sh.ldk, 0);
                 if constexpr (BF) load_vt(rv, 0);
                 rk.store(l.k[0], lane);
                 if constexpr (BF) rv.store(l.v[0], lane);
-                if (nch > 1) {
-                    load_tile(rk, kbase, krow, a.sh.ldk, 1);
-                    if constexpr (BF) load_vt(rv, 1);
-                }
+                load_tile(rk, kbase, krow, a.sh.ldk, 1);
+                if constexpr (BF) load_vt(rv, 1);
                 if constexpr (OUT) load_tile(rq, qbase, qrow, a.sh.ldq, 0);
                 lds_barrier();
             }
             for (int c = 0; c < nch; ++c) {
                 if (BUF == 1) lds_barrier();  // K of chunk c and Q of chunk c - 1 have been read
-                if (c + 1 < nch) {
-                    rk.store(l.k[(c + 1) & (BUF - 1)], lane);
-                    if constexpr (BF) rv.store(l.v[(c + 1) & (BUF - 1)], lane);
-                }
+                rk.store(l.k[(c + 1) & (BUF - 1)], lane);
+                if constexpr (BF) rv.store(l.v[(c + 1) & (BUF - 1)], lane);
                 if constexpr (OUT) rq.store(l.q[c & (BUF - 1)], lane);
-                if (c + 2 < nch) {
-                    load_tile(rk, kbase, krow, a.sh.ldk, c + 2);
-                    if constexpr (BF) load_vt(rv, c + 2);
-                }
-                if constexpr (OUT)
-                    if (c + 1 < nch) load_tile(rq, qbase, qrow, a.sh.ldq, c + 1);
+                load_tile(rk, kbase, krow, a.sh.ldk, c + 2);
+                if constexpr (BF) load_vt(rv, c + 2);
+                if constexpr (OUT) load_tile(rq, qbase, qrow, a.sh.ldq, c + 1);
                 lds_barrier();
             }
             return;
@@ -380,40 +378,36 @@ void k_delta_scan(ScanArgs a) {
                     outputs(c);
                 }
             } else {
-                // the first outputs' wave also stages K and v (chunk c + 1 while the state is at
-                // c), the second Q (chunk c)
-                Stage<BF, DK> rt;
-                StageV rv;
-                const int lead = wave == NB ? 1 : 0;
-                const unsigned char* base = lead ? kbase : qbase;
-                const int64_t step = lead ? krow : qrow, ld = lead ? a.sh.ldk : a.sh.ldq;
-                Tile<NI, DK>* tile = lead ? l.k : l.q;
+                // each also stages its half of the rows: K and v of chunk c + 1 while the state is
+                // at c, Q of chunk c
+                Stage<BF, DK, NB> rk, rq;
+                StageV<NB> rv;
+                const int w = wave - NB;
+                auto stage = [&](int c) {
+                    __builtin_amdgcn_s_sleep(kOutSleep);
+                    rk.store(l.k[(c + 1) & 1], lane, w);
+                    rv.store(l.v[(c + 1) & 1], lane, w);
+                    rq.store(l.q[c & 1], lane, w);
+                    load_tile(rk, kbase, krow, a.sh.ldk, c + 2, w);
+                    load_vt(rv, c + 2, w);
+                    load_tile(rq, qbase, qrow, a.sh.ldq, c + 1, w);
+                    __builtin_amdgcn_sched_barrier(0);
+                };
                 if (nch > 0) {
-                    load_tile(rt, base, step, ld, 0);
-                    if (lead) {
-                        load_vt(rv, 0);
-                        rt.store(tile[0], lane);
-                        rv.store(l.v[0], lane);
-                        if (nch > 1) {
-                            load_tile(rt, base, step, ld, 1);
-                            load_vt(rv, 1);
-                        }
-                    }
+                    load_tile(rk, kbase, krow, a.sh.ldk, 0, w);
+                    load_vt(rv, 0, w);
+                    rk.store(l.k[0], lane, w);
+                    rv.store(l.v[0], lane, w);
+                    load_tile(rk, kbase, krow, a.sh.ldk, 1, w);
+                    load_vt(rv, 1, w);
+                    load_tile(rq, qbase, qrow, a.sh.ldq, 0, w);
+                    lds_barrier();
+                    stage(0);
                     lds_barrier();
                 }
-                for (int c = 0; c < nch; ++c) {
-                    const int m = c + lead;
-                    __builtin_amdgcn_s_sleep(kOutSleep);
-                    if (m < nch) {
-                        rt.store(tile[m & 1], lane);
-                        if (lead) rv.store(l.v[m & 1], lane);
-                    }
-                    if (m + 1 < nch) {
-                        load_tile(rt, base, step, ld, m + 1);
-                        if (lead) load_vt(rv, m + 1);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (c > 0) outputs(c - 1);
+                for (int c = 1; c < nch; ++c) {
+                    stage(c);
+                    outputs(c - 1);
                     lds_barrier();
                 }
                 if (nch > 0) outputs(nch - 1);
@@ -461,9 +455,8 @@ void k_delta_scan(ScanArgs a) {
     Stage<BF, DK, Cfg::SELF ? 4 : 1> rk;
     StageV4 rv;
     auto self_load = [&](int c) {
-        rk.load(plain_buf(kbase + c * krow, (rows_in(c) - 1) * (uint32_t)(a.sh.ldk * E) + dk * E), (uint32_t)(a.sh.ldk * E), dk,
-                lane, wave);
-        rv.load(vbuf(c), ldv, wgcol, onm ? 0 : dv, lane, wave);
+        load_tile(rk, kbase, krow, a.sh.ldk, c, wave);
+        load_vt(rv, c, wave);
     };
     auto self_store = [&](int c) {
         if constexpr (Cfg::SELF) {
@@ -475,7 +468,7 @@ void k_delta_scan(ScanArgs a) {
         if constexpr (Cfg::SELF) {
             self_load(0);
             self_store(0);
-            self_load(nch > 1 ? 1 : 0);
+            self_load(1);
         }
         const RowBuf vb = vbuf(0), rb = plain_buf(rec, Rec<BF>::bytes);
 #pragma unroll
@@ -534,9 +527,9 @@ void k_delta_scan(ScanArgs a) {
                 for (int f = s * kTri / KS; f < (s + 1) * kTri / KS; ++f) load_t(Tn, rb, f);
             }
             if constexpr (Cfg::SELF)
-                if (s == KS - 1) {  // no branches: the last chunks store and load one that is not read
+                if (s == KS - 1) {
                     self_store(c + 1);
-                    self_load(c + 2 < nch ? c + 2 : nch - 1);
+                    self_load(c + 2);
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
