@@ -134,14 +134,6 @@ __device__ __forceinline__ void mma_tiles(const Frag<NA> (&a)[J], const Frag<NB>
                     c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j].p[i], b.p[k], c[j], 0, 0, 0);
         }
 }
-template <int N, int M>
-__device__ __forceinline__ Frag<N> first_parts(const Frag<M>& f) {
-    Frag<N> r;
-#pragma unroll
-    for (int n = 0; n < N; ++n) r.p[n] = f.p[n];
-    return r;
-}
-
 // eight consecutive elements as fp32 / as an operand; zeros where !ok
 __device__ __forceinline__ void load8(const __bf16* p, bool ok, float (&x)[8]) {
     bf16x8 v = {};
@@ -168,19 +160,6 @@ struct Raw16 {
 struct Raw32 {
     f32x4 lo, hi;
 };
-__device__ __forceinline__ Raw16 load_raw(const __bf16* p, bool ok) {
-    Raw16 r = {};
-    if (ok) r.v = *reinterpret_cast<const bf16x8*>(p);
-    return r;
-}
-__device__ __forceinline__ Raw32 load_raw(const float* p, bool ok) {
-    Raw32 r = {};
-    if (ok) {
-        r.lo = *reinterpret_cast<const f32x4*>(p);
-        r.hi = *reinterpret_cast<const f32x4*>(p + 4);
-    }
-    return r;
-}
 __device__ __forceinline__ Frag<1> to_frag(const Raw16& r) { return Frag<1>{{r.v}}; }
 __device__ __forceinline__ Frag<3> to_frag(const Raw32& r) {
     const float x[8] = {r.lo[0], r.lo[1], r.lo[2], r.lo[3], r.hi[0], r.hi[1], r.hi[2], r.hi[3]};
@@ -328,90 +307,17 @@ __device__ __forceinline__ Frag<N> buf_frag(RowBuf b, int at, int f, int lane) {
     return r;
 }
 
-// N (1 or 2) consecutive elements: raw registers, their values, and back
-template <bool BF, int N>
-struct Cols {
-    uint32_t w[BF ? 1 : N];
-};
-template <bool BF, int N>
-__device__ __forceinline__ void buf_cols(RowBuf b, uint32_t off, Cols<BF, N>& c) {
-    if constexpr (BF && N == 1)
-        c.w[0] = __builtin_amdgcn_raw_buffer_load_b16(b, (int)off, 0, 0);
-    else if constexpr (!BF && N == 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, (int)off, 0, 0));
-        c.w[0] = v[0];
-        c.w[1] = v[1];
-    } else
-        c.w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0);
-}
-template <bool BF, int N>
-__device__ __forceinline__ float col_value(const Cols<BF, N>& c, int j) {
-    if constexpr (BF) return __uint_as_float(j == 0 ? c.w[0] << 16 : c.w[0] & 0xffff0000u);
-    return __uint_as_float(c.w[BF ? 0 : j]);
-}
-template <bool BF, int N>
-__device__ __forceinline__ void buf_store(RowBuf b, uint32_t off, const float (&x)[N]) {
-    if constexpr (BF) {
-        typedef __bf16 bf16xn __attribute__((ext_vector_type(N)));
-        bf16xn v;
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = (__bf16)x[j];
-        if constexpr (N == 2)
-            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, (int)off, 0, 0);
-        else
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), b, (int)off, 0, 0);
-    } else if constexpr (N == 2) {
-        const u32x2 v = {__float_as_uint(x[0]), __float_as_uint(x[1])};
-        __builtin_amdgcn_raw_buffer_store_b64(v, b, (int)off, 0, 0);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), b, (int)off, 0, 0);
-    }
+template <bool BF>
+__device__ __forceinline__ void buf_store(RowBuf b, uint32_t off, float x) {
+    if constexpr (BF)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)x), b, (int)off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, (int)off, 0, 0);
 }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
     const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
     return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-// N (1 or 2) consecutive elements
-template <int N>
-__device__ __forceinline__ void load_cols(const __bf16* p, bool ok, float (&x)[N]) {
-    if constexpr (N == 2) {
-        uint32_t v = 0;
-        if (ok) v = *reinterpret_cast<const uint32_t*>(p);
-        x[0] = __uint_as_float(v << 16);
-        x[1] = __uint_as_float(v & 0xffff0000u);
-    } else {
-        x[0] = ok ? (float)p[0] : 0.f;
-    }
-}
-template <int N>
-__device__ __forceinline__ void load_cols(const float* p, bool ok, float (&x)[N]) {
-    if constexpr (N == 2) {
-        float2 v = make_float2(0.f, 0.f);
-        if (ok) v = *reinterpret_cast<const float2*>(p);
-        x[0] = v.x;
-        x[1] = v.y;
-    } else {
-        x[0] = ok ? p[0] : 0.f;
-    }
-}
-template <int N>
-__device__ __forceinline__ void store_cols(__bf16* p, const float (&x)[N]) {
-    if constexpr (N == 2) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        bf16x2 v = {(__bf16)x[0], (__bf16)x[1]};
-        *reinterpret_cast<bf16x2*>(p) = v;
-    } else {
-        p[0] = (__bf16)x[0];
-    }
-}
-template <int N>
-__device__ __forceinline__ void store_cols(float* p, const float (&x)[N]) {
-    if constexpr (N == 2)
-        *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
-    else
-        p[0] = x[0];
 }
 
 template <int N>
@@ -440,11 +346,6 @@ __device__ __forceinline__ void interleave() {
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
-
-// fragment number of block (row tile i, 32-column step s) of a lower / upper
-// block-triangular operand
-__device__ __forceinline__ constexpr int lower_frag(int i, int s) { return i < 2 ? i : 2 + (i - 2) * 2 + s; }
-__device__ __forceinline__ constexpr int upper_frag(int i, int s) { return i < 2 ? 2 * i + s : 2 + i; }
 
 // ---------------------------------------------------------------- sequences
 struct Seqs {

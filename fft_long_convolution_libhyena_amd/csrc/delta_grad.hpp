@@ -393,9 +393,8 @@ void k_delta_grad(GradArgs a) {
         for (int i = 0; i < 4; ++i) {
             const int k = 16 * m + col;
             const uint32_t off = k < dk ? (16 * w + 4 * g + i) * ldd + k * E : kNoElem;
-            const float x[1] = {dq[m][i]}, y[1] = {dkk[m][i]};
-            buf_store<BF, 1>(qo, off, x);
-            buf_store<BF, 1>(ko, off, y);
+            buf_store<BF>(qo, off, dq[m][i]);
+            buf_store<BF>(ko, off, dkk[m][i]);
         }
 }
 

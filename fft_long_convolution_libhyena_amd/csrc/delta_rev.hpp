@@ -303,8 +303,7 @@ void k_delta_rev(RevArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float x[1] = {y[t][j]};
-                buf_store<BF, 1>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + j) * ldo, x);
+                buf_store<BF>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + j) * ldo, y[t][j]);
             }
     };
     if (nch > 0) {

@@ -48,10 +48,7 @@ enum { kScanOut = 0, kScanKeep = 1, kScanEnds = 2 };
 
 // The outputs' waves rest for this many 64-clock units after a barrier, while the state
 // waves read K: both at once would halve the state's LDS rate where it waits for it.
-#ifndef HY_SLEEP
-#define HY_SLEEP 8
-#endif
-constexpr int kOutSleep = HY_SLEEP;
+constexpr int kOutSleep = 8;
 
 // Minus the identity, as left operands that take rows of a 32-row operand back to the
 // result tile (t even or odd) they came from.
@@ -316,8 +313,7 @@ void k_delta_scan(ScanArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x[1] = {y[t][i]};
-                buf_store<BF, 1>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + i) * ldo, x);
+                buf_store<BF>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + i) * ldo, y[t][i]);
             }
         op += (int64_t)kC * ldo;
     };
@@ -423,14 +419,22 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = drow(t, i);
-            S[t][i] = ps == 0 && a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
+            S[t][i] = ps == 0 && (ENDS || pc.count == 1) && a.s_in && k < dk && cok ? a.s_in[((n * hv + h) * dk + k) * dv + c0] : 0.f;
             if (onm) S[t][i] = k == c0 ? 1.f : 0.f;
         }
-    // ends of the piece in front: [slot][head] sized records
+    // A cut sequence's initial state goes to its first piece by way of the last one's unused
+    // record: the last piece may have written the final state in its place by then.
     const int64_t bsize = (int64_t)a.nb16 * MT * 256, msize = DK * DK * NS * 2;
-    if (!ENDS && ps > 0 && blk < a.nb16)
-        carry<NS, DK>(S, a.pieces.b + (pslot * hv + h) * bsize + blk * (MT * 256), hv * bsize, a.pieces.m + (pslot * hv + h) * msize,
-                      hv * msize, ps - 1, lane, minus);
+    float* bp = a.pieces.b + (pslot * hv + h) * bsize + blk * (MT * 256);  // the first piece's
+    const int64_t spare = (pc.count - 1) * (hv * bsize);
+    if (pc.count > 1 && !onm && blk < a.nb16) {
+        if (!ENDS)
+            carry<NS, DK>(S, ps > 0 ? bp : bp + spare, hv * bsize, a.pieces.m + (pslot * hv + h) * msize, hv * msize, ps - 1, lane,
+                          minus);
+        else if (ps == 0)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(bp + spare + (t * 64 + lane) * 4) = S[t];
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s) sf[s] = pair_frag<NS>(S[2 * s], S[2 * s + 1], minus);
 
@@ -640,14 +644,14 @@ void k_delta_scan(ScanArgs a) {
     }
     if (c < nch) chunk(c, Tab[0], Tab[BF ? 1 : 0]);
     if constexpr (ENDS) {
-        const int64_t at = (pslot + ps) * hv + h;
         if (!onm) {
             if (blk < a.nb16)
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
-                    *reinterpret_cast<f32x4*>(a.pieces.b + at * bsize + blk * (MT * 256) + (t * 64 + lane) * 4) = S[t];
+                    *reinterpret_cast<f32x4*>(bp + ps * (hv * bsize) + (t * 64 + lane) * 4) = S[t];
         } else if (c0 < DK) {
-            store_end<NS, DK>(a.pieces.m + at * msize, a.pieces.mt ? a.pieces.mt + at * msize : nullptr, S, c0, lane);
+            const int64_t at = ((pslot + ps) * hv + h) * msize;
+            store_end<NS, DK>(a.pieces.m + at, a.pieces.mt ? a.pieces.mt + at : nullptr, S, c0, lane);
         }
         return;
     }

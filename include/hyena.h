@@ -1,8 +1,10 @@
 /*
  * libhyena — the Hyena operator forward hot path, its backward, the whole
- * operator forward, the implicit filter generator, and the HyenaND variants
- * (per-sample filters, circular plans, gated 2-D and 3-D long convolutions), on
- * AMD MI355X (gfx950).
+ * operator forward, the implicit filter generator, the HyenaND variants
+ * (per-sample filters, circular plans, gated 2-D and 3-D long convolutions), and for
+ * layers that mix Hyena with linear attention the gated delta rule (whole sequences,
+ * its backward, single tokens against a pool of states) and the norm of queries and
+ * keys with position rotation, on AMD MI355X (gfx950).
  *
  * The operator (HyenaDNA walkthrough, section 2.1, the Hyena operator module and
  * its forward pass; section 2.2, the long-filter module and its FFT convolution).
@@ -667,8 +669,8 @@ typedef struct hyena_delta_inputs_s {
     const void* beta;
 } hyena_delta_inputs_t;
 
-/* Bytes of workspace hyena_delta_forward needs (chunks of 64 tokens: their
- * triangular factors, decays and transposed keys). Returns 0 for arguments that
+/* Bytes of workspace hyena_delta_forward needs (the triangular factors and decays of
+ * chunks of 64 tokens; states between the pieces of long sequences). Returns 0 for arguments that
  * the call would refuse, and where there are no tokens. seq_start is not read:
  * only whether it is NULL matters. */
 size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
@@ -684,9 +686,11 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
  * The state is held in fp32 from the first token to the last; bf16 outputs are
  * rounded once from sums whose operands are bf16 or sums of two bf16 parts, fp32
  * results have the accuracy of fp32 products. Decays below exp(-200) count as 0 and
- * g = -inf resets the state. Results do not depend on the other sequences of the
- * call, bit for bit when the sequence starts at the same offset within 64 tokens or
- * not. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
+ * g = -inf resets the state. Every sum has a fixed order: results are bitwise
+ * reproducible, and those of a sequence of up to 1536 tokens do not depend on the other
+ * sequences of the call. Longer ones are cut into pieces that run side by side where the
+ * call has few (sequence, head) pairs; how is a rule on the sizes, N and tokens among
+ * them, and another cut may round differently. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, heads_v not
  * a multiple of heads_k, bad ld or scale), HYENA_ERR_UNSUPPORTED (dims outside the
  * ranges above, heads_v > 65535, N > 2^24, tokens > 2^31, or more than 2^30 (chunk,

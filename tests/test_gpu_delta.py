@@ -85,6 +85,24 @@ def test_forward_cut_into_pieces(lens, packed, hk, hv, dk, dv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cut_sequences_keep_their_state_in_place(dtype):
+    """A cut sequence's first piece and its last both meet the state's memory."""
+    lens, hk, hv, dk, dv = [2000, 1900], 1, 2, 64, 64
+    d = D.make(lens, hk, hv, dk, dv, dtype, seed=12, decay=1e-3)
+    d["beta"] = d["beta"] * 0.0625
+    g = on_gpu(d)
+    args, start = [g[n] for n in ("q", "k", "v", "g", "beta")], D.starts(lens, "cuda")
+    r = rule(d, hk, hv, dk, dv, dtype)
+    o, s = r.forward(*args, state=g["state"], seq_start=start)
+    st = g["state"].clone()
+    o2, s2 = r.forward(*args, state=st, seq_start=start, state_out=st)
+    ro, rs = D.forward(d, dk ** -0.5)
+    assert s2.data_ptr() == st.data_ptr()
+    assert bool((o == o2).all()) and bool((s == s2).all())
+    assert D.rel(s, rs) <= TOL_LONG[dtype] and D.rel(o, ro) <= max(TOL_O[dtype], TOL_LONG[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T", [(1, 1), (2, 100), (3, 257), (2, 0)])
 def test_forward_batch_without_state(B, T, dtype):
     hk, hv, dk, dv = 2, 4, 64, 72
