@@ -714,7 +714,7 @@ size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, 
  *   [tokens][heads_v] of the dtype, rounded once from fp32 sums (over the value heads
  *   that share a key head, too); dstate_in [N][heads_v][dim_k][dim_v] fp32, or NULL.
  * The states are computed again from the inputs; nothing of the forward call is kept.
- * bf16 calls round the operands of the chunk-parallel products (the states and their
+ * bf16 calls round operands of the chunk-parallel products (the states and their
  * gradients at chunk borders, u, r) to bf16, the states themselves stay fp32 along
  * both scans. Every sum has a fixed order: results are bitwise reproducible. Rows
  * that belong to no sequence are left as they were. Arguments, workspace (of at least
