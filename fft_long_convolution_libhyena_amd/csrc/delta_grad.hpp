@@ -307,41 +307,45 @@ void k_delta_grad(GradArgs a) {
                 qqs[i] = fmaf(l.q.get(ti + i, 16 * m + col), qs[m][i], qqs[i]);
                 krs[i] = fmaf(kv, rs[m][i], krs[i]);
                 kus[i] = fmaf(kv, us[m][i], kus[i]);
+                if (i == 3) __builtin_amdgcn_sched_barrier(0);
             }
+        qqs = row_sum(qqs);
+        krs = row_sum(krs);
+        kus = row_sum(kus);
         const f32x4 gam = *reinterpret_cast<const f32x4*>(l.gam + ti), kap = *reinterpret_cast<const f32x4*>(l.kap + ti);
         const f32x4 bet = *reinterpret_cast<const f32x4*>(l.bet + ti);
+        // no branches around single elements: their decays are formed everywhere and selected
         float cx[4] = {};
+        double Gi[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 4; ++i) Gi[i] = l.G[ti + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j > w) continue;  // dp and z are zero there
+            const int tj = 16 * j + col;
+            const double Gj = l.G[tj];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int tj = 16 * j + col;
-                float wv = 0.f, mv = 0.f;
-                if (j <= w && tj <= ti + i) {
-                    const float d = decay(l.G[ti + i] - l.G[tj]);
-                    wv = a.sh.scale * d * dp[j][i];
-                    float x = wv * qk[j][i];
-                    if (tj < ti + i) {
-                        const float dz = d * z[j][i];
-                        mv = -bet[i] * dz;
-                        dbz[i] = fmaf(-dz, kk[j][i], dbz[i]);
-                        x = fmaf(mv, kk[j][i], x);
-                    }
-                    rx[i] += x;
-                    cx[j] += x;
-                }
+                const float e = decay(Gi[i] - Gj);
+                const float d = tj <= ti + i ? e : 0.f, ds = tj < ti + i ? e : 0.f;
+                const float wv = tj <= ti + i ? a.sh.scale * d * dp[j][i] : 0.f;
+                const float dz = tj < ti + i ? ds * z[j][i] : 0.f;
+                const float mv = -bet[i] * dz;
+                dbz[i] = fmaf(-dz, kk[j][i], dbz[i]);
+                const float x = fmaf(mv, kk[j][i], wv * qk[j][i]);
+                rx[i] += x;
+                cx[j] += x;
                 dp[j][i] = wv;
                 z[j][i] = mv;
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             cx[j] += __shfl_xor(cx[j], 16);
             cx[j] += __shfl_xor(cx[j], 32);
             if (g == 0) l.cs[w][16 * j + col] = cx[j];
         }
-        qqs = row_sum(qqs);
-        krs = row_sum(krs);
-        kus = row_sum(kus);
         rx = row_sum(rx);
         dbz = row_sum(dbz);
         if (col == 0) {
@@ -363,14 +367,8 @@ void k_delta_grad(GradArgs a) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int tj = 16 * j + col;
-                l.mat.w.put(ti + i, tj, dp[j][i]);
-                if (tj < ti + i) {
-                    l.mat.n.put(ti + i, tj, z[j][i]);
-                    l.mat.n.put(tj, ti + i, z[j][i]);
-                } else if (tj == ti + i) {
-                    l.mat.n.put(tj, tj, 0.f);
-                }
+                l.mat.w.put(ti + i, 16 * j + col, dp[j][i]);
+                l.mat.n.put(ti + i, 16 * j + col, z[j][i]);
             }
         __syncthreads();
         if (w == 0) {
@@ -396,30 +394,43 @@ void k_delta_grad(GradArgs a) {
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const auto na = l.mat.n.rows(lane, w, s);
-            const auto wa = l.mat.w.rows(lane, w, s);
-            const auto wt = l.mat.w.cols(lane, w, s);
+            const auto na = l.mat.n.rows(lane, w, s), wa = l.mat.w.rows(lane, w, s);
+            const auto nt = l.mat.n.cols(lane, w, s), wt = l.mat.w.cols(lane, w, s);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const auto kc = l.k.cols(lane, m, s);
-                if (2 * s <= w) dq[m] = mma(wa, kc, dq[m]);
-                dkk[m] = mma(na, kc, dkk[m]);
-                if (2 * s + 1 >= w) dkk[m] = mma(wt, l.q.cols(lane, m, s), dkk[m]);
+                if (2 * s <= w) {
+                    dq[m] = mma(wa, kc, dq[m]);
+                    dkk[m] = mma(na, kc, dkk[m]);
+                }
+                if (2 * s + 1 >= w) {
+                    dkk[m] = mma(nt, kc, dkk[m]);
+                    dkk[m] = mma(wt, l.q.cols(lane, m, s), dkk[m]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
-    const uint32_t ldd = (uint32_t)(a.sh.hk * dk) * E;
-    const RowBuf qo = row_buf((T*)a.dq + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
-    const RowBuf ko = row_buf((T*)a.dk + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
+    // whole rows out, through the tiles of K and Q: 16 bytes a lane in place of single elements
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = 16 * m + col;
-            const uint32_t off = k < dk ? (16 * w + 4 * g + i) * ldd + k * E : kNoElem;
-            buf_store<BF>(qo, off, dq[m][i]);
-            buf_store<BF>(ko, off, dkk[m][i]);
+            l.q.put(16 * w + 4 * g + i, 16 * m + col, dq[m][i]);
+            l.k.put(16 * w + 4 * g + i, 16 * m + col, dkk[m][i]);
         }
+    __syncthreads();
+    const uint32_t ldd = (uint32_t)(a.sh.hk * dk) * E;
+    const RowBuf qo = row_buf((T*)a.dq + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
+    const RowBuf ko = row_buf((T*)a.dk + (tok * a.sh.hk + hk) * (int64_t)dk, rows, ldd, dk * E);
+#pragma unroll
+    for (int e = 0; e < kC * (DK / V) / kThreads; ++e) {
+        const int x = e * kThreads + tid, t = x / (DK / V), k = x % (DK / V) * V;
+        const uint32_t off = k < dk ? t * ldd + k * E : kNoElem;
+        __builtin_amdgcn_raw_buffer_store_b128(*l.q.at16(t, k), qo, (int)off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(*l.k.at16(t, k), ko, (int)off, 0, 0);
+    }
 }
 
 }  // namespace delta
