@@ -131,20 +131,26 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
                 }
         }
         __syncthreads();  // K has been read: P takes its place
+        // no branches around single elements: their decays are formed everywhere and selected
+        const int t0 = 16 * wave + 4 * g;
+        double Gi[4];
+        float bi[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 4; ++i) {
+            Gi[i] = l.G[t0 + i];
+            bi[i] = l.beta[t0 + i];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int tj = 16 * j + col;
+            const double Gj = l.G[tj];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int ti = 16 * wave + 4 * g + i, tj = 16 * j + col;
-                float av = 0.f, pv = 0.f;
-                if (tj <= ti) {
-                    const float d = decay(l.G[ti] - l.G[tj]);
-                    pv = d * qk[j][i];
-                    if (tj < ti) av = l.beta[ti] * d * kk[j][i];
-                }
-                l.a[ti][tj] = av;
-                l.p[ti][tj] = pv;
+                const float d = decay(Gi[i] - Gj);
+                l.a[t0 + i][tj] = tj < t0 + i ? bi[i] * d * kk[j][i] : 0.f;
+                l.p[t0 + i][tj] = tj <= t0 + i ? d * qk[j][i] : 0.f;
             }
+        }
     }
     __syncthreads();
     if (!BWD)
