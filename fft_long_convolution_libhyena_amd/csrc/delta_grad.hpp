@@ -11,6 +11,10 @@
 //   dG_last += sum_i exp(G_last - G_i) k_i . (u dS1^T)_i + exp(G_last) <dS1, S0>,
 // and dg_t is the sum of dG_i over i >= t. (dbeta uses r itself, not beta r, so beta = 0
 // has its gradient.)
+// A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO, v,
+// u, r and the states' columns, the next step's loads in flight); wave w has rows 16 w of
+// every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
+// 8192 tokens, 6 heads of 128 x 128, bf16, 306 us (1235 MB, 4.1 TB/s).
 #pragma once
 #include "delta.hpp"
 

@@ -8,7 +8,11 @@
 // block of 16 columns, in whose registers dS stays (fp32, operands as bf16 parts), and
 // here an input wave a block, one chunk ahead, that makes what does not depend on dS
 // (P^T dO and Q^T diag(exp(G)) dO) and hands it over in LDS as fp32. The input waves of
-// bf16 calls also stage K, Q and dO; fp32 calls have a staging wave.
+// bf16 calls also stage K, Q and dO, half the rows each; fp32 calls have a staging wave.
+// Measured as the forward's scan: 358 us, 2.8 us a chunk (2.4 TB/s, matrix pipes 19%). Without
+// its stores 264, without its inputs too 259, the input waves alone 183: chain and stores
+// bound it. Stores from the input waves (results handed back in LDS) took 358 to 386, T^T a
+// chunk ahead in alternating registers 365.
 #pragma once
 #include "delta_scan.hpp"
 

@@ -1,9 +1,12 @@
 // The state scan of the gated delta rule. A workgroup carries NB blocks of 16 columns of
-// one (sequence, value head)'s state through its chunks; three kinds of waves share it:
+// one (sequence, value head)'s state through its chunks, or through those of a piece of the
+// sequence; three kinds of waves share it:
 //   state     one wave a block: e, u and the new state, all in its registers
 //   outputs   one wave a block, a chunk behind: o = scale (exp(G) Q S + P u)
-//   staging   brings K, Q (and bf16 v) of the next chunks into LDS: the two outputs'
-//             waves beside their work (bf16), or a wave of its own
+//   staging   brings K, Q (and bf16 v) of the next chunks into LDS: the outputs' waves, half
+//             the rows each (bf16), or a wave of its own
+// The scan that keeps states for the backward has no outputs, and the one that makes the
+// ends of pieces has only state waves, four a workgroup, which also stage (bf16).
 // The state is fp32 with its bf16 parts beside it as right-hand operands. With rows
 // numbered as in tile_row, every result of a chunk (the residual e, the written values u,
 // the new state) becomes the next product's operand in the lane that holds it: nothing on
@@ -14,11 +17,12 @@
 //
 // What bounds it: a state wave is alone on its SIMD, so its instructions (82 matrix, about
 // 300 vector for a chunk of a 128 x 16 block) run in order, matrix and vector ones
-// alternating; the chain over the chunks is sequential. Measured on the way, one chunk of
-// 64 tokens, 128 x 128 heads, bf16: tokens and state rows split over four waves, operands
-// exchanged in LDS with three barriers, 2.3 us for 32 columns; each wave loading K, Q and
-// K^T for itself, 2.0 us for 16 columns (a load of 16 rows of 64 bytes costs 60 clocks,
-// one of 1 KiB in a row 16).
+// alternating; the chain over the chunks is sequential. Measured, 8 sequences of 8192 tokens,
+// 6 heads of 128 x 128, bf16: 248 us, 1.9 us a chunk (192 workgroups on 256 CUs; 2.1 TB/s;
+// matrix pipes busy 29% of the CUs' cycles); keeping states 250 us. On the way, for a chunk:
+// tokens and state rows split over four waves, operands exchanged in LDS with three barriers,
+// 2.3 us for 32 columns; each wave loading K, Q and K^T for itself, 2.0 us for 16 columns (a
+// load of 16 rows of 64 bytes costs 60 clocks, one of 1 KiB in a row 16).
 #pragma once
 #include <type_traits>
 
@@ -47,7 +51,8 @@ struct ScanArgs {
 enum { kScanOut = 0, kScanKeep = 1, kScanEnds = 2 };
 
 // The outputs' waves rest for this many 64-clock units after a barrier, while the state
-// waves read K: both at once would halve the state's LDS rate where it waits for it.
+// waves read K: both at once would halve the state's LDS rate where it waits for it (8
+// sequences of 8192 tokens: 341 us without the rest, 318 with it).
 constexpr int kOutSleep = 8;
 
 // Minus the identity, as left operands that take rows of a 32-row operand back to the
