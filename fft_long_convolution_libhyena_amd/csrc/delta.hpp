@@ -12,10 +12,12 @@
 // Every product runs on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16) with fp32
 // accumulation. An fp32 value enters as a sum of bf16 parts (x = h1 + h2 + ..., each
 // the rounding of what the ones before it leave): two parts hold 16 bits, three 24.
-// bf16 plans give their inputs exactly in one part and carry the state, T and the
-// written values in two (relative error of the fp32 state measured 3e-6; one part
-// would leave 2e-3); fp32 plans use three parts throughout (1e-7), at 6 products for
-// each single one, still 2.7 times the rate of the fp32 matrix instruction.
+// bf16 plans give their inputs exactly in one part and carry the state and T in two; the
+// residuals and what a chunk adds to the state have three (relative error of the fp32
+// state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). Two also serve the
+// states between the pieces of cut sequences and, in the backward, dS and all that leads
+// to it. fp32 plans use three parts throughout (1e-7), at 6 products for each single one,
+// still 2.7 times the rate of the fp32 matrix instruction.
 //
 // Fragment layouts of v_mfma_f32_16x16x32_bf16, lane l, g = l / 16:
 //   A [16][32]: lane holds row l % 16, columns 8g .. 8g+7
@@ -50,6 +52,7 @@ struct Io<true> {
     using T = __bf16;
     static constexpr int NI = 1;  // parts of an input operand (exact)
     static constexpr int NS = 2;  // parts of the state, T and the written values
+    static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state
     static constexpr int NO = 2;  // parts of the state and of u against Q and P
     static constexpr int NP = 1;  // parts of P
 };
@@ -58,6 +61,7 @@ struct Io<false> {
     using T = float;
     static constexpr int NI = 3;
     static constexpr int NS = 3;
+    static constexpr int NE = 3;
     static constexpr int NO = 3;
     static constexpr int NP = 3;
 };

@@ -15,11 +15,12 @@
 // decays come as the preparation laid them out, 1 KiB a load, a chunk ahead. One barrier a
 // chunk (two where LDS holds one buffer of K and Q only: fp32, three parts).
 //
-// What bounds it: a state wave is alone on its SIMD, so its instructions (82 matrix, about
+// What bounds it: a state wave is alone on its SIMD, so its instructions (134 matrix, about
 // 300 vector for a chunk of a 128 x 16 block) run in order, matrix and vector ones
 // alternating; the chain over the chunks is sequential. Measured, 8 sequences of 8192 tokens,
-// 6 heads of 128 x 128, bf16: 248 us, 1.9 us a chunk (192 workgroups on 256 CUs; 2.1 TB/s;
-// matrix pipes busy 29% of the CUs' cycles); keeping states 250 us. On the way, for a chunk:
+// 6 heads of 128 x 128, bf16: 280 us, 2.2 us a chunk (192 workgroups on 256 CUs; 1.9 TB/s;
+// matrix pipes busy 29% of the CUs' cycles), 248 with residuals in two parts as the scan that
+// keeps states has them (250). On the way, for a chunk:
 // tokens and state rows split over four waves, operands exchanged in LDS with three barriers,
 // 2.3 us for 32 columns; each wave loading K, Q and K^T for itself, 2.0 us for 16 columns (a
 // load of 16 rows of 64 bytes costs 60 clocks, one of 1 KiB in a row 16).
@@ -228,7 +229,9 @@ void k_delta_scan(ScanArgs a) {
     using Cfg = ScanCfg<BF, DK, MODE>;
     constexpr bool OUT = Cfg::OUT, ENDS = Cfg::ENDS;
     constexpr int KS = DK / 32, MT = DK / 16, NB = Cfg::NB, BUF = Cfg::BUF;
-    constexpr int NI = IO::NI, NS = IO::NS, NP = IO::NP, NO = IO::NO;
+    // states kept for the backward are rounded to the element type, those at the ends of pieces
+    // carried on in NS parts
+    constexpr int NI = IO::NI, NS = IO::NS, NE = OUT ? IO::NE : NS, NP = IO::NP, NO = IO::NO;
     constexpr uint32_t E = sizeof(T);
     extern __shared__ __align__(16) unsigned char lds_raw[];
     typename Cfg::Lds& l = *reinterpret_cast<typename Cfg::Lds*>(lds_raw);
@@ -495,7 +498,7 @@ void k_delta_scan(ScanArgs a) {
     const bool kept = MODE == kScanKeep && blk < a.nb16;
     unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
     unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
-    constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;  // matrix instructions per product
+    constexpr int X2 = NI == 1 ? NE : 6, X3 = NS == 3 ? 6 : NE == 3 ? 5 : 3;  // matrix instructions per product
     // one chunk; T alternates between two sets of registers
     auto chunk = [&](int c, Frag<NS>(&Tf)[kTri], Frag<NS>(&Tn)[kTri]) {
         if (c + 1 < nch) rec += recstep;  // loaded for the next chunk; the last one reads itself again
@@ -546,7 +549,7 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) kt[0][m] = K.cols(lane, m, 0);
         __builtin_amdgcn_sched_barrier(0);
-        Frag<NS> ef[2];
+        Frag<NE> ef[2];
         auto residual = [&](int p) {
 #pragma unroll
             for (int t = 2 * p; t < 2 * p + 2; ++t) {
@@ -562,7 +565,7 @@ void k_delta_scan(ScanArgs a) {
                 if (!BF) load_v(vb, t);
                 load_gam(rb, t);
             }
-            ef[p] = pair_frag<NS>(x[2 * p], x[2 * p + 1], minus);
+            ef[p] = pair_frag<NE>(x[2 * p], x[2 * p + 1], minus);
         };
         residual(0);
         __builtin_amdgcn_sched_barrier(0);
@@ -574,8 +577,8 @@ void k_delta_scan(ScanArgs a) {
         interleave<4 * X3, 4, 1>();
         const Frag<NS> t1[2] = {Tf[3], Tf[5]};
         mma_tiles(t1, ef[1], u + 2);
-        Frag<NS> kf[2];
-        kf[0] = pair_frag<NS>(kap[0] * u[0], kap[1] * u[1], minus);
+        Frag<NE> kf[2];
+        kf[0] = pair_frag<NE>(kap[0] * u[0], kap[1] * u[1], minus);
 #pragma unroll
         for (int m = 0; m < MT; ++m) S[m] *= glast;
         interleave<2 * X3, 12, 0>();
@@ -617,7 +620,7 @@ void k_delta_scan(ScanArgs a) {
         };
 #pragma unroll
         for (int p = 0; p < KS; ++p) update(0, p);
-        kf[1] = pair_frag<NS>(kap[2] * u[2], kap[3] * u[3], minus);
+        kf[1] = pair_frag<NE>(kap[2] * u[2], kap[3] * u[3], minus);
         load_kap(rb, 2);
         load_kap(rb, 3);
         interleave<MT * X2, 5, 1>();
