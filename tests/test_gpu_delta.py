@@ -311,3 +311,33 @@ def test_runs_on_the_callers_stream():
     torch.cuda.synchronize()
     for o, s in outs:
         assert torch.equal(o, want) and torch.equal(s, ws)
+
+
+def test_captured_cut_sequences_replay():
+    """A sequence long enough to be cut, forward and backward, captured once; replays follow
+    new inputs, with eager work between them."""
+    lens, hk, hv, dk, dv = [2300], 1, 2, 64, 64
+    ds = [D.make(lens, hk, hv, dk, dv, "bf16", seed=s, decay=1e-2) for s in (31, 32, 33)]
+    r = rule(ds[0], hk, hv, dk, dv, "bf16")
+    start = D.starts(lens, "cuda")
+    bufs = {n: ds[0][n].cuda() for n in ("q", "k", "v", "g", "beta", "state", "do", "dstate")}
+
+    def both(b):
+        o, s = r.forward(*(b[n] for n in ("q", "k", "v", "g", "beta")), state=b["state"], seq_start=start)
+        return [o, s, *r.backward(*(b[n] for n in ("q", "k", "v", "g", "beta", "do")), state=b["state"],
+                                  dstate_out=b["dstate"], seq_start=start)]
+
+    both(bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(bufs)
+    for d in ds:
+        want = both({n: d[n].cuda() for n in bufs})
+        torch.cuda.synchronize()
+        for n in bufs:
+            bufs[n].copy_(d[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert bool((x == y).all())

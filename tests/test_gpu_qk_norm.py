@@ -189,3 +189,46 @@ def test_norm_then_delta_rule_then_backward(dtype):
     assert D.rel(o.flatten(0, 1), ref) <= tol
     for got, exact in zip((dq, dk, dv, dg, db), want):
         assert D.rel(got.flatten(0, 1), exact) <= tol_grad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_prefill_and_single_tokens(dtype):
+    """Serving: ragged prompts normed, prefilled into a pool of states, then three tokens of
+    each row, one at a time, against the same chain in 64 bits."""
+    from fft_long_convolution_libhyena_amd import DeltaRule, QKNorm
+
+    hk, hv, dim, lens, extra = 2, 4, 64, [130, 1, 67], 3
+    total = [n + extra for n in lens]
+    gen = torch.Generator().manual_seed(21)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k = (torch.randn(sum(total), hk, dim, generator=gen).to(dt) for _ in range(2))
+    d = D.make(total, hk, hv, dim, dim, dtype, seed=22)
+    freq = 10000.0 ** (-torch.arange(32).float() / 32)
+    pos = torch.cat([torch.arange(n) for n in total])
+    m = QKNorm(hk, hk, dim, dtype=dtype, kind="l2", freq=freq.cuda())
+    rule = DeltaRule(hk, hv, dim, dim, dtype)
+    begin = [sum(total[:i]) for i in range(len(total))]
+    prompt = torch.cat([torch.arange(b, b + n) for b, n in zip(begin, lens)])
+    x = dict(q=q, k=k, v=d["v"], g=d["g"], beta=d["beta"])
+    cut = {n: t[prompt].cuda() for n, t in x.items()}
+    qn, kn = m.forward(cut["q"], cut["k"], pos[prompt].cuda())
+    o, states = rule.forward(qn, kn, cut["v"], cut["g"], cut["beta"], state=d["state"].cuda(), seq_start=D.starts(lens, "cuda"))
+    pool = torch.full((5, hv, dim, dim), float("nan"), device="cuda")
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = states
+    out = [o[sum(lens[:i]):sum(lens[:i + 1])] for i in range(len(lens))]
+    for t in range(extra):
+        at = torch.tensor([b + n + t for b, n in zip(begin, lens)])
+        one = {n: y[at].cuda().unsqueeze(1) for n, y in x.items()}
+        qn, kn = m.forward(one["q"], one["k"], pos[at].cuda().unsqueeze(1))
+        o1 = rule.step(qn, kn, one["v"], one["g"], one["beta"], pool, slots=slots)
+        out = [torch.cat([a, b]) for a, b in zip(out, o1)]
+    y = dict(d, q=reference(q.double(), None, pos, freq, "l2", False, 1e-6), k=reference(k.double(), None, pos, freq, "l2", False, 1e-6))
+    ro, rs = D.forward(y, dim ** -0.5)
+    # the parts' own tolerances and one more rounding of the normed vectors, which the state
+    # takes over too; they add in squares
+    tol = 2.0 ** -8 * (4 + 1) ** 0.5 if dtype == "bf16" else 2 * 416 * 2.0 ** -24
+    tol_state = 2.0 ** -8 * 2 ** 0.5 if dtype == "bf16" else 2 * 416 * 2.0 ** -24
+    assert D.rel(torch.cat(out), ro) <= tol
+    assert D.rel(pool[slots.long()], rs) <= tol_state
+    assert bool(pool[[1, 3]].isnan().all())
