@@ -26,6 +26,7 @@ struct GradArgs {
     Shape sh;
     const void *q, *k, *v, *g, *beta, *dout;
     const void *s0, *ds1, *u, *r;  // the scans' fragments
+    const float* dot;              // bf16: <dS1, S0>, a value a column of v
     void *dq, *dk;       // [tokens][hk][dk]
     void *dg, *dbeta;    // [tokens][hv]
 };
@@ -214,17 +215,10 @@ void k_delta_grad(GradArgs a) {
                     pd[f][j] = __builtin_bit_cast(u32x4, buf_f4(db, s0 + f * 512 * E + 16 * j, 0));
                 }
         };
-        auto dot16 = [&](const u32x4& x, const u32x4& y) {
+        auto dot4 = [&](const u32x4& x, const u32x4& y) {
             float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (BF) {
-                    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
-                    s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
-                } else {
-                    s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
-                }
-            }
+            for (int i = 0; i < 4; ++i) s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
             return s;
         };
         fetch(0);
@@ -243,7 +237,8 @@ void k_delta_grad(GradArgs a) {
         }
         f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
         f32x4 rvt = {};
-        float sd = 0.f;
+        float sd = 0.f;  // this thread's part of <dS1, S0>
+        if (BF && tid < 16 * nb16) sd = a.dot[fidx * 16 + tid];
         for (int c0 = 0; c0 < dv; c0 += 32) {
             __syncthreads();  // the step before (or the head before) has read its tiles
 #pragma unroll
@@ -258,8 +253,9 @@ void k_delta_grad(GradArgs a) {
                 const int x = NF * w + f;  // block x / KS, step x % KS
                 l.step.s.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, ps[f]);
                 l.step.d.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, pd[f]);
+                if constexpr (!BF)
 #pragma unroll
-                for (int j = 0; j < NV; ++j) sd += dot16(ps[f][j], pd[f][j]);
+                    for (int j = 0; j < NV; ++j) sd += dot4(ps[f][j], pd[f][j]);
             }
             if (c0 + 32 < dv) fetch(c0 + 32);
             lds_barrier();

@@ -9,10 +9,10 @@
 // here an input wave a block, one chunk ahead, that makes what does not depend on dS
 // (P^T dO and Q^T diag(exp(G)) dO) and hands it over in LDS as fp32. The input waves of
 // bf16 calls also stage K, Q and dO, half the rows each; fp32 calls have a staging wave.
-// Measured as the forward's scan: 358 us, 2.8 us a chunk (2.4 TB/s, matrix pipes 19%). Without
-// its stores 264, without its inputs too 259, the input waves alone 183: chain and stores
-// bound it. Stores from the input waves (results handed back in LDS) took 358 to 386, T^T a
-// chunk ahead in alternating registers 365.
+// Measured as the forward's scan: 410 us, 3.2 us a chunk (3 TB/s); without <dS1, S0> 358,
+// without stores too 264, without the inputs 259, the input waves alone 183: chain and
+// memory bound it. Stores from the input waves (results handed back in LDS) took 358 to 386
+// in place of 358, T^T a chunk ahead in alternating registers 365.
 #pragma once
 #include "delta_scan.hpp"
 
@@ -30,6 +30,8 @@ struct RevArgs {
     void* ds1;             // dS behind every chunk, as fragments
     void* r;               // as fragments
     void* dv;              // [tokens][hv][dv] (output)
+    const void *s0, *s0_rest;  // bf16: the states' fragments, both parts
+    float* dot;            // bf16: <dS1, S0> of every chunk, a value a column of v
     Pieces pieces;
     int nblk, nb16;
 };
@@ -300,6 +302,23 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
         for (int f = 0; f < kTri; ++f) Tt[f] = buf_frag<NS>(bb, 0, f, lane);
     };
+    // bf16: <dS1, S0> goes into dg of every token of the chunk and beyond, so it is formed here
+    // from both parts of both (from the gradient kernel's one each, dg was up to 6.7e-3 off where
+    // the final states' gradient outweighs the outputs'; 3e-3 so). It is the diagonal of
+    // S0^T dS1, whose left operand is the fragment as it lies.
+    Frag<2> s0f[BF && !ENDS ? KS : 1];
+    auto load_s0 = [&](int i, int s) {
+        const int64_t at = (((slot0 + nch - 1 - i) * hv + h) * a.nb16 + blk) * (KS * 512 * E);
+        const uint32_t bytes = blk < a.nb16 ? KS * 512 * E : 0;
+        s0f[s].p[0] = buf_frag<1>(plain_buf((const unsigned char*)a.s0 + at, bytes), 0, s, lane).p[0];
+        s0f[s].p[1] = buf_frag<1>(plain_buf((const unsigned char*)a.s0_rest + at, bytes), 0, s, lane).p[0];
+    };
+    auto store_dot = [&](int i, const f32x4& d) {
+        const int64_t at = ((slot0 + nch - 1 - i) * hv + h) * (int64_t)(16 * a.nb16);
+        const float lo = col & 1 ? d[1] : d[0], hi = col & 1 ? d[3] : d[2], x = col & 2 ? hi : lo;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), plain_buf(a.dot + at, 64 * a.nb16),
+                                              (int)(col >> 2 == g ? 4 * c0 : kNoElem), 0, 0);
+    };
     auto store_rows = [&](void* dst, const f32x4(&y)[4], int i) {
         const RowBuf b = plain_buf((unsigned char*)dst + ((first + (int64_t)(nch - 1 - i) * kC) * hv + h) * (int64_t)dv * E,
                                    (rows_in(i) - 1) * ldo + dv * E);
@@ -313,6 +332,10 @@ void k_delta_rev(RevArgs a) {
     if (nch > 0) {
         load_sc(0);
         load_t(0);
+        if constexpr (BF && !ENDS) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) load_s0(0, s);
+        }
         lds_barrier();  // Q and dO of the first chunk
         if (Cfg::STAGER) lds_barrier();
         lds_barrier();  // its inputs and K
@@ -336,7 +359,7 @@ void k_delta_rev(RevArgs a) {
         };
         read_rows(0);
         read_rows(1);
-        f32x4 xu[4];
+        f32x4 xu[4], dot = {};
 #pragma unroll
         for (int t = 0; t < 4; ++t) xu[t] = in.u[t][lane];
         __builtin_amdgcn_sched_barrier(0);
@@ -344,6 +367,10 @@ void k_delta_rev(RevArgs a) {
         for (int s = 0; s < KS; ++s) {
             mma_tiles(ka[s & 1], sf[s], x);
             if (s + 2 < KS) read_rows(s + 2);
+            if constexpr (BF && !ENDS) {
+                dot = mma(s0f[s], sf[s], dot);
+                load_s0(nx, s);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         Frag<NI> kt[2][MT];
@@ -351,6 +378,7 @@ void k_delta_rev(RevArgs a) {
         for (int m = 0; m < MT; ++m) kt[1][m] = K.cols(lane, m, 1);
         __builtin_amdgcn_sched_barrier(0);
         Frag<NS> uf[2];
+        if constexpr (BF && !ENDS) store_dot(i, dot);
         auto du = [&](int p) {
 #pragma unroll
             for (int t = 2 * p; t < 2 * p + 2; ++t) x[t] = kap[t] * x[t] + xu[t];

@@ -20,7 +20,7 @@
 // alternating; the chain over the chunks is sequential. Measured, 8 sequences of 8192 tokens,
 // 6 heads of 128 x 128, bf16: 280 us, 2.2 us a chunk (192 workgroups on 256 CUs; 1.9 TB/s;
 // matrix pipes busy 29% of the CUs' cycles), 248 with residuals in two parts as the scan that
-// keeps states has them (250). On the way, for a chunk:
+// keeps states has them (288 with both parts of the states stored, 250 with one). On the way, for a chunk:
 // tokens and state rows split over four waves, operands exchanged in LDS with three barriers,
 // 2.3 us for 32 columns; each wave loading K, Q and K^T for itself, 2.0 us for 16 columns (a
 // load of 16 rows of 64 bytes costs 60 clocks, one of 1 KiB in a row 16).
@@ -41,6 +41,7 @@ struct ScanArgs {
     float* s_out;       // likewise, or null
     void* o;            // [tokens][hv][dv] (outputs)
     void* s0;           // state before every chunk, as fragments (for the backward)
+    void* s0_rest;      // its second bf16 parts (bf16)
     void* u;            // written values, as fragments (for the backward)
     Pieces pieces;
     int nblk;           // workgroups per head
@@ -496,6 +497,7 @@ void k_delta_scan(ScanArgs a) {
     }
     // this block's fragments of the backward, one chunk's behind another's
     const bool kept = MODE == kScanKeep && blk < a.nb16;
+    const int64_t rest = kept && BF ? (unsigned char*)a.s0_rest - (unsigned char*)a.s0 : 0;
     unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
     unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
     constexpr int X2 = NI == 1 ? NE : 6, X3 = NS == 3 ? 6 : NE == 3 ? 5 : 3;  // matrix instructions per product
@@ -507,7 +509,10 @@ void k_delta_scan(ScanArgs a) {
         if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) store_frag<BF>(s0p + s * 512 * E, lane, S[2 * s], S[2 * s + 1]);
+                for (int s = 0; s < KS; ++s) {
+                    store_frag<BF>(s0p + s * 512 * E, lane, S[2 * s], S[2 * s + 1]);
+                    if constexpr (BF) *reinterpret_cast<bf16x8*>(s0p + rest + s * 512 * E + lane * 16) = sf[s].p[1];
+                }
             s0p += (int64_t)hv * a.nb16 * (KS * 512 * E);
         }
         __builtin_amdgcn_sched_barrier(0);

@@ -102,6 +102,26 @@ def test_zero_strength_and_resets_have_their_gradients():
     assert float(got[4][20:80, 0].abs().max()) > 0
 
 
+def test_gate_gradients_of_carried_states():
+    """With nothing written and no outputs' gradient, dg is <dS, S> decayed, here a tenth of
+    what it is for unrelated dS and S. Both enter in two bf16 parts, off by 2^-16 at most in
+    each product (errors add in squares; three, with the product of second parts), and the
+    result is rounded once."""
+    lens, hv, dk, dv = [70, 5, 64], 2, 64, 64
+    d = D.make(lens, 1, hv, dk, dv, "bf16", seed=41)
+    d["beta"].zero_()
+    d["do"].zero_()
+    s, ds = d["state"], d["dstate"]
+    along = (s * ds).sum((2, 3), keepdim=True) / (ds * ds).sum((2, 3), keepdim=True)
+    size = (s * ds).square().sum((2, 3)).sqrt()
+    d["state"] = s + ds * (0.1 * (size / (ds * ds).sum((2, 3)))[:, :, None, None] - along)
+    got = run(d, "bf16", (1, hv, dk, dv))[3].cpu().double()
+    want = D.backward(d, dk ** -0.5)[3]
+    spread = (d["state"].double() * d["dstate"].double()).square().sum((2, 3)).sqrt()
+    bound = torch.cat([spread[i].expand(n, hv) for i, n in enumerate(lens)]) * 3 ** 0.5 * 2.0 ** -16
+    assert bool(((got - want).abs() <= want.abs() * 2.0 ** -8 + bound).all())
+
+
 def test_batch_layout_matches_packed():
     from fft_long_convolution_libhyena_amd import DeltaRule
 
