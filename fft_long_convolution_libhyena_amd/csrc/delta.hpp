@@ -16,7 +16,8 @@
 // residuals and what a chunk adds to the state have three (relative error of the fp32
 // state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). Two also serve the
 // states between the pieces of cut sequences and, in the backward, dS and all that leads
-// to it. fp32 plans use three parts throughout (1e-7), at 6 products for each single one,
+// to it. P has one: it enters outputs alone, which are rounded to bf16 (2.2e-3 off, rounding
+// by itself leaves 1.7e-3; two parts would be 12 products a chunk more). fp32 plans use three parts throughout (1e-7), at 6 products for each single one,
 // still 2.7 times the rate of the fp32 matrix instruction.
 //
 // Fragment layouts of v_mfma_f32_16x16x32_bf16, lane l, g = l / 16:
@@ -505,7 +506,9 @@ struct Prep {
 // block of 16 columns, the state (its gradient) as KS, a 64-token array as two operand
 // fragments in the element type, 16 or 32 bytes a lane: lane l has column l % 16 of the
 // block, elements 8 (l / 16) .. + 7 of 32. One contiguous store of 1 KiB in place of
-// sixteen of 32-byte pieces.
+// sixteen of 32-byte pieces. bf16 calls round them to bf16 for these products, whose results
+// are rounded to bf16 too: dq, dk 2.5e-3 off (rounding by itself 1.7e-3); all four in two
+// parts would move 1.2 GB more beside 2.9 (8 sequences of 8192 tokens).
 template <bool BF>
 __device__ __forceinline__ void store_frag(unsigned char* p, int lane, const f32x4& a, const f32x4& b) {
     if constexpr (BF) {
@@ -523,9 +526,9 @@ constexpr int64_t kMaxLd = int64_t(1) << 22;  // elements: 64 rows stay below 2^
 
 constexpr int kCus = 256;
 // Shorter pieces gain nothing: the ends' launch and the carries (5 us a piece) cost what the
-// shorter scans save. One bf16 sequence, 6 heads of 128, cut and whole: 1600 tokens 58 and
-// 57 us, 2048 64 and 68, 4096 88 and 120, 16384 163 and 424; backward 137 and 132, 143 and
-// 155, 201 and 273, 459 and 1029.
+// shorter scans save. One bf16 sequence, 6 heads of 128, cut and whole: 1600 tokens 59 and
+// 63 us, 2048 65 and 76, 4096 90 and 138, 16384 167 and 492; backward 134 and 136, 139 and
+// 162, 199 and 285, 485 and 1085.
 constexpr int64_t kMinPiece = 8;
 
 struct PrepArgs;
