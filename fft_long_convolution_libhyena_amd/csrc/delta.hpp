@@ -17,8 +17,9 @@
 // state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). Two also serve the
 // states between the pieces of cut sequences and, in the backward, dS and all that leads
 // to it. P has one: it enters outputs alone, which are rounded to bf16 (2.2e-3 off, rounding
-// by itself leaves 1.7e-3; two parts would be 12 products a chunk more). fp32 plans use three parts throughout (1e-7), at 6 products for each single one,
-// still 2.7 times the rate of the fp32 matrix instruction.
+// by itself leaves 1.7e-3; two parts would be 12 products a chunk more). fp32 plans use three
+// parts throughout (1e-7), at 6 products for each single one, still 2.7 times the rate of the
+// fp32 matrix instruction.
 //
 // Fragment layouts of v_mfma_f32_16x16x32_bf16, lane l, g = l / 16:
 //   A [16][32]: lane holds row l % 16, columns 8g .. 8g+7
