@@ -16,8 +16,8 @@
 // residuals and what a chunk adds to the state have three (relative error of the fp32
 // state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). Two also serve the
 // states between the pieces of cut sequences and, in the backward, dS and all that leads
-// to it. P has one: it enters outputs alone, which are rounded to bf16 (2.2e-3 off, rounding
-// by itself leaves 1.7e-3; two parts would be 12 products a chunk more). fp32 plans use three
+// to it. P has two as well: with one the outputs are 2.2e-3 off, with two 1.7e-3, which is what
+// their own rounding leaves (12 products a chunk more, off the chain). fp32 plans use three
 // parts throughout (1e-7), at 6 products for each single one, still 2.7 times the rate of the
 // fp32 matrix instruction.
 //
@@ -56,7 +56,7 @@ struct Io<true> {
     static constexpr int NS = 2;  // parts of the state, T and the written values
     static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state
     static constexpr int NO = 2;  // parts of the state and of u against Q and P
-    static constexpr int NP = 1;  // parts of P
+    static constexpr int NP = 2;  // parts of P
 };
 template <>
 struct Io<false> {
