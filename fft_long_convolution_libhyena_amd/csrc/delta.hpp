@@ -478,6 +478,12 @@ __device__ __forceinline__ double chunk_decay(float g, int lane) {
     return G;
 }
 
+// The backward takes dbeta = r . (u / beta), so a write strength of zero is held at 2^-90
+// in what it solves for u: the residual u / beta is then there for it, with room for its
+// parts above the smallest fp32, and what is written beside it is 1e-27 of a residual.
+constexpr float kMinBeta = 0x1p-90f;
+__device__ __forceinline__ float held_beta(float b) { return fabsf(b) < kMinBeta ? kMinBeta : b; }
+
 __device__ __forceinline__ float decay(double d) { return __builtin_amdgcn_exp2f((float)d); }
 
 struct Shape {

@@ -127,7 +127,7 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
     }
     hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, b.s0, b.s0_rest, b.dot,
                             b.pieces, 0, 0};
-    hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->v, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, b.dot, dq, dk, dg, dbeta};
+    hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, b.dot, dq, dk, dg, dbeta};
     hipError_t e;
     if (c.bf)
         e = c.dkp == 64 ? hy::launch_back_t<true, 64>(c, r, g, stream) : hy::launch_back_t<true, 128>(c, r, g, stream);

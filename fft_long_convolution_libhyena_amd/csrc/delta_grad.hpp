@@ -4,14 +4,15 @@
 // W_ij = scale D_ij (dO_i . u_j) for j <= i, M_ij = -beta_i D_ij (r_i . u_j) for j < i:
 //   dQ = scale diag(exp G) dO S0^T + W K
 //   dK = -diag(exp(G) beta) r S0^T + diag(exp(G_last - G)) u dS1^T + W^T Q + (M + M^T) K
-//   dbeta_i = r_i . v_i - exp(G_i) k_i . (r S0^T)_i - sum_j D_ij (k_i . k_j) (r_i . u_j)
+//   dbeta_i = r_i . u_i / beta_i
 //   dG_i = scale exp(G_i) q_i . (dO S0^T)_i - beta_i exp(G_i) k_i . (r S0^T)_i
 //          + sum_j X_ij - sum_j X_ji - exp(G_last - G_i) k_i . (u dS1^T)_i,
 //   X_ij = W_ij q_i . k_j + M_ij k_i . k_j,
 //   dG_last += sum_i exp(G_last - G_i) k_i . (u dS1^T)_i + exp(G_last) <dS1, S0>,
-// and dg_t is the sum of dG_i over i >= t. (dbeta uses r itself, not beta r, so beta = 0
-// has its gradient.)
-// A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO, v,
+// and dg_t is the sum of dG_i over i >= t. u_i / beta_i is what the state's answer to k_i
+// lacks of v_i. Formed here as that difference, r . v - r . answer, it would keep the roundings
+// of both where they cancel (an answer within 1% of v: dbeta 0.18 off); beta = 0 is held at 2^-90.
+// A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO,
 // u, r and the states' columns, the next step's loads in flight); wave w has rows 16 w of
 // every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
 // 8192 tokens, 6 heads of 128 x 128, bf16, 306 us (1235 MB, 4.1 TB/s).
@@ -24,7 +25,7 @@ namespace delta {
 struct GradArgs {
     Seqs seqs;
     Shape sh;
-    const void *q, *k, *v, *g, *beta, *dout;
+    const void *q, *k, *g, *beta, *dout;
     const void *s0, *ds1, *u, *r;  // the scans' fragments
     const float* dot;              // bf16: <dS1, S0>, a value a column of v
     void *dq, *dk;       // [tokens][hk][dk]
@@ -125,7 +126,7 @@ template <bool BF, int DK>
 struct GradLds {
     GradTile<BF, kC, DK> k, q;
     struct Steps {
-        GradTile<BF, kC, 32> o, v;
+        GradTile<BF, kC, 32> o;
         StepTile<BF, kC> u, r;
         StepTile<BF, DK> s, d;
     };
@@ -137,7 +138,7 @@ struct GradLds {
         Mats mat;    // after the last of them
     };
     double G[kC];
-    float gam[kC], kap[kC], bet[kC], rv[kC], row[kC], krs[kC], kus[kC], dbz[kC];
+    float gam[kC], kap[kC], bet[kC], row[kC], kus[kC], ru[kC];
     float cs[4][kC];
     float red[4];
 };
@@ -165,8 +166,7 @@ void k_delta_grad(GradArgs a) {
     const int64_t tok = uniform64(rg.first + c * kC);
     const int rows = __builtin_amdgcn_readfirstlane((int)(rg.len - c * kC < kC ? rg.len - c * kC : kC));
     const int hv = a.sh.hv, dk = a.sh.dk, dv = a.sh.dv;
-    const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E, ldv = (uint32_t)a.sh.ldv * E,
-                   ldo = (uint32_t)(hv * dv) * E;
+    const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldq = (uint32_t)a.sh.ldq * E, ldo = (uint32_t)(hv * dv) * E;
 
     {  // K and Q
         const RowBuf kb = row_buf((const T*)a.k + tok * a.sh.ldk + (int64_t)hk * dk, rows, ldk, dk * E);
@@ -186,20 +186,17 @@ void k_delta_grad(GradArgs a) {
         const int nb16 = (dv + 15) / 16;
         const int64_t fidx = (slot * hv + h) * nb16;  // first block's fragments
         const RowBuf ob = row_buf((const T*)a.dout + obase, rows, ldo, dv * E);
-        const RowBuf vb = row_buf((const T*)a.v + tok * a.sh.ldv + (int64_t)h * dv, rows, ldv, dv * E);
         const RowBuf ub = plain_buf((const T*)a.u + fidx * 1024, nb16 * 1024 * E), rb = plain_buf((const T*)a.r + fidx * 1024, nb16 * 1024 * E);
         const RowBuf sb = plain_buf((const T*)a.s0 + fidx * KS * 512, nb16 * KS * 512 * E);
         const RowBuf db = plain_buf((const T*)a.ds1 + fidx * KS * 512, nb16 * KS * 512 * E);
         // a step's 2 blocks: wave w stages fragment w of the four of u and r and fragments
         // NF w .. of the 2 KS of the states; blocks past the last read zeros
-        u32x4 po[NR], pv[NR], pu[NV], pr[NV], ps[NF][NV], pd[NF][NV];
+        u32x4 po[NR], pu[NV], pr[NV], ps[NF][NV], pd[NF][NV];
         auto fetch = [&](int c0) {
             const bool ok = c0 + scol < dv;
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
+            for (int i = 0; i < NR; ++i)
                 po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem, 0));
-                pv[i] = __builtin_bit_cast(u32x4, buf_f4(vb, ok ? (i * RPP + srow) * ldv + (c0 + scol) * E : kNoElem, 0));
-            }
             const uint32_t b0 = (c0 / 16) * 1024 * E + w * 512 * E + lane * 8 * E;
             const uint32_t s0 = (c0 / 16) * (KS * 512) * E + NF * w * 512 * E + lane * 8 * E;
 #pragma unroll
@@ -236,16 +233,12 @@ void k_delta_grad(GradArgs a) {
             l.bet[lane] = bv;
         }
         f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
-        f32x4 rvt = {};
         float sd = 0.f;  // this thread's part of <dS1, S0>
         if (BF && tid < 16 * nb16) sd = a.dot[fidx * 16 + tid];
         for (int c0 = 0; c0 < dv; c0 += 32) {
             __syncthreads();  // the step before (or the head before) has read its tiles
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                *l.step.o.at16(i * RPP + srow, scol) = po[i];
-                *l.step.v.at16(i * RPP + srow, scol) = pv[i];
-            }
+            for (int i = 0; i < NR; ++i) *l.step.o.at16(i * RPP + srow, scol) = po[i];
             l.step.u.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pu);
             l.step.r.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pr);
 #pragma unroll
@@ -260,7 +253,6 @@ void k_delta_grad(GradArgs a) {
             if (c0 + 32 < dv) fetch(c0 + 32);
             lds_barrier();
             const auto ao = l.step.o.rows(lane, w, 0), ar = l.step.r.op(lane, w), au = l.step.u.op(lane, w);
-            rvt = mma(ar, l.step.v.rows(lane, w, 0), rvt);  // its diagonal is r . v
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= w) {
@@ -297,7 +289,7 @@ void k_delta_grad(GradArgs a) {
                 for (int i = 0; i < 4; ++i) x[i] += __shfl_xor(x[i], d);
             return x;
         };
-        f32x4 qqs = {}, krs = {}, kus = {}, rx = {}, dbz = {};
+        f32x4 qqs = {}, krs = {}, kus = {}, rx = {};
         const int ti = 16 * w + 4 * g;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -315,6 +307,13 @@ void k_delta_grad(GradArgs a) {
         const f32x4 gam = *reinterpret_cast<const f32x4*>(l.gam + ti), kap = *reinterpret_cast<const f32x4*>(l.kap + ti);
         const f32x4 bet = *reinterpret_cast<const f32x4*>(l.bet + ti);
         // no branches around single elements: their decays are formed everywhere and selected
+        if (col >> 2 == g) {  // this lane has a diagonal element of its wave's tile
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j == w && (col & 3) == i) l.ru[16 * w + col] = z[j][i];
+        }
         float cx[4] = {};
         double Gi[4];
 #pragma unroll
@@ -331,7 +330,6 @@ void k_delta_grad(GradArgs a) {
                 const float wv = tj <= ti + i ? a.sh.scale * d * dp[j][i] : 0.f;
                 const float dz = tj < ti + i ? ds * z[j][i] : 0.f;
                 const float mv = -bet[i] * dz;
-                dbz[i] = fmaf(-dz, kk[j][i], dbz[i]);
                 const float x = fmaf(mv, kk[j][i], wv * qk[j][i]);
                 rx[i] += x;
                 cx[j] += x;
@@ -347,17 +345,9 @@ void k_delta_grad(GradArgs a) {
             if (g == 0) l.cs[w][16 * j + col] = cx[j];
         }
         rx = row_sum(rx);
-        dbz = row_sum(dbz);
         if (col == 0) {
             *reinterpret_cast<f32x4*>(l.row + ti) = a.sh.scale * gam * qqs - bet * gam * krs + rx;
-            *reinterpret_cast<f32x4*>(l.krs + ti) = gam * krs;
             *reinterpret_cast<f32x4*>(l.kus + ti) = kap * kus;
-            *reinterpret_cast<f32x4*>(l.dbz + ti) = dbz;
-        }
-        if (col >> 2 == g) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if ((col & 3) == i) l.rv[16 * w + col] = rvt[i];
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sd += __shfl_xor(sd, d);
@@ -384,7 +374,7 @@ void k_delta_grad(GradArgs a) {
             }
             if (lane < rows) {
                 ((T*)a.dg)[(tok + lane) * hv + h] = (T)(float)d;
-                ((T*)a.dbeta)[(tok + lane) * hv + h] = (T)(l.rv[lane] - l.krs[lane] + l.dbz[lane]);
+                ((T*)a.dbeta)[(tok + lane) * hv + h] = (T)(l.ru[lane] / held_beta(l.bet[lane]));
             }
         }
 #pragma unroll

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     const double G = chunk_decay(gv, lane);
     if (wave == 0) {
         l.G[lane] = G;
-        l.beta[lane] = bv;
+        l.beta[lane] = BWD ? held_beta(bv) : bv;
     } else if (wave == 1) {
         const double last = __shfl(G, 63);
         float* sc = reinterpret_cast<float*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::sc);

@@ -716,8 +716,9 @@ size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, 
  * The states are computed again from the inputs; nothing of the forward call is kept.
  * bf16 calls round operands of the chunk-parallel products (the states and their
  * gradients at chunk borders, u, r) to bf16, the states themselves stay fp32 along
- * both scans. Every sum has a fixed order: results are bitwise reproducible. Rows
- * that belong to no sequence are left as they were. Arguments, workspace (of at least
+ * both scans. dbeta is formed from the residual v - answer itself and stays exact where
+ * the state predicts v; for it, strengths below 2^-90 count as 2^-90. Every sum has a fixed
+ * order: results are bitwise reproducible. Rows that belong to no sequence are left as they were. Arguments, workspace (of at least
  * hyena_delta_backward_workspace_bytes) and errors otherwise as in
  * hyena_delta_forward. Outputs must not alias inputs or each other. */
 hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
