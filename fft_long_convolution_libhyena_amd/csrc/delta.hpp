@@ -57,6 +57,7 @@ struct Io<true> {
     static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state
     static constexpr int NO = 2;  // parts of the state and of u against Q and P
     static constexpr int NP = 2;  // parts of P
+    static constexpr int NK = 2;  // parts of what the backward's scans keep
 };
 template <>
 struct Io<false> {
@@ -66,6 +67,7 @@ struct Io<false> {
     static constexpr int NE = 3;
     static constexpr int NO = 3;
     static constexpr int NP = 3;
+    static constexpr int NK = 1;  // kept as fp32
 };
 
 // Row r of row tile t as the scans number them: the pair of tiles 2s, 2s + 1 covers
@@ -511,16 +513,22 @@ struct Prep {
 
 // What the backward's scans leave for the chunk-parallel part: per (slot, value head) and
 // block of 16 columns, the state (its gradient) as KS, a 64-token array as two operand
-// fragments in the element type, 16 or 32 bytes a lane: lane l has column l % 16 of the
-// block, elements 8 (l / 16) .. + 7 of 32. One contiguous store of 1 KiB in place of
-// sixteen of 32-byte pieces. bf16 calls round them to bf16 for these products, whose results
-// are rounded to bf16 too: dq, dk 2.5e-3 off (rounding by itself 1.7e-3); all four in two
-// parts would move 1.2 GB more beside 2.9 (8 sequences of 8192 tokens).
-template <bool BF>
-__device__ __forceinline__ void store_frag(unsigned char* p, int lane, const f32x4& a, const f32x4& b) {
+// fragments, the bf16 parts behind each other or fp32, 16 or 32 bytes a lane: lane l has
+// column l % 16 of the block, elements 8 (l / 16) .. + 7 of 32. One contiguous store of 1 KiB
+// in place of sixteen of 32-byte pieces. With one part each, dk and dg were up to 3e-3 off and
+// dbeta 3.4e-3 (rounding by itself leaves 1.7e-3); the second parts are 0.5 GB of 4.2 that the
+// backward of 8 sequences of 8192 tokens moves.
+template <bool BF, int KS>
+struct Kept {
+    static constexpr int frag = 512 * (BF ? 2 : 4);                 // bytes of a fragment
+    static constexpr int state = KS * frag, row = 2 * frag;         // of one part of a state, of a 64-token array
+    static constexpr int states = Io<BF>::NK * state, rows = Io<BF>::NK * row;
+};
+template <bool BF, int N>
+__device__ __forceinline__ void keep_frag(unsigned char* p, int part, int lane, const f32x4& a, const f32x4& b, const Frag<N>& f) {
     if constexpr (BF) {
-        const u32x4 w = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(b[0], b[1]), pack2(b[2], b[3])};
-        *reinterpret_cast<u32x4*>(p + lane * 16) = w;
+#pragma unroll
+        for (int n = 0; n < Io<BF>::NK; ++n) *reinterpret_cast<bf16x8*>(p + n * part + lane * 16) = f.p[n];
     } else {
         *reinterpret_cast<f32x4*>(p + lane * 32) = a;
         *reinterpret_cast<f32x4*>(p + lane * 32 + 16) = b;

@@ -19,8 +19,7 @@ namespace {
 struct BackLayout {
     Prep prep;
     Pieces pieces;
-    void *s0, *s0_rest, *ds1, *u, *r;
-    float* dot;
+    void *s0, *ds1, *u, *r;
     size_t bytes;
 };
 
@@ -32,12 +31,10 @@ BackLayout back_layout(const DeltaCall& c, unsigned char* base) {
         at += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    const size_t e = c.bf ? 2 : 4;
-    const size_t cols = (size_t)c.slots * c.shape.hv * ((c.shape.dv + 15) / 16 * 16) * e;  // of every slot and head
+    // of every slot and head, two bf16 parts or fp32
+    const size_t cols = (size_t)c.slots * c.shape.hv * ((c.shape.dv + 15) / 16 * 16) * 4;
     const size_t states = cols * c.dkp, rows = cols * kC;
     b.s0 = take(states);
-    if (c.bf) b.s0_rest = take(states);
-    if (c.bf) b.dot = (float*)take(cols * 2);
     b.ds1 = take(states);
     b.u = take(rows);
     b.r = take(rows);
@@ -120,14 +117,12 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
         f.prep = b.prep;
         f.s_in = state_in;
         f.s0 = b.s0;
-        f.s0_rest = b.s0_rest;
         f.u = b.u;
         f.pieces = b.pieces;
         if (hy::delta_scan(c, true, f, stream) != hipSuccess) return HYENA_ERR_DEVICE;
     }
-    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, dv, b.s0, b.s0_rest, b.dot,
-                            b.pieces, 0, 0};
-    hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, b.dot, dq, dk, dg, dbeta};
+    hy::delta::RevArgs r{c.seqs, c.shape, in->q, in->k, b.prep, dout, dstate_out, dstate_in, b.ds1, b.r, b.pieces, 0, 0};
+    hy::delta::GradArgs g{c.seqs, c.shape, in->q, in->k, in->g, in->beta, dout, b.s0, b.ds1, b.u, b.r, dq, dk, dv, dg, dbeta};
     hipError_t e;
     if (c.bf)
         e = c.dkp == 64 ? hy::launch_back_t<true, 64>(c, r, g, stream) : hy::launch_back_t<true, 128>(c, r, g, stream);

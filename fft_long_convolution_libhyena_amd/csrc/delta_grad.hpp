@@ -1,10 +1,10 @@
 // The backward's chunk-parallel part: with the state S0 before and its gradient dS1
 // behind every chunk, the written values u and the residuals' gradients r, the gradients
-// of q, k, g and beta. Per chunk and value head, with D_ij = exp(G_i - G_j),
+// of q, k, v, g and beta. Per chunk and value head, with D_ij = exp(G_i - G_j),
 // W_ij = scale D_ij (dO_i . u_j) for j <= i, M_ij = -beta_i D_ij (r_i . u_j) for j < i:
 //   dQ = scale diag(exp G) dO S0^T + W K
 //   dK = -diag(exp(G) beta) r S0^T + diag(exp(G_last - G)) u dS1^T + W^T Q + (M + M^T) K
-//   dbeta_i = r_i . u_i / beta_i
+//   dV = diag(beta) r,   dbeta_i = r_i . u_i / beta_i
 //   dG_i = scale exp(G_i) q_i . (dO S0^T)_i - beta_i exp(G_i) k_i . (r S0^T)_i
 //          + sum_j X_ij - sum_j X_ji - exp(G_last - G_i) k_i . (u dS1^T)_i,
 //   X_ij = W_ij q_i . k_j + M_ij k_i . k_j,
@@ -13,8 +13,8 @@
 // lacks of v_i. Formed here as that difference, r . v - r . answer, it would keep the roundings
 // of both where they cancel (an answer within 1% of v: dbeta 0.18 off); beta = 0 is held at 2^-90.
 // A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO,
-// u, r and the states' columns, the next step's loads in flight); wave w has rows 16 w of
-// every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
+// u, r and the states' columns, the next step's loads in flight), bf16 calls in two halves,
+// the states' second parts in the place of the first; wave w has rows 16 w of every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
 // 8192 tokens, 6 heads of 128 x 128, bf16, 306 us (1235 MB, 4.1 TB/s).
 #pragma once
 #include "delta.hpp"
@@ -26,9 +26,9 @@ struct GradArgs {
     Seqs seqs;
     Shape sh;
     const void *q, *k, *g, *beta, *dout;
-    const void *s0, *ds1, *u, *r;  // the scans' fragments
-    const float* dot;              // bf16: <dS1, S0>, a value a column of v
+    const void *s0, *ds1, *u, *r;  // as Kept
     void *dq, *dk;       // [tokens][hk][dk]
+    void* dv;            // [tokens][hv][dv]
     void *dg, *dbeta;    // [tokens][hv]
 };
 
@@ -98,9 +98,8 @@ struct StepTile<false, W> : GradTile<false, W, 32> {
     __device__ __forceinline__ Frag<3> op(int lane, int m) const { return this->rows(lane, m, 0); }
 };
 
-// A 64 x 64 matrix as a left operand: in bf16 calls two tiles, its parts. W enters dQ and dK
-// beside u, rounded once already: with one part each the errors of dQ and dK were 1.7 times
-// those of rounding the results alone, with two 1.5 times, at 7% of the kernel's time.
+// A 64 x 64 matrix as a left operand: in bf16 calls two tiles, its parts (with one each dQ and
+// dK were off by a fifth more than by their own rounding; 7% of the kernel's time).
 template <bool BF>
 struct GradMat {
     GradTile<BF, kC, kC> part[BF ? 2 : 1];
@@ -127,8 +126,8 @@ struct GradLds {
     GradTile<BF, kC, DK> k, q;
     struct Steps {
         GradTile<BF, kC, 32> o;
-        StepTile<BF, kC> u, r;
-        StepTile<BF, DK> s, d;
+        StepTile<BF, kC> u[Io<BF>::NK], r[Io<BF>::NK];
+        StepTile<BF, DK> s, d;  // one part at a time
     };
     struct Mats {
         GradMat<BF> w, n;
@@ -154,6 +153,8 @@ void k_delta_grad(GradArgs a) {
     constexpr int NR = kC / RPP;                  // passes for 64 rows
     constexpr int NV = (int)E / 2;                // 16-byte pieces of a lane's part of a fragment
     constexpr int NF = DK / 64;                   // state fragments a wave stages (of 2 KS)
+    constexpr int NK = Io<BF>::NK;
+    using Kp = Kept<BF, KS>;
     extern __shared__ __align__(16) unsigned char lds_raw[];
     GradLds<BF, DK>& l = *reinterpret_cast<GradLds<BF, DK>*>(lds_raw);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -186,36 +187,69 @@ void k_delta_grad(GradArgs a) {
         const int nb16 = (dv + 15) / 16;
         const int64_t fidx = (slot * hv + h) * nb16;  // first block's fragments
         const RowBuf ob = row_buf((const T*)a.dout + obase, rows, ldo, dv * E);
-        const RowBuf ub = plain_buf((const T*)a.u + fidx * 1024, nb16 * 1024 * E), rb = plain_buf((const T*)a.r + fidx * 1024, nb16 * 1024 * E);
-        const RowBuf sb = plain_buf((const T*)a.s0 + fidx * KS * 512, nb16 * KS * 512 * E);
-        const RowBuf db = plain_buf((const T*)a.ds1 + fidx * KS * 512, nb16 * KS * 512 * E);
+        const RowBuf vo = row_buf((T*)a.dv + obase, rows, ldo, dv * E);
+        const RowBuf ub = plain_buf((const unsigned char*)a.u + fidx * Kp::rows, nb16 * Kp::rows);
+        const RowBuf rb = plain_buf((const unsigned char*)a.r + fidx * Kp::rows, nb16 * Kp::rows);
+        const RowBuf sb = plain_buf((const unsigned char*)a.s0 + fidx * Kp::states, nb16 * Kp::states);
+        const RowBuf db = plain_buf((const unsigned char*)a.ds1 + fidx * Kp::states, nb16 * Kp::states);
         // a step's 2 blocks: wave w stages fragment w of the four of u and r and fragments
         // NF w .. of the 2 KS of the states; blocks past the last read zeros
-        u32x4 po[NR], pu[NV], pr[NV], ps[NF][NV], pd[NF][NV];
+        u32x4 po[NR], pu[NK][NV], pr[NK][NV], ps[NK][NF][NV], pd[NK][NF][NV];
+        auto fetch_states = [&](int c0, int n) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const int x = NF * w + f;  // block x / KS, step x % KS
+                const uint32_t s0 = (c0 / 16 + x / KS) * Kp::states + n * Kp::state + (x % KS) * Kp::frag + lane * 8 * E;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    ps[n][f][j] = __builtin_bit_cast(u32x4, buf_f4(sb, s0 + 16 * j, 0));
+                    pd[n][f][j] = __builtin_bit_cast(u32x4, buf_f4(db, s0 + 16 * j, 0));
+                }
+            }
+        };
         auto fetch = [&](int c0) {
             const bool ok = c0 + scol < dv;
 #pragma unroll
             for (int i = 0; i < NR; ++i)
                 po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem, 0));
-            const uint32_t b0 = (c0 / 16) * 1024 * E + w * 512 * E + lane * 8 * E;
-            const uint32_t s0 = (c0 / 16) * (KS * 512) * E + NF * w * 512 * E + lane * 8 * E;
+            const uint32_t b0 = (c0 / 16 + (w >> 1)) * Kp::rows + (w & 1) * Kp::frag + lane * 8 * E;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                pu[j] = __builtin_bit_cast(u32x4, buf_f4(ub, b0 + 16 * j, 0));
-                pr[j] = __builtin_bit_cast(u32x4, buf_f4(rb, b0 + 16 * j, 0));
+            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    pu[n][j] = __builtin_bit_cast(u32x4, buf_f4(ub, b0 + n * Kp::row + 16 * j, 0));
+                    pr[n][j] = __builtin_bit_cast(u32x4, buf_f4(rb, b0 + n * Kp::row + 16 * j, 0));
+                }
+            fetch_states(c0, 0);
+        };
+        auto put_states = [&](int n) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const int x = NF * w + f;
+                l.step.s.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, ps[n][f]);
+                l.step.d.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, pd[n][f]);
             }
+        };
+        // <dS1, S0> goes into dg of every token of the chunk and beyond: from all parts of both
+        // (with one each dg was up to 6.7e-3 off where the final states' gradient outweighs the
+        // outputs')
+        auto dot_states = [&]() {
+            float s = 0.f;
 #pragma unroll
             for (int f = 0; f < NF; ++f)
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    ps[f][j] = __builtin_bit_cast(u32x4, buf_f4(sb, s0 + f * 512 * E + 16 * j, 0));
-                    pd[f][j] = __builtin_bit_cast(u32x4, buf_f4(db, s0 + f * 512 * E + 16 * j, 0));
-                }
-        };
-        auto dot4 = [&](const u32x4& x, const u32x4& y) {
-            float s = 0.f;
+                for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (BF) {
+                            auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+                            auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
+                            s = fmaf(lo(ps[0][f][j][i]) + lo(ps[1][f][j][i]), lo(pd[0][f][j][i]) + lo(pd[1][f][j][i]), s);
+                            s = fmaf(hi(ps[0][f][j][i]) + hi(ps[1][f][j][i]), hi(pd[0][f][j][i]) + hi(pd[1][f][j][i]), s);
+                        } else {
+                            s = fmaf(__uint_as_float(ps[0][f][j][i]), __uint_as_float(pd[0][f][j][i]), s);
+                        }
+                    }
             return s;
         };
         fetch(0);
@@ -234,29 +268,55 @@ void k_delta_grad(GradArgs a) {
         }
         f32x4 dp[4] = {}, z[4] = {}, qs[MT] = {}, rs[MT] = {}, us[MT] = {};
         float sd = 0.f;  // this thread's part of <dS1, S0>
-        if (BF && tid < 16 * nb16) sd = a.dot[fidx * 16 + tid];
         for (int c0 = 0; c0 < dv; c0 += 32) {
             __syncthreads();  // the step before (or the head before) has read its tiles
 #pragma unroll
             for (int i = 0; i < NR; ++i) *l.step.o.at16(i * RPP + srow, scol) = po[i];
-            l.step.u.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pu);
-            l.step.r.put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pr);
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const int x = NF * w + f;  // block x / KS, step x % KS
-                l.step.s.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, ps[f]);
-                l.step.d.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, pd[f]);
-                if constexpr (!BF)
-#pragma unroll
-                    for (int j = 0; j < NV; ++j) sd += dot4(ps[f][j], pd[f][j]);
+            for (int n = 0; n < NK; ++n) {
+                l.step.u[n].put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pu[n]);
+                l.step.r[n].put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pr[n]);
             }
-            if (c0 + 32 < dv) fetch(c0 + 32);
+            put_states(0);
+            if constexpr (BF) {
+                fetch_states(c0, 1);
+            } else {
+                sd += dot_states();
+                if (c0 + 32 < dv) fetch(c0 + 32);
+            }
             lds_barrier();
-            const auto ao = l.step.o.rows(lane, w, 0), ar = l.step.r.op(lane, w), au = l.step.u.op(lane, w);
+            auto parts = [&](const StepTile<BF, kC>(&t)[NK], int m) {
+                if constexpr (BF)
+                    return Frag<2>{{t[0].op(lane, m).p[0], t[1].op(lane, m).p[0]}};
+                else
+                    return t[0].op(lane, m);
+            };
+            const auto ao = l.step.o.rows(lane, w, 0);
+            const auto ar = parts(l.step.r, w), au = parts(l.step.u, w);
+            {  // dv: this lane has eight columns of one token of r
+                const int t = 16 * w + col, at = c0 + 8 * g;
+                const uint32_t off = at < dv ? t * ldo + at * E : kNoElem;
+                const float b = l.bet[t];
+                if constexpr (BF) {
+                    u32x4 x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = pack2(b * ((float)ar.p[0][2 * i] + (float)ar.p[1][2 * i]),
+                                     b * ((float)ar.p[0][2 * i + 1] + (float)ar.p[1][2 * i + 1]));
+                    __builtin_amdgcn_raw_buffer_store_b128(x, vo, (int)off, 0, 0);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f32x4 x = *reinterpret_cast<const f32x4*>(l.step.r[0].at16(t, 8 * g + 4 * j));
+                        x *= b;
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), vo, (int)(off + 16 * j), 0, 0);
+                    }
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j <= w) {
-                    const auto b = l.step.u.op(lane, j);
+                    const auto b = parts(l.step.u, j);
                     dp[j] = mma(ao, b, dp[j]);
                     z[j] = mma(ar, b, z[j]);
                 }
@@ -266,6 +326,21 @@ void k_delta_grad(GradArgs a) {
                 qs[m] = mma(ao, b, qs[m]);
                 rs[m] = mma(ar, b, rs[m]);
                 us[m] = mma(au, l.step.d.op(lane, m), us[m]);
+            }
+            if constexpr (BF) {
+                lds_barrier();  // the first parts have been read
+                put_states(1);
+                sd += dot_states();
+                if (c0 + 32 < dv) fetch(c0 + 32);
+                lds_barrier();
+                const Frag<1> r0{{ar.p[0]}}, u0{{au.p[0]}};
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const auto b = l.step.s.op(lane, m);
+                    qs[m] = mma(ao, b, qs[m]);
+                    rs[m] = mma(r0, b, rs[m]);
+                    us[m] = mma(u0, l.step.d.op(lane, m), us[m]);
+                }
             }
         }
         // k_i . k_j and q_i . k_j

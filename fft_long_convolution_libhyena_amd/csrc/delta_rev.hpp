@@ -2,14 +2,13 @@
 // of the state, and solves for r, the gradient of the residuals. With dS1 the gradient of
 // the state behind a chunk and the forward's T, P, decays:
 //   dU = P^T (scale dO) + diag(exp(G_last - G)) K dS1,        r = T^T dU,
-//   dV = diag(beta) r,
 //   dS0 = exp(G_last) dS1 + Q^T diag(scale exp(G)) dO - K^T diag(exp(G) beta) r.
 // The same shape as the forward's scan, and the same division: a state wave for each
 // block of 16 columns, in whose registers dS stays (fp32, operands as bf16 parts), and
 // here an input wave a block, one chunk ahead, that makes what does not depend on dS
 // (P^T dO and Q^T diag(exp(G)) dO) and hands it over in LDS as fp32. The input waves of
 // bf16 calls also stage K, Q and dO, half the rows each; fp32 calls have a staging wave.
-// Measured as the forward's scan: 410 us, 3.2 us a chunk (3 TB/s); without <dS1, S0> 358,
+// Measured as the forward's scan: 358 us, 2.8 us a chunk;
 // without stores too 264, without the inputs 259, the input waves alone 183: chain and
 // memory bound it. Stores from the input waves (results handed back in LDS) took 358 to 386
 // in place of 358, T^T a chunk ahead in alternating registers 365.
@@ -27,11 +26,8 @@ struct RevArgs {
     const void* dout;      // [tokens][hv][dv]
     const float* ds_out;   // [N][hv][dk][dv] gradient of the final states, or null
     float* ds_in;          // likewise of the initial states (output), or null
-    void* ds1;             // dS behind every chunk, as fragments
-    void* r;               // as fragments
-    void* dv;              // [tokens][hv][dv] (output)
-    const void *s0, *s0_rest;  // bf16: the states' fragments, both parts
-    float* dot;            // bf16: <dS1, S0> of every chunk, a value a column of v
+    void* ds1;             // dS behind every chunk, as Kept
+    void* r;               // likewise
     Pieces pieces;
     int nblk, nb16;
 };
@@ -302,44 +298,14 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
         for (int f = 0; f < kTri; ++f) Tt[f] = buf_frag<NS>(bb, 0, f, lane);
     };
-    // bf16: <dS1, S0> goes into dg of every token of the chunk and beyond, so it is formed here
-    // from both parts of both (from the gradient kernel's one each, dg was up to 6.7e-3 off where
-    // the final states' gradient outweighs the outputs'; 3e-3 so). It is the diagonal of
-    // S0^T dS1, whose left operand is the fragment as it lies.
-    Frag<2> s0f[BF && !ENDS ? KS : 1];
-    auto load_s0 = [&](int i, int s) {
-        const int64_t at = (((slot0 + nch - 1 - i) * hv + h) * a.nb16 + blk) * (KS * 512 * E);
-        const uint32_t bytes = blk < a.nb16 ? KS * 512 * E : 0;
-        s0f[s].p[0] = buf_frag<1>(plain_buf((const unsigned char*)a.s0 + at, bytes), 0, s, lane).p[0];
-        s0f[s].p[1] = buf_frag<1>(plain_buf((const unsigned char*)a.s0_rest + at, bytes), 0, s, lane).p[0];
-    };
-    auto store_dot = [&](int i, const f32x4& d) {
-        const int64_t at = ((slot0 + nch - 1 - i) * hv + h) * (int64_t)(16 * a.nb16);
-        const float lo = col & 1 ? d[1] : d[0], hi = col & 1 ? d[3] : d[2], x = col & 2 ? hi : lo;
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), plain_buf(a.dot + at, 64 * a.nb16),
-                                              (int)(col >> 2 == g ? 4 * c0 : kNoElem), 0, 0);
-    };
-    auto store_rows = [&](void* dst, const f32x4(&y)[4], int i) {
-        const RowBuf b = plain_buf((unsigned char*)dst + ((first + (int64_t)(nch - 1 - i) * kC) * hv + h) * (int64_t)dv * E,
-                                   (rows_in(i) - 1) * ldo + dv * E);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                buf_store<BF>(b, ooff + (32 * (t >> 1) + 4 * (t & 1) + j) * ldo, y[t][j]);
-            }
-    };
     if (nch > 0) {
         load_sc(0);
         load_t(0);
-        if constexpr (BF && !ENDS) {
-#pragma unroll
-            for (int s = 0; s < KS; ++s) load_s0(0, s);
-        }
         lds_barrier();  // Q and dO of the first chunk
         if (Cfg::STAGER) lds_barrier();
         lds_barrier();  // its inputs and K
     }
+    using Kp = Kept<BF, KS>;
     constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;
     for (int i = 0; i < nch; ++i) {
         const int nx = i + 1 < nch ? i + 1 : i;
@@ -349,7 +315,7 @@ void k_delta_rev(RevArgs a) {
         if (!ENDS && blk < a.nb16)
 #pragma unroll
             for (int s = 0; s < KS; ++s)
-                store_frag<BF>((unsigned char*)a.ds1 + (fr * KS + s) * (512 * E), lane, S[2 * s], S[2 * s + 1]);
+                keep_frag<BF>((unsigned char*)a.ds1 + fr * Kp::states + s * Kp::frag, Kp::state, lane, S[2 * s], S[2 * s + 1], sf[s]);
         // dU = P^T dO + diag(exp(G_last - G)) K dS
         f32x4 x[4] = {};
         Frag<NI> ka[2][4];
@@ -359,7 +325,7 @@ void k_delta_rev(RevArgs a) {
         };
         read_rows(0);
         read_rows(1);
-        f32x4 xu[4], dot = {};
+        f32x4 xu[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) xu[t] = in.u[t][lane];
         __builtin_amdgcn_sched_barrier(0);
@@ -367,10 +333,6 @@ void k_delta_rev(RevArgs a) {
         for (int s = 0; s < KS; ++s) {
             mma_tiles(ka[s & 1], sf[s], x);
             if (s + 2 < KS) read_rows(s + 2);
-            if constexpr (BF && !ENDS) {
-                dot = mma(s0f[s], sf[s], dot);
-                load_s0(nx, s);
-            }
             __builtin_amdgcn_sched_barrier(0);
         }
         Frag<NI> kt[2][MT];
@@ -378,7 +340,6 @@ void k_delta_rev(RevArgs a) {
         for (int m = 0; m < MT; ++m) kt[1][m] = K.cols(lane, m, 1);
         __builtin_amdgcn_sched_barrier(0);
         Frag<NS> uf[2];
-        if constexpr (BF && !ENDS) store_dot(i, dot);
         auto du = [&](int p) {
 #pragma unroll
             for (int t = 2 * p; t < 2 * p + 2; ++t) x[t] = kap[t] * x[t] + xu[t];
@@ -418,12 +379,8 @@ void k_delta_rev(RevArgs a) {
         if (!ENDS && blk < a.nb16)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                store_frag<BF>((unsigned char*)a.r + (fr * 2 + s) * (512 * E), lane, r[2 * s], r[2 * s + 1]);
-        if constexpr (!ENDS) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) r[t] *= bet[t];
-            store_rows(a.dv, r, i);
-        }
+                keep_frag<BF>((unsigned char*)a.r + fr * Kp::rows + s * Kp::frag, Kp::row, lane, r[2 * s], r[2 * s + 1],
+                              pair_frag<BF ? IO::NK : 1>(r[2 * s], r[2 * s + 1], minus));
         load_sc(nx);
         __builtin_amdgcn_sched_barrier(0);
         update(0, 0);

@@ -40,9 +40,8 @@ struct ScanArgs {
     const float* s_in;  // [N][hv][dk][dv] or null (zeros)
     float* s_out;       // likewise, or null
     void* o;            // [tokens][hv][dv] (outputs)
-    void* s0;           // state before every chunk, as fragments (for the backward)
-    void* s0_rest;      // its second bf16 parts (bf16)
-    void* u;            // written values, as fragments (for the backward)
+    void* s0;           // state before every chunk, as Kept (for the backward)
+    void* u;            // written values, likewise
     Pieces pieces;
     int nblk;           // workgroups per head
     int nbv;            // of them, those on columns of v; the others on M's (ends)
@@ -230,8 +229,7 @@ void k_delta_scan(ScanArgs a) {
     using Cfg = ScanCfg<BF, DK, MODE>;
     constexpr bool OUT = Cfg::OUT, ENDS = Cfg::ENDS;
     constexpr int KS = DK / 32, MT = DK / 16, NB = Cfg::NB, BUF = Cfg::BUF;
-    // states kept for the backward are rounded to the element type, those at the ends of pieces
-    // carried on in NS parts
+    // states kept for the backward and at the ends of pieces are carried on in NS parts
     constexpr int NI = IO::NI, NS = IO::NS, NE = OUT ? IO::NE : NS, NP = IO::NP, NO = IO::NO;
     constexpr uint32_t E = sizeof(T);
     extern __shared__ __align__(16) unsigned char lds_raw[];
@@ -497,9 +495,9 @@ void k_delta_scan(ScanArgs a) {
     }
     // this block's fragments of the backward, one chunk's behind another's
     const bool kept = MODE == kScanKeep && blk < a.nb16;
-    const int64_t rest = kept && BF ? (unsigned char*)a.s0_rest - (unsigned char*)a.s0 : 0;
-    unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(KS * 512 * E);
-    unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)(1024 * E);
+    using Kp = Kept<BF, KS>;
+    unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)Kp::states;
+    unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)Kp::rows;
     constexpr int X2 = NI == 1 ? NE : 6, X3 = NS == 3 ? 6 : NE == 3 ? 5 : 3;  // matrix instructions per product
     // one chunk; T alternates between two sets of registers
     auto chunk = [&](int c, Frag<NS>(&Tf)[kTri], Frag<NS>(&Tn)[kTri]) {
@@ -509,11 +507,8 @@ void k_delta_scan(ScanArgs a) {
         if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    store_frag<BF>(s0p + s * 512 * E, lane, S[2 * s], S[2 * s + 1]);
-                    if constexpr (BF) *reinterpret_cast<bf16x8*>(s0p + rest + s * 512 * E + lane * 16) = sf[s].p[1];
-                }
-            s0p += (int64_t)hv * a.nb16 * (KS * 512 * E);
+                for (int s = 0; s < KS; ++s) keep_frag<BF>(s0p + s * Kp::frag, Kp::state, lane, S[2 * s], S[2 * s + 1], sf[s]);
+            s0p += (int64_t)hv * a.nb16 * Kp::states;
         }
         __builtin_amdgcn_sched_barrier(0);
         // e = V - exp(G) K S; LDS reads two steps ahead of their products
@@ -635,8 +630,10 @@ void k_delta_scan(ScanArgs a) {
         } else if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) store_frag<BF>(up + s * 512 * E, lane, u[2 * s], u[2 * s + 1]);
-            up += (int64_t)hv * a.nb16 * (1024 * E);
+                for (int s = 0; s < 2; ++s)
+                    keep_frag<BF>(up + s * Kp::frag, Kp::row, lane, u[2 * s], u[2 * s + 1],
+                                  pair_frag<BF ? IO::NK : 1>(u[2 * s], u[2 * s + 1], minus));
+            up += (int64_t)hv * a.nb16 * Kp::rows;
         }
         // the new state's parts, two tiles at a time: first part a step behind the products,
         // its remainder and second part another step, so that none waits for a result

@@ -701,8 +701,8 @@ hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N
                                    hipStream_t stream);
 
 /* Bytes of workspace hyena_delta_backward needs: the forward's, the states before and
- * the state gradients behind every chunk of 64 tokens, and two arrays like o. Returns 0
- * as hyena_delta_workspace_bytes. */
+ * the state gradients behind every chunk of 64 tokens, and two arrays of o's shape, all at
+ * four bytes a value. Returns 0 as hyena_delta_workspace_bytes. */
 size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                             const int64_t* seq_start);
 
@@ -714,9 +714,8 @@ size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, 
  *   [tokens][heads_v] of the dtype, rounded once from fp32 sums (over the value heads
  *   that share a key head, too); dstate_in [N][heads_v][dim_k][dim_v] fp32, or NULL.
  * The states are computed again from the inputs; nothing of the forward call is kept.
- * bf16 calls round operands of the chunk-parallel products (the states and their
- * gradients at chunk borders, u, r) to bf16, the states themselves stay fp32 along
- * both scans. dbeta is formed from the residual v - answer itself and stays exact where
+ * Operands of bf16 calls are bf16 or sums of two bf16 parts, the states and their
+ * gradients stay fp32 along both scans. dbeta is formed from the residual v - answer itself and stays exact where
  * the state predicts v; for it, strengths below 2^-90 count as 2^-90. Every sum has a fixed
  * order: results are bitwise reproducible. Rows that belong to no sequence are left as they were. Arguments, workspace (of at least
  * hyena_delta_backward_workspace_bytes) and errors otherwise as in

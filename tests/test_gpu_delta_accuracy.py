@@ -5,6 +5,10 @@ cases, and is then one step off: the square of the difference to the exact resul
 rounding is at most sum step_i d_i. Steps are at most 2^-7 of the value, so by Cauchy's
 inequality the relative 2-norm of that difference is at most sqrt(2^-7 delta), delta being
 that of d. (Rounding an operand to one bf16 part alone makes it 1e-3 and more.)
+
+A first bf16 part leaves at most 2^-8 of a value and a second rounds what is left, by at most
+2^-9 of it: TWO. A product of two such values leaves out that of the second parts: CROSS. Such
+errors add in squares.
 """
 import math
 
@@ -14,6 +18,8 @@ import torch
 import _delta as D
 
 pytestmark = pytest.mark.gpu
+
+TWO, CROSS = 2.0 ** -17, 2.0 ** -16
 
 
 def rounded(delta):
@@ -27,9 +33,8 @@ def rounded(delta):
     ([1900], 1, 1, 64, 64, True),  # cut into pieces
 ])
 def test_outputs_are_rounded_once(lens, hk, hv, dk, dv, use_state):
-    """S, u and P enter in two bf16 parts each, off by half a step of the second, 2^-9 of 2^-9;
-    the products of second parts are left out, 2^-18 for each of the two sums. Five errors of
-    2^-18 in squares, and sums of up to 128 + 64 fp32 terms."""
+    """S, u and P enter in two bf16 parts each, and the products of P's and u's second parts are
+    left out (q has one part); sums of up to 128 + 64 fp32 terms."""
     from fft_long_convolution_libhyena_amd import DeltaRule
 
     d = D.make(lens, hk, hv, dk, dv, "bf16", seed=dk + len(lens))
@@ -37,7 +42,7 @@ def test_outputs_are_rounded_once(lens, hk, hv, dk, dv, use_state):
     o, _ = DeltaRule(hk, hv, dk, dv).forward(*(g[n] for n in ("q", "k", "v", "g", "beta")),
                                              state=g["state"] if use_state else None, seq_start=D.starts(lens, "cuda"))
     want = D.forward(d, dk ** -0.5, use_state)[0].to(torch.bfloat16)
-    assert D.rel(o, want) <= rounded(math.sqrt(5) * 2.0 ** -18 + 192 * 2.0 ** -24)
+    assert D.rel(o, want) <= rounded(math.sqrt(3 * TWO ** 2 + CROSS ** 2) + 192 * 2.0 ** -24)
 
 
 def with_residuals(lens, hk, hv, dk, dv, dtype, seed, share):
@@ -70,13 +75,13 @@ def gradients(d, dims, dtype="bf16", scale=None):
 @pytest.mark.parametrize("lens,hk,hv,dk,dv", [([150, 64], 1, 2, 128, 128), ([100], 2, 2, 64, 72)])
 def test_strengths_gradients_where_the_state_predicts_the_values(lens, hk, hv, dk, dv, share, dtype):
     """dbeta is r . (v - answer): with v close to the answer neither may enter rounded by itself.
-    The residual comes from products with S and T in two (fp32: three) parts, each off by 2^-18
-    (sums of 192 terms of 2^-24) of an answer 1 / share times as large; r, the residual and
-    the result are rounded once in bf16 calls (fp32: two chained sums)."""
+    The residual comes from products with S and T in two (fp32: three) parts (and sums of 192
+    terms of 2^-24) of an answer 1 / share times as large; r, the residual and the result are
+    rounded once at most in bf16 calls (fp32: two chained sums)."""
     d = with_residuals(lens, hk, hv, dk, dv, dtype, dk, share)
     d["beta"][::7] = 0  # no residual may need beta to be seen
     got, want = gradients(d, (hk, hv, dk, dv), dtype)[4], D.backward(d, dk ** -0.5)[4]
-    tol = (math.sqrt(3) * 2.0 ** -8 + math.sqrt(2) * 2.0 ** -18 / share if dtype == "bf16"
+    tol = (math.sqrt(3) * 2.0 ** -8 + math.sqrt(2) * TWO / share if dtype == "bf16"
            else 192 * 2.0 ** -24 * (2 + 1 / share))
     assert D.rel(got, want) <= tol
     assert D.rel(got[::7], want[::7]) <= tol
@@ -95,3 +100,24 @@ def test_values_without_strength_do_not_reach_other_gradients():
     rest = [t for t in range(150) if t != 40]
     assert D.rel(got[4][rest], plain[4][rest]) <= 2.0 ** -8
     assert D.rel(got[4][40], want[4][40]) <= 2 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [
+    ([64], 1, 1, 64, 64),
+    ([300, 77], 1, 2, 128, 128),
+    ([150, 0, 33], 2, 4, 72, 40),
+    ([130], 1, 1, 40, 256),
+    ([1900], 1, 2, 64, 64),  # cut into pieces
+])
+def test_gradients_are_rounded_once(lens, hk, hv, dk, dv):
+    """Seven operands of two parts on the way to u or r, and six in the gradients' own products
+    (S0, dS1, u, r, W, M); products of second parts are left out in five (T e and T^T dU, u
+    dS1^T, r S0^T, r u^T); three chained sums of up to 192 fp32 terms. dg sums a chunk's
+    differences of such products, which partly cancel: twice that."""
+    d = D.make(lens, hk, hv, dk, dv, "bf16", seed=dk + len(lens))
+    delta = math.sqrt(13 * TWO ** 2 + 5 * CROSS ** 2) + 3 * 192 * 2.0 ** -24
+    got, want = gradients(d, (hk, hv, dk, dv)), D.backward(d, dk ** -0.5)
+    for i, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        tol = rounded(2 * delta if name == "dg" else delta)
+        off = D.rel(got[i], want[i].to(torch.bfloat16))
+        assert off <= tol, (name, off, tol)
