@@ -14,9 +14,9 @@
 // the rounding of what the ones before it leave): two parts hold 16 bits, three 24.
 // bf16 plans give their inputs exactly in one part and carry the state and T in two; the
 // residuals and what a chunk adds to the state have three (relative error of the fp32
-// state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). Two also serve the
-// states between the pieces of cut sequences and, in the backward, dS and all that leads
-// to it. P has two as well: with one the outputs are 2.2e-3 off, with two 1.7e-3, which is what
+// state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). So have, in the backward,
+// P, dU, r and exp(G) dO, which lead to dS (the fp32 gradient of the state 3e-6 off with two).
+// Two also serve the states between the pieces of cut sequences. P has two as well: with one the outputs are 2.2e-3 off, with two 1.7e-3, which is what
 // their own rounding leaves (12 products a chunk more, off the chain). fp32 plans use three
 // parts throughout (1e-7), at 6 products for each single one, still 2.7 times the rate of the
 // fp32 matrix instruction.
@@ -54,7 +54,7 @@ struct Io<true> {
     using T = __bf16;
     static constexpr int NI = 1;  // parts of an input operand (exact)
     static constexpr int NS = 2;  // parts of the state, T and the written values
-    static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state
+    static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state; their gradients'
     static constexpr int NO = 2;  // parts of the state and of u against Q and P
     static constexpr int NP = 2;  // parts of P
     static constexpr int NK = 2;  // parts of what the backward's scans keep
@@ -504,7 +504,7 @@ struct Rec {
     static constexpr int sc = p + kTri * Io<BF>::NP * kFragBytes;
     static constexpr int bytes = sc + 1024;
     static constexpr int pt = kTri * Io<BF>::NS * kFragBytes;          // backward: T^T at 0, P^T here
-    static constexpr int back = 2 * kTri * Io<BF>::NS * kFragBytes;
+    static constexpr int back = kTri * (Io<BF>::NS + Io<BF>::NE) * kFragBytes;
 };
 struct Prep {
     unsigned char* rec;   // [slot][value head]

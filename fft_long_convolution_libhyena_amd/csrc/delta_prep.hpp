@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
     if (!BWD)
         write_tri<IO::NP, false>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::p), tid);
     else
-        write_tri<IO::NS, true>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.back + sh_idx * Rec<BF>::back + Rec<BF>::pt), tid);
+        write_tri<IO::NE, true>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.back + sh_idx * Rec<BF>::back + Rec<BF>::pt), tid);
     __syncthreads();
 
     // T over P. Diagonal block `wave`: column `col` of the inverse, x_i = e_i - sum_{j<i} A_ij x_j

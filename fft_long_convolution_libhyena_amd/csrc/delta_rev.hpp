@@ -63,7 +63,7 @@ void k_delta_rev(RevArgs a) {
     using T = typename IO::T;
     using Cfg = RevCfg<BF, DK>;
     constexpr int KS = DK / 32, MT = DK / 16, NB = Cfg::NB, BUF = Cfg::BUF;
-    constexpr int NI = IO::NI, NS = IO::NS;
+    constexpr int NI = IO::NI, NS = IO::NS, NG = IO::NE, NE = ENDS ? NS : IO::NE;
     constexpr uint32_t E = sizeof(T);
     extern __shared__ __align__(16) unsigned char lds_raw[];
     typename Cfg::Lds& l = *reinterpret_cast<typename Cfg::Lds*>(lds_raw);
@@ -143,7 +143,7 @@ void k_delta_rev(RevArgs a) {
     };
 
     if (wave >= NB) {
-        Frag<NS> Pt[kTri];
+        Frag<NG> Pt[kTri];
         f32x4 gam[4];
         uint32_t O[4][4];  // fp32 dO, a chunk ahead
         auto load = [&](int i) {
@@ -151,7 +151,7 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) gam[t] = buf_f4(rb, drow(t, 0) * 4, Rec<BF>::sc);
 #pragma unroll
-            for (int f = 0; f < kTri; ++f) Pt[f] = buf_frag<NS>(bb, Rec<BF>::pt, f, lane);
+            for (int f = 0; f < kTri; ++f) Pt[f] = buf_frag<NG>(bb, Rec<BF>::pt, f, lane);
             if constexpr (!BF) {
                 const RowBuf ob = plain_buf(obase + (nch - 1 - i) * orow, (rows_in(i) - 1) * ldo + dv * E);
 #pragma unroll
@@ -188,15 +188,15 @@ void k_delta_rev(RevArgs a) {
                 for (int s = 0; s < 2; ++s) of[s] = pair_frag<NI>(o[2 * s], o[2 * s + 1], minus);
             }
             f32x4 x[4] = {};
-            const Frag<NS> p0[2] = {Pt[0], Pt[2]}, p1[4] = {Pt[1], Pt[3], Pt[4], Pt[5]};
+            const Frag<NG> p0[2] = {Pt[0], Pt[2]}, p1[4] = {Pt[1], Pt[3], Pt[4], Pt[5]};
             mma_tiles(p0, of[0], x);
             mma_tiles(p1, of[1], x);
 #pragma unroll
             for (int t = 0; t < 4; ++t) out.u[t][lane] = a.sh.scale * x[t];
-            Frag<NS> gf[2];
+            Frag<NG> gf[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                gf[s] = pair_frag<NS>(a.sh.scale * gam[2 * s] * o[2 * s], a.sh.scale * gam[2 * s + 1] * o[2 * s + 1], minus);
+                gf[s] = pair_frag<NG>(a.sh.scale * gam[2 * s] * o[2 * s], a.sh.scale * gam[2 * s + 1] * o[2 * s + 1], minus);
             load(i + 1 < nch ? i + 1 : nch - 1);
 #pragma unroll
             for (int m = 0; m < MT; m += 2) {
@@ -306,7 +306,7 @@ void k_delta_rev(RevArgs a) {
         lds_barrier();  // its inputs and K
     }
     using Kp = Kept<BF, KS>;
-    constexpr int X2 = NI * NS == 2 ? 2 : 6, X3 = NS == 2 ? 3 : 6;
+    constexpr int X2 = NI == 1 ? NE : 6, X3 = NS == 3 ? 6 : NE == 3 ? 5 : 3;  // matrix instructions per product
     for (int i = 0; i < nch; ++i) {
         const int nx = i + 1 < nch ? i + 1 : i;
         const Tile<NI, DK>& K = l.k[i & (BUF - 1)];
@@ -339,11 +339,11 @@ void k_delta_rev(RevArgs a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) kt[1][m] = K.cols(lane, m, 1);
         __builtin_amdgcn_sched_barrier(0);
-        Frag<NS> uf[2];
+        Frag<NE> uf[2];
         auto du = [&](int p) {
 #pragma unroll
             for (int t = 2 * p; t < 2 * p + 2; ++t) x[t] = kap[t] * x[t] + xu[t];
-            uf[p] = pair_frag<NS>(x[2 * p], x[2 * p + 1], minus);
+            uf[p] = pair_frag<NE>(x[2 * p], x[2 * p + 1], minus);
         };
         du(1);
         __builtin_amdgcn_sched_barrier(0);
@@ -355,9 +355,9 @@ void k_delta_rev(RevArgs a) {
         interleave<4 * X3, 4, 0>();
         mma_tiles(t0, uf[0], r);
         // -diag(exp(G) beta) r as an operand, the second half first
-        Frag<NS> rf[2];
+        Frag<NE> rf[2];
         auto rpart = [&](int p) {
-            rf[p] = pair_frag<NS>(-gam[2 * p] * bet[2 * p] * r[2 * p], -gam[2 * p + 1] * bet[2 * p + 1] * r[2 * p + 1], minus);
+            rf[p] = pair_frag<NE>(-gam[2 * p] * bet[2 * p] * r[2 * p], -gam[2 * p + 1] * bet[2 * p + 1] * r[2 * p + 1], minus);
         };
         rpart(1);
 #pragma unroll

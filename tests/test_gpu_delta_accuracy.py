@@ -121,3 +121,46 @@ def test_gradients_are_rounded_once(lens, hk, hv, dk, dv):
         tol = rounded(2 * delta if name == "dg" else delta)
         off = D.rel(got[i], want[i].to(torch.bfloat16))
         assert off <= tol, (name, off, tol)
+
+
+def test_states_take_what_is_written_in_fp32():
+    """With keys along the axes and no state before, the state's row i is exp(G_last - G_i) beta_i
+    v_i alone, of which a bf16 call's operands hold all 24 bits in three parts: off by 2^-24 each
+    for two products, the decay (twice, its exponent and the exp2) and the third part. Two parts
+    would leave 2^-17 at most, 2e-6 in the mean."""
+    from fft_long_convolution_libhyena_amd import DeltaRule
+
+    lens, hv, dk, dv = [64, 50], 2, 64, 72
+    d = D.make(lens, 1, hv, dk, dv, "bf16", seed=4)
+    d["k"] = torch.eye(64)[torch.cat([torch.randperm(n) for n in lens])][:, None].bfloat16()
+    g = {n: d[n].cuda() for n in ("q", "k", "v", "g", "beta")}
+    _, s = DeltaRule(1, hv, dk, dv).forward(*g.values(), seq_start=D.starts(lens, "cuda"))
+    assert D.rel(s, D.forward(d, 1.0, use_state=False)[1]) <= 5 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("lens,dk,dv", [([64, 30], 64, 64), ([300, 77], 128, 72)])
+def test_state_gradients_take_the_outputs_in_fp32(lens, dk, dv):
+    """With beta = 0 the initial state's gradient is the sum of exp(G) scale q do over the tokens
+    and the decayed final one: exact products of q with three parts of the rest, off by 2^-24
+    for each of two products and a decay (twice), and fp32 sums of 64 terms and of the chunks;
+    errors add in squares. Two parts would leave 2e-6 and more."""
+    d = D.make(lens, 1, 2, dk, dv, "bf16", seed=dk)
+    d["beta"].zero_()
+    got, want = gradients(d, (1, 2, dk, dv))[5], D.backward(d, dk ** -0.5)[5]
+    assert D.rel(got, want) <= math.sqrt(4 + 64 + max(lens) // 64 + 1) * 2.0 ** -24
+
+
+def test_state_gradients_follow_the_residuals_in_fp32():
+    """With keys along the axes r is dU and the initial state's gradient a sum of -exp(G) beta k r
+    and exp(G) scale q do: here of the first alone, do reaching it through P^T (q = k), with
+    all of dU and r in three parts. Off by 2^-24 for P's product and decay, three products and
+    two decays more."""
+    lens, hv, dk, dv = [64], 2, 64, 64
+    d = D.make(lens, 1, hv, dk, dv, "bf16", seed=6)
+    d["k"] = torch.eye(64)[:, None].bfloat16()
+    d["q"] = d["k"].clone()
+    d["dstate"].zero_()
+    got, want = gradients(d, (1, hv, dk, dv))[5], D.backward(d, dk ** -0.5)[5]
+    # exp(G) (scale do - beta r), r = scale do: exact but for what the two leave, 1 / (1 - beta) more
+    size = (d["do"].double() ** 2 * dk ** -1.0).sum().sqrt()
+    assert float((got.double().cpu() - want).norm()) <= 8 * 2.0 ** -24 * float(size)
