@@ -260,6 +260,16 @@ def _dense(t, name, shape, dtype, device) -> int:
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, {got}")
 
 
+def _workspace(torch, workspace, need, device):
+    """(tensor, address, bytes) of a plan-less call's workspace: the caller's, or `need` bytes."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the GPU that holds q")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def kernel_synthesis(params, z, out=None):
     """hyena_kernel_synthesis: the input-dependent kernels of B samples.
     `params` has the fields of synth.SynthParams as fp32 device tensors (grid and
@@ -847,11 +857,11 @@ class QKNorm:
         dw_q, dw_k = (torch.empty(self.dim, dtype=torch.float32, device=dev) if w is not None else None
                       for w in (self.w_q, self.w_k))
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        if workspace is None and (dw_q is not None or dw_k is not None):
-            workspace = torch.empty(self.backward_workspace_bytes(args[1], dev), dtype=torch.uint8, device=dev)
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        ws, ws_bytes = None, 0
+        if workspace is not None or dw_q is not None or dw_k is not None:
+            workspace, ws, ws_bytes = _workspace(torch, workspace, self.backward_workspace_bytes(args[1], dev), dev)
         _launch(torch, "hyena_qk_norm_backward", self.lib.hyena_qk_norm_backward, dev, *args, *up, dqp, dkp, ptr(dw_q),
-                ptr(dw_k), ptr(workspace), ws_bytes)
+                ptr(dw_k), ws, ws_bytes)
         return dq, dk, dw_q, dw_k
 
 
@@ -907,14 +917,6 @@ class DeltaRule:
         return int(self.lib.hyena_delta_backward_workspace_bytes(self._params(None), int(N), int(tokens),
                                                                  16 if packed else None))
 
-    def _workspace(self, workspace, need, device):
-        if workspace is None:
-            workspace = self._torch.empty(need, dtype=self._torch.uint8, device=device)
-            return workspace, workspace.data_ptr(), need
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the GPU that holds q")
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
     def _out(self, t, name, shape, dtype, device):
         if t is None:
             t = self._torch.empty(shape, dtype=dtype, device=device)
@@ -936,7 +938,7 @@ class DeltaRule:
         state_out, fp = self._out(state_out, "state_out", states, torch.float32, dev)
         params = self._params(scale)
         need = self.lib.hyena_delta_workspace_bytes(params, N, tokens, starts)
-        workspace, ws, ws_bytes = self._workspace(workspace, need, dev)
+        workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
         _launch(torch, "hyena_delta_forward", self.lib.hyena_delta_forward, dev, params, N, tokens, starts, inputs, sp, op,
                 fp, ws, ws_bytes)
         return o, state_out
@@ -957,7 +959,7 @@ class DeltaRule:
         out.append(torch.empty(states, dtype=torch.float32, device=dev))
         params = self._params(scale)
         need = self.lib.hyena_delta_backward_workspace_bytes(params, N, tokens, starts)
-        workspace, ws, ws_bytes = self._workspace(workspace, need, dev)
+        workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
         _launch(torch, "hyena_delta_backward", self.lib.hyena_delta_backward, dev, params, N, tokens, starts, inputs, sp,
                 dop, dsp, *(t.data_ptr() for t in out), ws, ws_bytes)
         return tuple(out)
