@@ -34,6 +34,7 @@ constexpr int kNormAhead = 4;
 // 25.3 and 31.4.
 constexpr int kNormWaves = 2048;
 constexpr int kNormBackWgs = 1024;    // at most, in the backward: partial sums of dw
+constexpr int64_t kNormMaxWgs = ((int64_t(1) << 32) - 1) / kNormThreads;  // a launch takes fewer than 2^32 threads
 
 struct NormArgs {
     const void *q, *k;
@@ -293,7 +294,7 @@ NormGrid norm_grid(const hyena_qk_norm_params_t& p, int64_t tokens, bool back) {
         const int64_t most = kNormBackWgs / g.y < 1 ? 1 : kNormBackWgs / g.y;
         x = x > most ? most : x;
     }
-    g.x = (unsigned)x;
+    g.x = (unsigned)(x < kNormMaxWgs ? x : kNormMaxWgs);  // a workgroup walks over the tokens beyond
     return g;
 }
 
