@@ -539,6 +539,12 @@ constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxSeqs = int64_t(1) << 24;
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // elements: 64 rows stay below 2^31 bytes
 
+// A launch takes fewer than 2^32 threads along an axis.
+constexpr bool fits_launch(int64_t blocks, int64_t threads) { return blocks < ((int64_t(1) << 32) + threads - 1) / threads; }
+// workgroups a (sequence, value head) of the scans, and their threads
+constexpr int scan_columns(bool bf) { return bf ? 32 : 16; }
+constexpr int scan_threads(bool bf) { return bf ? 256 : 192; }
+
 constexpr int kCus = 256;
 // Shorter pieces gain nothing: the ends' launch and the carries (5 us a piece) cost what the
 // shorter scans save. One bf16 sequence, 6 heads of 128, cut and whole: 1600 tokens 59 and
@@ -561,10 +567,12 @@ struct DeltaCall {
     int dkp;  // dim_k rounded up to 64 or 128
 };
 
-// shape alone; and with the sequences and (unless null) the inputs: fills c
+// shape alone; and with the sequences and (unless null) the inputs: fills c; and whether the
+// launches over whole sequences take that many
 hyena_status_t delta_check_shape(const hyena_delta_params_t* p, DeltaCall& c);
 hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
                            const hyena_delta_inputs_t* in, DeltaCall& c);
+hyena_status_t delta_check_launches(const DeltaCall& c);
 // bytes of the preparation's workspace; pointers from base
 size_t delta_prep_layout(const DeltaCall& c, bool bwd, unsigned char* base, delta::Prep& o);
 hipError_t delta_prep(const DeltaCall& c, bool bwd, const delta::Prep& o, hipStream_t st);

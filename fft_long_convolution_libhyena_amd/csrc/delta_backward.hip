@@ -47,6 +47,7 @@ hipError_t launch_rev_t(const DeltaCall& c, RevArgs a, hipStream_t st) {
     using Cfg = RevCfg<BF, DK>;
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
     static_assert(lds <= 160 * 1024, "LDS of a CU");
+    static_assert(16 * Cfg::NB == scan_columns(BF) && Cfg::threads <= scan_threads(BF), "what delta_check_launches takes it for");
     a.nblk = (c.shape.dv + 16 * Cfg::NB - 1) / (16 * Cfg::NB);
     a.nb16 = (c.shape.dv + 15) / 16;
     const int64_t pairs = (a.pieces.slots * c.shape.hv + 7) / 8 * 8;
@@ -86,7 +87,7 @@ extern "C" {
 size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                             const int64_t* seq_start) {
     hy::DeltaCall c;
-    if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
+    if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK || hy::delta_check_launches(c) != HYENA_OK) return 0;
     return hy::back_layout(c, nullptr).bytes;
 }
 
@@ -98,7 +99,8 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
     using hy::aligned16;
     hy::DeltaCall c;
     if (!in) return HYENA_ERR_INVALID_ARG;
-    const hyena_status_t st = hy::delta_check(params, N, tokens, seq_start, in, c);
+    hyena_status_t st = hy::delta_check(params, N, tokens, seq_start, in, c);
+    if (st == HYENA_OK) st = hy::delta_check_launches(c);
     if (st != HYENA_OK) return st;
     const void* need_rows[] = {dout, dq, dk, dv, dg, dbeta};
     for (const void* p : need_rows)

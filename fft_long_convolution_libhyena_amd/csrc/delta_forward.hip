@@ -51,6 +51,14 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
     return HYENA_OK;
 }
 
+hyena_status_t delta_check_launches(const DeltaCall& c) {
+    const int w = scan_columns(c.bf);
+    const int64_t pairs = (c.seqs.N * c.shape.hv + 7) / 8 * 8;
+    return fits_launch(c.slots, kThreads) && fits_launch(pairs * ((c.shape.dv + w - 1) / w), scan_threads(c.bf))
+               ? HYENA_OK
+               : HYENA_ERR_UNSUPPORTED;
+}
+
 size_t delta_prep_layout(const DeltaCall& c, bool bwd, unsigned char* base, Prep& o) {
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -85,6 +93,8 @@ template <bool BF, int DK, int MODE>
 hipError_t launch_scan_t(const DeltaCall& c, ScanArgs a, hipStream_t st) {
     using Cfg = ScanCfg<BF, DK, MODE>;
     constexpr int lds = (int)sizeof(typename Cfg::Lds);
+    static_assert(Cfg::ENDS || (16 * Cfg::NB == scan_columns(BF) && Cfg::threads <= scan_threads(BF)),
+                  "what delta_check_launches takes them for (the ends run on few workgroups)");
     const int w = 16 * Cfg::NB;
     a.nbv = (c.shape.dv + w - 1) / w;
     a.nblk = a.nbv + (Cfg::ENDS ? (DK + w - 1) / w : 0);
@@ -168,7 +178,7 @@ extern "C" {
 size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                    const int64_t* seq_start) {
     hy::DeltaCall c;
-    if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
+    if (hy::delta_check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK || hy::delta_check_launches(c) != HYENA_OK) return 0;
     hy::delta::Prep o;
     hy::delta::Pieces p;
     return hy::delta_prep_layout(c, false, nullptr, o) + hy::delta_pieces_layout(c, false, nullptr, p);
@@ -181,7 +191,8 @@ hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N
     using hy::aligned16;
     hy::DeltaCall c;
     if (!in) return HYENA_ERR_INVALID_ARG;
-    const hyena_status_t st = hy::delta_check(params, N, tokens, seq_start, in, c);
+    hyena_status_t st = hy::delta_check(params, N, tokens, seq_start, in, c);
+    if (st == HYENA_OK) st = hy::delta_check_launches(c);
     if (st != HYENA_OK) return st;
     if ((tokens > 0 && !o) || !aligned16(o) || !aligned16(state_in) || !aligned16(state_out))
         return HYENA_ERR_INVALID_ARG;

@@ -175,12 +175,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_delta_step(StepArgs a) {
         if (cok && r0 + 8 * i < dk) *reinterpret_cast<f32x4*>(sp + (int64_t)(r0 + 8 * i) * dv) = S[i];
 }
 
+// a head's blocks together, so that q, k and the slots are read once for them (one wave a
+// workgroup: 36.9 us in place of 34.2 at 96 rows of 16 heads of 128 x 128, the same at 1 to 32)
+int step_waves(const StepArgs& a) { return a.nblk < kMaxWaves ? a.nblk : kMaxWaves; }
+
 template <bool BF, int DK>
 hipError_t launch_step_t(const StepArgs& a, hipStream_t st) {
-    // a head's blocks together, so that q, k and the slots are read once for them (one wave a
-    // workgroup: 36.9 us in place of 34.2 at 96 rows of 16 heads of 128 x 128, the same at 1 to 32)
     const int64_t rows = a.B * a.sh.hv;
-    const int waves = a.nblk < kMaxWaves ? a.nblk : kMaxWaves;
+    const int waves = step_waves(a);
     hipLaunchKernelGGL((k_delta_step<BF, DK>), dim3((unsigned)rows, (unsigned)((a.nblk + waves - 1) / waves)),
                        dim3(64 * waves), 0, st, a);
     return hipGetLastError();
@@ -204,6 +206,7 @@ hyena_status_t hyena_delta_step(const hyena_delta_params_t* params, int64_t B, i
     if (!slots && num_states < B) return HYENA_ERR_INVALID_ARG;
     hy::StepArgs a{c.shape, in->q, in->k, in->v, in->g, in->beta, states, slots, B, T, num_states, o,
                    (c.shape.dv + 31) / 32};
+    if (!hy::delta::fits_launch(B * c.shape.hv, 64 * hy::step_waves(a))) return HYENA_ERR_UNSUPPORTED;
     hipError_t e;
     if (c.bf)
         e = c.dkp == 64 ? hy::launch_step_t<true, 64>(a, stream) : hy::launch_step_t<true, 128>(a, stream);

@@ -693,8 +693,10 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
  * them, and another cut may round differently. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, heads_v not
  * a multiple of heads_k, bad ld or scale), HYENA_ERR_UNSUPPORTED (dims outside the
- * ranges above, heads_v > 65535, N > 2^24, tokens > 2^31, or more than 2^30 (chunk,
- * head) or 2^26 (sequence, head) pairs), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+ * ranges above, heads_v > 65535, N > 2^24, tokens > 2^31, more than 2^30 (chunk,
+ * head) or 2^26 (sequence, head) pairs, or a launch of 2^32 threads or more: 256 for each
+ * chunk, and for each (sequence, head) pair 256 for every 32 columns of dim_v, in fp32 192
+ * for every 16), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
 hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                    const int64_t* seq_start, const hyena_delta_inputs_t* in, const float* state_in,
                                    void* o, float* state_out, void* workspace, size_t workspace_bytes,
@@ -736,7 +738,9 @@ hyena_status_t hyena_delta_backward(const hyena_delta_params_t* params, int64_t 
  *          successive tokens of it. A row whose slot is outside [0, num_states) gives
  *          zeros and touches no state (rows that pad a captured batch).
  * All arithmetic is fp32. Enqueued on `stream`; no workspace. Errors as
- * hyena_delta_forward, of N = B and tokens = B*T; HYENA_ERR_INVALID_ARG also for
+ * hyena_delta_forward, of N = B and tokens = B*T, but for the launch: HYENA_ERR_UNSUPPORTED
+ * where 64 threads for every 32 columns of dim_v (at most 256) of each (row, head) pair
+ * are 2^32 or more; HYENA_ERR_INVALID_ARG also for
  * B, T or num_states below 1 and for NULL slots with num_states < B. */
 hyena_status_t hyena_delta_step(const hyena_delta_params_t* params, int64_t B, int64_t T,
                                 const hyena_delta_inputs_t* in, float* states, int64_t num_states,
