@@ -45,7 +45,7 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
     c.seqs.tokens = tokens;
     c.seqs.T = seq_start ? 0 : tokens / N;
     c.seqs.cpt = (c.seqs.T + kC - 1) / kC;
-    c.slots = seq_start ? tokens / kC + N : N * c.seqs.cpt;
+    c.slots = tokens < 1 ? 0 : seq_start ? tokens / kC + N : N * c.seqs.cpt;
     // one workgroup per (slot, value head) and per column block of a (sequence, value head)
     if (c.slots * p->heads_v > (int64_t(1) << 30) || N * p->heads_v > (int64_t(1) << 26)) return HYENA_ERR_UNSUPPORTED;
     return HYENA_OK;

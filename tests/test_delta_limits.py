@@ -43,3 +43,11 @@ def test_many_chunks_of_one_sequence(lib):  # noqa: F811
 def test_steps(lib, hv, dv, B):  # noqa: F811
     p = small(heads_v=hv, dim_v=dv)
     assert lib.hyena_delta_step(ctypes.byref(p), B, 1, ctypes.byref(rows(p)), P, B, None, P, None) == UNSUPPORTED
+
+
+def test_no_tokens_need_no_workspace(lib):  # noqa: F811
+    """Packed sequences that are all empty have no chunks, whatever their number."""
+    for start in (None, P):
+        for N in (1, 2, 1000):
+            assert lib.hyena_delta_workspace_bytes(ctypes.byref(params()), N, 0, start) == 0
+            assert lib.hyena_delta_backward_workspace_bytes(ctypes.byref(params()), N, 0, start) == 0
