@@ -21,6 +21,7 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
     if (N < 1 || tokens < 0 || (!seq_start && tokens % N)) return HYENA_ERR_INVALID_ARG;
     if (!(p->scale >= -3.402823466e38f && p->scale <= 3.402823466e38f)) return HYENA_ERR_INVALID_ARG;
     if (((uintptr_t)seq_start & 7u) != 0) return HYENA_ERR_INVALID_ARG;
+    if (p->heads_v * p->dim_v > kMaxLd || p->heads_k * p->dim_k > kMaxLd) return HYENA_ERR_UNSUPPORTED;
     if (in) {
         c.in = *in;
         const void* rows[] = {in->q, in->k, in->v};
@@ -38,8 +39,7 @@ hyena_status_t delta_check(const hyena_delta_params_t* p, int64_t N, int64_t tok
         c.shape.ldk = in->ldk;
         c.shape.ldv = in->ldv;
     }
-    if (N > kMaxSeqs || tokens > kMaxTokens || p->heads_v * p->dim_v > kMaxLd || p->heads_k * p->dim_k > kMaxLd)
-        return HYENA_ERR_UNSUPPORTED;
+    if (N > kMaxSeqs || tokens > kMaxTokens) return HYENA_ERR_UNSUPPORTED;
     c.seqs.start = seq_start;
     c.seqs.N = N;
     c.seqs.tokens = tokens;

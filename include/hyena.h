@@ -656,7 +656,7 @@ typedef struct hyena_delta_params_s {
 /* Device arrays of one call. Token t's heads lie behind each other at
  *   q + t*ldq, k + t*ldk [heads_k][dim_k],   v + t*ldv [heads_v][dim_v]
  * (elements; q, k and v may be column ranges of one projection's rows); ld* at
- * least the heads' width, a multiple of 16 bytes and at most 2^31.
+ * least the heads' width, a multiple of 16 bytes and at most 2^22.
  * g, beta [tokens][heads_v], dense, aligned to their elements. */
 typedef struct hyena_delta_inputs_s {
     const void* q;
@@ -690,13 +690,15 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
  * reproducible, and those of a sequence of up to 1536 tokens do not depend on the other
  * sequences of the call. Longer ones are cut into pieces that run side by side where the
  * call has few (sequence, head) pairs; how is a rule on the sizes, N and tokens among
- * them, and another cut may round differently. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
- * pointers, sizes below 1, tokens not a multiple of N without seq_start, heads_v not
- * a multiple of heads_k, bad ld or scale), HYENA_ERR_UNSUPPORTED (dims outside the
- * ranges above, heads_v > 65535, N > 2^24, tokens > 2^31, more than 2^30 (chunk,
- * head) or 2^26 (sequence, head) pairs, or a launch of 2^32 threads or more: 256 for each
- * chunk, and for each (sequence, head) pair 256 for every 32 columns of dim_v, in fp32 192
- * for every 16), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+ * them, and another cut may round differently. Outputs must not alias inputs, but for
+ * state_out. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
+ * pointers, sizes below 1, tokens not a multiple of N without seq_start, heads_v not a
+ * multiple of heads_k, bad ld or scale), HYENA_ERR_UNSUPPORTED (dims outside the ranges
+ * above, heads_v > 65535, heads_k * dim_k or heads_v * dim_v > 2^22, N > 2^24,
+ * tokens > 2^31, more than 2^30 (chunk, head) or 2^26 (sequence, head) pairs, or a launch
+ * of 2^32 threads or more: 256 for each chunk, and for each (sequence, head) pair 256 for
+ * every 32 columns of dim_v, in fp32 192 for every 16), HYENA_ERR_WORKSPACE,
+ * HYENA_ERR_DEVICE. */
 hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                    const int64_t* seq_start, const hyena_delta_inputs_t* in, const float* state_in,
                                    void* o, float* state_out, void* workspace, size_t workspace_bytes,

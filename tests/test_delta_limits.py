@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_delta_args import P, UNSUPPORTED, WORKSPACE, backward, forward, inputs, lib, params  # noqa: F401
+from test_delta_args import INVALID, P, UNSUPPORTED, WORKSPACE, backward, forward, inputs, lib, params  # noqa: F401
 
 
 def small(**kw):
@@ -51,3 +51,20 @@ def test_no_tokens_need_no_workspace(lib):  # noqa: F811
         for N in (1, 2, 1000):
             assert lib.hyena_delta_workspace_bytes(ctypes.byref(params()), N, 0, start) == 0
             assert lib.hyena_delta_backward_workspace_bytes(ctypes.byref(params()), N, 0, start) == 0
+
+
+@pytest.mark.parametrize("which", ["ldq", "ldk", "ldv"])
+def test_strides_between_tokens(lib, which):  # noqa: F811
+    """At most 2^22 elements: a chunk's 64 rows are addressed with 32 bits."""
+    assert forward(lib, i=inputs(**{which: 1 << 22}), ws=None) == WORKSPACE
+    assert forward(lib, i=inputs(**{which: (1 << 22) + 8})) == INVALID
+    assert backward(lib, i=inputs(**{which: 1 << 22}), ws=None) == WORKSPACE
+    assert backward(lib, i=inputs(**{which: (1 << 22) + 8})) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(heads_k=1, heads_v=65528, dim_v=72), dict(heads_k=65528, heads_v=65528, dim_k=72, dim_v=8)])
+def test_rows_wider_than_a_stride(lib, kw):  # noqa: F811
+    p, wide = params(**kw), dict(ldq=1 << 23, ldk=1 << 23, ldv=1 << 23)
+    assert forward(lib, p, N=1, tokens=64, i=inputs(**wide)) == UNSUPPORTED
+    assert lib.hyena_delta_workspace_bytes(ctypes.byref(p), 1, 64, None) == 0
+    assert lib.hyena_delta_step(ctypes.byref(p), 1, 1, ctypes.byref(inputs(**wide)), P, 1, None, P, None) == UNSUPPORTED
