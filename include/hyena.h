@@ -686,7 +686,10 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
  * The state is held in fp32 from the first token to the last; bf16 outputs are
  * rounded once from sums whose operands are bf16 or sums of two bf16 parts, fp32
  * results have the accuracy of fp32 products. Decays below exp(-200) count as 0 and
- * g = -inf resets the state. Every sum has a fixed order: results are bitwise
+ * g = -inf resets the state. A value that is not finite (but for g = -inf) spoils what
+ * follows it, as in the recurrence, and the tokens in front of it in its own chunk (64
+ * tokens, counted from the sequence's first): of v in its column, of k, g and beta in their
+ * value heads. One of q spoils its token alone. Every sum has a fixed order: results are bitwise
  * reproducible, and those of a sequence of up to 1536 tokens do not depend on the other
  * sequences of the call. Longer ones are cut into pieces that run side by side where the
  * call has few (sequence, head) pairs; how is a rule on the sizes, N and tokens among

@@ -29,3 +29,47 @@ def test_empty_sequences_need_no_workspace(packed, dtype):
     assert r.lib.hyena_delta_backward(r._params(None), N, 0, start, ctypes.byref(none), s.data_ptr(), None, ds.data_ptr(), None,
                                       None, None, None, None, dout.data_ptr(), None, 0, stream) == 0
     assert torch.equal(out, s) and torch.equal(dout, ds)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+def test_where_a_value_that_is_not_finite_shows(name, bad, dtype):
+    """q's in its token; v's in its column from the token's chunk on, the others' in their value
+    heads from that chunk on: earlier chunks, other heads and other sequences keep their bits."""
+    from fft_long_convolution_libhyena_amd import DeltaRule
+
+    hk, hv, dk, dv, lens = 2, 4, 64, 40, [200, 90]
+    d = D.make(lens, hk, hv, dk, dv, dtype, seed=17)
+    r = DeltaRule(hk, hv, dk, dv, dtype)
+
+    def call():
+        return r.forward(*(d[n].cuda() for n in ("q", "k", "v", "g", "beta")), state=d["state"].cuda(), seq_start=D.starts(lens, "cuda"))
+
+    o0, s0 = call()
+    d[name][100, 1, ...] = bad  # head 1, token 36 of the second chunk
+    if name == "v":
+        d[name][100, 1, :] = 0.5
+        d[name][100, 1, 3] = bad
+    o, s = call()
+    heads = {"q": [2, 3], "k": [2, 3]}.get(name, [1])
+    same = torch.ones_like(o, dtype=torch.bool)
+    if name == "q":
+        same[100, heads] = False
+    elif name == "v":
+        same[64:200, 1] = False
+    else:
+        same[64:200, heads] = False
+    assert torch.equal(o[same], o0[same]) and bool(torch.isfinite(o[same]).all())
+    if name == "v":  # its other columns were changed here, but are finite
+        fine = torch.isfinite(o[64:200, 1])
+        assert bool(fine[..., [i for i in range(dv) if i != 3]].all()) and not bool(fine[36:, 3].any())
+    others = [i for i in range(hv) if i not in heads]
+    assert torch.equal(s[1], s0[1]) and torch.equal(s[0, others], s0[0, others])
+    if name != "g" or bad != float("inf"):  # exp(inf) may meet a zero or an infinity first
+        assert not bool(torch.isfinite(o[100, heads] if name != "v" else o[100, 1, 3]).all())
+    if name == "q":
+        assert torch.equal(s, s0)
+    elif name == "v":
+        keep = [i for i in range(dv) if i != 3]
+        assert bool(torch.isfinite(s[0, 1][:, keep]).all()) and not bool(torch.isfinite(s[0, 1][:, 3]).any())
