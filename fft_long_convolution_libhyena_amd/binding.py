@@ -37,7 +37,7 @@ EXPORTS = ("hyena_plan_create", "hyena_plan_create_path", "hyena_plan_create_ex"
            "hyena_filter_spectrum2d_batched", "hyena_conv2d_forward_per_sample", "hyena_filter_spectrum3d_batched",
            "hyena_conv3d_forward_per_sample", "hyena_plan2d_create_ex", "hyena_plan3d_create_ex",
            "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_delta_workspace_bytes",
-           "hyena_delta_forward", "hyena_delta_backward_workspace_bytes", "hyena_delta_backward", "hyena_delta_step",
+           "hyena_delta_forward", "hyena_delta_clear_rows", "hyena_delta_backward_workspace_bytes", "hyena_delta_backward", "hyena_delta_step",
            "hyena_qk_norm_forward", "hyena_qk_norm_backward_workspace_bytes", "hyena_qk_norm_backward",
            "hyena_status_string")
 
@@ -189,6 +189,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.hyena_delta_workspace_bytes.restype = sz
     lib.hyena_delta_forward.argtypes = [dp, i64, i64, vp, di, vp, vp, vp, vp, sz, vp]
     lib.hyena_delta_forward.restype = ci
+    lib.hyena_delta_clear_rows.argtypes = [i64, i64, vp, ci, ctypes.POINTER(vp), ctypes.POINTER(i64), vp]
+    lib.hyena_delta_clear_rows.restype = ci
     lib.hyena_delta_backward_workspace_bytes.argtypes = [dp, i64, i64, vp]
     lib.hyena_delta_backward_workspace_bytes.restype = sz
     lib.hyena_delta_backward.argtypes = [dp, i64, i64, vp, di] + [vp] * 10 + [sz, vp]
@@ -923,22 +925,34 @@ class DeltaRule:
             return t, t.data_ptr()
         return t, _dense(t, name, shape, dtype, device)
 
+    def _clear(self, N, tokens, starts, device, *outs):
+        """Zeros in the rows of fresh outputs that belong to no sequence (and are not written)."""
+        if tokens:
+            n = len(outs)
+            _launch(self._torch, "hyena_delta_clear_rows", self.lib.hyena_delta_clear_rows, device, N, tokens, starts, n,
+                    (ctypes.c_void_p * n)(*(t.data_ptr() for t in outs)),
+                    (ctypes.c_int64 * n)(*(t.stride(0) * t.element_size() for t in outs)))
+
     def forward(self, q, k, v, g, beta, state=None, scale=None, seq_start=None, o=None, state_out=None,
                 workspace=None):
         """hyena_delta_forward: q, k [B, T, heads_k, dim_k], v [B, T, heads_v, dim_v] (views with
         one stride between tokens are taken as they are), g, beta [B, T, heads_v]; or all with
         [tokens] in place of [B, T] and seq_start [N + 1] int64 offsets on the device. state
-        [N, heads_v, dim_k, dim_v] fp32 or None (zeros). Returns (o like v, the final states)."""
+        [N, heads_v, dim_k, dim_v] fp32 or None (zeros). Returns (o like v, the final states); rows
+        that belong to no sequence are zeros in o, but left as they were in an o that is given."""
         torch = self._torch
         dev, rows, N, tokens, starts = self._sequences(q, seq_start)
         inputs = self._inputs(q, k, v, g, beta, rows, dev)
         states = self.state_shape(N)
         sp = _dense(state, "state", states, torch.float32, dev) if state is not None else None
+        fresh = o is None
         o, op = self._out(o, "o", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
         state_out, fp = self._out(state_out, "state_out", states, torch.float32, dev)
         params = self._params(scale)
         need = self.lib.hyena_delta_workspace_bytes(params, N, tokens, starts)
         workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
+        if fresh and starts is not None:
+            self._clear(N, tokens, starts, dev, o)
         _launch(torch, "hyena_delta_forward", self.lib.hyena_delta_forward, dev, params, N, tokens, starts, inputs, sp, op,
                 fp, ws, ws_bytes)
         return o, state_out
@@ -946,20 +960,24 @@ class DeltaRule:
     def backward(self, q, k, v, g, beta, do, state=None, dstate_out=None, scale=None, seq_start=None, workspace=None):
         """hyena_delta_backward: the gradients (dq, dk, dv, dg, dbeta, dstate) of the forward's
         inputs (dense, in the dtype; dstate fp32) for the gradient do [like o] of its outputs and,
-        unless None, dstate_out [N, heads_v, dim_k, dim_v] fp32 of its final states."""
+        unless None, dstate_out [N, heads_v, dim_k, dim_v] fp32 of its final states. Rows that
+        belong to no sequence have gradients of zero."""
         torch = self._torch
         dev, rows, N, tokens, starts = self._sequences(q, seq_start)
         inputs = self._inputs(q, k, v, g, beta, rows, dev)
-        Hk, Hv, Dk, Dv, states = self.heads_k, self.heads_v, self.dim_k, self.dim_v, self.state_shape(N)
-        dop = _dense(do, "do", (*rows, Hv, Dv), self.io_dtype, dev)
+        states = self.state_shape(N)
+        dop = _dense(do, "do", (*rows, self.heads_v, self.dim_v), self.io_dtype, dev)
         sp, dsp = (_dense(t, name, states, torch.float32, dev) if t is not None else None
                    for name, t in (("state", state), ("dstate_out", dstate_out)))
+        Hk, Hv, Dk, Dv = self.heads_k, self.heads_v, self.dim_k, self.dim_v
         out = [torch.empty((*rows, *shape), dtype=self.io_dtype, device=dev)
                for shape in ((Hk, Dk), (Hk, Dk), (Hv, Dv), (Hv,), (Hv,))]
         out.append(torch.empty(states, dtype=torch.float32, device=dev))
         params = self._params(scale)
         need = self.lib.hyena_delta_backward_workspace_bytes(params, N, tokens, starts)
         workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
+        if starts is not None:
+            self._clear(N, tokens, starts, dev, *out[:5])
         _launch(torch, "hyena_delta_backward", self.lib.hyena_delta_backward, dev, params, N, tokens, starts, inputs, sp,
                 dop, dsp, *(t.data_ptr() for t in out), ws, ws_bytes)
         return tuple(out)

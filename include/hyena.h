@@ -707,6 +707,16 @@ hyena_status_t hyena_delta_forward(const hyena_delta_params_t* params, int64_t N
                                    void* o, float* state_out, void* workspace, size_t workspace_bytes,
                                    hipStream_t stream);
 
+/* Zeros the rows of `count` (1 to 8) arrays [tokens][row_bytes] that belong to no sequence
+ * of a packed call, those in front of seq_start[0] and from seq_start[N] on: outputs of the
+ * calls here leave them as they were, and gradients of inputs that were not read are 0.
+ * arrays and row_bytes are host arrays; each array and row 2-byte aligned. Offsets outside
+ * [0, tokens] are held to it. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or
+ * misaligned pointers, N < 1, tokens < 0, count or a row's size out of range),
+ * HYENA_ERR_DEVICE. */
+hyena_status_t hyena_delta_clear_rows(int64_t N, int64_t tokens, const int64_t* seq_start, int count,
+                                      void* const* arrays, const int64_t* row_bytes, hipStream_t stream);
+
 /* Bytes of workspace hyena_delta_backward needs: the forward's, the states before and
  * the state gradients behind every chunk of 64 tokens, and two arrays of o's shape, all at
  * four bytes a value. Returns 0 as hyena_delta_workspace_bytes. */

@@ -68,3 +68,15 @@ def test_rows_wider_than_a_stride(lib, kw):  # noqa: F811
     assert forward(lib, p, N=1, tokens=64, i=inputs(**wide)) == UNSUPPORTED
     assert lib.hyena_delta_workspace_bytes(ctypes.byref(p), 1, 64, None) == 0
     assert lib.hyena_delta_step(ctypes.byref(p), 1, 1, ctypes.byref(inputs(**wide)), P, 1, None, P, None) == UNSUPPORTED
+
+
+def test_clearing_rows(lib):  # noqa: F811
+    def clear(N=2, tokens=8, start=P, count=2, arrays=(P, P + 2), sizes=(16, 6)):
+        n = len(arrays)
+        return lib.hyena_delta_clear_rows(N, tokens, start, count, (ctypes.c_void_p * n)(*arrays), (ctypes.c_int64 * n)(*sizes), None)
+
+    for kw in (dict(N=0), dict(tokens=-1), dict(start=None), dict(start=P + 4), dict(count=0), dict(count=9),
+               dict(arrays=(None, P)), dict(arrays=(P + 1, P)), dict(sizes=(0, 6)), dict(sizes=(16, 7)), dict(sizes=(-2, 6))):
+        assert clear(**kw) == INVALID, kw
+    assert lib.hyena_delta_clear_rows(2, 8, P, 1, None, None, None) == INVALID
+    assert clear(tokens=0) == 0

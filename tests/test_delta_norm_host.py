@@ -52,3 +52,22 @@ def test_delta_rule_refuses_a_workspace_it_cannot_write(launches, backward):
         with pytest.raises(ValueError):
             r.backward(*x, x[2], workspace=ws) if backward else r.forward(*x, workspace=ws)
     assert not launches
+
+
+def test_rows_of_no_sequence_are_cleared_in_what_the_call_allocates(launches):
+    """They have no result: o's are dropped, and their gradient is 0. A caller's o is left as it was."""
+    r, tokens = DeltaRule(1, 2, 64, 64), 7
+    x = [torch.zeros(tokens, h, 64, dtype=torch.bfloat16) for h in (1, 1, 2)]
+    x += [torch.zeros(tokens, 2, dtype=torch.bfloat16) for _ in range(2)]
+    start = torch.tensor([1, 3, 6])
+    cleared = lambda: [(a[:4], list(a[4]), list(a[5])) for n, a in launches if n == "hyena_delta_clear_rows"]  # noqa: E731
+    o, _ = r.forward(*x, seq_start=start)
+    want = [((2, tokens, start.data_ptr(), 1), [o.data_ptr()], [2 * 64 * 2])]
+    assert cleared() == want and launches[-1][0] == "hyena_delta_forward"
+    r.forward(*x, seq_start=start, o=o)
+    r.forward(*(t[None] for t in x))  # every row belongs to a sequence
+    r.backward(*(t[None] for t in x), x[2][None])
+    assert cleared() == want
+    grads = r.backward(*x, x[2], seq_start=start)[:5]
+    want.append(((2, tokens, start.data_ptr(), 5), [t.data_ptr() for t in grads], [128, 128, 256, 4, 4]))
+    assert cleared() == want and launches[-1][0] == "hyena_delta_backward"
