@@ -29,6 +29,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/hyena.h"
 
 namespace hy {
@@ -57,7 +59,7 @@ struct Io<true> {
     static constexpr int NE = 3;  // parts of the residuals and of what a chunk adds to the state; their gradients'
     static constexpr int NO = 2;  // parts of the state and of u against Q and P
     static constexpr int NP = 2;  // parts of P
-    static constexpr int NK = 2;  // parts of what the backward's scans keep
+    static constexpr int NK = 2;  // parts of what the backward's scans keep, in its products
 };
 template <>
 struct Io<false> {
@@ -67,7 +69,7 @@ struct Io<false> {
     static constexpr int NE = 3;
     static constexpr int NO = 3;
     static constexpr int NP = 3;
-    static constexpr int NK = 1;  // kept as fp32
+    static constexpr int NK = 1;  // as fp32
 };
 
 // Row r of row tile t as the scans number them: the pair of tiles 2s, 2s + 1 covers
@@ -513,27 +515,67 @@ struct Prep {
 
 // What the backward's scans leave for the chunk-parallel part: per (slot, value head) and
 // block of 16 columns, the state (its gradient) as KS, a 64-token array as two operand
-// fragments, the bf16 parts behind each other or fp32, 16 or 32 bytes a lane: lane l has
-// column l % 16 of the block, elements 8 (l / 16) .. + 7 of 32. One contiguous store of 1 KiB
-// in place of sixteen of 32-byte pieces. With one part each, dk and dg were up to 3e-3 off and
-// dbeta 3.4e-3 (rounding by itself leaves 1.7e-3); the second parts are 0.5 GB of 4.2 that the
-// backward of 8 sequences of 8192 tokens moves.
+// fragments: lane l has column l % 16 of the block, elements 8 (l / 16) .. + 7 of 32. One
+// contiguous store of 1 KiB in place of sixteen of 32-byte pieces. bf16 calls keep 24 bits of
+// an fp32 value, the upper 16 of a lane's eight in 16 bytes and the rest in 8 behind them: with
+// bf16 alone, dk and dg were up to 3e-3 off and dbeta 3.4e-3 (rounding by itself leaves 1.7e-3);
+// with a second bf16 part the scans and the gradients of 8 sequences of 8192 tokens, which are
+// bound by these bytes, take 1209 us in place of 1118.
 template <bool BF, int KS>
 struct Kept {
-    static constexpr int frag = 512 * (BF ? 2 : 4);                 // bytes of a fragment
-    static constexpr int state = KS * frag, row = 2 * frag;         // of one part of a state, of a 64-token array
-    static constexpr int states = Io<BF>::NK * state, rows = Io<BF>::NK * row;
+    static constexpr int frag = 512 * (BF ? 3 : 4);  // bytes of a fragment
+    static constexpr int state = KS * frag, rows = 2 * frag;
 };
-template <bool BF, int N>
-__device__ __forceinline__ void keep_frag(unsigned char* p, int part, int lane, const f32x4& a, const f32x4& b, const Frag<N>& f) {
+// Fragment s of those at p (n of them; nothing is kept where !ok). bf16 calls store without a
+// branch: the reverse scan's packing then shares a schedule with the products around it (402 us
+// in place of 450). Its fp32 calls, whose registers are all taken, and the forward's keeping
+// scan (297 us in place of 310) fare better with one.
+template <bool BF>
+__device__ __forceinline__ void keep_frag(unsigned char* p, bool ok, int n, int s, int lane, const f32x4& a, const f32x4& b) {
     if constexpr (BF) {
+        uint32_t t[8];
 #pragma unroll
-        for (int n = 0; n < Io<BF>::NK; ++n) *reinterpret_cast<bf16x8*>(p + n * part + lane * 16) = f.p[n];
-    } else {
-        *reinterpret_cast<f32x4*>(p + lane * 32) = a;
-        *reinterpret_cast<f32x4*>(p + lane * 32 + 16) = b;
+        for (int i = 0; i < 4; ++i) {
+            t[i] = __float_as_uint(a[i]) + 0x80u;
+            t[4 + i] = __float_as_uint(b[i]) + 0x80u;
+        }
+        u32x4 hi;
+        u32x2 lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hi[i] = __builtin_amdgcn_perm(t[2 * i + 1], t[2 * i], 0x07060302);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            lo[i] = __builtin_amdgcn_perm(t[4 * i + 1], t[4 * i], 0x0c0c0501) | __builtin_amdgcn_perm(t[4 * i + 3], t[4 * i + 2], 0x05010c0c);
+        const RowBuf to = plain_buf(p, ok ? n * 1536 : 0);
+        __builtin_amdgcn_raw_buffer_store_b128(hi, to, lane * 16, s * 1536, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(lo, to, lane * 8, s * 1536 + 1024, 0);
+    } else if (ok) {
+        *reinterpret_cast<f32x4*>(p + s * 2048 + lane * 32) = a;
+        *reinterpret_cast<f32x4*>(p + s * 2048 + lane * 32 + 16) = b;
     }
 }
+// a lane's part of a kept fragment, on its way and as eight values
+template <bool BF>
+struct KeptRaw {
+    u32x4 a;
+    typename std::conditional<BF, u32x2, u32x4>::type b;
+    __device__ __forceinline__ void load(RowBuf from, uint32_t frag, int lane) {
+        a = __builtin_bit_cast(u32x4, buf_f4(from, frag + lane * (BF ? 16 : 32), 0));
+        if constexpr (BF)
+            b = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(from, (int)(frag + 1024 + lane * 8), 0, 0));
+        else
+            b = __builtin_bit_cast(u32x4, buf_f4(from, frag + lane * 32 + 16, 0));
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (BF)
+                x[i] = __uint_as_float(__builtin_amdgcn_perm(a[i >> 1], b[i >> 2], (i & 1 ? 0x0706000c : 0x0504000c) | ((i & 3) << 8)));
+            else
+                x[i] = __uint_as_float(i < 4 ? a[i & 3] : b[i & 3]);
+        }
+    }
+};
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxSeqs = int64_t(1) << 24;

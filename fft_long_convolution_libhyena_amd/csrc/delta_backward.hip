@@ -31,8 +31,7 @@ BackLayout back_layout(const DeltaCall& c, unsigned char* base) {
         at += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    // of every slot and head, two bf16 parts or fp32
-    const size_t cols = (size_t)c.slots * c.shape.hv * ((c.shape.dv + 15) / 16 * 16) * 4;
+    const size_t cols = (size_t)c.slots * c.shape.hv * ((c.shape.dv + 15) / 16 * 16) * (c.bf ? 3 : 4);  // as Kept
     const size_t states = cols * c.dkp, rows = cols * kC;
     b.s0 = take(states);
     b.ds1 = take(states);

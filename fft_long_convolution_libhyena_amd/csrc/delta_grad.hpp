@@ -14,7 +14,7 @@
 // of both where they cancel (an answer within 1% of v: dbeta 0.18 off); beta = 0 is held at 2^-90.
 // A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO,
 // u, r and the states' columns, the next step's loads in flight), bf16 calls in two halves,
-// the states' second parts in the place of the first; wave w has rows 16 w of every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
+// dS1 in the place of S0; wave w has rows 16 w of every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
 // 8192 tokens, 6 heads of 128 x 128, bf16, 306 us (1235 MB, 4.1 TB/s).
 #pragma once
 #include "delta.hpp"
@@ -86,14 +86,14 @@ template <bool BF, int W>
 struct StepTile;
 template <int W>
 struct StepTile<true, W> : GradTile<true, 32, W> {
-    __device__ __forceinline__ void put8(int c, int e, const u32x4 (&x)[1]) { *this->at16(c, e) = x[0]; }
+    __device__ __forceinline__ void put8(int c, int e, const bf16x8& x) { *this->at16(c, e) = __builtin_bit_cast(u32x4, x); }
     __device__ __forceinline__ Frag<1> op(int lane, int m) const { return this->cols(lane, m, 0); }
 };
 template <int W>
 struct StepTile<false, W> : GradTile<false, W, 32> {
-    __device__ __forceinline__ void put8(int c, int e, const u32x4 (&x)[2]) {
+    __device__ __forceinline__ void put8(int c, int e, const float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) this->put(e + i, c, __uint_as_float(x[i >> 2][i & 3]));
+        for (int i = 0; i < 8; ++i) this->put(e + i, c, x[i]);
     }
     __device__ __forceinline__ Frag<3> op(int lane, int m) const { return this->rows(lane, m, 0); }
 };
@@ -127,7 +127,7 @@ struct GradLds {
     struct Steps {
         GradTile<BF, kC, 32> o;
         StepTile<BF, kC> u[Io<BF>::NK], r[Io<BF>::NK];
-        StepTile<BF, DK> s, d;  // one part at a time
+        StepTile<BF, DK> st[2];  // bf16: both parts of S0, then of dS1; fp32: S0 and dS1
     };
     struct Mats {
         GradMat<BF> w, n;
@@ -151,7 +151,6 @@ void k_delta_grad(GradArgs a) {
     constexpr int V = 16 / (int)E, LPR = 32 / V;  // elements of 16 bytes; lanes of a 32-element row
     constexpr int RPP = kThreads / LPR;           // rows one pass of the workgroup stages
     constexpr int NR = kC / RPP;                  // passes for 64 rows
-    constexpr int NV = (int)E / 2;                // 16-byte pieces of a lane's part of a fragment
     constexpr int NF = DK / 64;                   // state fragments a wave stages (of 2 KS)
     constexpr int NK = Io<BF>::NK;
     using Kp = Kept<BF, KS>;
@@ -190,67 +189,68 @@ void k_delta_grad(GradArgs a) {
         const RowBuf vo = row_buf((T*)a.dv + obase, rows, ldo, dv * E);
         const RowBuf ub = plain_buf((const unsigned char*)a.u + fidx * Kp::rows, nb16 * Kp::rows);
         const RowBuf rb = plain_buf((const unsigned char*)a.r + fidx * Kp::rows, nb16 * Kp::rows);
-        const RowBuf sb = plain_buf((const unsigned char*)a.s0 + fidx * Kp::states, nb16 * Kp::states);
-        const RowBuf db = plain_buf((const unsigned char*)a.ds1 + fidx * Kp::states, nb16 * Kp::states);
+        const RowBuf sb = plain_buf((const unsigned char*)a.s0 + fidx * Kp::state, nb16 * Kp::state);
+        const RowBuf db = plain_buf((const unsigned char*)a.ds1 + fidx * Kp::state, nb16 * Kp::state);
         // a step's 2 blocks: wave w stages fragment w of the four of u and r and fragments
         // NF w .. of the 2 KS of the states; blocks past the last read zeros
-        u32x4 po[NR], pu[NK][NV], pr[NK][NV], ps[NK][NF][NV], pd[NK][NF][NV];
-        auto fetch_states = [&](int c0, int n) {
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const int x = NF * w + f;  // block x / KS, step x % KS
-                const uint32_t s0 = (c0 / 16 + x / KS) * Kp::states + n * Kp::state + (x % KS) * Kp::frag + lane * 8 * E;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    ps[n][f][j] = __builtin_bit_cast(u32x4, buf_f4(sb, s0 + 16 * j, 0));
-                    pd[n][f][j] = __builtin_bit_cast(u32x4, buf_f4(db, s0 + 16 * j, 0));
-                }
-            }
-        };
+        u32x4 po[NR];
+        KeptRaw<BF> pu, pr, ps[NF], pd[NF];
         auto fetch = [&](int c0) {
             const bool ok = c0 + scol < dv;
 #pragma unroll
             for (int i = 0; i < NR; ++i)
                 po[i] = __builtin_bit_cast(u32x4, buf_f4(ob, ok ? (i * RPP + srow) * ldo + (c0 + scol) * E : kNoElem, 0));
-            const uint32_t b0 = (c0 / 16 + (w >> 1)) * Kp::rows + (w & 1) * Kp::frag + lane * 8 * E;
-#pragma unroll
-            for (int n = 0; n < NK; ++n)
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    pu[n][j] = __builtin_bit_cast(u32x4, buf_f4(ub, b0 + n * Kp::row + 16 * j, 0));
-                    pr[n][j] = __builtin_bit_cast(u32x4, buf_f4(rb, b0 + n * Kp::row + 16 * j, 0));
-                }
-            fetch_states(c0, 0);
-        };
-        auto put_states = [&](int n) {
+            const uint32_t rows = (c0 / 16) * Kp::rows + w * Kp::frag, states = (c0 / 16) * Kp::state + NF * w * Kp::frag;
+            pu.load(ub, rows, lane);
+            pr.load(rb, rows, lane);
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                const int x = NF * w + f;
-                l.step.s.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, ps[n][f]);
-                l.step.d.put8(16 * (x / KS) + col, 32 * (x % KS) + 8 * g, pd[n][f]);
+                ps[f].load(sb, states + f * Kp::frag, lane);
+                pd[f].load(db, states + f * Kp::frag, lane);
             }
         };
-        // <dS1, S0> goes into dg of every token of the chunk and beyond: from all parts of both
-        // (with one each dg was up to 6.7e-3 off where the final states' gradient outweighs the
-        // outputs')
+        // into LDS: rows' fragment w, all parts; the states', first parts (the second returned)
+        auto put_rows = [&](StepTile<BF, kC>(&t)[NK], const KeptRaw<BF>& p) {
+            float x[8];
+            p.get(x);
+            const int c = 16 * (w >> 1) + col, e = 32 * (w & 1) + 8 * g;
+            if constexpr (BF) {
+                const Frag<NK> f = split8<NK>(x);
+#pragma unroll
+                for (int n = 0; n < NK; ++n) t[n].put8(c, e, f.p[n]);
+            } else {
+                t[0].put8(c, e, x);
+            }
+        };
+        auto put_state = [&](const KeptRaw<BF>(&p)[NF], int t) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const int x = NF * w + f, c = 16 * (x / KS) + col, e = 32 * (x % KS) + 8 * g;  // block x / KS, step x % KS
+                float y[8];
+                p[f].get(y);
+                if constexpr (BF) {
+                    const Frag<NK> parts = split8<NK>(y);
+#pragma unroll
+                    for (int n = 0; n < NK; ++n) l.step.st[n].put8(c, e, parts.p[n]);
+                } else {
+                    l.step.st[t].put8(c, e, y);
+                }
+            }
+        };
+        // <dS1, S0> goes into dg of every token of the chunk and beyond: from all bits of both
+        // (from bf16 alone dg was up to 6.7e-3 off where the final states' gradient outweighs
+        // the outputs')
         auto dot_states = [&]() {
-            float s = 0.f;
+            float dot = 0.f;
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
+            for (int f = 0; f < NF; ++f) {
+                float s[8], d[8];
+                ps[f].get(s);
+                pd[f].get(d);
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (BF) {
-                            auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
-                            auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
-                            s = fmaf(lo(ps[0][f][j][i]) + lo(ps[1][f][j][i]), lo(pd[0][f][j][i]) + lo(pd[1][f][j][i]), s);
-                            s = fmaf(hi(ps[0][f][j][i]) + hi(ps[1][f][j][i]), hi(pd[0][f][j][i]) + hi(pd[1][f][j][i]), s);
-                        } else {
-                            s = fmaf(__uint_as_float(ps[0][f][j][i]), __uint_as_float(pd[0][f][j][i]), s);
-                        }
-                    }
-            return s;
+                for (int i = 0; i < 8; ++i) dot = fmaf(s[i], d[i], dot);
+            }
+            return dot;
         };
         fetch(0);
         if (w == 0) {
@@ -272,20 +272,20 @@ void k_delta_grad(GradArgs a) {
             __syncthreads();  // the step before (or the head before) has read its tiles
 #pragma unroll
             for (int i = 0; i < NR; ++i) *l.step.o.at16(i * RPP + srow, scol) = po[i];
-#pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                l.step.u[n].put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pu[n]);
-                l.step.r[n].put8(16 * (w >> 1) + col, 32 * (w & 1) + 8 * g, pr[n]);
-            }
-            put_states(0);
-            if constexpr (BF) {
-                fetch_states(c0, 1);
-            } else {
-                sd += dot_states();
+            put_rows(l.step.u, pu);
+            __builtin_amdgcn_sched_barrier(0);
+            put_rows(l.step.r, pr);
+            __builtin_amdgcn_sched_barrier(0);
+            put_state(ps, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            sd += dot_states();
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!BF) {
+                put_state(pd, 1);
                 if (c0 + 32 < dv) fetch(c0 + 32);
             }
             lds_barrier();
-            auto parts = [&](const StepTile<BF, kC>(&t)[NK], int m) {
+            auto parts = [&](const auto& t, int m) {
                 if constexpr (BF)
                     return Frag<2>{{t[0].op(lane, m).p[0], t[1].op(lane, m).p[0]}};
                 else
@@ -322,24 +322,21 @@ void k_delta_grad(GradArgs a) {
                 }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const auto b = l.step.s.op(lane, m);
+                const auto b = parts(l.step.st, m);
                 qs[m] = mma(ao, b, qs[m]);
                 rs[m] = mma(ar, b, rs[m]);
-                us[m] = mma(au, l.step.d.op(lane, m), us[m]);
+                if constexpr (!BF) us[m] = mma(au, l.step.st[1].op(lane, m), us[m]);
+                if (BF && (m & 1)) __builtin_amdgcn_sched_barrier(0);
             }
             if constexpr (BF) {
-                lds_barrier();  // the first parts have been read
-                put_states(1);
-                sd += dot_states();
+                lds_barrier();  // S0 has been read
+                put_state(pd, 0);
                 if (c0 + 32 < dv) fetch(c0 + 32);
                 lds_barrier();
-                const Frag<1> r0{{ar.p[0]}}, u0{{au.p[0]}};
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const auto b = l.step.s.op(lane, m);
-                    qs[m] = mma(ao, b, qs[m]);
-                    rs[m] = mma(r0, b, rs[m]);
-                    us[m] = mma(u0, l.step.d.op(lane, m), us[m]);
+                    us[m] = mma(au, parts(l.step.st, m), us[m]);
+                    if (m & 1) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }

@@ -312,10 +312,16 @@ void k_delta_rev(RevArgs a) {
         const Tile<NI, DK>& K = l.k[i & (BUF - 1)];
         const RevInputs<DK>& in = l.x[wave][i & 1];
         const int64_t fr = ((slot0 + nch - 1 - i) * hv + h) * a.nb16 + blk;  // this block's fragments
-        if (!ENDS && blk < a.nb16)
+        auto keep_s = [&](int s) {
+            keep_frag<BF>((unsigned char*)a.ds1 + fr * Kp::state, blk < a.nb16, KS, s, lane, S[2 * s], S[2 * s + 1]);
+        };
+        auto keep_r = [&](const f32x4(&r)[4], int s) {
+            keep_frag<BF>((unsigned char*)a.r + fr * Kp::rows, blk < a.nb16, 2, s, lane, r[2 * s], r[2 * s + 1]);
+        };
+        if constexpr (!ENDS && !BF) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                keep_frag<BF>((unsigned char*)a.ds1 + fr * Kp::states + s * Kp::frag, Kp::state, lane, S[2 * s], S[2 * s + 1], sf[s]);
+            for (int s = 0; s < KS; ++s) keep_s(s);
+        }
         // dU = P^T dO + diag(exp(G_last - G)) K dS
         f32x4 x[4] = {};
         Frag<NI> ka[2][4];
@@ -333,6 +339,7 @@ void k_delta_rev(RevArgs a) {
         for (int s = 0; s < KS; ++s) {
             mma_tiles(ka[s & 1], sf[s], x);
             if (s + 2 < KS) read_rows(s + 2);
+            if constexpr (!ENDS && BF) keep_s(s);
             __builtin_amdgcn_sched_barrier(0);
         }
         Frag<NI> kt[2][MT];
@@ -376,11 +383,10 @@ void k_delta_rev(RevArgs a) {
         for (int p = 0; p < KS; ++p) update(1, p);
         rpart(0);
         interleave<MT * X2, 5, 0>();
-        if (!ENDS && blk < a.nb16)
+        if constexpr (!ENDS && !BF) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                keep_frag<BF>((unsigned char*)a.r + fr * Kp::rows + s * Kp::frag, Kp::row, lane, r[2 * s], r[2 * s + 1],
-                              pair_frag<BF ? IO::NK : 1>(r[2 * s], r[2 * s + 1], minus));
+            for (int s = 0; s < 2; ++s) keep_r(r, s);
+        }
         load_sc(nx);
         __builtin_amdgcn_sched_barrier(0);
         update(0, 0);
@@ -389,8 +395,11 @@ void k_delta_rev(RevArgs a) {
         for (int p = 1; p < KS; ++p) {
             update(0, p);
             parts(p - 1);
+            if constexpr (!ENDS && BF)
+                if (p < 3) keep_r(r, p - 1);  // (heads of 64 have one such step: the other half below)
             interleave<2 * X2, 6, 0>();
         }
+        if constexpr (!ENDS && BF && KS == 2) keep_r(r, 1);
         parts(KS - 1);
         if (BUF == 1) lds_barrier();
         lds_barrier();

@@ -25,8 +25,6 @@
 // 2.3 us for 32 columns; each wave loading K, Q and K^T for itself, 2.0 us for 16 columns (a
 // load of 16 rows of 64 bytes costs 60 clocks, one of 1 KiB in a row 16).
 #pragma once
-#include <type_traits>
-
 #include "delta.hpp"
 
 namespace hy {
@@ -496,7 +494,7 @@ void k_delta_scan(ScanArgs a) {
     // this block's fragments of the backward, one chunk's behind another's
     const bool kept = MODE == kScanKeep && blk < a.nb16;
     using Kp = Kept<BF, KS>;
-    unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)Kp::states;
+    unsigned char* s0p = !kept ? nullptr : (unsigned char*)a.s0 + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)Kp::state;
     unsigned char* up = !kept ? nullptr : (unsigned char*)a.u + ((slot0 * hv + h) * a.nb16 + blk) * (int64_t)Kp::rows;
     constexpr int X2 = NI == 1 ? NE : 6, X3 = NS == 3 ? 6 : NE == 3 ? 5 : 3;  // matrix instructions per product
     // one chunk; T alternates between two sets of registers
@@ -507,8 +505,8 @@ void k_delta_scan(ScanArgs a) {
         if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) keep_frag<BF>(s0p + s * Kp::frag, Kp::state, lane, S[2 * s], S[2 * s + 1], sf[s]);
-            s0p += (int64_t)hv * a.nb16 * Kp::states;
+                for (int s = 0; s < KS; ++s) keep_frag<BF>(s0p, true, KS, s, lane, S[2 * s], S[2 * s + 1]);
+            s0p += (int64_t)hv * a.nb16 * Kp::state;
         }
         __builtin_amdgcn_sched_barrier(0);
         // e = V - exp(G) K S; LDS reads two steps ahead of their products
@@ -630,9 +628,7 @@ void k_delta_scan(ScanArgs a) {
         } else if constexpr (MODE == kScanKeep) {
             if (kept)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    keep_frag<BF>(up + s * Kp::frag, Kp::row, lane, u[2 * s], u[2 * s + 1],
-                                  pair_frag<BF ? IO::NK : 1>(u[2 * s], u[2 * s + 1], minus));
+                for (int s = 0; s < 2; ++s) keep_frag<BF>(up, true, 2, s, lane, u[2 * s], u[2 * s + 1]);
             up += (int64_t)hv * a.nb16 * Kp::rows;
         }
         // the new state's parts, two tiles at a time: first part a step behind the products,

@@ -719,7 +719,7 @@ hyena_status_t hyena_delta_clear_rows(int64_t N, int64_t tokens, const int64_t* 
 
 /* Bytes of workspace hyena_delta_backward needs: the forward's, the states before and
  * the state gradients behind every chunk of 64 tokens, and two arrays of o's shape, all at
- * four bytes a value. Returns 0 as hyena_delta_workspace_bytes. */
+ * three (bf16) or four bytes a value. Returns 0 as hyena_delta_workspace_bytes. */
 size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, int64_t N, int64_t tokens,
                                             const int64_t* seq_start);
 

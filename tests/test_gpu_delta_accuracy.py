@@ -110,12 +110,13 @@ def test_values_without_strength_do_not_reach_other_gradients():
     ([1900], 1, 2, 64, 64),  # cut into pieces
 ])
 def test_gradients_are_rounded_once(lens, hk, hv, dk, dv):
-    """Seven operands of two parts on the way to u or r, and six in the gradients' own products
-    (S0, dS1, u, r, W, M); products of second parts are left out in five (T e and T^T dU, u
-    dS1^T, r S0^T, r u^T); three chained sums of up to 192 fp32 terms. dg sums a chunk's
+    """Seven operands of two parts on the way to u or r and two in the gradients' own products (W,
+    M), four that were kept in 24 bits, 16 of them significant, and so are off by 2^-16 (S0, dS1,
+    u, r); products of second parts are left out in five (T e and T^T dU, u dS1^T, r S0^T,
+    r u^T); three chained sums of up to 192 fp32 terms. dg sums a chunk's
     differences of such products, which partly cancel: twice that."""
     d = D.make(lens, hk, hv, dk, dv, "bf16", seed=dk + len(lens))
-    delta = math.sqrt(13 * TWO ** 2 + 5 * CROSS ** 2) + 3 * 192 * 2.0 ** -24
+    delta = math.sqrt(9 * TWO ** 2 + 4 * 2.0 ** -32 + 5 * CROSS ** 2) + 3 * 192 * 2.0 ** -24
     got, want = gradients(d, (hk, hv, dk, dv)), D.backward(d, dk ** -0.5)
     for i, name in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
         tol = rounded(2 * delta if name == "dg" else delta)
