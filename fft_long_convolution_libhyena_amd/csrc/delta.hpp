@@ -324,6 +324,13 @@ __device__ __forceinline__ void buf_store(RowBuf b, uint32_t off, float x) {
     else
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, (int)off, 0, 0);
 }
+template <bool BF>
+__device__ __forceinline__ float buf_elem(RowBuf b, uint32_t off) {
+    if constexpr (BF)
+        return __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, (int)off, 0, 0) << 16);
+    else
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)off, 0, 0));
+}
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
     const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
@@ -520,7 +527,7 @@ struct Prep {
 // an fp32 value, the upper 16 of a lane's eight in 16 bytes and the rest in 8 behind them: with
 // bf16 alone, dk and dg were up to 3e-3 off and dbeta 3.4e-3 (rounding by itself leaves 1.7e-3);
 // with a second bf16 part the scans and the gradients of 8 sequences of 8192 tokens, which are
-// bound by these bytes, take 1209 us in place of 1118.
+// bound by these bytes, take 1209 us in place of 1100.
 template <bool BF, int KS>
 struct Kept {
     static constexpr int frag = 512 * (BF ? 3 : 4);  // bytes of a fragment

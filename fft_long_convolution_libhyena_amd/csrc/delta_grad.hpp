@@ -254,12 +254,8 @@ void k_delta_grad(GradArgs a) {
         };
         fetch(0);
         if (w == 0) {
-            float gv = 0.f, bv = 0.f;
-            if (lane < rows) {
-                gv = (float)((const T*)a.g)[(tok + lane) * hv + h];
-                bv = (float)((const T*)a.beta)[(tok + lane) * hv + h];
-            }
-            const double G = chunk_decay(gv, lane);
+            const float bv = buf_elem<BF>(row_buf((const T*)a.beta + tok * hv + h, rows, hv * E, E), lane * (hv * E));
+            const double G = chunk_decay(buf_elem<BF>(row_buf((const T*)a.g + tok * hv + h, rows, hv * E, E), lane * (hv * E)), lane);
             const double last = __shfl(G, 63);
             l.G[lane] = G;
             l.gam[lane] = decay(G);
@@ -340,6 +336,10 @@ void k_delta_grad(GradArgs a) {
                 }
             }
         }
+        // the lane anew, so that no address below is formed before the steps and held through them
+        int thread = tid;
+        asm("" : "+v"(thread));
+        const int lane = thread & 63, g = lane >> 4, col = lane & 15;
         // k_i . k_j and q_i . k_j
         f32x4 kk[4] = {}, qk[4] = {};
 #pragma unroll
@@ -444,10 +444,8 @@ void k_delta_grad(GradArgs a) {
                 const double up = __shfl_down(d, s);
                 if (lane + s < 64) d += up;
             }
-            if (lane < rows) {
-                ((T*)a.dg)[(tok + lane) * hv + h] = (T)(float)d;
-                ((T*)a.dbeta)[(tok + lane) * hv + h] = (T)(l.ru[lane] / held_beta(l.bet[lane]));
-            }
+            buf_store<BF>(row_buf((T*)a.dg + tok * hv + h, rows, hv * E, E), lane * (hv * E), (float)d);
+            buf_store<BF>(row_buf((T*)a.dbeta + tok * hv + h, rows, hv * E, E), lane * (hv * E), l.ru[lane] / held_beta(l.bet[lane]));
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
