@@ -16,10 +16,10 @@
 // residuals and what a chunk adds to the state have three (relative error of the fp32
 // state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). So have, in the backward,
 // P, dU, r and exp(G) dO, which lead to dS (the fp32 gradient of the state 3e-6 off with two).
-// Two also serve the states between the pieces of cut sequences. P has two as well: with one the outputs are 2.2e-3 off, with two 1.7e-3, which is what
-// their own rounding leaves (12 products a chunk more, off the chain). fp32 plans use three
-// parts throughout (1e-7), at 6 products for each single one, still 2.7 times the rate of the
-// fp32 matrix instruction.
+// Two also serve the states between the pieces of cut sequences, and P: with one the
+// outputs are 2.2e-3 off, with two 1.7e-3, which is what their own rounding leaves (12
+// products a chunk more, off the chain). fp32 plans use three parts throughout (1e-7), at 6
+// products for each single one, still 2.7 times the rate of the fp32 matrix instruction.
 //
 // Fragment layouts of v_mfma_f32_16x16x32_bf16, lane l, g = l / 16:
 //   A [16][32]: lane holds row l % 16, columns 8g .. 8g+7
@@ -214,7 +214,8 @@ __device__ __forceinline__ f32x4 buf_f4(RowBuf b, uint32_t off, int soff) {
 }
 // 64 rows of DK elements in LDS as bf16 parts, read as operands along the rows (K S, Q S)
 // or across them (K^T u, by the transposing LDS read). Rows are 64 bytes longer than
-// their data, and eight rows shift by 16 bytes: both reads then spread over all banks.
+// their data, and eight rows shift by 16 bytes, so that consecutive rows start on other banks.
+// Bank conflicts still take 31% of the scans' LDS cycles (42% of the ends'), by counter.
 template <int NI, int DK>
 struct Tile {
     static constexpr int pitch = 2 * DK + 64;
@@ -596,9 +597,9 @@ constexpr int scan_threads(bool bf) { return bf ? 256 : 192; }
 
 constexpr int kCus = 256;
 // Shorter pieces gain nothing: the ends' launch and the carries (5 us a piece) cost what the
-// shorter scans save. One bf16 sequence, 6 heads of 128, cut and whole: 1600 tokens 59 and
-// 63 us, 2048 65 and 76, 4096 90 and 138, 16384 167 and 492; backward 134 and 136, 139 and
-// 162, 199 and 285, 485 and 1085.
+// shorter scans save. One bf16 sequence, 6 heads of 128, cut and whole: 1600 tokens 58 and
+// 62 us, 2048 65 and 76, 4096 95 and 139, 16384 178 and 507; backward 138 and 141, 143 and
+// 167, 205 and 294, 504 and 1121.
 constexpr int64_t kMinPiece = 8;
 
 struct PrepArgs;

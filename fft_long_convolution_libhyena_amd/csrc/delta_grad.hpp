@@ -14,8 +14,9 @@
 // of both where they cancel (an answer within 1% of v: dbeta 0.18 off); beta = 0 is held at 2^-90.
 // A workgroup holds K and Q in LDS and walks over 32 columns of v's width at a time (dO,
 // u, r and the states' columns, the next step's loads in flight), bf16 calls in two halves,
-// dS1 in the place of S0; wave w has rows 16 w of every product. Bound by bytes and their latency with two workgroups a CU: 8 sequences of
-// 8192 tokens, 6 heads of 128 x 128, bf16, 306 us (1235 MB, 4.1 TB/s).
+// dS1 in the place of S0; wave w has rows 16 w of every product. Bound by bytes and their
+// latency with two workgroups a CU: 8 sequences of 8192 tokens, 6 heads of 128 x 128, bf16,
+// 380 us (1568 MB, 4.1 TB/s).
 #pragma once
 #include "delta.hpp"
 

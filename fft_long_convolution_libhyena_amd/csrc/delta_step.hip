@@ -8,8 +8,9 @@
 // head's state in registers: lane l has columns 4 (l % 8) .. +3 of rows l/8, l/8 + 8,
 // ...; a row's 32 columns are one 128-byte line, and the sums over rows end in three
 // exchanges between lanes 8, 16 and 32 apart. Bound by the state's bytes: 96 rows of 16 heads
-// of 128 x 128 (201 MB read and written) take 34 us, 5.9 TB/s; a single row of 6 heads 6 us in
-// a graph, a launch and one trip to memory.
+// of 128 x 128 (201 MB read and written) take 35 us, 5.8 TB/s; a single row of 6 heads 6.4 us in
+// a graph: a launch and three trips to memory, each of which waits for the one before (the
+// slot, the other rows' slots with the state under way, the token).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -12,7 +12,7 @@
 // A group keeps its token and walks over heads, several in flight: the angles'
 // reduction (64 bits: positions reach far beyond where a 32-bit product keeps a fraction of
 // a turn) and sine are paid once a token and lane. Sums over the 8 elements and the G lanes
-// are fp32; the weights' gradients are summed in a fixed order (lane, workgroup, then over
+// are fp32 (a head whose squares pass 3e38 in sum gives zeros); the weights' gradients are summed in a fixed order (lane, workgroup, then over
 // workgroups in 64 bits).
 #include <hip/hip_runtime.h>
 #include <math.h>

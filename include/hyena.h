@@ -770,7 +770,8 @@ hyena_status_t hyena_delta_step(const hyena_delta_params_t* params, int64_t B, i
  *   y = n * w, then for i < F the pair (y[i], y[i+F]) (HYENA_ROT_HALVES) or
  *   (y[2i], y[2i+1]) (HYENA_ROT_PAIRS) turned by the angle position * freq[i]:
  *   (a, b) -> (a cos - b sin, a sin + b cos).
- * Angles are formed and reduced in fp64, everything else is fp32 and rounded once.
+ * Angles are formed and reduced in fp64, everything else is fp32 and rounded once. The
+ * squares of a head sum up below 3e38 (elements to 1e18): past that the head's result is 0.
  * ------------------------------------------------------------------------ */
 typedef enum { HYENA_NORM_RMS = 0, HYENA_NORM_L2 = 1 } hyena_norm_t;
 typedef enum { HYENA_ROT_HALVES = 0, HYENA_ROT_PAIRS = 1 } hyena_rot_t;

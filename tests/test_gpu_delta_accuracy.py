@@ -133,7 +133,7 @@ def test_states_take_what_is_written_in_fp32():
 
     lens, hv, dk, dv = [64, 50], 2, 64, 72
     d = D.make(lens, 1, hv, dk, dv, "bf16", seed=4)
-    d["k"] = torch.eye(64)[torch.cat([torch.randperm(n) for n in lens])][:, None].bfloat16()
+    d["k"] = torch.eye(64)[torch.cat([torch.randperm(n, generator=torch.Generator().manual_seed(n)) for n in lens])][:, None].bfloat16()
     g = {n: d[n].cuda() for n in ("q", "k", "v", "g", "beta")}
     _, s = DeltaRule(1, hv, dk, dv).forward(*g.values(), seq_start=D.starts(lens, "cuda"))
     assert D.rel(s, D.forward(d, 1.0, use_state=False)[1]) <= 5 * 2.0 ** -24
