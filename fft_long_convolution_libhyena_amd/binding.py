@@ -860,7 +860,7 @@ class QKNorm:
                       for w in (self.w_q, self.w_k))
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
         ws, ws_bytes = None, 0
-        if workspace is not None or dw_q is not None or dw_k is not None:
+        if dw_q is not None or dw_k is not None:
             workspace, ws, ws_bytes = _workspace(torch, workspace, self.backward_workspace_bytes(args[1], dev), dev)
         _launch(torch, "hyena_qk_norm_backward", self.lib.hyena_qk_norm_backward, dev, *args, *up, dqp, dkp, ptr(dw_q),
                 ptr(dw_k), ws, ws_bytes)

@@ -14,7 +14,7 @@
 // the rounding of what the ones before it leave): two parts hold 16 bits, three 24.
 // bf16 plans give their inputs exactly in one part and carry the state and T in two; the
 // residuals and what a chunk adds to the state have three (relative error of the fp32
-// state measured 3e-7; with two 3e-6, 8% faster; with one 2e-3). So have, in the backward,
+// state measured 3e-7 to 7e-7; with two 3e-6, 8% faster; with one 2e-3). So have, in the backward,
 // P, dU, r and exp(G) dO, which lead to dS (the fp32 gradient of the state 3e-6 off with two).
 // Two also serve the states between the pieces of cut sequences, and P: with one the
 // outputs are 2.2e-3 off, with two 1.7e-3, which is what their own rounding leaves (12

@@ -339,7 +339,7 @@ void k_delta_grad(GradArgs a) {
         }
         // the lane anew, so that no address below is formed before the steps and held through them
         int thread = tid;
-        asm("" : "+v"(thread));
+        asm volatile("" : "+v"(thread));
         const int lane = thread & 63, g = lane >> 4, col = lane & 15;
         // k_i . k_j and q_i . k_j
         f32x4 kk[4] = {}, qk[4] = {};

@@ -36,11 +36,13 @@ def test_norm_backward_takes_a_dense_workspace(launches):
     ws = torch.empty(1 << 20, dtype=torch.uint8)
     m.backward(*norm_inputs(), workspace=ws)
     m.backward(*norm_inputs())
-    QKNorm(2, 1, 64).backward(*norm_inputs())  # no weights: none needed
-    assert [n for n, _ in launches] == ["hyena_qk_norm_backward"] * 3
+    plain = QKNorm(2, 1, 64)  # no weights: none is needed, and one that is given is not looked at
+    plain.backward(*norm_inputs())
+    plain.backward(*norm_inputs(), workspace=torch.empty(8, dtype=torch.uint8, device="meta"))
+    assert [n for n, _ in launches] == ["hyena_qk_norm_backward"] * 4
     assert launches[0][1][-2:] == (ws.data_ptr(), 1 << 20)
     need = m.backward_workspace_bytes(3, torch.device("cpu"))
-    assert need > 0 and launches[1][1][-1] == need and launches[2][1][-2:] == (None, 0)
+    assert need > 0 and launches[1][1][-1] == need and launches[2][1][-2:] == launches[3][1][-2:] == (None, 0)
 
 
 @pytest.mark.parametrize("backward", [False, True])
