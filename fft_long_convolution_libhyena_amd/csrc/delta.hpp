@@ -72,6 +72,9 @@ struct Io<false> {
     static constexpr int NK = 1;  // as fp32
 };
 
+// Fragment f of a lower triangular operand: its row tile and its half of the columns
+__device__ __forceinline__ constexpr int tri_row(int f) { return f < 2 ? f : 2 + ((f - 2) >> 1); }
+__device__ __forceinline__ constexpr int tri_half(int f) { return f < 2 ? 0 : (f - 2) & 1; }
 // Row r of row tile t as the scans number them: the pair of tiles 2s, 2s + 1 covers
 // rows 32 s .. 32 s + 31 such that the result rows that one lane holds in both (4 g + i
 // of each) are rows 32 s + 8 g .. + 7 in order, which is what the same lane must hold
@@ -344,6 +347,45 @@ __device__ __forceinline__ Frag<N> get_frag(const __bf16* frag, int part_stride,
 #pragma unroll
     for (int n = 0; n < N; ++n) f.p[n] = *reinterpret_cast<const bf16x8*>(frag + n * part_stride + lane * 8);
     return f;
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+// What is not finite must not reach tokens in front of it, but zeros of T and of P (and of the
+// remainders' operand) multiply it there. Where a chunk's outputs show that they met such a
+// value, they are made again: rows of x (four tiles, numbered as tile_row has them) from a
+// column's first that is not finite on are cleared, and `poison` marks these rows of the result.
+// One comparison and a branch a chunk, off the chain, where all is finite (in the state waves,
+// whose schedule a branch cuts in two, they took 3% of the scan).
+__device__ __forceinline__ int clear_from_first(f32x4 (&x)[4], int lane) {
+    const int g = lane >> 4;
+    int first = 64;
+#pragma unroll
+    for (int t = 3; t >= 0; --t)
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const int row = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + i;
+            if (!finite(x[t][i]) && row < first) first = row;
+        }
+#pragma unroll
+    for (int d = 16; d < 64; d <<= 1) {
+        const int other = __shfl_xor(first, d);
+        first = other < first ? other : first;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (32 * (t >> 1) + 8 * g + 4 * (t & 1) + i >= first) x[t][i] = 0.f;
+    return first;
+}
+__device__ __forceinline__ void poison(f32x4 (&x)[4], int first, int lane) {
+    const int g = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (32 * (t >> 1) + 8 * g + 4 * (t & 1) + i >= first) x[t][i] = __builtin_nanf("");
 }
 
 // Instruction order of the region before it: N times one matrix instruction followed by

@@ -28,7 +28,7 @@ struct PrepLds {
         float p[kC][kMP];            // then P, then T
     };
     double G[kC];
-    float beta[kC];
+    float beta[kC], kk[kC];
 };
 
 // a 64 x 64 matrix in LDS (or its transpose; or with column c scaled by scale[c]) as
@@ -37,8 +37,8 @@ template <int N, bool TRANS>
 __device__ __forceinline__ void write_tri(const float (*m)[kMP], const float* scale, __bf16* dst, int tid) {
     for (int e = tid; e < kTri * 64; e += kThreads) {
         const int f = e >> 6, lane = e & 63;
-        const int i = TRANS ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : 2 + ((f - 2) >> 1));
-        const int s = TRANS ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : (f - 2) & 1);
+        const int i = TRANS ? (f < 4 ? f >> 1 : f - 2) : tri_row(f);
+        const int s = TRANS ? (f < 4 ? f & 1 : 1) : tri_half(f);
         const int row = tile_row(i, lane & 15), c0 = 32 * s + 8 * (lane >> 4);
         float x[8];
 #pragma unroll
@@ -132,6 +132,13 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
                     qk[j] = mma(qa, kb, qk[j]);
                 }
         }
+        if (!BWD && col >> 2 == g) {  // this lane has a k_t . k_t
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j == wave && (col & 3) == i) l.kk[row] = kk[j][i];
+        }
         __syncthreads();  // K has been read: P takes its place
         // no branches around single elements: their decays are formed everywhere and selected
         const int t0 = 16 * wave + 4 * g;
@@ -155,6 +162,18 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
         }
     }
     __syncthreads();
+    // From the first token on whose k, g or beta is not finite, the rows of A and P are cleared,
+    // so that no part of T or P of the tokens in front of it meets it; T's diagonal marks them
+    // below (the forward; the backward's gradients reach back anyway).
+    int good = kC;
+    if (!BWD) {
+        const uint64_t bad = __ballot(!(finite(l.kk[lane]) && finite(l.beta[lane]) && finite((float)l.G[lane])));
+        if (__builtin_expect(bad != 0, 0)) {
+            good = __builtin_ctzll(bad);
+            for (int e = good * kC + tid; e < kC * kC; e += kThreads) l.a[e / kC][e % kC] = l.p[e / kC][e % kC] = 0.f;
+            __syncthreads();
+        }
+    }
     if (!BWD)
         write_tri<IO::NP, false>(l.p, nullptr, reinterpret_cast<__bf16*>(a.out.rec + sh_idx * Rec<BF>::bytes + Rec<BF>::p), tid);
     else
@@ -205,6 +224,13 @@ __global__ __launch_bounds__(kThreads) void k_delta_prep(PrepArgs a) {
                 y = __builtin_amdgcn_mfma_f32_16x16x4f32(l.p[b + col][b + 4 * g + s], x[s], y, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) l.p[b + 4 * g + i][16 * j + col] = -y[i];
+        }
+        __syncthreads();
+    }
+    if (!BWD && good < kC) {
+        if (wave == 0 && lane >= good) {
+            l.p[lane][lane] = __builtin_nanf("");
+            l.beta[lane] = 1.f;
         }
         __syncthreads();
     }

@@ -98,6 +98,8 @@ struct ScanCfg {
     static constexpr bool STAGER = !(BF && (OUT || ENDS));       // a wave that only stages
     static constexpr bool SELF = BF && ENDS;                      // the state waves stage
     static constexpr int threads = 64 * ((OUT ? 2 : 1) * NB + (STAGER ? 1 : 0));
+    // waves a SIMD: two workgroups share a CU where their LDS lets them (bf16, heads up to 64)
+    static constexpr int eu = threads > 256 || (BF && OUT && DK == 64) ? 2 : 1;
     struct None {};
     struct LdsOut {
         Tile<Io<BF>::NI, DK> k[BUF], q[BUF];
@@ -220,7 +222,7 @@ __device__ __forceinline__ constexpr int waves_of() {
 }
 
 template <bool BF, int DK, int MODE>
-__global__ __launch_bounds__((ScanCfg<BF, DK, MODE>::threads)) __attribute__((amdgpu_waves_per_eu((ScanCfg<BF, DK, MODE>::threads > 256 ? 2 : 1))))
+__global__ __launch_bounds__((ScanCfg<BF, DK, MODE>::threads)) __attribute__((amdgpu_waves_per_eu((ScanCfg<BF, DK, MODE>::eu))))
 void k_delta_scan(ScanArgs a) {
     using IO = Io<BF>;
     using T = typename IO::T;
@@ -334,6 +336,57 @@ void k_delta_scan(ScanArgs a) {
 #pragma unroll
                 for (int f = 0; f < kTri; ++f) Pf[f] = buf_frag<NP>(rb, Rec<BF>::p, f, lane);
             };
+            // The outputs again where u or S is not finite: u from its residuals, K, v, T and the
+            // decays read once more
+            auto causal = [&](int c, const auto& q, const auto& in, f32x4(&y)[4]) {
+                const uint32_t ldk = (uint32_t)a.sh.ldk * E, ldv = (uint32_t)a.sh.ldv * E;
+                const RowBuf kb = plain_buf(kbase + c * krow, (rows_in(c) - 1) * ldk + dk * E), rb = plain_buf(rec, Rec<BF>::bytes);
+                const RowBuf vb = plain_buf(vbase + c * vrow, (rows_in(c) - 1) * ldv + dv * E);
+                f32x4 e[4] = {}, u[4] = {};
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[t] = f32x4{};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const Frag<NO> sp = get_frag<NO>(&in.s[s][0][0], 512, lane);
+                    const int k = 32 * s + 8 * g;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        Raw<BF> r;
+                        buf_raw(kb, k < dk ? tile_row(t, col) * ldk + k * E : kNoElem, r);
+                        e[t] = mma(to_frag(r), sp, e[t]);
+                        y[t] = mma(q.rows(lane, t, s), sp, y[t]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const f32x4 gt = buf_f4(rb, drow(t, 0) * 4, Rec<BF>::sc);
+                    y[t] *= gt;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        e[t][i] = fmaf(-gt[i], e[t][i], buf_elem<BF>(vb, cok ? drow(t, i) * ldv + c0 * E : kNoElem));
+                }
+                const int first = clear_from_first(e, lane);
+                {
+                    const Frag<IO::NE> half[2] = {pair_frag<IO::NE>(e[0], e[1], minus), pair_frag<IO::NE>(e[2], e[3], minus)};
+#pragma unroll
+                    for (int f = 0; f < kTri; ++f) {
+                        u[tri_row(f)] = mma(buf_frag<NS>(rb, Rec<BF>::t, f, lane), half[tri_half(f)], u[tri_row(f)]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                int from = clear_from_first(u, lane);  // T's diagonal marks tokens, too
+                from = from < first ? from : first;
+                const Frag<NO> half[2] = {pair_frag<NO>(u[0], u[1], minus), pair_frag<NO>(u[2], u[3], minus)};
+#pragma unroll
+                for (int f = 0; f < kTri; ++f) {
+                    y[tri_row(f)] = mma(buf_frag<NP>(rb, Rec<BF>::p, f, lane), half[tri_half(f)], y[tri_row(f)]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                poison(y, from, lane);
+                __builtin_amdgcn_s_waitcnt(0);  // nothing of this is under way where the paths meet again
+                __builtin_amdgcn_sched_barrier(0);
+            };
             auto outputs = [&](int c) {
                 const Exchange<BF, DK>& in = l.x[wave - NB][c & 1];
                 const Tile<NI, DK>& q = l.q[c & (BUF - 1)];
@@ -364,6 +417,7 @@ void k_delta_scan(ScanArgs a) {
                 mma_tiles(p0, u0, y);
                 mma_tiles(p1, u1, y + 2);
                 __builtin_amdgcn_sched_barrier(0);
+                if (__builtin_expect(__any(!finite(y[2][0])), 0)) causal(c, q, in, y);  // a row that has met all of u
                 if (c + 1 < nch) rec += recstep;
                 load();
 #pragma unroll

@@ -686,10 +686,9 @@ size_t hyena_delta_workspace_bytes(const hyena_delta_params_t* params, int64_t N
  * The state is held in fp32 from the first token to the last; bf16 outputs are
  * rounded once from sums whose operands are bf16 or sums of two bf16 parts, fp32
  * results have the accuracy of fp32 products. Decays below exp(-200) count as 0 and
- * g = -inf resets the state. A value that is not finite (but for g = -inf) spoils what
- * follows it, as in the recurrence, and the tokens in front of it in its own chunk (64
- * tokens, counted from the sequence's first): of v in its column, of k, g and beta in their
- * value heads. One of q spoils its token alone. Every sum has a fixed order: results are bitwise
+ * g = -inf resets the state. A value that is not finite (but for g = -inf) spoils its token
+ * and what follows in the sequence, as in the recurrence, and nothing in front of it: of v
+ * in its column, of k, g and beta in their value heads. One of q spoils its token alone. Every sum has a fixed order: results are bitwise
  * reproducible, and those of a sequence of up to 1536 tokens do not depend on the other
  * sequences of the call. Longer ones are cut into pieces that run side by side where the
  * call has few (sequence, head) pairs; how is a rule on the sizes, N and tokens among
@@ -732,7 +731,8 @@ size_t hyena_delta_backward_workspace_bytes(const hyena_delta_params_t* params, 
  *   that share a key head, too); dstate_in [N][heads_v][dim_k][dim_v] fp32, or NULL.
  * The states are computed again from the inputs; nothing of the forward call is kept.
  * Operands of bf16 calls are bf16 or sums of two bf16 parts, the states and their
- * gradients stay fp32 along both scans. dbeta is formed from the residual v - answer itself and stays exact where
+ * gradients stay fp32 along both scans. Values that are not finite spoil the gradients of
+ * their sequence's earlier tokens, too. dbeta is formed from the residual v - answer itself and stays exact where
  * the state predicts v; for it, strengths below 2^-90 count as 2^-90. Every sum has a fixed
  * order: results are bitwise reproducible. Rows that belong to no sequence are left as they were. Arguments, workspace (of at least
  * hyena_delta_backward_workspace_bytes) and errors otherwise as in

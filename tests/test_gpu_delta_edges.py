@@ -35,8 +35,8 @@ def test_empty_sequences_need_no_workspace(packed, dtype):
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
 def test_where_a_value_that_is_not_finite_shows(name, bad, dtype):
-    """q's in its token; v's in its column from the token's chunk on, the others' in their value
-    heads from that chunk on: earlier chunks, other heads and other sequences keep their bits."""
+    """q's in its token; v's in its column from the token on, the others' in their value heads
+    from there on: earlier tokens, other heads and other sequences keep their bits."""
     from fft_long_convolution_libhyena_amd import DeltaRule
 
     hk, hv, dk, dv, lens = 2, 4, 64, 40, [200, 90]
@@ -57,9 +57,9 @@ def test_where_a_value_that_is_not_finite_shows(name, bad, dtype):
     if name == "q":
         same[100, heads] = False
     elif name == "v":
-        same[64:200, 1] = False
+        same[100:200, 1] = False
     else:
-        same[64:200, heads] = False
+        same[100:200, heads] = False
     assert torch.equal(o[same], o0[same]) and bool(torch.isfinite(o[same]).all())
     if name == "v":  # its other columns were changed here, but are finite
         fine = torch.isfinite(o[64:200, 1])
@@ -101,3 +101,61 @@ def test_rows_of_no_sequence_have_no_gradient(dtype):
         assert bool((t[:front] == 0).all()) and bool((t[-back:] == 0).all())
     for a, b in zip(grads, plain):
         assert torch.equal(a[front:-back], b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 40), (128, 128), (40, 72)])
+@pytest.mark.parametrize("at", [0, 5, 36, 63])
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta"])
+def test_what_is_not_finite_reaches_no_earlier_token(name, at, dk, dv, dtype):
+    """The mixer is causal: tokens in front of a NaN or an infinity keep their bits, also those of
+    its own chunk of 64, and no token behind it looks as if nothing had happened."""
+    from fft_long_convolution_libhyena_amd import DeltaRule
+
+    hk, hv, lens = 1, 2, [170, 64]
+    d = D.make(lens, hk, hv, dk, dv, dtype, seed=19)
+    r = DeltaRule(hk, hv, dk, dv, dtype)
+
+    def call():
+        return r.forward(*(d[n].cuda() for n in ("q", "k", "v", "g", "beta")), state=d["state"].cuda(), seq_start=D.starts(lens, "cuda"))
+
+    o0, s0 = call()
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        if name == "g" and bad == float("-inf"):
+            continue  # a reset, and finite
+        keep = d[name].clone()
+        t = 64 + at
+        d[name][t] = bad
+        if name == "v":
+            d[name][t, :, 1:] = keep[t, :, 1:]
+        o, s = call()
+        d[name] = keep
+        assert torch.equal(o[:t], o0[:t]), bad
+        assert torch.equal(o[170:], o0[170:]) and torch.equal(s[1], s0[1])
+        if name == "q":
+            assert torch.equal(o[t + 1:], o0[t + 1:]) and not bool(torch.isfinite(o[t]).any()) and torch.equal(s, s0)
+        elif name == "v":
+            assert torch.equal(o[..., 1:], o0[..., 1:]) and torch.equal(s[..., 1:], s0[..., 1:])
+            assert not bool(torch.isfinite(o[t:170, :, 0]).any()) and not bool(torch.isfinite(s[0, ..., 0]).any())
+        else:
+            assert not bool(torch.isfinite(o[t:170]).any()) and not bool(torch.isfinite(s[0]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_what_is_not_finite_reaches_no_earlier_token_of_a_cut_sequence(name, dtype):
+    from fft_long_convolution_libhyena_amd import DeltaRule
+
+    lens, at = [2300], 1100
+    d = D.make(lens, 1, 2, 64, 64, dtype, seed=20, decay=1e-2)
+    r = DeltaRule(1, 2, 64, 64, dtype)
+    call = lambda: r.forward(*(d[n].cuda() for n in ("q", "k", "v", "g", "beta")), state=d["state"].cuda(),  # noqa: E731
+                             seq_start=D.starts(lens, "cuda"))
+    o0, _ = call()
+    d[name][at, :, 0] = float("nan")
+    o, s = call()
+    assert torch.equal(o[:at], o0[:at])
+    after = slice(0, 1) if name == "v" else slice(None)
+    assert bool(o[at:, :, after].isnan().all()) and bool(s[..., after].isnan().all())
+    if name == "v":
+        assert torch.equal(o[..., 1:], o0[..., 1:])
