@@ -16,7 +16,7 @@
 // u, r and the states' columns, the next step's loads in flight), bf16 calls in two halves,
 // dS1 in the place of S0; wave w has rows 16 w of every product. Bound by bytes and their
 // latency with two workgroups a CU: 8 sequences of 8192 tokens, 6 heads of 128 x 128, bf16,
-// 380 us (1568 MB, 4.1 TB/s).
+// 378 us (1571 MB, 4.2 TB/s).
 #pragma once
 #include "delta.hpp"
 

@@ -1,7 +1,7 @@
 // Chunk-parallel preparation of the gated delta rule: the decays, T = (I + A)^-1 and
 // P of every (chunk, value head), written as matrix-core fragments so that the scans
 // read them 16 bytes per lane without staging. Bound by those records' and the operands'
-// bytes: 8 sequences of 8192 tokens, 6 heads of 128, bf16, 82 us (367 MB, 4.5 TB/s), for the
+// bytes: 8 sequences of 8192 tokens, 6 heads of 128, bf16, 84 us (367 MB, 4.4 TB/s), for the
 // backward, with T^T and P^T, 97 us (480 MB, 5.0 TB/s).
 #pragma once
 #include "delta.hpp"

@@ -8,7 +8,7 @@
 // here an input wave a block, one chunk ahead, that makes what does not depend on dS
 // (P^T dO and Q^T diag(exp(G)) dO) and hands it over in LDS as fp32. The input waves of
 // bf16 calls also stage K, Q and dO, half the rows each; fp32 calls have a staging wave.
-// Measured as the forward's scan: 403 us, 3.1 us a chunk (2.4 TB/s). Chain and memory bound
+// Measured as the forward's scan: 401 us, 3.1 us a chunk (2.4 TB/s). Chain and memory bound
 // it: with P, dU and r in two parts, and bf16 alone kept, it took 358, without stores 264, without
 // the inputs 259, the input waves alone 183. Stores from the input waves (results handed back in
 // LDS) took 358 to 386 in place of 358, T^T a chunk ahead in alternating registers 365.

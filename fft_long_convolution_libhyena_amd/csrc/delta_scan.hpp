@@ -18,7 +18,7 @@
 // What bounds it: a state wave is alone on its SIMD, so its instructions (134 matrix, about
 // 300 vector for a chunk of a 128 x 16 block) run in order, matrix and vector ones
 // alternating; the chain over the chunks is sequential. Measured, 8 sequences of 8192 tokens,
-// 6 heads of 128 x 128, bf16: 296 us, 2.3 us a chunk (192 workgroups on 256 CUs; 1.9 TB/s;
+// 6 heads of 128 x 128, bf16: 290 us, 2.3 us a chunk (192 workgroups on 256 CUs; 1.9 TB/s;
 // matrix pipes busy 33% of the CUs' cycles); the scan that keeps states, with residuals in two
 // parts and 453 MB to write, 300. On the way, for a chunk: tokens and state rows split over four
 // waves, operands exchanged in LDS with three barriers, 2.3 us for 32 columns; each wave loading
