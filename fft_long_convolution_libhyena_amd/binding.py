@@ -39,6 +39,10 @@ EXPORTS = ("hyena_plan_create", "hyena_plan_create_path", "hyena_plan_create_ex"
            "hyena_forward_noalloc", "hyena_kernel_synthesis", "hyena_delta_workspace_bytes",
            "hyena_delta_forward", "hyena_delta_clear_rows", "hyena_delta_backward_workspace_bytes", "hyena_delta_backward", "hyena_delta_step",
            "hyena_qk_norm_forward", "hyena_qk_norm_backward_workspace_bytes", "hyena_qk_norm_backward",
+           "hyena_qk_norm_axes_forward", "hyena_qk_norm_axes_backward", "hyena_recurrence_workspace_bytes",
+           "hyena_recurrence_forward", "hyena_recurrence_backward_workspace_bytes", "hyena_recurrence_backward",
+           "hyena_recurrence_step", "hyena_residual_norm_forward", "hyena_residual_norm_backward_workspace_bytes",
+           "hyena_residual_norm_backward",
            "hyena_status_string")
 
 
@@ -78,6 +82,23 @@ class QKNormParamsStruct(ctypes.Structure):
     _fields_ = [("heads_q", ctypes.c_int64), ("heads_k", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("rot", ctypes.c_int64), ("kind", ctypes.c_int), ("layout", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("eps", ctypes.c_float), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("freq", ctypes.c_void_p)]
+
+
+class RecurrenceParamsStruct(ctypes.Structure):
+    """hyena_recurrence_params_t: channels, dtype and the rates' device pointer."""
+    _fields_ = [("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("rate", ctypes.c_void_p)]
+
+
+class RecurrenceInputsStruct(ctypes.Structure):
+    """hyena_recurrence_inputs_t: device pointers of x, r and i, each with its token stride."""
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("r", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("i", ctypes.c_void_p), ("ldi", ctypes.c_int64)]
+
+
+class ResidualNormParamsStruct(ctypes.Structure):
+    """hyena_residual_norm_params_t: columns, types, 8-bit block, eps and the weight's device pointer."""
+    _fields_ = [("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("block", ctypes.c_int64), ("eps", ctypes.c_float), ("w", ctypes.c_void_p)]
 
 
 class HyenaError(RuntimeError):
@@ -204,6 +225,28 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.hyena_qk_norm_backward_workspace_bytes.restype = sz
     lib.hyena_qk_norm_backward.argtypes = [qp, i64, vp, i64, vp, i64] + [vp] * 8 + [sz, vp]
     lib.hyena_qk_norm_backward.restype = ci
+    lib.hyena_qk_norm_axes_forward.argtypes = [qp, vp, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.hyena_qk_norm_axes_forward.restype = ci
+    lib.hyena_qk_norm_axes_backward.argtypes = [qp, vp, i64, i64, vp, i64, vp, i64] + [vp] * 8 + [sz, vp]
+    lib.hyena_qk_norm_axes_backward.restype = ci
+    rp, ri = ctypes.POINTER(RecurrenceParamsStruct), ctypes.POINTER(RecurrenceInputsStruct)
+    lib.hyena_recurrence_workspace_bytes.argtypes = [rp, i64, i64, vp]
+    lib.hyena_recurrence_workspace_bytes.restype = sz
+    lib.hyena_recurrence_forward.argtypes = [rp, i64, i64, vp, ri, vp, vp, vp, vp, vp, sz, vp]
+    lib.hyena_recurrence_forward.restype = ci
+    lib.hyena_recurrence_backward_workspace_bytes.argtypes = [rp, i64, i64, vp, vp]
+    lib.hyena_recurrence_backward_workspace_bytes.restype = sz
+    lib.hyena_recurrence_backward.argtypes = [rp, i64, i64, vp, ri] + [vp] * 10 + [sz, vp]
+    lib.hyena_recurrence_backward.restype = ci
+    lib.hyena_recurrence_step.argtypes = [rp, i64, i64, ri, vp, i64, vp, vp, vp]
+    lib.hyena_recurrence_step.restype = ci
+    np_ = ctypes.POINTER(ResidualNormParamsStruct)
+    lib.hyena_residual_norm_forward.argtypes = [np_, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.hyena_residual_norm_forward.restype = ci
+    lib.hyena_residual_norm_backward_workspace_bytes.argtypes = [np_, i64]
+    lib.hyena_residual_norm_backward_workspace_bytes.restype = sz
+    lib.hyena_residual_norm_backward.argtypes = [np_, i64, vp, i64] + [vp] * 6 + [sz, vp]
+    lib.hyena_residual_norm_backward.restype = ci
     lib.hyena_status_string.argtypes = [ci]
     lib.hyena_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -785,10 +828,13 @@ class QKNorm:
     """Norms of queries and keys for each head with the position rotation (hyena_qk_norm_* of
     include/hyena.h): kind "rms" or "l2"; w_q, w_k [dim] fp32 weights or None; freq [F] fp32
     radians per position of the F rotated pairs, or None; pairs: neighbours (2i, 2i+1) are
-    rotated instead of the halves (i, i + F). The tensors given here are used by every call."""
+    rotated instead of the halves (i, i + F); axis [F] int32, for tokens that lie on several axes
+    (time, height and width of a video's patches): positions then hold one position for each
+    axis, and pair f turns by positions[.., axis[f]] * freq[f]. The tensors given here are used
+    by every call."""
 
     def __init__(self, heads_q: int, heads_k: int, dim: int, dtype: str = "bf16", kind: str = "rms", eps: float = 1e-6,
-                 w_q=None, w_k=None, freq=None, pairs: bool = False):
+                 w_q=None, w_k=None, freq=None, pairs: bool = False, axis=None):
         import torch
 
         self._torch = torch
@@ -803,6 +849,10 @@ class QKNorm:
             if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()
                                   or (n is not None and t.numel() != n)):
                 raise ValueError(f"{name} must be a contiguous fp32 vector" + (f" of {n}" if n else ""))
+        self.axis = axis
+        if axis is not None and (freq is None or axis.dtype != torch.int32 or axis.shape != freq.shape
+                                 or not axis.is_contiguous() or axis.device != freq.device):
+            raise ValueError("axis must be a contiguous int32 vector with an entry for each of freq, where freq is")
 
     def _params(self, device):
         ptr = []
@@ -822,12 +872,19 @@ class QKNorm:
         tokens = rows[0] if len(rows) == 1 else rows[0] * rows[1]
         qp, ldq = _token_rows(q, "q", rows, self.heads_q, self.dim, self.io_dtype, dev)
         kp, ldk = _token_rows(k, "k", rows, self.heads_k, self.dim, self.io_dtype, dev)
-        pos = None
+        pos, shape, axes = None, rows, ()
+        if self.axis is not None:
+            n = positions.shape[-1] if positions is not None and positions.dim() == len(rows) + 1 else 1
+            shape, axes = (*rows, n), (self.axis.data_ptr(), n)
         if positions is not None:
-            pos = _dense(positions, "positions", rows, self._torch.int64, dev)
+            pos = _dense(positions, "positions", shape, self._torch.int64, dev)
         elif self.freq is not None and self.freq.numel():
             raise ValueError("positions are needed for the rotation")
-        return dev, rows, (ctypes.byref(self._params(dev)), tokens, qp, ldq, kp, ldk, pos)
+        return dev, rows, (ctypes.byref(self._params(dev)), *axes, tokens, qp, ldq, kp, ldk, pos)
+
+    def _call(self, direction):
+        name = f"hyena_qk_norm_{'axes_' if self.axis is not None else ''}{direction}"
+        return name, getattr(self.lib, name)
 
     def _out(self, t, name, rows, heads, device):
         shape = (*rows, heads, self.dim)
@@ -838,11 +895,12 @@ class QKNorm:
 
     def forward(self, q, k, positions=None, q_out=None, k_out=None):
         """hyena_qk_norm_forward: q [tokens or B, T, heads_q, dim], k [.., heads_k, dim] (one stride
-        between tokens), positions int64 of the tokens' shape -> (q_out, k_out), dense."""
+        between tokens), positions int64 of the tokens' shape (with axis: [.., axes]) -> (q_out,
+        k_out), dense."""
         dev, rows, args = self._args(q, k, positions)
         q_out, qp = self._out(q_out, "q_out", rows, self.heads_q, dev)
         k_out, kp = self._out(k_out, "k_out", rows, self.heads_k, dev)
-        _launch(self._torch, "hyena_qk_norm_forward", self.lib.hyena_qk_norm_forward, dev, *args, qp, kp)
+        _launch(self._torch, *self._call("forward"), dev, *args, qp, kp)
         return q_out, k_out
 
     def backward_workspace_bytes(self, tokens: int, device) -> int:
@@ -861,9 +919,9 @@ class QKNorm:
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
         ws, ws_bytes = None, 0
         if dw_q is not None or dw_k is not None:
-            workspace, ws, ws_bytes = _workspace(torch, workspace, self.backward_workspace_bytes(args[1], dev), dev)
-        _launch(torch, "hyena_qk_norm_backward", self.lib.hyena_qk_norm_backward, dev, *args, *up, dqp, dkp, ptr(dw_q),
-                ptr(dw_k), ws, ws_bytes)
+            tokens = rows[0] if len(rows) == 1 else rows[0] * rows[1]
+            workspace, ws, ws_bytes = _workspace(torch, workspace, self.backward_workspace_bytes(tokens, dev), dev)
+        _launch(torch, *self._call("backward"), dev, *args, *up, dqp, dkp, ptr(dw_q), ptr(dw_k), ws, ws_bytes)
         return dq, dk, dw_q, dw_k
 
 
@@ -996,3 +1054,218 @@ class DeltaRule:
         _launch(torch, "hyena_delta_step", self.lib.hyena_delta_step, dev, self._params(scale), B, rows[1], inputs, stp, num,
                 slp, op)
         return o
+
+
+def _rows_of(t, name, rows, dim, dtype, device):
+    """Address and row stride of t [*rows, dim], as _token_rows."""
+    try:
+        if t.shape == (*rows, dim) and t.dtype is dtype and t.device == device and t.is_contiguous():
+            at = t.data_ptr()
+            if not (at | dim * dtype.itemsize) & 15:
+                return at, dim
+        return _token_rows(t.unsqueeze(-2), name, rows, 1, dim, dtype, device)
+    except AttributeError:
+        raise ValueError(f"{name} must be a tensor, got {type(t).__name__}") from None
+
+
+class GatedRecurrence:
+    """The gated linear recurrence (hyena_recurrence_* of include/hyena.h): dim channels, rate
+    [dim] fp32 on the device, above 0, dtype "f32" or "bf16". Tensors must be on one device and
+    calls run there, on its current stream; rate is used by every call."""
+
+    CARRY = 128  # HYENA_RECURRENCE_CARRY
+
+    def __init__(self, dim: int, rate, dtype: str = "bf16"):
+        import torch
+
+        self._torch = torch
+        self.lib = load_library()
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype must be one of {list(_DTYPES)}")
+        self.dim, self.dtype, self.rate = int(dim), dtype, rate
+        self.io_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        if getattr(rate, "dtype", None) != torch.float32 or rate.shape != (self.dim,) or not rate.is_contiguous():
+            raise ValueError(f"rate must be a contiguous fp32 vector of {self.dim}")
+
+    def _params(self, device=None):
+        if device is not None and self.rate.device != device:
+            raise ValueError("rate must be on the GPU that holds x")
+        return ctypes.byref(RecurrenceParamsStruct(self.dim, _DTYPES[self.dtype], self.rate.data_ptr()))
+
+    def state_shape(self, N: int):
+        return (int(N), self.dim)
+
+    def carries_shape(self, tokens: int):
+        """Of the states that a forward keeps for its backward, one every CARRY tokens."""
+        return (-(-int(tokens) // self.CARRY), self.dim)
+
+    def _inputs(self, x, r, i, rows, device):
+        return ctypes.byref(RecurrenceInputsStruct(*(
+            v for name, t in (("x", x), ("r", r), ("i", i)) for v in _rows_of(t, name, rows, self.dim, self.io_dtype, device))))
+
+    def _sequences(self, x, seq_start):
+        """(device, rows, N, tokens, address of seq_start) of x [B, T, dim] or packed [tokens, dim]."""
+        dev = _gpu_of(x, "x")
+        rows = tuple(x.shape[:-1])
+        if seq_start is None:
+            if len(rows) != 2:
+                raise ValueError("x must be [B, T, dim], or [tokens, dim] with seq_start")
+            return dev, rows, rows[0], rows[0] * rows[1], None
+        if len(rows) != 1:
+            raise ValueError("x must be [tokens, dim] with seq_start")
+        if seq_start.dim() != 1 or seq_start.numel() < 2:
+            raise ValueError("seq_start must hold N + 1 offsets")
+        N = int(seq_start.numel()) - 1
+        return dev, rows, N, rows[0], _dense(seq_start, "seq_start", (N + 1,), self._torch.int64, dev)
+
+    _out, _clear = DeltaRule._out, DeltaRule._clear
+
+    def workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
+        return int(self.lib.hyena_recurrence_workspace_bytes(self._params(), int(N), int(tokens), 16 if packed else None))
+
+    def backward_workspace_bytes(self, N: int, tokens: int, packed: bool = False, carries: bool = False) -> int:
+        return int(self.lib.hyena_recurrence_backward_workspace_bytes(
+            self._params(), int(N), int(tokens), 16 if packed else None, 16 if carries else None))
+
+    def forward(self, x, r, i, state=None, seq_start=None, y=None, state_out=None, carries=None, workspace=None):
+        """hyena_recurrence_forward: x, r, i [B, T, dim] (views with one stride between tokens are
+        taken as they are), or [tokens, dim] with seq_start [N + 1] int64 offsets on the device;
+        state [N, dim] fp32 or None (zeros); carries, unless None, an fp32 tensor of
+        carries_shape(tokens) to fill for the backward. Returns (y like x, the final states); rows
+        that belong to no sequence are zeros in y, but left as they were in a y that is given."""
+        torch = self._torch
+        dev, rows, N, tokens, starts = self._sequences(x, seq_start)
+        inputs, params = self._inputs(x, r, i, rows, dev), self._params(dev)
+        states = self.state_shape(N)
+        sp = _dense(state, "state", states, torch.float32, dev) if state is not None else None
+        cp = _dense(carries, "carries", self.carries_shape(tokens), torch.float32, dev) if carries is not None else None
+        fresh = y is None
+        y, yp = self._out(y, "y", (*rows, self.dim), self.io_dtype, dev)
+        state_out, fp = self._out(state_out, "state_out", states, torch.float32, dev)
+        need = self.lib.hyena_recurrence_workspace_bytes(params, N, tokens, starts)
+        workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
+        if fresh and starts is not None:
+            self._clear(N, tokens, starts, dev, y)
+        _launch(torch, "hyena_recurrence_forward", self.lib.hyena_recurrence_forward, dev, params, N, tokens, starts, inputs,
+                sp, yp, fp, cp, ws, ws_bytes)
+        return y, state_out
+
+    def backward(self, x, r, i, dy, state=None, dstate_out=None, seq_start=None, carries=None, workspace=None):
+        """hyena_recurrence_backward: the gradients (dx, dr, di, drate, dstate) of the forward's inputs
+        (dense, in the dtype; drate and dstate fp32) for the gradient dy [like y] of its outputs and,
+        unless None, dstate_out [N, dim] fp32 of its final states. carries: what the forward of the
+        same inputs filled, or None. Rows that belong to no sequence have gradients of zero."""
+        torch = self._torch
+        dev, rows, N, tokens, starts = self._sequences(x, seq_start)
+        inputs, params = self._inputs(x, r, i, rows, dev), self._params(dev)
+        states = self.state_shape(N)
+        dyp = _dense(dy, "dy", (*rows, self.dim), self.io_dtype, dev)
+        sp, dsp = (_dense(t, name, states, torch.float32, dev) if t is not None else None
+                   for name, t in (("state", state), ("dstate_out", dstate_out)))
+        cp = _dense(carries, "carries", self.carries_shape(tokens), torch.float32, dev) if carries is not None else None
+        out = [torch.empty((*rows, self.dim), dtype=self.io_dtype, device=dev) for _ in range(3)]
+        out += [torch.empty(shape, dtype=torch.float32, device=dev) for shape in ((self.dim,), states)]
+        need = self.lib.hyena_recurrence_backward_workspace_bytes(params, N, tokens, starts, cp)
+        workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
+        if starts is not None:
+            self._clear(N, tokens, starts, dev, *out[:3])
+        _launch(torch, "hyena_recurrence_backward", self.lib.hyena_recurrence_backward, dev, params, N, tokens, starts, inputs,
+                sp, cp, dyp, dsp, *(t.data_ptr() for t in out), ws, ws_bytes)
+        return tuple(out)
+
+    def step(self, x, r, i, states, slots=None, y=None):
+        """hyena_recurrence_step: T further tokens of B rows (x, r, i [B, T, dim]) against states
+        [num, dim] fp32, updated in place; slots [B] int32 names each row's state. Returns y like x."""
+        torch = self._torch
+        dev, rows, B, _, _ = self._sequences(x, None)
+        inputs = self._inputs(x, r, i, rows, dev)
+        num = states.shape[0] if states.dim() == 2 else 0
+        stp = _dense(states, "states", (num, self.dim), torch.float32, dev)
+        slp = _dense(slots, "slots", (B,), torch.int32, dev) if slots is not None else None
+        y, yp = self._out(y, "y", (*rows, self.dim), self.io_dtype, dev)
+        _launch(torch, "hyena_recurrence_step", self.lib.hyena_recurrence_step, dev, self._params(dev), B, rows[1], inputs, stp,
+                num, slp, yp)
+        return y
+
+
+class ResidualNorm:
+    """The addition to the residual stream with the root-mean-square norm (hyena_residual_norm_* of
+    include/hyena.h): dim columns, w [dim] fp32 weight or None; dtype "bf16" or "f32" of the rows, the
+    residual the same or, with wide_residual, fp32; bits8: outputs in 8 bits (float8_e4m3fn) with
+    fp32 scales, one a row or, with block = 128, one for 128 columns. w is used by every call."""
+
+    def __init__(self, dim: int, w=None, dtype: str = "bf16", wide_residual: bool = False, eps: float = 1e-6,
+                 bits8: bool = False, block: int = 0):
+        import torch
+
+        self._torch = torch
+        self.lib = load_library()
+        if dtype not in _DTYPES or block not in (0, 128):
+            raise ValueError(f"dtype must be one of {list(_DTYPES)}, block 0 or 128")
+        self.dim, self.dtype, self.w, self.eps = int(dim), dtype, w, float(eps)
+        self.bits8, self.block = bool(bits8), int(block)
+        self.io_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.residual_dtype = torch.float32 if wide_residual else self.io_dtype
+        if w is not None and (w.dtype != torch.float32 or w.shape != (self.dim,) or not w.is_contiguous()):
+            raise ValueError(f"w must be a contiguous fp32 vector of {self.dim}")
+
+    def _params(self, device=None):
+        if device is not None and self.w is not None and self.w.device != device:
+            raise ValueError("w must be on the GPU that holds the rows")
+        return ctypes.byref(ResidualNormParamsStruct(
+            self.dim, _DTYPES[self.dtype], HYENA_BF16 if self.residual_dtype == self._torch.bfloat16 else HYENA_F32, self.block,
+            self.eps, self.w.data_ptr() if self.w is not None else None))
+
+    def _rows(self, x, name):
+        dev, rows = _gpu_of(x, name), tuple(x.shape[:-1])
+        if len(rows) not in (1, 2):
+            raise ValueError(f"{name} must be [rows, dim] or [B, T, dim]")
+        return dev, rows, rows[0] if len(rows) == 1 else rows[0] * rows[1]
+
+    _out = DeltaRule._out
+
+    def forward(self, x, residual=None, y=None, scales=None, sum_out=None):
+        """hyena_residual_norm_forward: x [.., dim] and residual, like x or None (one stride between rows)
+        -> (y, s), with bits8 (y, scales, s): s the sum, the next layer's residual. Without a residual s
+        is x itself where it has the residual's type. sum_out may be the residual."""
+        torch = self._torch
+        dev, rows, n = self._rows(x, "x")
+        xp, ldx = _rows_of(x, "x", rows, self.dim, self.io_dtype, dev)
+        rp, ldr = (_rows_of(residual, "residual", rows, self.dim, self.residual_dtype, dev) if residual is not None
+                   else (None, self.dim))
+        y, yp = self._out(y, "y", (*rows, self.dim), torch.float8_e4m3fn if self.bits8 else self.io_dtype, dev)
+        cp = None
+        if self.bits8:
+            scales, cp = self._out(scales, "scales", (*rows, -(-self.dim // 128) if self.block else 1), torch.float32, dev)
+        if residual is None and sum_out is None and self.residual_dtype is self.io_dtype:
+            sum_out, sp = x, None
+        else:
+            sum_out, sp = self._out(sum_out, "sum_out", (*rows, self.dim), self.residual_dtype, dev)
+        _launch(torch, "hyena_residual_norm_forward", self.lib.hyena_residual_norm_forward, dev, self._params(dev), n, xp, ldx,
+                rp, ldr, yp, cp, sp)
+        return (y, scales, sum_out) if self.bits8 else (y, sum_out)
+
+    def backward_workspace_bytes(self, rows: int) -> int:
+        return int(self.lib.hyena_residual_norm_backward_workspace_bytes(self._params(), int(rows)))
+
+    def backward(self, s, dy, dsum=None, workspace=None):
+        """hyena_residual_norm_backward: (dx, dresidual, dw) for the forward's sums s, the gradient dy
+        [like y, in the rows' dtype] of its outputs and, unless None, dsum of its sums. dx and dresidual are one
+        tensor where their types are the same; dw is None without a weight."""
+        torch = self._torch
+        dev, rows, n = self._rows(s, "s")
+        sp, lds = _rows_of(s, "s", rows, self.dim, self.residual_dtype, dev)
+        shape = (*rows, self.dim)
+        dyp = _dense(dy, "dy", shape, self.io_dtype, dev)
+        dsp = _dense(dsum, "dsum", shape, self.residual_dtype, dev) if dsum is not None else None
+        dx, dxp = self._out(None, "dx", shape, self.io_dtype, dev)
+        dres, drp = dx, None
+        if self.residual_dtype is not self.io_dtype:
+            dres, drp = self._out(None, "dresidual", shape, self.residual_dtype, dev)
+        dw, dwp, ws, ws_bytes = None, None, None, 0
+        if self.w is not None:
+            dw, dwp = self._out(None, "dw", (self.dim,), torch.float32, dev)
+            workspace, ws, ws_bytes = _workspace(torch, workspace, self.backward_workspace_bytes(n), dev)
+        _launch(torch, "hyena_residual_norm_backward", self.lib.hyena_residual_norm_backward, dev, self._params(dev), n, sp, lds,
+                dyp, dsp, dxp, drp, dwp, ws, ws_bytes)
+        return dx, dres, dw

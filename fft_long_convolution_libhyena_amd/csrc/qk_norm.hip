@@ -40,6 +40,8 @@ struct NormArgs {
     const void *q, *k;
     int64_t ldq, ldk;
     const int64_t* pos;
+    const int32_t* axis;    // [rot]: which of a token's `axes` positions turns a pair, or null (one position)
+    int axes;
     const void *dqo, *dko;  // backward: upstream gradients
     void *qo, *ko;          // outputs (forward), dq and dk (backward), dense
     const float *wq, *wk, *freq;
@@ -143,9 +145,16 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
         for (int i = 0; i < 8; ++i) w[t][i] = wp ? wp[4 * (i < 4 ? qa : qb) + (i & 3)] : 1.f;
     }
     float fr[4] = {};
+    int ax[4] = {};
     if (turns)
 #pragma unroll
-        for (int p = 0; p < 4; ++p) fr[p] = a.freq[4 * lane + p];
+        for (int p = 0; p < 4; ++p) {
+            fr[p] = a.freq[4 * lane + p];
+            if (a.axis) {
+                const int i = a.axis[4 * lane + p];
+                ax[p] = i < 0 ? 0 : i < a.axes ? i : a.axes - 1;
+            }
+        }
     float dw[2][8] = {};
     const int heads = a.hq + a.hk;
     const int h0 = blockIdx.y * a.per, h1 = h0 + a.per < heads ? h0 + a.per : heads;
@@ -169,10 +178,16 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
         fetch(h0);
         float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
         if (turns && tok) {
-            const double pos = (double)a.pos[t];
+            double pos[4];
+            if (a.axis) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) pos[p] = (double)a.pos[t * a.axes + ax[p]];
+            } else {
+                pos[0] = pos[1] = pos[2] = pos[3] = (double)a.pos[t];
+            }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const double u = pos * (double)fr[p] * 0.15915494309189533577;  // turns
+                const double u = pos[p] * (double)fr[p] * 0.15915494309189533577;  // turns
                 sincospif((float)(2.0 * (u - rint(u))), &s[p], &c[p]);
             }
         }
@@ -370,6 +385,71 @@ hyena_status_t norm_check(const hyena_qk_norm_params_t* p, int64_t tokens, const
     return HYENA_OK;
 }
 
+// the forward of both entry points (axis null: one position a token)
+hyena_status_t norm_forward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes, int64_t tokens,
+                            const void* q, int64_t ldq, const void* k, int64_t ldk, const int64_t* positions,
+                            void* q_out, void* k_out, hipStream_t stream) {
+    NormArgs a;
+    const hyena_status_t st = norm_check(params, tokens, q, ldq, k, ldk, positions, a);
+    if (st != HYENA_OK) return st;
+    if (tokens > 0 && (!q_out || !k_out)) return HYENA_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(k_out)) return HYENA_ERR_INVALID_ARG;
+    if (tokens == 0) return HYENA_OK;
+    a.axis = axis;
+    a.axes = (int)axes;
+    a.qo = q_out;
+    a.ko = k_out;
+    const NormGrid g = norm_grid(*params, tokens, false);
+    a.per = g.per;
+    const bool halves = params->layout == HYENA_ROT_HALVES && params->rot > 0;
+    const hipError_t e = launch_norm<false>(params->dtype == HYENA_BF16, halves, a, g, stream);
+    return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
+}
+
+hyena_status_t norm_backward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes, int64_t tokens,
+                             const void* q, int64_t ldq, const void* k, int64_t ldk, const int64_t* positions,
+                             const void* dq_out, const void* dk_out, void* dq, void* dk, float* dw_q, float* dw_k,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    NormArgs a;
+    const hyena_status_t st = norm_check(params, tokens, q, ldq, k, ldk, positions, a);
+    if (st != HYENA_OK) return st;
+    const void* rows[] = {dq_out, dk_out, dq, dk};
+    for (const void* p : rows)
+        if ((tokens > 0 && !p) || !aligned16(p)) return HYENA_ERR_INVALID_ARG;
+    if (((uintptr_t)dw_q | (uintptr_t)dw_k) & 3u) return HYENA_ERR_INVALID_ARG;
+    const bool sums = dw_q || dw_k;
+    const size_t need = sums ? hyena_qk_norm_backward_workspace_bytes(params, tokens) : 0;
+    if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
+    if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
+    const NormGrid g = norm_grid(*params, tokens, true);
+    hipError_t e = hipSuccess;
+    if (tokens > 0) {
+        a.axis = axis;
+        a.axes = (int)axes;
+        a.dqo = dq_out;
+        a.dko = dk_out;
+        a.qo = dq;
+        a.ko = dk;
+        a.part = sums ? (float*)workspace : nullptr;
+        a.per = g.per;
+        const bool halves = params->layout == HYENA_ROT_HALVES && params->rot > 0;
+        e = launch_norm<true>(params->dtype == HYENA_BF16, halves, a, g, stream);
+    }
+    if (e == hipSuccess && sums) {  // without tokens: zeros
+        const int64_t n = tokens > 0 ? (int64_t)g.x * g.y : 0;
+        hipLaunchKernelGGL(k_qk_norm_dw, dim3((unsigned)((2 * params->dim + 31) / 32)), dim3(1024), 0, stream,
+                           (const float*)workspace, n, (int)params->dim, dw_q, dw_k);
+        e = hipGetLastError();
+    }
+    return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
+}
+
+// what the entry points with several axes check in front of the rest
+hyena_status_t axes_check(const hyena_qk_norm_params_t* p, const int32_t* axis, int64_t axes) {
+    if (!p || axes < 1 || ((uintptr_t)axis & 3u) || (p->rot > 0 && !axis)) return HYENA_ERR_INVALID_ARG;
+    return axes > 8 ? HYENA_ERR_UNSUPPORTED : HYENA_OK;
+}
+
 }  // namespace
 }  // namespace hy
 
@@ -378,20 +458,15 @@ extern "C" {
 hyena_status_t hyena_qk_norm_forward(const hyena_qk_norm_params_t* params, int64_t tokens, const void* q, int64_t ldq,
                                      const void* k, int64_t ldk, const int64_t* positions, void* q_out, void* k_out,
                                      hipStream_t stream) {
-    using hy::aligned16;
-    hy::NormArgs a;
-    const hyena_status_t st = hy::norm_check(params, tokens, q, ldq, k, ldk, positions, a);
+    return hy::norm_forward(params, nullptr, 1, tokens, q, ldq, k, ldk, positions, q_out, k_out, stream);
+}
+
+hyena_status_t hyena_qk_norm_axes_forward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes,
+                                          int64_t tokens, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                          const int64_t* positions, void* q_out, void* k_out, hipStream_t stream) {
+    const hyena_status_t st = hy::axes_check(params, axis, axes);
     if (st != HYENA_OK) return st;
-    if (tokens > 0 && (!q_out || !k_out)) return HYENA_ERR_INVALID_ARG;
-    if (!aligned16(q_out) || !aligned16(k_out)) return HYENA_ERR_INVALID_ARG;
-    if (tokens == 0) return HYENA_OK;
-    a.qo = q_out;
-    a.ko = k_out;
-    const hy::NormGrid g = hy::norm_grid(*params, tokens, false);
-    a.per = g.per;
-    const bool halves = params->layout == HYENA_ROT_HALVES && params->rot > 0;
-    const hipError_t e = hy::launch_norm<false>(params->dtype == HYENA_BF16, halves, a, g, stream);
-    return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
+    return hy::norm_forward(params, axis, axes, tokens, q, ldq, k, ldk, positions, q_out, k_out, stream);
 }
 
 size_t hyena_qk_norm_backward_workspace_bytes(const hyena_qk_norm_params_t* params, int64_t tokens) {
@@ -404,37 +479,19 @@ hyena_status_t hyena_qk_norm_backward(const hyena_qk_norm_params_t* params, int6
                                       const void* k, int64_t ldk, const int64_t* positions, const void* dq_out,
                                       const void* dk_out, void* dq, void* dk, float* dw_q, float* dw_k, void* workspace,
                                       size_t workspace_bytes, hipStream_t stream) {
-    using hy::aligned16;
-    hy::NormArgs a;
-    const hyena_status_t st = hy::norm_check(params, tokens, q, ldq, k, ldk, positions, a);
+    return hy::norm_backward(params, nullptr, 1, tokens, q, ldq, k, ldk, positions, dq_out, dk_out, dq, dk, dw_q, dw_k,
+                             workspace, workspace_bytes, stream);
+}
+
+hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes,
+                                           int64_t tokens, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                           const int64_t* positions, const void* dq_out, const void* dk_out, void* dq,
+                                           void* dk, float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+    const hyena_status_t st = hy::axes_check(params, axis, axes);
     if (st != HYENA_OK) return st;
-    const void* rows[] = {dq_out, dk_out, dq, dk};
-    for (const void* p : rows)
-        if ((tokens > 0 && !p) || !aligned16(p)) return HYENA_ERR_INVALID_ARG;
-    if (((uintptr_t)dw_q | (uintptr_t)dw_k) & 3u) return HYENA_ERR_INVALID_ARG;
-    const bool sums = dw_q || dw_k;
-    const size_t need = sums ? hyena_qk_norm_backward_workspace_bytes(params, tokens) : 0;
-    if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
-    if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
-    const hy::NormGrid g = hy::norm_grid(*params, tokens, true);
-    hipError_t e = hipSuccess;
-    if (tokens > 0) {
-        a.dqo = dq_out;
-        a.dko = dk_out;
-        a.qo = dq;
-        a.ko = dk;
-        a.part = sums ? (float*)workspace : nullptr;
-        a.per = g.per;
-        const bool halves = params->layout == HYENA_ROT_HALVES && params->rot > 0;
-        e = hy::launch_norm<true>(params->dtype == HYENA_BF16, halves, a, g, stream);
-    }
-    if (e == hipSuccess && sums) {  // without tokens: zeros
-        const int64_t n = tokens > 0 ? (int64_t)g.x * g.y : 0;
-        hipLaunchKernelGGL(hy::k_qk_norm_dw, dim3((unsigned)((2 * params->dim + 31) / 32)), dim3(1024), 0, stream,
-                           (const float*)workspace, n, (int)params->dim, dw_q, dw_k);
-        e = hipGetLastError();
-    }
-    return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
+    return hy::norm_backward(params, axis, axes, tokens, q, ldq, k, ldk, positions, dq_out, dk_out, dq, dk, dw_q, dw_k,
+                             workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -2,9 +2,10 @@
  * libhyena — the Hyena operator forward hot path, its backward, the whole
  * operator forward, the implicit filter generator, the HyenaND variants
  * (per-sample filters, circular plans, gated 2-D and 3-D long convolutions), and for
- * layers that mix Hyena with linear attention the gated delta rule (whole sequences,
- * its backward, single tokens against a pool of states) and the norm of queries and
- * keys with position rotation, on AMD MI355X (gfx950).
+ * layers that mix Hyena with linear attention the gated delta rule and the gated linear
+ * recurrence (whole sequences, their backward, single tokens against a pool of states), the
+ * norm of queries and keys with position rotation and the residual norm in front of a
+ * layer, on AMD MI355X (gfx950).
  *
  * The operator (HyenaDNA walkthrough, section 2.1, the Hyena operator module and
  * its forward pass; section 2.2, the long-filter module and its FFT convolution).
@@ -815,6 +816,156 @@ hyena_status_t hyena_qk_norm_backward(const hyena_qk_norm_params_t* params, int6
                                       const void* k, int64_t ldk, const int64_t* positions, const void* dq_out,
                                       const void* dk_out, void* dq, void* dk, float* dw_q, float* dw_k, void* workspace,
                                       size_t workspace_bytes, hipStream_t stream);
+
+/* The same with a position of its own for every axis that a token lies on (time, height and
+ * width of a video's patches, say): positions [tokens][axes] int64, device, and pair i
+ * turns by positions[t][axis[i]] * freq[i]. axis [F] int32, device (NULL if F = 0); values
+ * outside [0, axes) are held to it. How the pairs are shared out, in sections or by turns, is
+ * axis alone. 1 <= axes <= 8. Workspace, layout and errors otherwise as above;
+ * HYENA_ERR_INVALID_ARG also for axes < 1 and a NULL or misaligned axis,
+ * HYENA_ERR_UNSUPPORTED for axes > 8. */
+hyena_status_t hyena_qk_norm_axes_forward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes,
+                                          int64_t tokens, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                          const int64_t* positions, void* q_out, void* k_out, hipStream_t stream);
+hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params, const int32_t* axis, int64_t axes,
+                                           int64_t tokens, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                           const int64_t* positions, const void* dq_out, const void* dk_out, void* dq,
+                                           void* dk, float* dw_q, float* dw_k, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence: a causal mixer whose state is one value a channel. For
+ * every channel of a sequence, with the pre-activations r and i, the channel's rate c > 0
+ * and the state h, for each token in order
+ *   log a = -c sig(r);   h <- a h + sqrt(1 - a^2) sig(i) x;   y = h,   sig(z) = 1 / (1 + exp(-z)).
+ *
+ * The calls take no plan: they run on the current device, which must be the one
+ * that holds the buffers. Tokens lie behind each other as for the gated delta rule: N
+ * sequences of tokens / N each (seq_start NULL), or packed with N + 1 offsets in device
+ * memory under the same rules. Rows that belong to no sequence are neither read nor written.
+ * ------------------------------------------------------------------------ */
+#define HYENA_RECURRENCE_CARRY 128 /* tokens between the states that the forward keeps for its backward */
+
+typedef struct hyena_recurrence_params_s {
+    int64_t dim;         /* channels: a multiple of 8, at most 2^20 */
+    hyena_dtype_t dtype; /* of x, r, i, y and their gradients */
+    const float* rate;   /* [dim] fp32, device: c, above 0 and finite */
+} hyena_recurrence_params_t;
+
+/* Token t's channels lie at x + t*ldx, r + t*ldr, i + t*ldi (elements; column ranges of one
+ * projection's rows may be given as they lie); ld* at least dim, a multiple of 16 bytes and at
+ * most 2^22. */
+typedef struct hyena_recurrence_inputs_s {
+    const void* x;
+    int64_t ldx;
+    const void* r;
+    int64_t ldr;
+    const void* i;
+    int64_t ldi;
+} hyena_recurrence_inputs_t;
+
+/* Bytes of workspace hyena_recurrence_forward needs. Returns 0 for arguments that the call
+ * would refuse, and where there are no tokens. seq_start is not read. */
+size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
+                                        const int64_t* seq_start);
+
+/* The recurrence over whole sequences.
+ *   state_in  [N][dim] fp32, device, or NULL (zeros)
+ *   y         [tokens][dim] of the dtype, device (output)
+ *   state_out [N][dim] fp32, device (output), or NULL. An empty sequence passes its state on.
+ *   carries   [ceil(tokens / HYENA_RECURRENCE_CARRY)][dim] fp32, device (output), or NULL: the states
+ *             in front of rows 0, 128, 256, ..., which spare hyena_recurrence_backward a pass over
+ *             the inputs
+ *   workspace at least hyena_recurrence_workspace_bytes(...) bytes, 16-byte aligned
+ * All arithmetic is fp32 and y is rounded once. A value that is not finite spoils its channel of its
+ * sequence from its token on and nothing else. Every sum has a fixed order: results are bitwise
+ * reproducible; where a sequence lies among the rows may change their rounding. Outputs must not alias
+ * inputs. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
+ * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
+ * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 128, or 2^23 or
+ * more pairs of 128 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
+                                        const int64_t* seq_start, const hyena_recurrence_inputs_t* in,
+                                        const float* state_in, void* y, float* state_out, float* carries,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace hyena_recurrence_backward needs, with carries or (NULL) without; the
+ * pointers are not followed. Returns 0 as hyena_recurrence_workspace_bytes. */
+size_t hyena_recurrence_backward_workspace_bytes(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
+                                                 const int64_t* seq_start, const float* carries);
+
+/* Backward of hyena_recurrence_forward: with the forward's inputs and the gradients
+ *   dy         [tokens][dim] of the dtype, of y
+ *   dstate_out [N][dim] fp32, of the final states, or NULL (zeros)
+ * of one scalar, its gradients with respect to every input (outputs, dense): dx, dr, di
+ * [tokens][dim] of the dtype, drate [dim] fp32 (the whole sum over the tokens) and dstate_in [N][dim]
+ * fp32 or NULL. carries: what the forward of the same inputs and states wrote, or NULL (then they
+ * are computed again). Where sqrt(1 - a^2) falls to 0 (r far below 0), dr goes to 0 with it. Values that
+ * are not finite spoil their channel's gradients in their sequence, in front of them too, and the
+ * channel's drate. Sums and errors otherwise as the forward's. Outputs must not alias inputs or
+ * each other. */
+hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
+                                         const int64_t* seq_start, const hyena_recurrence_inputs_t* in,
+                                         const float* state_in, const float* carries, const void* dy,
+                                         const float* dstate_out, void* dx, void* dr, void* di, float* drate,
+                                         float* dstate_in, void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+
+/* The recurrent form: T further tokens of each of B rows, row b's at b*T .. b*T + T - 1 of the
+ * inputs and of y [B*T][dim]; states [num_states][dim] fp32, read and updated in place once each; slots
+ * [B] int32 or NULL, both exactly as for hyena_delta_step: rows that name the same slot are
+ * successive tokens of it, a slot outside [0, num_states) gives zeros. Enqueued on `stream`; no
+ * workspace. Errors as hyena_recurrence_forward, of N = B and tokens = B*T (HYENA_ERR_UNSUPPORTED where
+ * 2^24 pairs of a row and 512 channels are reached), and HYENA_ERR_INVALID_ARG for B, T or num_states below 1 and for NULL slots with
+ * num_states < B. */
+hyena_status_t hyena_recurrence_step(const hyena_recurrence_params_t* params, int64_t B, int64_t T,
+                                     const hyena_recurrence_inputs_t* in, float* states, int64_t num_states,
+                                     const int32_t* slots, void* y, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Residual norm: the addition to the residual stream and the root-mean-square norm in front of
+ * the next layer in one pass. For a token's row x [dim]:
+ *   s = residual + x,   y = s / sqrt(mean(s^2) + eps) * w.
+ * The norm is that of the fp32 sum; s is rounded to the residual's type where it is stored. In 8
+ * bits (e4m3: 4 exponent and 3 mantissa bits, no infinities) y is divided by the scale of its
+ * row or block of 128 columns, the largest |y| there / 448 (at least 2^-126; 1 where all are 0),
+ * and rounded to nearest even. Sums are fp32; the squares of a row sum up below 3e38: past that y is 0. An
+ * infinity or NaN spoils its row; 8-bit scales come from the values that are not NaN.
+ * ------------------------------------------------------------------------ */
+typedef struct hyena_residual_norm_params_s {
+    int64_t dim;                  /* a multiple of 8, at most 16384 */
+    hyena_dtype_t dtype;          /* of x, y and their gradients */
+    hyena_dtype_t residual_dtype; /* of the residual, s and their gradients; HYENA_F32 where dtype is */
+    int64_t block;                /* of 8-bit outputs: 128 columns a scale, or 0: one a row */
+    float eps;                    /* above 0, finite */
+    const float* w;               /* [dim] fp32, device, or NULL (ones) */
+} hyena_residual_norm_params_t;
+
+/* x [rows][dim] with ldx elements between rows (at least dim, a multiple of 16 bytes, at most 2^31);
+ * residual likewise, or NULL (s = x); y [rows][dim], dense: of the dtype, or where scales is not NULL in 8
+ * bits, with scales [rows][1 or ceil(dim / 128)] fp32; sum [rows][dim], dense: s, or NULL. Runs on
+ * the current device, no plan. y, scales and sum must not alias the inputs, but sum may be the
+ * residual itself where that is dense. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned pointers, bad sizes,
+ * ld, eps, block or types), HYENA_ERR_UNSUPPORTED (dim outside the range above, a bf16 residual of fp32
+ * rows, rows > 2^31), HYENA_ERR_DEVICE. */
+hyena_status_t hyena_residual_norm_forward(const hyena_residual_norm_params_t* params, int64_t rows, const void* x,
+                                           int64_t ldx, const void* residual, int64_t ldr, void* y, float* scales,
+                                           void* sum, hipStream_t stream);
+
+/* Bytes of workspace hyena_residual_norm_backward needs where it sums the weight's gradient (partial
+ * sums of at most 1024 workgroups). Returns 0 for arguments that the call would refuse and for rows = 0. */
+size_t hyena_residual_norm_backward_workspace_bytes(const hyena_residual_norm_params_t* params, int64_t rows);
+
+/* Backward: for the stored sums s [rows][dim] (with lds elements between rows, as ldx) and the gradients dy (of the
+ * dtype, dense) of y and dsum (of the residual's type, dense; NULL: zeros) of s, the gradient of x and of the
+ * residual, which is one and the same, rounded to either type: dx [rows][dim] of the dtype and
+ * dresidual of the residual's, dense (outputs; NULL where not wanted, not all three), and dw [dim] fp32 (output, or
+ * NULL), a complete sum in a fixed order. An output in 8 bits has the gradients of the values before
+ * they were rounded. workspace: as above, 16-byte aligned; ignored without dw. Errors as the forward's, and
+ * HYENA_ERR_WORKSPACE. Outputs must not alias inputs, but dresidual may be dsum. */
+hyena_status_t hyena_residual_norm_backward(const hyena_residual_norm_params_t* params, int64_t rows, const void* s,
+                                            int64_t lds, const void* dy, const void* dsum, void* dx, void* dresidual,
+                                            float* dw, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char* hyena_status_string(hyena_status_t s);
