@@ -4,14 +4,14 @@
 //   log a = -c sig(r),   h <- a h + m sig(i) x,   m = sqrt(1 - a^2),   y = h.
 // A run of tokens acts on the state as h -> A h + H (A the product of its a, H what it
 // gives from zero), and runs join: (A2, H2) after (A1, H1) is (A2 A1, A2 H1 + H2). So the
-// tokens, all sequences behind each other, are cut into chunks of 128, whose (A, H) need
+// tokens, all sequences behind each other, are cut into chunks, whose (A, H) need
 // only their own tokens; the states in front of the chunks follow from these. A token that
 // begins a sequence takes its initial state in and lets nothing of what lies in front through
 // (not as a factor 0: an infinity there must not become NaN here).
 //
-// A workgroup has one chunk and 128 channels: a wave 16 tokens, a lane two channels. All
-// tokens of a lane are loaded at once and their a and b = m sig(i) x stay in registers from
-// the first pass (which gives the wave's A and H) to the second (which gives the outputs).
+// A workgroup has one chunk and 128 channels: a wave 16 (backward: 8) tokens, a lane two channels. All
+// tokens of a lane are loaded at once and stay in registers from the first pass (which gives
+// the wave's A and H) to the second (which gives the outputs).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -22,13 +22,15 @@
 namespace hy {
 namespace rec {
 
-constexpr int kChunk = HYENA_RECURRENCE_CARRY;
-constexpr int kSpan = 16;                // tokens a wave
-constexpr int kWaves = kChunk / kSpan;
+constexpr int kWaves = 8;                // of a workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - kChunk;
+// Tokens a wave, forward and backward (which holds twice as much of each)
+constexpr int kForwardSpan = 16, kBackwardSpan = 8;
+constexpr int kForwardChunk = kWaves * kForwardSpan, kBackwardChunk = kWaves * kBackwardSpan;
+static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY && kForwardChunk % kBackwardChunk == 0, "states kept for the backward");
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - kForwardChunk;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ sequences
@@ -60,8 +62,9 @@ struct Seqs {
     __device__ __forceinline__ int end() const { return start ? at(N) : tokens; }
 };
 
-// What a wave's 16 tokens t0 .. are: those of some sequence are [lo, hi); bit s of `first`:
+// What a wave's S tokens t0 .. are: those of some sequence are [lo, hi); bit s of `first`:
 // token t0 + s begins a sequence, of `last`: ends one.
+template <int S>
 struct Span {
     int t0, lo, hi;
     uint32_t first, last;
@@ -69,18 +72,18 @@ struct Span {
     __device__ __forceinline__ Span(const Seqs& q, int t) : t0(t), first(0), last(0) {
         const int b = q.begin(), e = q.end();
         lo = b > t0 ? b : t0;
-        hi = e < t0 + kSpan ? e : t0 + kSpan;
+        hi = e < t0 + S ? e : t0 + S;
         if (lo >= hi) {
             lo = hi = t0;
             return;
         }
-        uint32_t starts = 0;  // of tokens t0 .. t0 + 16
+        uint32_t starts = 0;  // of tokens t0 .. t0 + S
         for (int n = q.of(lo); n <= q.N; ++n) {
             const int s = q.at(n < 0 ? 0 : n);
-            if (s > t0 + kSpan) break;
+            if (s > t0 + S) break;
             if (s >= t0) starts |= 1u << (s - t0);
         }
-        first = starts & ((1u << kSpan) - 1);
+        first = starts & ((1u << S) - 1);
         last = starts >> 1;
         if (hi == e) last |= 1u << (hi - 1 - t0);
         // offsets that decrease may name tokens outside [lo, hi)
@@ -88,10 +91,9 @@ struct Span {
         first &= mine;
         last &= mine;
     }
-    __device__ __forceinline__ bool has(int s) const { return t0 + s >= lo && t0 + s < hi; }
-    __device__ __forceinline__ bool whole() const { return hi - lo == kSpan; }
-    __device__ __forceinline__ int row(int s) const {  // a row that may be read
-        const int t = t0 + s;
+    __device__ __forceinline__ bool has(int k) const { return t0 + k >= lo && t0 + k < hi; }
+    __device__ __forceinline__ int row(int k) const {  // a row that may be read
+        const int t = t0 + k;
         return t < lo ? lo : t >= hi ? hi - 1 : t;
     }
 };
@@ -162,6 +164,76 @@ __device__ __forceinline__ void gate(float x, float r, float i, float rate, floa
     b = __builtin_amdgcn_sqrtf(q) * sigmoid(i) * x;
 }
 
+// ------------------------------------------------------------------ states between chunks
+
+// Chunks pass their states on inside one launch. Workgroups take chunks in the order of a
+// ticket; each publishes its (A, H) as soon as it has its own tokens, and only then waits for
+// those in front of it. What it waits for belongs to lower tickets, which have been drawn by workgroups that
+// run, so every wait ends; a bound on the polls ends it whatever a caller does to the workspace
+// (states are NaN then). A word of 64 bits holds both values of a channel and that they are
+// there, so no fences are needed: 0 until then, with bit 63 set (A >= 0), and A = 2 for a
+// chunk in which a sequence begins (its H is a state). The last of every 32 chunks publishes, as such
+// a word, the state behind it; so a chunk folds at most 32 words, always in the same order, and states run
+// through long sequences at a hop for 32 chunks. A wave polls four words at once.
+constexpr int kGroup = 32;
+constexpr int kPolls = 1 << 20;  // about a second
+constexpr float kReset = 2.f;
+static_assert(kGroup == 4 * kWaves, "four words a wave");
+
+using Word = unsigned long long;
+__device__ __forceinline__ Word make_word(float A, float H) {
+    A = A == A ? A : 0.f;  // H is NaN where A is
+    return (Word)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H);
+}
+__device__ __forceinline__ void join_word(float A, float H, float& h) { h = A == kReset ? H : fmaf(A, h, H); }
+
+__device__ __forceinline__ void publish(Word* words, int order, int dim, int col, const float (&A)[kVec], const float (&H)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        __hip_atomic_store(words + (int64_t)order * dim + col + j, make_word(A[j], H[j]), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// (A, H) of this wave's words: 4 wave .. of those in front of chunk `order` in its group, the first of
+// which is the last of the group before
+__device__ __forceinline__ void look_back(const Word* words, int order, int dim, int col, int wave, float (&A)[kVec],
+                                          float (&H)[kVec]) {
+    const int base = (order & ~(kGroup - 1)) - 1;
+    Word v[4][kVec];
+    for (int polls = 0;; ++polls) {
+        Word there = ~(Word)0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = base + 4 * wave + k;
+            const bool need = at >= 0 && at < order;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                v[k][j] = (Word)0xbf800000u << 32;  // (1, 0): nothing happens
+                if (need) v[k][j] = __hip_atomic_load(words + (int64_t)at * dim + col + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                there &= v[k][j];
+            }
+        }
+        if (__all((int)(there >> 63))) break;
+        if (polls >= kPolls) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[3][j] = make_word(kReset, __uint_as_float(0x7fc00000u));
+            break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        A[j] = 1.f;
+        H[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float((uint32_t)(v[k][j] >> 32) & 0x7fffffffu), h = __uint_as_float((uint32_t)v[k][j]);
+            join_word(a, h, H[j]);
+            A[j] = a == kReset || A[j] == kReset ? kReset : A[j] * a;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host side
 
 struct Call {
@@ -169,17 +241,19 @@ struct Call {
     hyena_recurrence_inputs_t in;
     Seqs seqs;
     bool bf;
-    int64_t chunks, blocks;  // chunks of tokens, blocks of channels
+    int64_t chunks, back_chunks, blocks;  // chunks of tokens (forward, backward), blocks of channels
 };
 
 hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
                      const hyena_recurrence_inputs_t* in, Call& c);
-// the states in front of every chunk; ends: [chunks][dim]
-hipError_t forward_carries(const Call& c, const float* state_in, float2* ends, float* carry, hipStream_t st);
-// states of sequences without tokens
-hipError_t pass_empty(const Call& c, const float* from, float* to, hipStream_t st);
-// states between the chunks from their (A, H), in order (dir 1) or from the last chunk (-1)
-hipError_t join_chunks(const Call& c, const float2* ends, float* carry, int dir, hipStream_t st);
+// 64-bit values at the head of a workspace that start() clears: the tickets of up to two launches, then the words
+constexpr int kHead = 2;
+inline int64_t word_count(const Call& c, int64_t chunks) { return chunks > 1 ? chunks * c.p.dim : 0; }
+// Clears `n` values of 64 bits and passes the states of sequences without tokens on; no launch without either.
+hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, hipStream_t st);
+// y, state_out and carry may each be null
+hipError_t forward(const Call& c, const float* state_in, void* y, float* state_out, float* carry, uint32_t* ticket,
+                   Word* words, hipStream_t st);
 
 }  // namespace rec
 }  // namespace hy

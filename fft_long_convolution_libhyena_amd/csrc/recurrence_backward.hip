@@ -24,72 +24,77 @@ struct BackwardArgs {
     const float* dstate_out;
     void *dx, *dr, *di;
     float* dstate_in;
-    float2* ends;         // [chunks][dim]: (A, G); A = -1: a sequence ends inside
-    const float* carry;   // [chunks][dim]: states in front of the chunks
-    const float* behind;  // [chunks][dim]: g behind the chunks
-    float* part;          // [chunks][dim]: sums of W
-    int dim;
+    const float* carry;  // [chunks][dim]: states in front of the chunks
+    float* part;         // [chunks][dim]: sums of W
+    uint32_t* ticket;
+    Word* words;         // [chunks][dim], from the last chunk on; null: one chunk
+    int dim, chunks, blocks;
 };
 
-template <bool BF, bool ENDS>
+// One chunk and 128 channels, the chunks from the last to the first.
+template <bool BF>
 __global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols], sG[kWaves][kCols];
+    constexpr int S = kBackwardSpan;
+    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols], sG[kWaves][kCols], sBackA[kWaves][kCols], sBackG[kWaves][kCols];
     __shared__ int sFirst[kWaves], sLast[kWaves];
+    __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int chunk = blockIdx.x, at = kVec * lane;
-    const int own = blockIdx.y * kCols + at;
+    int ticket = blockIdx.x;
+    if (p.words) {
+        if (threadIdx.x == 0) sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        ticket = __builtin_amdgcn_readfirstlane(sTicket);
+    }
+    const int order = ticket / p.blocks, chunk = p.chunks - 1 - order, at = kVec * lane;
+    if (chunk < 0) return;  // only where a caller's workspace is not this call's alone
+    const int own = (ticket - order * p.blocks) * kCols + at;
     const bool ok = own < p.dim;
     const int col = ok ? own : p.dim - kVec;
-    const Span span(p.seqs, chunk * kChunk + wave * kSpan);
+    const Span<S> span(p.seqs, chunk * kBackwardChunk + wave * S);
     auto state = [&](const float* from, int s, float (&h)[kVec]) {
         int n = p.seqs.of(span.t0 + s);
         n = n < 0 ? 0 : n;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = from ? from[(int64_t)n * p.dim + col + j] : 0.f;
     };
-    Raw x[kSpan], dy[kSpan];
-    float w[kSpan][kVec], a[kSpan][kVec], si[kSpan][kVec];  // w = -log a
+    Raw x[S], dy[S];
+    float w[S][kVec], si[S][kVec];  // w = -log a, sig(i)
     float A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {}, rate[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
     const bool some = span.hi > span.lo;
     if (some) {
-        Raw r[kSpan], i[kSpan];
+        Raw r[S], i[S];
+        float a[S][kVec];
 #pragma unroll
-        for (int s = 0; s < kSpan; ++s) {
+        for (int s = 0; s < S; ++s) {
             const int row = span.row(s);
             r[s] = load_row<BF>(p.in.r, p.in.ldr, row, col);
             dy[s] = load_row<BF>(p.dy, p.dim, row, col);
-            if constexpr (!ENDS) {
-                x[s] = load_row<BF>(p.in.x, p.in.ldx, row, col);
-                i[s] = load_row<BF>(p.in.i, p.in.ldi, row, col);
-            }
+            x[s] = load_row<BF>(p.in.x, p.in.ldx, row, col);
+            i[s] = load_row<BF>(p.in.i, p.in.ldi, row, col);
         }
 #pragma unroll
-        for (int s = 0; s < kSpan; ++s) {
+        for (int s = 0; s < S; ++s) {
             float rv[kVec], xv[kVec], iv[kVec];
             Io<BF>::get(r[s], rv);
-            if constexpr (!ENDS) {
-                Io<BF>::get(x[s], xv);
-                Io<BF>::get(i[s], iv);
-            }
+            Io<BF>::get(x[s], xv);
+            Io<BF>::get(i[s], iv);
             if (span.first >> s & 1) state(p.state_in, s, H);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 float q;
                 w[s][j] = rate[j] * sigmoid(rv[j]);
+                si[s][j] = sigmoid(iv[j]);
                 decay(w[s][j], a[s][j], q);
                 if (!span.has(s)) a[s][j] = 1.f;
                 A[j] *= a[s][j];
-                if constexpr (!ENDS) {
-                    si[s][j] = sigmoid(iv[j]);
-                    if (span.has(s)) H[j] = fmaf(a[s][j], H[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
-                }
+                if (span.has(s)) H[j] = fmaf(a[s][j], H[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
             }
         }
 #pragma unroll
-        for (int s = kSpan - 1; s >= 0; --s) {
+        for (int s = S - 1; s >= 0; --s) {
             float d[kVec];
             Io<BF>::get(dy[s], d);
             if (span.last >> s & 1) state(p.dstate_out, s, G);
@@ -109,60 +114,75 @@ __global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
         sLast[wave] = span.last != 0;
     }
     __syncthreads();
-    if constexpr (ENDS) {
-        if (wave == 0 && ok) {
-            float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
-            bool reset = false;
-            for (int w = kWaves - 1; w >= 0; --w) {
-                const bool rs = sLast[w];
-                reset |= rs;
+    float g[kVec] = {}, h[kVec] = {};
+    if (p.words) {
+        const bool publishes = wave == 0 && ok && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
+        float cA[kVec], cG[kVec];
+        if (publishes) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                cA[j] = 1.f;
+                cG[j] = 0.f;
+            }
+            for (int k = kWaves - 1; k >= 0; --k)
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    const float wA = sA[w][at + j], wG = sG[w][at + j];
-                    cG[j] = rs ? wG : fmaf(wA, cG[j], wG);
-                    cA[j] *= wA;
+                    const float wA = sLast[k] ? kReset : sA[k][at + j];
+                    join_word(wA, sG[k][at + j], cG[j]);
+                    cA[j] = wA == kReset || cA[j] == kReset ? kReset : cA[j] * wA;
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                p.ends[(int64_t)chunk * p.dim + own + j] = float2{reset ? -1.f : cA[j], cG[j]};
+            if (!ends) publish(p.words, order, p.dim, own, cA, cG);
         }
-        return;
+        if (order) {
+            float bA[kVec], bG[kVec];
+            look_back(p.words, order, p.dim, col, wave, bA, bG);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                sBackA[wave][at + j] = bA[j];
+                sBackG[wave][at + j] = bG[j];
+            }
+            __syncthreads();
+            for (int k = 0; k < kWaves; ++k)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) join_word(sBackA[k][at + j], sBackG[k][at + j], g[j]);
+        }
+        if (publishes && ends) {
+            float e[kVec], reset[kVec];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                e[j] = g[j];
+                join_word(cA[j], cG[j], e[j]);
+                reset[j] = kReset;
+            }
+            publish(p.words, order, p.dim, own, reset, e);
+        }
     }
     float sum[kVec] = {};
     if (some) {
-        float h[kVec], g[kVec];
+        for (int k = kWaves - 1; k > wave; --k)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
-            g[j] = p.behind[(int64_t)chunk * p.dim + col + j];
-        }
-        for (int k = 0; k < wave; ++k) {
-            const bool rs = sFirst[k];
+            for (int j = 0; j < kVec; ++j) join_word(sLast[k] ? kReset : sA[k][at + j], sG[k][at + j], g[j]);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) h[j] = rs ? sH[k][at + j] : fmaf(sA[k][at + j], h[j], sH[k][at + j]);
-        }
-        for (int k = kWaves - 1; k > wave; --k) {
-            const bool rs = sLast[k];
+        for (int j = 0; j < kVec; ++j) h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
+        for (int k = 0; k < wave; ++k)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) g[j] = rs ? sG[k][at + j] : fmaf(sA[k][at + j], g[j], sG[k][at + j]);
-        }
-        float before[kSpan][kVec];
+            for (int j = 0; j < kVec; ++j) join_word(sFirst[k] ? kReset : sA[k][at + j], sH[k][at + j], h[j]);
+        float before[S][kVec];
 #pragma unroll
-        for (int s = 0; s < kSpan; ++s) {
+        for (int s = 0; s < S; ++s) {
             float xv[kVec];
             Io<BF>::get(x[s], xv);
             if (span.first >> s & 1) state(p.state_in, s, h);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 before[s][j] = h[j];
-                float ar, q;
-                decay(w[s][j], ar, q);
-                if (span.has(s)) h[j] = fmaf(a[s][j], h[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
+                float a, q;
+                decay(w[s][j], a, q);
+                if (span.has(s)) h[j] = fmaf(a, h[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
             }
         }
 #pragma unroll
-        for (int s = kSpan - 1; s >= 0; --s) {
+        for (int s = S - 1; s >= 0; --s) {
             if (!span.has(s)) continue;
             float xv[kVec], d[kVec], ox[kVec], orr[kVec], oi[kVec];
             Io<BF>::get(x[s], xv);
@@ -171,17 +191,17 @@ __global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float dh = d[j] + g[j];
-                float ar, q;
-                decay(w[s][j], ar, q);
+                float a, q;
+                decay(w[s][j], a, q);
                 q += 1e-37f;  // w / m is 0 where both are
                 const float rs = __builtin_amdgcn_rsqf(q), m = q * rs;
                 ox[j] = dh * m * si[s][j];
                 oi[j] = ox[j] * xv[j] * (1.f - si[s][j]);
-                const float aw = a[s][j] * w[s][j];
-                const float W = dh * (a[s][j] * aw * rs * si[s][j] * xv[j] - aw * before[s][j]);
+                const float aw = a * w[s][j];
+                const float W = dh * (a * aw * rs * si[s][j] * xv[j] - aw * before[s][j]);
                 orr[j] = fmaf(-w[s][j], __builtin_amdgcn_rcpf(rate[j]), 1.f) * W;
                 sum[j] += W;
-                g[j] = a[s][j] * dh;
+                g[j] = a * dh;
             }
             if (ok) {
                 store_row<BF>(p.dx, p.dim, span.t0 + s, own, ox);
@@ -204,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             float t = 0.f;
-            for (int w = 0; w < kWaves; ++w) t += sH[w][at + j];
+            for (int k = 0; k < kWaves; ++k) t += sH[k][at + j];
             p.part[(int64_t)chunk * p.dim + own + j] = t;
         }
 }
@@ -215,8 +235,17 @@ __global__ __launch_bounds__(1024) void k_rec_drate(const float* part, const flo
     __shared__ double red[32][33];
     const int c = threadIdx.x & 31, r = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
     double s = 0;
-    if (e < dim)
-        for (int64_t i = r; i < chunks; i += 32) s += (double)part[i * dim + e];
+    if (e < dim) {
+        int64_t i = r;
+        for (; i + 224 < chunks; i += 256) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = part[(i + 32 * j) * dim + e];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += (double)x[j];
+        }
+        for (; i < chunks; i += 32) s += (double)part[i * dim + e];
+    }
     red[r][c] = s;
     __syncthreads();
     for (int d = 16; d > 0; d >>= 1) {
@@ -226,20 +255,22 @@ __global__ __launch_bounds__(1024) void k_rec_drate(const float* part, const flo
     if (r == 0 && e < dim) drate[e] = (float)(red[0][c] / (double)rate[e]);
 }
 
+// What start() clears (tickets, then the words of the backward and, without carries, the
+// forward), then the partial sums and, without carries, the states in front of the chunks
 struct Layout {
-    float2* ends;
-    float *carry, *behind, *part;
+    Word* head;
+    int64_t clear;  // words
+    float *part, *carry;
     size_t bytes;
 };
 Layout layout(const Call& c, bool carries, void* base) {
-    const size_t n = (size_t)(c.chunks * c.p.dim);
+    const int64_t n = word_count(c, c.back_chunks) + (carries ? 0 : word_count(c, c.chunks)), kept = c.back_chunks * c.p.dim;
     Layout l;
-    unsigned char* at = (unsigned char*)base;
-    l.ends = (float2*)at;
-    l.behind = (float*)(at + 8 * n);
-    l.part = l.behind + n;
-    l.carry = l.part + n;
-    l.bytes = (carries ? 16 : 20) * n;
+    l.head = (Word*)base;
+    l.clear = n ? kHead + n : 0;
+    l.part = (float*)(l.head + l.clear);
+    l.carry = l.part + kept;
+    l.bytes = (size_t)l.clear * sizeof(Word) + (size_t)kept * (carries ? 4 : 8);
     return l;
 }
 
@@ -278,30 +309,27 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
     if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return HYENA_ERR_WORKSPACE;
     if (l.bytes && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     const int dim = (int)params->dim;
-    hipError_t e = rec::pass_empty(c, dstate_out, dstate_in, stream);
+    hipError_t e = rec::start(c, l.head, l.clear, dstate_out, dstate_in, stream);
     if (e == hipSuccess && tokens > 0) {
-        if (!carries) e = rec::forward_carries(c, state_in, l.ends, l.carry, stream);
+        rec::Word* const words = l.head + rec::kHead;
+        uint32_t* const tickets = (uint32_t*)l.head;
+        if (!carries)
+            e = rec::forward(c, state_in, nullptr, nullptr, l.carry, tickets + 1, words + rec::word_count(c, c.back_chunks),
+                             stream);
         if (e != hipSuccess) return HYENA_ERR_DEVICE;
-        rec::BackwardArgs a{c.seqs,  c.in, params->rate, state_in, dy,       dstate_out,
-                            dx,      dr,   di,           dstate_in, l.ends,  carries ? carries : l.carry,
-                            l.behind, l.part, dim};
-        const dim3 grid((unsigned)c.chunks, (unsigned)c.blocks), block(rec::kThreads);
+        rec::BackwardArgs a{c.seqs, c.in,      params->rate, state_in, dy,      dstate_out,
+                            dx,     dr,        di,           dstate_in, carries ? carries : l.carry,
+                            l.part, tickets,   c.back_chunks > 1 ? words : nullptr, dim, (int)c.back_chunks, (int)c.blocks};
+        const dim3 grid((unsigned)(c.back_chunks * c.blocks)), block(rec::kThreads);
         if (c.bf)
-            hipLaunchKernelGGL((rec::k_rec_backward<true, true>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<true>, grid, block, 0, stream, a);
         else
-            hipLaunchKernelGGL((rec::k_rec_backward<false, true>), grid, block, 0, stream, a);
-        e = hipGetLastError();
-        if (e == hipSuccess) e = rec::join_chunks(c, l.ends, l.behind, -1, stream);
-        if (e != hipSuccess) return HYENA_ERR_DEVICE;
-        if (c.bf)
-            hipLaunchKernelGGL((rec::k_rec_backward<true, false>), grid, block, 0, stream, a);
-        else
-            hipLaunchKernelGGL((rec::k_rec_backward<false, false>), grid, block, 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<false>, grid, block, 0, stream, a);
         e = hipGetLastError();
     }
     if (e == hipSuccess) {
         hipLaunchKernelGGL(rec::k_rec_drate, dim3((unsigned)((dim + 31) / 32)), dim3(1024), 0, stream, l.part,
-                           params->rate, drate, c.chunks, dim);
+                           params->rate, drate, c.back_chunks, dim);
         e = hipGetLastError();
     }
     return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;

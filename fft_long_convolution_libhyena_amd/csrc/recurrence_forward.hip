@@ -13,37 +13,37 @@ struct ForwardArgs {
     hyena_recurrence_inputs_t in;
     const float *rate, *state_in;
     void* y;
-    float* state_out;
-    float2* ends;        // [chunks][dim]: (A, H) of the chunks; A = -1: a sequence begins inside
-    float* carry;        // [chunks][dim]: states in front of the chunks
-    int dim;
+    float *state_out, *carry;  // or null
+    uint32_t* ticket;
+    Word* words;               // [chunks][dim]; null: one chunk
+    int dim, chunks, blocks;
 };
 
-// One chunk and 128 channels; ENDS: only (A, H) of the chunk, otherwise the outputs from
-// the state in front of it.
-template <bool BF, bool ENDS>
+// One chunk and 128 channels.
+template <bool BF>
 __global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols];
-    __shared__ int sReset[kWaves];
+    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols], sBackA[kWaves][kCols], sBackH[kWaves][kCols];
+    __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int chunk = blockIdx.x, at = kVec * lane;
-    const int own = blockIdx.y * kCols + at;
+    int ticket = blockIdx.x;
+    if (p.words) {
+        if (threadIdx.x == 0) sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        ticket = __builtin_amdgcn_readfirstlane(sTicket);
+    }
+    const int chunk = ticket / p.blocks, at = kVec * lane;
+    if (chunk >= p.chunks) return;  // only where a caller's workspace is not this call's alone
+    const int own = (ticket - chunk * p.blocks) * kCols + at;
     const bool ok = own < p.dim;
     const int col = ok ? own : p.dim - kVec;  // lanes behind the last channel load along
-    const Span span(p.seqs, chunk * kChunk + wave * kSpan);
-    float a[kSpan][kVec], b[kSpan][kVec];
+    const Span<kForwardSpan> span(p.seqs, chunk * kForwardChunk + wave * kForwardSpan);
+    float a[kForwardSpan][kVec], b[kForwardSpan][kVec];
     float A[kVec] = {1.f, 1.f}, H[kVec] = {};
-    auto begin = [&](int s, float (&h)[kVec]) {  // the initial state of the sequence that token s begins
-        int n = p.seqs.of(span.t0 + s);
-        n = n < 0 ? 0 : n;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) h[j] = p.state_in ? p.state_in[(int64_t)n * p.dim + col + j] : 0.f;
-    };
     if (span.hi > span.lo) {
-        Raw x[kSpan], r[kSpan], i[kSpan];
+        Raw x[kForwardSpan], r[kForwardSpan], i[kForwardSpan];
 #pragma unroll
-        for (int s = 0; s < kSpan; ++s) {
+        for (int s = 0; s < kForwardSpan; ++s) {
             const int row = span.row(s);
             x[s] = load_row<BF>(p.in.x, p.in.ldx, row, col);
             r[s] = load_row<BF>(p.in.r, p.in.ldr, row, col);
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
 #pragma unroll
-        for (int s = 0; s < kSpan; ++s) {
+        for (int s = 0; s < kForwardSpan; ++s) {
             float xv[kVec], rv[kVec], iv[kVec];
             Io<BF>::get(x[s], xv);
             Io<BF>::get(r[s], rv);
@@ -66,58 +66,83 @@ __global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
                     a[s][j] = 1.f;
                     b[s][j] = 0.f;
                 }
-            if (span.first >> s & 1) begin(s, H);
+            if (span.first >> s & 1) {  // from the sequence's initial state, and from nothing in front of it
+                int n = p.seqs.of(span.t0 + s);
+                n = n < 0 ? 0 : n;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                H[j] = fmaf(a[s][j], H[j], b[s][j]);
-                A[j] *= a[s][j];
+                for (int j = 0; j < kVec; ++j) {
+                    if (p.state_in) b[s][j] = fmaf(a[s][j], p.state_in[(int64_t)n * p.dim + col + j], b[s][j]);
+                    H[j] = b[s][j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    H[j] = fmaf(a[s][j], H[j], b[s][j]);
+                    A[j] *= a[s][j];
+                }
             }
         }
     }
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        sA[wave][at + j] = A[j];
+        sA[wave][at + j] = span.first ? kReset : A[j];
         sH[wave][at + j] = H[j];
     }
-    if (lane == 0) sReset[wave] = span.first != 0;
     __syncthreads();
-    if constexpr (ENDS) {
-        if (wave == 0 && ok) {
-            float cA[kVec] = {1.f, 1.f}, cH[kVec] = {};
-            bool reset = false;
-            for (int w = 0; w < kWaves; ++w) {
-                const bool rs = sReset[w];
-                reset |= rs;
+    float h[kVec] = {};
+    if (p.words) {
+        const bool publishes = wave == 0 && ok && chunk + 1 < p.chunks, ends = (chunk & (kGroup - 1)) == kGroup - 1;
+        float cA[kVec], cH[kVec];
+        if (publishes) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                cA[j] = 1.f;
+                cH[j] = 0.f;
+            }
+            for (int k = 0; k < kWaves; ++k)
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    const float wA = sA[w][at + j], wH = sH[w][at + j];
-                    cH[j] = rs ? wH : fmaf(wA, cH[j], wH);
-                    cA[j] *= wA;
+                    const float wA = sA[k][at + j];
+                    join_word(wA, sH[k][at + j], cH[j]);
+                    cA[j] = wA == kReset || cA[j] == kReset ? kReset : cA[j] * wA;
                 }
+            if (!ends) publish(p.words, chunk, p.dim, own, cA, cH);
+        }
+        if (chunk) {
+            float bA[kVec], bH[kVec];
+            look_back(p.words, chunk, p.dim, col, wave, bA, bH);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                sBackA[wave][at + j] = bA[j];
+                sBackH[wave][at + j] = bH[j];
             }
+            __syncthreads();
+            for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                p.ends[(int64_t)chunk * p.dim + own + j] = float2{reset ? -1.f : cA[j], cH[j]};
+                for (int j = 0; j < kVec; ++j) join_word(sBackA[k][at + j], sBackH[k][at + j], h[j]);
         }
-        return;
-    }
-    if (span.hi <= span.lo) return;
-    float h[kVec];
+        if (publishes && ends) {
+            float e[kVec], reset[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
-    for (int w = 0; w < wave; ++w) {
-        const bool rs = sReset[w];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float wH = sH[w][at + j];
-            h[j] = rs ? wH : fmaf(sA[w][at + j], h[j], wH);
+            for (int j = 0; j < kVec; ++j) {
+                e[j] = h[j];
+                join_word(cA[j], cH[j], e[j]);
+                reset[j] = kReset;
+            }
+            publish(p.words, chunk, p.dim, own, reset, e);
         }
     }
+    for (int k = 0; k < wave; ++k)
 #pragma unroll
-    for (int s = 0; s < kSpan; ++s) {
-        if (span.first >> s & 1) begin(s, h);
+        for (int j = 0; j < kVec; ++j) join_word(sA[k][at + j], sH[k][at + j], h[j]);
+    if (p.carry && span.t0 % kBackwardChunk == 0 && span.t0 < p.seqs.tokens && ok)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) h[j] = fmaf(a[s][j], h[j], b[s][j]);
+        for (int j = 0; j < kVec; ++j) p.carry[(int64_t)(span.t0 / kBackwardChunk) * p.dim + own + j] = h[j];
+    if (!p.y || span.hi <= span.lo) return;
+#pragma unroll
+    for (int s = 0; s < kForwardSpan; ++s) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) h[j] = span.first >> s & 1 ? b[s][j] : fmaf(a[s][j], h[j], b[s][j]);
         if (ok && span.has(s)) store_row<BF>(p.y, p.dim, span.t0 + s, own, h);
         if (p.state_out && (span.last >> s & 1) && ok) {
             int n = p.seqs.of(span.t0 + s);
@@ -128,42 +153,40 @@ __global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
     }
 }
 
-// states between the chunks of one channel, in order (DIR 1) or from the last (DIR -1)
-__global__ __launch_bounds__(64) void k_rec_carry(const float2* ends, float* carry, int chunks, int dim, int dir) {
-    const int col = blockIdx.x * 64 + threadIdx.x;
-    if (col >= dim) return;
-    float h = 0.f;
-    for (int k = 0; k < chunks; ++k) {
-        const int64_t e = (int64_t)(dir > 0 ? k : chunks - 1 - k) * dim + col;
-        const float2 v = ends[e];
-        carry[e] = h;
-        h = v.x < 0.f ? v.y : fmaf(v.x, h, v.y);
-    }
-}
-
-// A sequence without tokens passes its state on.
-__global__ __launch_bounds__(256) void k_rec_empty(Seqs q, const float* from, float* to, int dim) {
-    for (int n = blockIdx.x; n < q.N; n += gridDim.x) {
-        if (q.at(n + 1) > q.at(n)) continue;
-        for (int c = threadIdx.x; c < dim; c += 256) {
-            const int64_t e = (int64_t)n * dim + c;
-            to[e] = from ? from[e] : 0.f;
+// Clears what the chunks' words and tickets lie in; a sequence without tokens passes its state on.
+__global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs q, const float* from, float* to, int dim) {
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) clear[e] = 0;
+    if (to)
+        for (int s = blockIdx.x; s < q.N; s += gridDim.x) {
+            if (q.at(s + 1) > q.at(s)) continue;
+            for (int c = threadIdx.x; c < dim; c += 256) {
+                const int64_t e = (int64_t)s * dim + c;
+                to[e] = from ? from[e] : 0.f;
+            }
         }
-    }
 }
 
 }  // namespace
 
-hipError_t join_chunks(const Call& c, const float2* ends, float* carry, int dir, hipStream_t st) {
-    hipLaunchKernelGGL(k_rec_carry, dim3((unsigned)((c.p.dim + 63) / 64)), dim3(64), 0, st, ends, carry, (int)c.chunks,
-                       (int)c.p.dim, dir);
+hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, hipStream_t st) {
+    if (!(c.seqs.start || c.seqs.T == 0)) to = nullptr;  // every sequence has tokens
+    if (!n && !to) return hipSuccess;
+    int64_t wgs = (n + 1023) / 1024;
+    wgs = to && wgs < c.seqs.N ? c.seqs.N : wgs;
+    hipLaunchKernelGGL(k_rec_start, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, st, (Word*)clear, n, c.seqs, from, to,
+                       (int)c.p.dim);
     return hipGetLastError();
 }
 
-hipError_t pass_empty(const Call& c, const float* from, float* to, hipStream_t st) {
-    if (!to || !(c.seqs.start || c.seqs.T == 0)) return hipSuccess;
-    hipLaunchKernelGGL(k_rec_empty, dim3((unsigned)(c.seqs.N < 4096 ? c.seqs.N : 4096)), dim3(256), 0, st, c.seqs, from,
-                       to, (int)c.p.dim);
+hipError_t forward(const Call& c, const float* state_in, void* y, float* state_out, float* carry, uint32_t* ticket,
+                   Word* words, hipStream_t st) {
+    ForwardArgs a{c.seqs, c.in,   c.p.rate, state_in, y, state_out, carry, ticket, c.chunks > 1 ? words : nullptr,
+                  (int)c.p.dim, (int)c.chunks, (int)c.blocks};
+    const dim3 grid((unsigned)(c.chunks * c.blocks));
+    if (c.bf)
+        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(kThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -177,9 +200,10 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
         return HYENA_ERR_UNSUPPORTED;
     c.p = *p;
     c.bf = p->dtype == HYENA_BF16;
-    c.chunks = (tokens + kChunk - 1) / kChunk;
+    c.chunks = (tokens + kForwardChunk - 1) / kForwardChunk;
+    c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
     c.blocks = (p->dim + kCols - 1) / kCols;
-    if (c.chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
+    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
     c.seqs = Seqs{seq_start, (int)N, (int)tokens, (int)(tokens / N)};
     if (!in) return HYENA_OK;
     c.in = *in;
@@ -192,18 +216,6 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
     return HYENA_OK;
 }
 
-hipError_t forward_carries(const Call& c, const float* state_in, float2* ends, float* carry, hipStream_t st) {
-    ForwardArgs a{c.seqs, c.in, c.p.rate, state_in, nullptr, nullptr, ends, carry, (int)c.p.dim};
-    const dim3 grid((unsigned)c.chunks, (unsigned)c.blocks);
-    if (c.bf)
-        hipLaunchKernelGGL((k_rec_forward<true, true>), grid, dim3(kThreads), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_rec_forward<false, true>), grid, dim3(kThreads), 0, st, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    return join_chunks(c, ends, carry, 1, st);
-}
-
 }  // namespace rec
 }  // namespace hy
 
@@ -213,7 +225,8 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
                                         const int64_t* seq_start) {
     hy::rec::Call c;
     if (hy::rec::check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
-    return (size_t)(c.chunks * params->dim) * 12;
+    const int64_t n = hy::rec::word_count(c, c.chunks);
+    return n ? (size_t)(hy::rec::kHead + n) * sizeof(hy::rec::Word) : 0;
 }
 
 hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
@@ -230,20 +243,10 @@ hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params,
     const size_t need = hyena_recurrence_workspace_bytes(params, N, tokens, seq_start);
     if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
-    hipError_t e = rec::pass_empty(c, state_in, state_out, stream);
-    if (e == hipSuccess && tokens > 0) {
-        float2* ends = (float2*)workspace;
-        float* carry = carries ? carries : (float*)(ends + c.chunks * params->dim);
-        e = rec::forward_carries(c, state_in, ends, carry, stream);
-        if (e != hipSuccess) return HYENA_ERR_DEVICE;
-        rec::ForwardArgs a{c.seqs, c.in, params->rate, state_in, y, state_out, ends, carry, (int)params->dim};
-        const dim3 grid((unsigned)c.chunks, (unsigned)c.blocks);
-        if (c.bf)
-            hipLaunchKernelGGL((rec::k_rec_forward<true, false>), grid, dim3(rec::kThreads), 0, stream, a);
-        else
-            hipLaunchKernelGGL((rec::k_rec_forward<false, false>), grid, dim3(rec::kThreads), 0, stream, a);
-        e = hipGetLastError();
-    }
+    rec::Word* head = (rec::Word*)workspace;
+    hipError_t e = rec::start(c, head, (int64_t)(need / sizeof(rec::Word)), state_in, state_out, stream);
+    if (e == hipSuccess && tokens > 0)
+        e = rec::forward(c, state_in, y, state_out, carries, (uint32_t*)head, head + rec::kHead, stream);
     return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;
 }
 
