@@ -58,44 +58,34 @@ struct Seqs {
         }
         return lo - 1;
     }
-    __device__ __forceinline__ int begin() const { return start ? at(0) : 0; }
-    __device__ __forceinline__ int end() const { return start ? at(N) : tokens; }
 };
 
-// What a wave's S tokens t0 .. are: those of some sequence are [lo, hi); bit s of `first`:
-// token t0 + s begins a sequence, of `last`: ends one.
+// What a wave's S tokens t0 .. are; lane s finds out about token t0 + s. Bit s of `have`: it is of some
+// sequence, of `first`: begins one, of `last`: ends one. Offsets that decrease give other bits, but
+// sequences and rows stay in range. Tokens of no sequence lie in front of the first and behind the last
+// one, so what they do to states reaches no other token: they take part with the values of some row.
 template <int S>
 struct Span {
-    int t0, lo, hi;
-    uint32_t first, last;
+    int t0, mine;  // mine: the sequence of this lane's token
+    uint32_t have, first, last;
 
-    __device__ __forceinline__ Span(const Seqs& q, int t) : t0(t), first(0), last(0) {
-        const int b = q.begin(), e = q.end();
-        lo = b > t0 ? b : t0;
-        hi = e < t0 + S ? e : t0 + S;
-        if (lo >= hi) {
-            lo = hi = t0;
-            return;
-        }
-        uint32_t starts = 0;  // of tokens t0 .. t0 + S
-        for (int n = q.of(lo); n <= q.N; ++n) {
-            const int s = q.at(n < 0 ? 0 : n);
-            if (s > t0 + S) break;
-            if (s >= t0) starts |= 1u << (s - t0);
-        }
-        first = starts & ((1u << S) - 1);
-        last = starts >> 1;
-        if (hi == e) last |= 1u << (hi - 1 - t0);
-        // offsets that decrease may name tokens outside [lo, hi)
-        const uint32_t mine = ((1u << (hi - t0)) - 1) & ~((1u << (lo - t0)) - 1);
-        first &= mine;
-        last &= mine;
+    __device__ __forceinline__ Span(const Seqs& q, int t0_) : t0(t0_) {
+        const int t = t0 + (threadIdx.x & 63);
+        const bool in = (threadIdx.x & 63) < S && t < q.tokens;
+        mine = in ? q.of(t) : -1;
+        const bool some = mine >= 0 && mine < q.N;
+        mine = some ? mine : 0;
+        const int end = some ? q.at(mine + 1) : 0;
+        have = (uint32_t)__ballot(some && t < end);
+        first = (uint32_t)__ballot(some && t < end && q.at(mine) == t);
+        last = (uint32_t)__ballot(some && t + 1 == end);
     }
-    __device__ __forceinline__ bool has(int k) const { return t0 + k >= lo && t0 + k < hi; }
-    __device__ __forceinline__ int row(int k) const {  // a row that may be read
-        const int t = t0 + k;
-        return t < lo ? lo : t >= hi ? hi - 1 : t;
-    }
+    __device__ __forceinline__ bool has(int s) const { return have >> s & 1; }
+    __device__ __forceinline__ bool begins(int s) const { return first >> s & 1; }
+    __device__ __forceinline__ bool ends(int s) const { return last >> s & 1; }
+    __device__ __forceinline__ int sequence(int s) const { return __builtin_amdgcn_readlane(mine, s); }
+    // a row of some sequence, from t0 on: token s's, where it has one (not without any)
+    __device__ __forceinline__ int row(int s) const { return has(s) ? s : __builtin_ctz(have); }
 };
 
 // ------------------------------------------------------------------ values
@@ -127,16 +117,36 @@ struct Io<false> {
     static __device__ __forceinline__ Raw put(const float (&x)[kVec]) { return Raw{x[0], x[1]}; }
 };
 
+// Rows t0 .. of an array, read and written by buffer instructions: the row is a scalar offset and the
+// lane's channels a constant one, so an access costs no vector arithmetic; a lane behind the last channel
+// has the offset kNone outside of the range, loads 0 and stores nothing.
+constexpr int kNone = (int)0x80000000u;
 template <bool BF>
-__device__ __forceinline__ typename Io<BF>::Raw load_row(const void* base, int64_t ld, int row, int col) {
-    const char* p = (const char*)base + (int64_t)row * ld * Io<BF>::kBytes;
-    return *reinterpret_cast<const typename Io<BF>::Raw*>(p + (uint32_t)(col * Io<BF>::kBytes));
-}
-template <bool BF>
-__device__ __forceinline__ void store_row(void* base, int64_t ld, int row, int col, const float (&x)[kVec]) {
-    char* p = (char*)base + (int64_t)row * ld * Io<BF>::kBytes;
-    *reinterpret_cast<typename Io<BF>::Raw*>(p + (uint32_t)(col * Io<BF>::kBytes)) = Io<BF>::put(x);
-}
+struct Rows {
+    __amdgpu_buffer_rsrc_t buf;
+    int pitch;  // bytes
+
+    // rows: at most 64; 64 * 2^22 * 4 bytes stay below kNone
+    __device__ __forceinline__ Rows(const void* base, int64_t ld, int t0, int rows, int dim) {
+        pitch = (int)ld * Io<BF>::kBytes;
+        buf = __builtin_amdgcn_make_buffer_rsrc((char*)const_cast<void*>(base) + (int64_t)t0 * ld * Io<BF>::kBytes, 0,
+                                                rows > 0 ? (rows - 1) * pitch + dim * Io<BF>::kBytes : 0, 0x00020000);
+    }
+    __device__ __forceinline__ typename Io<BF>::Raw load(int row, int at) const {
+        if constexpr (BF)
+            return __builtin_amdgcn_raw_buffer_load_b32(buf, at, row * pitch, 0);
+        else
+            return __builtin_bit_cast(typename Io<BF>::Raw, __builtin_amdgcn_raw_buffer_load_b64(buf, at, row * pitch, 0));
+    }
+    __device__ __forceinline__ void store(int row, int at, const float (&x)[kVec]) const {
+        if constexpr (BF) {
+            __builtin_amdgcn_raw_buffer_store_b32(Io<BF>::put(x), buf, at, row * pitch, 0);
+        } else {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, Io<BF>::put(x)), buf, at, row * pitch, 0);
+        }
+    }
+};
 
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
@@ -146,23 +156,30 @@ __device__ __forceinline__ float sigmoid(float x) {
 // w times a polynomial (a fit of degree 5 at Chebyshev points, 5e-9 off) with half a step of error and no
 // bias, and q = e (1 + a) keeps e's digits. (With the exponential instruction, a step off to one
 // side, states of 2000 tokens with a around 0.999 were 2.7e-6 off in place of 5e-7.)
-__device__ __forceinline__ void decay(float w, float& a, float& q) {
-    float p = fmaf(w, -0.0011237150756642222f, 0.008190003223717213f);
-    p = fmaf(w, p, -0.04163024201989174f);
-    p = fmaf(w, p, 0.16666245460510254f);
-    p = fmaf(w, p, -0.4999998211860657f);
-    p = fmaf(w, p, 1.f);
-    const float far = __builtin_amdgcn_exp2f(-kLog2e * w);
-    const bool near = w < 0.5f;
-    const float e = near ? w * p : 1.f - far;
-    a = near ? 1.f - e : far;
-    q = fmaf(e, a, e);
+// near (of the wave): all w are known to be below 1/2, as rates below 1/2 make them.
+__device__ __forceinline__ void decay(const float (&w)[kVec], bool near, float (&a)[kVec], float (&q)[kVec]) {
+    float e[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        float p = fmaf(w[j], -0.0011237150756642222f, 0.008190003223717213f);
+        p = fmaf(w[j], p, -0.04163024201989174f);
+        p = fmaf(w[j], p, 0.16666245460510254f);
+        p = fmaf(w[j], p, -0.4999998211860657f);
+        p = fmaf(w[j], p, 1.f);
+        e[j] = w[j] * p;
+        a[j] = 1.f - e[j];
+    }
+    if (!near)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const float far = __builtin_amdgcn_exp2f(-kLog2e * w[j]);
+            a[j] = w[j] < 0.5f ? a[j] : far;
+            e[j] = w[j] < 0.5f ? e[j] : 1.f - far;
+        }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) q[j] = fmaf(e[j], a[j], e[j]);
 }
-__device__ __forceinline__ void gate(float x, float r, float i, float rate, float& a, float& b) {
-    float q;
-    decay(rate * sigmoid(r), a, q);
-    b = __builtin_amdgcn_sqrtf(q) * sigmoid(i) * x;
-}
+__device__ __forceinline__ bool near_rates(const float (&rate)[kVec]) { return __all(rate[0] < 0.5f && rate[1] < 0.5f); }
 
 // ------------------------------------------------------------------ states between chunks
 
@@ -177,61 +194,74 @@ __device__ __forceinline__ void gate(float x, float r, float i, float rate, floa
 // through long sequences at a hop for 32 chunks. A wave polls four words at once.
 constexpr int kGroup = 32;
 constexpr int kPolls = 1 << 20;  // about a second
-constexpr float kReset = 2.f;
 static_assert(kGroup == 4 * kWaves, "four words a wave");
 
 using Word = unsigned long long;
-__device__ __forceinline__ Word make_word(float A, float H) {
-    A = A == A ? A : 0.f;  // H is NaN where A is
-    return (Word)(__float_as_uint(A) | 0x80000000u) << 32 | __float_as_uint(H);
-}
-__device__ __forceinline__ void join_word(float A, float H, float& h) { h = A == kReset ? H : fmaf(A, h, H); }
+constexpr uint32_t kResetWord = 0xc0000000u;  // the high half: A = -2
 
-__device__ __forceinline__ void publish(Word* words, int order, int dim, int col, const float (&A)[kVec], const float (&H)[kVec]) {
+// (A, H) of a lane's two channels
+typedef float Link __attribute__((ext_vector_type(4)));  // A, A, H, H
+__device__ __forceinline__ void join_link(bool reset, const Link& v, float (&h)[kVec]) {
+    h[0] = reset ? v[2] : fmaf(v[0], h[0], v[2]);
+    h[1] = reset ? v[3] : fmaf(v[1], h[1], v[3]);
+}
+
+__device__ __forceinline__ void publish(Word* words, int order, int dim, int col, bool reset, const float (&A)[kVec],
+                                        const float (&H)[kVec]) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-        __hip_atomic_store(words + (int64_t)order * dim + col + j, make_word(A[j], H[j]), __ATOMIC_RELAXED,
+    for (int j = 0; j < kVec; ++j) {
+        const float a = A[j] == A[j] ? A[j] : 0.f;  // H is NaN where A is
+        const uint32_t hi = reset ? kResetWord : __float_as_uint(a) | 0x80000000u;
+        __hip_atomic_store(words + (int64_t)order * dim + col + j, (Word)hi << 32 | __float_as_uint(H[j]), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
+    }
 }
 
 // (A, H) of this wave's words: 4 wave .. of those in front of chunk `order` in its group, the first of
-// which is the last of the group before
-__device__ __forceinline__ void look_back(const Word* words, int order, int dim, int col, int wave, float (&A)[kVec],
-                                          float (&H)[kVec]) {
-    const int base = (order & ~(kGroup - 1)) - 1;
+// which is the last of the group before. Returns whether a sequence begins among them.
+__device__ __forceinline__ bool look_back(const Word* words, int order, int dim, int col, int wave, Link& link) {
+    const int base = (order & ~(kGroup - 1)) - 1 + 4 * wave;
     Word v[4][kVec];
     for (int polls = 0;; ++polls) {
         Word there = ~(Word)0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int at = base + 4 * wave + k;
-            const bool need = at >= 0 && at < order;
+            const int at = base + k;
+            if (at >= 0 && at < order) {
+                const Word* p = words + (int64_t)at * dim;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                v[k][j] = (Word)0xbf800000u << 32;  // (1, 0): nothing happens
-                if (need) v[k][j] = __hip_atomic_load(words + (int64_t)at * dim + col + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                there &= v[k][j];
+                for (int j = 0; j < kVec; ++j) {
+                    v[k][j] = __hip_atomic_load(p + (uint32_t)(col + j), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    there &= v[k][j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[k][j] = (Word)0xbf800000u << 32;  // (1, 0): nothing happens
             }
         }
         if (__all((int)(there >> 63))) break;
         if (polls >= kPolls) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) v[3][j] = make_word(kReset, __uint_as_float(0x7fc00000u));
+            for (int j = 0; j < kVec; ++j) v[3][j] = (Word)kResetWord << 32 | 0x7fc00000u;
             break;
         }
         __builtin_amdgcn_s_sleep(1);
     }
+    bool any = false;
+    link = Link{1.f, 1.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        A[j] = 1.f;
-        H[j] = 0.f;
+    for (int k = 0; k < 4; ++k) {
+        // the same for all channels
+        const bool reset = __builtin_amdgcn_readfirstlane((int)(v[k][0] >> 32)) == (int)kResetWord;
+        any |= reset;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float a = __uint_as_float((uint32_t)(v[k][j] >> 32) & 0x7fffffffu), h = __uint_as_float((uint32_t)v[k][j]);
-            join_word(a, h, H[j]);
-            A[j] = a == kReset || A[j] == kReset ? kReset : A[j] * a;
+        for (int j = 0; j < kVec; ++j) {
+            const float a = fabsf(__uint_as_float((uint32_t)(v[k][j] >> 32))), h = __uint_as_float((uint32_t)v[k][j]);
+            link[2 + j] = reset ? h : fmaf(a, link[2 + j], h);
+            link[j] *= a;
         }
     }
+    return any;
 }
 
 // ------------------------------------------------------------------ host side

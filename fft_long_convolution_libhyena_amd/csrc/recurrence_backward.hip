@@ -33,11 +33,12 @@ struct BackwardArgs {
 
 // One chunk and 128 channels, the chunks from the last to the first.
 template <bool BF>
-__global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
+__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
     using Raw = typename Io<BF>::Raw;
     constexpr int S = kBackwardSpan;
-    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols], sG[kWaves][kCols], sBackA[kWaves][kCols], sBackG[kWaves][kCols];
-    __shared__ int sFirst[kWaves], sLast[kWaves];
+    __shared__ Link sOwn[kWaves][64], sBehind[kWaves][64];
+    __shared__ float2 sG[kWaves][64];
+    __shared__ int sFirst[kWaves], sLast[kWaves], sBehindReset[kWaves];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ticket = blockIdx.x;
@@ -46,187 +47,174 @@ __global__ __launch_bounds__(kThreads) void k_rec_backward(BackwardArgs p) {
         __syncthreads();
         ticket = __builtin_amdgcn_readfirstlane(sTicket);
     }
-    const int order = ticket / p.blocks, chunk = p.chunks - 1 - order, at = kVec * lane;
+    const int order = (uint32_t)ticket / (uint32_t)p.blocks, chunk = p.chunks - 1 - order;
     if (chunk < 0) return;  // only where a caller's workspace is not this call's alone
-    const int own = (ticket - order * p.blocks) * kCols + at;
+    const int own = (ticket - order * p.blocks) * kCols + kVec * lane;
     const bool ok = own < p.dim;
-    const int col = ok ? own : p.dim - kVec;
+    const int col = ok ? own : p.dim - kVec, at = ok ? own * Io<BF>::kBytes : kNone;
     const Span<S> span(p.seqs, chunk * kBackwardChunk + wave * S);
+    const int rows = p.seqs.tokens - span.t0 < S ? p.seqs.tokens - span.t0 : S;
     auto state = [&](const float* from, int s, float (&h)[kVec]) {
-        int n = p.seqs.of(span.t0 + s);
-        n = n < 0 ? 0 : n;
+        const int64_t n = span.sequence(s);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) h[j] = from ? from[(int64_t)n * p.dim + col + j] : 0.f;
+        for (int j = 0; j < kVec; ++j) h[j] = from ? from[n * p.dim + col + j] : 0.f;
     };
     Raw x[S], dy[S];
-    float w[S][kVec], si[S][kVec];  // w = -log a, sig(i)
-    float A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {}, rate[kVec];
+    float w[S][kVec], si[S][kVec], a[S][kVec], b[S][kVec];  // w = -log a, sig(i), a, m sig(i) x
+    float rate[kVec], A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
-    const bool some = span.hi > span.lo;
-    if (some) {
+    const bool near = near_rates(rate);
+    if (span.have) {
         Raw r[S], i[S];
-        float a[S][kVec];
+        const Rows<BF> xs(p.in.x, p.in.ldx, span.t0, rows, p.dim), rs(p.in.r, p.in.ldr, span.t0, rows, p.dim),
+            is(p.in.i, p.in.ldi, span.t0, rows, p.dim), ds(p.dy, p.dim, span.t0, rows, p.dim);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int row = span.row(s);
-            r[s] = load_row<BF>(p.in.r, p.in.ldr, row, col);
-            dy[s] = load_row<BF>(p.dy, p.dim, row, col);
-            x[s] = load_row<BF>(p.in.x, p.in.ldx, row, col);
-            i[s] = load_row<BF>(p.in.i, p.in.ldi, row, col);
+            r[s] = rs.load(row, at);
+            i[s] = is.load(row, at);
+            x[s] = xs.load(row, at);
+            dy[s] = ds.load(row, at);
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float rv[kVec], xv[kVec], iv[kVec];
+            float rv[kVec], xv[kVec], iv[kVec], q[kVec];
             Io<BF>::get(r[s], rv);
             Io<BF>::get(x[s], xv);
             Io<BF>::get(i[s], iv);
-            if (span.first >> s & 1) state(p.state_in, s, H);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                float q;
                 w[s][j] = rate[j] * sigmoid(rv[j]);
                 si[s][j] = sigmoid(iv[j]);
-                decay(w[s][j], a[s][j], q);
-                if (!span.has(s)) a[s][j] = 1.f;
+            }
+            decay(w[s], near, a[s], q);
+            if (span.begins(s)) state(p.state_in, s, H);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                b[s][j] = __builtin_amdgcn_sqrtf(q[j]) * si[s][j] * xv[j];
+                H[j] = fmaf(a[s][j], H[j], b[s][j]);
                 A[j] *= a[s][j];
-                if (span.has(s)) H[j] = fmaf(a[s][j], H[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
             }
         }
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             float d[kVec];
             Io<BF>::get(dy[s], d);
-            if (span.last >> s & 1) state(p.dstate_out, s, G);
-            if (span.has(s))
+            if (span.ends(s)) state(p.dstate_out, s, G);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) G[j] = a[s][j] * (d[j] + G[j]);
+            for (int j = 0; j < kVec; ++j) G[j] = a[s][j] * (d[j] + G[j]);
         }
     }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        sA[wave][at + j] = A[j];
-        sH[wave][at + j] = H[j];
-        sG[wave][at + j] = G[j];
-    }
+    sOwn[wave][lane] = Link{A[0], A[1], H[0], H[1]};
+    sG[wave][lane] = float2{G[0], G[1]};
     if (lane == 0) {
         sFirst[wave] = span.first != 0;
         sLast[wave] = span.last != 0;
     }
     __syncthreads();
+    auto behind = [&](int k) {  // (A, G) of wave k
+        const Link v = sOwn[k][lane];
+        const float2 u = sG[k][lane];
+        return Link{v[0], v[1], u.x, u.y};
+    };
     float g[kVec] = {}, h[kVec] = {};
     if (p.words) {
-        const bool publishes = wave == 0 && ok && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
-        float cA[kVec], cG[kVec];
+        const bool publishes = wave == 0 && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
+        float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
+        bool reset = false;
         if (publishes) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                cA[j] = 1.f;
-                cG[j] = 0.f;
+            for (int k = kWaves - 1; k >= 0; --k) {
+                const Link v = behind(k);
+                const bool rs = __builtin_amdgcn_readfirstlane(sLast[k]);
+                reset |= rs;
+                join_link(rs, v, cG);
+                cA[0] *= v[0];
+                cA[1] *= v[1];
             }
-            for (int k = kWaves - 1; k >= 0; --k)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const float wA = sLast[k] ? kReset : sA[k][at + j];
-                    join_word(wA, sG[k][at + j], cG[j]);
-                    cA[j] = wA == kReset || cA[j] == kReset ? kReset : cA[j] * wA;
-                }
-            if (!ends) publish(p.words, order, p.dim, own, cA, cG);
+            if (!ends && ok) publish(p.words, order, p.dim, own, reset, cA, cG);
         }
         if (order) {
-            float bA[kVec], bG[kVec];
-            look_back(p.words, order, p.dim, col, wave, bA, bG);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                sBackA[wave][at + j] = bA[j];
-                sBackG[wave][at + j] = bG[j];
-            }
+            Link back;
+            const bool rs = look_back(p.words, order, p.dim, col, wave, back);
+            sBehind[wave][lane] = back;
+            if (lane == 0) sBehindReset[wave] = rs;
             __syncthreads();
-            for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) join_word(sBackA[k][at + j], sBackG[k][at + j], g[j]);
+            for (int k = 0; k < kWaves; ++k) join_link(__builtin_amdgcn_readfirstlane(sBehindReset[k]), sBehind[k][lane], g);
         }
         if (publishes && ends) {
-            float e[kVec], reset[kVec];
+            float e[kVec];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                e[j] = g[j];
-                join_word(cA[j], cG[j], e[j]);
-                reset[j] = kReset;
-            }
-            publish(p.words, order, p.dim, own, reset, e);
+            for (int j = 0; j < kVec; ++j) e[j] = reset ? cG[j] : fmaf(cA[j], g[j], cG[j]);
+            if (ok) publish(p.words, order, p.dim, own, true, e, e);
         }
     }
     float sum[kVec] = {};
-    if (some) {
-        for (int k = kWaves - 1; k > wave; --k)
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) join_word(sLast[k] ? kReset : sA[k][at + j], sG[k][at + j], g[j]);
+    if (span.have) {
+        for (int k = kWaves - 1; k > wave; --k) join_link(__builtin_amdgcn_readfirstlane(sLast[k]), behind(k), g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
-        for (int k = 0; k < wave; ++k)
+        for (int k = 0; k < wave; ++k) join_link(__builtin_amdgcn_readfirstlane(sFirst[k]), sOwn[k][lane], h);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) join_word(sFirst[k] ? kReset : sA[k][at + j], sH[k][at + j], h[j]);
-        float before[S][kVec];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float xv[kVec];
-            Io<BF>::get(x[s], xv);
-            if (span.first >> s & 1) state(p.state_in, s, h);
+        for (int s = 0; s < S; ++s) {  // b becomes the states in front of the tokens
+            if (span.begins(s)) state(p.state_in, s, h);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                before[s][j] = h[j];
-                float a, q;
-                decay(w[s][j], a, q);
-                if (span.has(s)) h[j] = fmaf(a, h[j], __builtin_amdgcn_sqrtf(q) * si[s][j] * xv[j]);
+                const float before = h[j];
+                h[j] = fmaf(a[s][j], h[j], b[s][j]);
+                b[s][j] = before;
             }
         }
+        float per_rate[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) per_rate[j] = -__builtin_amdgcn_rcpf(rate[j]);
+        const Rows<BF> oxs(p.dx, p.dim, span.t0, rows, p.dim), ors(p.dr, p.dim, span.t0, rows, p.dim),
+            ois(p.di, p.dim, span.t0, rows, p.dim);
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             if (!span.has(s)) continue;
-            float xv[kVec], d[kVec], ox[kVec], orr[kVec], oi[kVec];
+            float xv[kVec], d[kVec], ox[kVec], orr[kVec], oi[kVec], again[kVec], q[kVec];
             Io<BF>::get(x[s], xv);
             Io<BF>::get(dy[s], d);
-            if (span.last >> s & 1) state(p.dstate_out, s, g);
+            if (span.ends(s)) state(p.dstate_out, s, g);
+            decay(w[s], near, again, q);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float dh = d[j] + g[j];
-                float a, q;
-                decay(w[s][j], a, q);
-                q += 1e-37f;  // w / m is 0 where both are
-                const float rs = __builtin_amdgcn_rsqf(q), m = q * rs;
-                ox[j] = dh * m * si[s][j];
-                oi[j] = ox[j] * xv[j] * (1.f - si[s][j]);
-                const float aw = a * w[s][j];
-                const float W = dh * (a * aw * rs * si[s][j] * xv[j] - aw * before[s][j]);
-                orr[j] = fmaf(-w[s][j], __builtin_amdgcn_rcpf(rate[j]), 1.f) * W;
+                q[j] += 1e-37f;  // w / m is 0 where both are
+                const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si[s][j] * xv[j], aw = a[s][j] * w[s][j];
+                ox[j] = dh * (q[j] * rs) * si[s][j];
+                oi[j] = ox[j] * fmaf(-si[s][j], xv[j], xv[j]);
+                const float W = dh * aw * fmaf(a[s][j] * rs, sx, -b[s][j]);
+                orr[j] = fmaf(w[s][j], per_rate[j], 1.f) * W;
                 sum[j] += W;
-                g[j] = a * dh;
+                g[j] = a[s][j] * dh;
             }
-            if (ok) {
-                store_row<BF>(p.dx, p.dim, span.t0 + s, own, ox);
-                store_row<BF>(p.dr, p.dim, span.t0 + s, own, orr);
-                store_row<BF>(p.di, p.dim, span.t0 + s, own, oi);
-                if (p.dstate_in && (span.first >> s & 1)) {
-                    int n = p.seqs.of(span.t0 + s);
-                    n = n < 0 ? 0 : n;
+            oxs.store(s, at, ox);
+            ors.store(s, at, orr);
+            ois.store(s, at, oi);
+            if (p.dstate_in && span.begins(s) && ok) {
+                const int64_t n = span.sequence(s);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) p.dstate_in[(int64_t)n * p.dim + own + j] = g[j];
-                }
+                for (int j = 0; j < kVec; ++j) p.dstate_in[n * p.dim + own + j] = g[j];
             }
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) sH[wave][at + j] = sum[j];
+    sG[wave][lane] = float2{sum[0], sum[1]};
     __syncthreads();
-    if (wave == 0 && ok)
+    if (wave == 0 && ok) {
+        float2 t{0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            float t = 0.f;
-            for (int k = 0; k < kWaves; ++k) t += sH[k][at + j];
-            p.part[(int64_t)chunk * p.dim + own + j] = t;
+        for (int k = 0; k < kWaves; ++k) {
+            const float2 v = sG[k][lane];
+            t.x += v.x;
+            t.y += v.y;
         }
+        *reinterpret_cast<float2*>(p.part + (int64_t)chunk * p.dim + own) = t;
+    }
 }
 
 // drate: 32 channels x 32 rows of threads over the chunks' sums

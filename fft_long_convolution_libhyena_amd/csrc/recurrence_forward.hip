@@ -21,9 +21,11 @@ struct ForwardArgs {
 
 // One chunk and 128 channels.
 template <bool BF>
-__global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
+__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    __shared__ float sA[kWaves][kCols], sH[kWaves][kCols], sBackA[kWaves][kCols], sBackH[kWaves][kCols];
+    constexpr int S = kForwardSpan;
+    __shared__ Link sOwn[kWaves][64], sBack[kWaves][64];
+    __shared__ int sOwnReset[kWaves], sBackReset[kWaves];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ticket = blockIdx.x;
@@ -32,123 +34,108 @@ __global__ __launch_bounds__(kThreads) void k_rec_forward(ForwardArgs p) {
         __syncthreads();
         ticket = __builtin_amdgcn_readfirstlane(sTicket);
     }
-    const int chunk = ticket / p.blocks, at = kVec * lane;
+    const int chunk = (uint32_t)ticket / (uint32_t)p.blocks;
     if (chunk >= p.chunks) return;  // only where a caller's workspace is not this call's alone
-    const int own = (ticket - chunk * p.blocks) * kCols + at;
+    const int own = (ticket - chunk * p.blocks) * kCols + kVec * lane;
     const bool ok = own < p.dim;
-    const int col = ok ? own : p.dim - kVec;  // lanes behind the last channel load along
-    const Span<kForwardSpan> span(p.seqs, chunk * kForwardChunk + wave * kForwardSpan);
-    float a[kForwardSpan][kVec], b[kForwardSpan][kVec];
+    const int col = ok ? own : p.dim - kVec, at = ok ? own * Io<BF>::kBytes : kNone;
+    const Span<S> span(p.seqs, chunk * kForwardChunk + wave * S);
+    const int rows = p.seqs.tokens - span.t0 < S ? p.seqs.tokens - span.t0 : S;
+    float a[S][kVec], b[S][kVec];
     float A[kVec] = {1.f, 1.f}, H[kVec] = {};
-    if (span.hi > span.lo) {
-        Raw x[kForwardSpan], r[kForwardSpan], i[kForwardSpan];
+    if (span.have) {
+        Raw x[S], r[S], i[S];
+        const Rows<BF> xs(p.in.x, p.in.ldx, span.t0, rows, p.dim), rs(p.in.r, p.in.ldr, span.t0, rows, p.dim),
+            is(p.in.i, p.in.ldi, span.t0, rows, p.dim);
 #pragma unroll
-        for (int s = 0; s < kForwardSpan; ++s) {
+        for (int s = 0; s < S; ++s) {
             const int row = span.row(s);
-            x[s] = load_row<BF>(p.in.x, p.in.ldx, row, col);
-            r[s] = load_row<BF>(p.in.r, p.in.ldr, row, col);
-            i[s] = load_row<BF>(p.in.i, p.in.ldi, row, col);
+            r[s] = rs.load(row, at);
+            i[s] = is.load(row, at);
+            x[s] = xs.load(row, at);
         }
         float rate[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
+        const bool near = near_rates(rate);
 #pragma unroll
-        for (int s = 0; s < kForwardSpan; ++s) {
-            float xv[kVec], rv[kVec], iv[kVec];
+        for (int s = 0; s < S; ++s) {
+            float xv[kVec], rv[kVec], iv[kVec], w[kVec], q[kVec];
             Io<BF>::get(x[s], xv);
             Io<BF>::get(r[s], rv);
             Io<BF>::get(i[s], iv);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) gate(xv[j], rv[j], iv[j], rate[j], a[s][j], b[s][j]);
-            if (!span.has(s))
+            for (int j = 0; j < kVec; ++j) w[j] = rate[j] * sigmoid(rv[j]);
+            decay(w, near, a[s], q);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) b[s][j] = __builtin_amdgcn_sqrtf(q[j]) * sigmoid(iv[j]) * xv[j];
+            if (span.begins(s)) {  // from the sequence's initial state, and from nothing in front of it
+                const int64_t n = span.sequence(s);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
-                    a[s][j] = 1.f;
-                    b[s][j] = 0.f;
+                    if (p.state_in) b[s][j] = fmaf(a[s][j], p.state_in[n * p.dim + col + j], b[s][j]);
+                    H[j] = 0.f;
                 }
-            if (span.first >> s & 1) {  // from the sequence's initial state, and from nothing in front of it
-                int n = p.seqs.of(span.t0 + s);
-                n = n < 0 ? 0 : n;
+            }
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    if (p.state_in) b[s][j] = fmaf(a[s][j], p.state_in[(int64_t)n * p.dim + col + j], b[s][j]);
-                    H[j] = b[s][j];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    H[j] = fmaf(a[s][j], H[j], b[s][j]);
-                    A[j] *= a[s][j];
-                }
+            for (int j = 0; j < kVec; ++j) {
+                H[j] = fmaf(a[s][j], H[j], b[s][j]);
+                A[j] *= a[s][j];
             }
         }
     }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        sA[wave][at + j] = span.first ? kReset : A[j];
-        sH[wave][at + j] = H[j];
-    }
+    sOwn[wave][lane] = Link{A[0], A[1], H[0], H[1]};
+    if (lane == 0) sOwnReset[wave] = span.first != 0;
     __syncthreads();
     float h[kVec] = {};
     if (p.words) {
-        const bool publishes = wave == 0 && ok && chunk + 1 < p.chunks, ends = (chunk & (kGroup - 1)) == kGroup - 1;
-        float cA[kVec], cH[kVec];
+        const bool publishes = wave == 0 && chunk + 1 < p.chunks, ends = (chunk & (kGroup - 1)) == kGroup - 1;
+        float cA[kVec] = {1.f, 1.f}, cH[kVec] = {};
+        bool reset = false;
         if (publishes) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                cA[j] = 1.f;
-                cH[j] = 0.f;
+            for (int k = 0; k < kWaves; ++k) {
+                const Link v = sOwn[k][lane];
+                const bool rs = __builtin_amdgcn_readfirstlane(sOwnReset[k]);
+                reset |= rs;
+                join_link(rs, v, cH);
+                cA[0] *= v[0];
+                cA[1] *= v[1];
             }
-            for (int k = 0; k < kWaves; ++k)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const float wA = sA[k][at + j];
-                    join_word(wA, sH[k][at + j], cH[j]);
-                    cA[j] = wA == kReset || cA[j] == kReset ? kReset : cA[j] * wA;
-                }
-            if (!ends) publish(p.words, chunk, p.dim, own, cA, cH);
+            if (!ends && ok) publish(p.words, chunk, p.dim, own, reset, cA, cH);
         }
         if (chunk) {
-            float bA[kVec], bH[kVec];
-            look_back(p.words, chunk, p.dim, col, wave, bA, bH);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                sBackA[wave][at + j] = bA[j];
-                sBackH[wave][at + j] = bH[j];
-            }
+            Link back;
+            const bool rs = look_back(p.words, chunk, p.dim, col, wave, back);
+            sBack[wave][lane] = back;
+            if (lane == 0) sBackReset[wave] = rs;
             __syncthreads();
-            for (int k = 0; k < kWaves; ++k)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) join_word(sBackA[k][at + j], sBackH[k][at + j], h[j]);
+            for (int k = 0; k < kWaves; ++k) join_link(__builtin_amdgcn_readfirstlane(sBackReset[k]), sBack[k][lane], h);
         }
         if (publishes && ends) {
-            float e[kVec], reset[kVec];
+            float e[kVec];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                e[j] = h[j];
-                join_word(cA[j], cH[j], e[j]);
-                reset[j] = kReset;
-            }
-            publish(p.words, chunk, p.dim, own, reset, e);
+            for (int j = 0; j < kVec; ++j) e[j] = reset ? cH[j] : fmaf(cA[j], h[j], cH[j]);
+            if (ok) publish(p.words, chunk, p.dim, own, true, e, e);
         }
     }
-    for (int k = 0; k < wave; ++k)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) join_word(sA[k][at + j], sH[k][at + j], h[j]);
+    for (int k = 0; k < wave; ++k) join_link(__builtin_amdgcn_readfirstlane(sOwnReset[k]), sOwn[k][lane], h);
     if (p.carry && span.t0 % kBackwardChunk == 0 && span.t0 < p.seqs.tokens && ok)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) p.carry[(int64_t)(span.t0 / kBackwardChunk) * p.dim + own + j] = h[j];
-    if (!p.y || span.hi <= span.lo) return;
+    if (!p.y || !span.have) return;
+    const Rows<BF> ys(p.y, p.dim, span.t0, rows, p.dim);
 #pragma unroll
-    for (int s = 0; s < kForwardSpan; ++s) {
+    for (int s = 0; s < S; ++s) {
+        if (span.begins(s)) h[0] = h[1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) h[j] = span.first >> s & 1 ? b[s][j] : fmaf(a[s][j], h[j], b[s][j]);
-        if (ok && span.has(s)) store_row<BF>(p.y, p.dim, span.t0 + s, own, h);
-        if (p.state_out && (span.last >> s & 1) && ok) {
-            int n = p.seqs.of(span.t0 + s);
-            n = n < 0 ? 0 : n;
+        for (int j = 0; j < kVec; ++j) h[j] = fmaf(a[s][j], h[j], b[s][j]);
+        if (span.has(s)) ys.store(s, at, h);
+        if (span.ends(s) && p.state_out && ok) {
+            const int64_t n = span.sequence(s);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) p.state_out[(int64_t)n * p.dim + own + j] = h[j];
+            for (int j = 0; j < kVec; ++j) p.state_out[n * p.dim + own + j] = h[j];
         }
     }
 }

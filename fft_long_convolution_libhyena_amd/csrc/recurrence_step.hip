@@ -23,6 +23,15 @@ struct StepArgs {
 };
 
 template <bool BF>
+__device__ __forceinline__ void take(const void* base, int64_t e, float (&x)[kVec]) {
+    Io<BF>::get(*reinterpret_cast<const typename Io<BF>::Raw*>((const char*)base + e * Io<BF>::kBytes), x);
+}
+template <bool BF>
+__device__ __forceinline__ void put(void* base, int64_t e, const float (&x)[kVec]) {
+    *reinterpret_cast<typename Io<BF>::Raw*>((char*)base + e * Io<BF>::kBytes) = Io<BF>::put(x);
+}
+
+template <bool BF>
 __global__ __launch_bounds__(kStepThreads) void k_rec_step(StepArgs p) {
     __shared__ int next_row, seen;
     const int tid = threadIdx.x;
@@ -33,7 +42,7 @@ __global__ __launch_bounds__(kStepThreads) void k_rec_step(StepArgs p) {
     if (slot < 0 || slot >= p.num_states) {  // a row without a state: zeros out
         const float zero[kVec] = {};
         if (ok)
-            for (int64_t t = 0; t < p.T; ++t) store_row<BF>((char*)p.y + (row * p.T + t) * p.dim * Io<BF>::kBytes, 0, 0, col, zero);
+            for (int64_t t = 0; t < p.T; ++t) put<BF>(p.y, (row * p.T + t) * p.dim + col, zero);
         return;
     }
     float* const sp = p.states + slot * p.dim + col;
@@ -74,16 +83,16 @@ __global__ __launch_bounds__(kStepThreads) void k_rec_step(StepArgs p) {
             for (int64_t t = 0; t < p.T; ++t) {
                 const int64_t tok = row * p.T + t;
                 float x[kVec], r[kVec], i[kVec];
-                Io<BF>::get(load_row<BF>((const char*)p.in.x + tok * p.in.ldx * Io<BF>::kBytes, 0, 0, col), x);
-                Io<BF>::get(load_row<BF>((const char*)p.in.r + tok * p.in.ldr * Io<BF>::kBytes, 0, 0, col), r);
-                Io<BF>::get(load_row<BF>((const char*)p.in.i + tok * p.in.ldi * Io<BF>::kBytes, 0, 0, col), i);
+                take<BF>(p.in.x, tok * p.in.ldx + col, x);
+                take<BF>(p.in.r, tok * p.in.ldr + col, r);
+                take<BF>(p.in.i, tok * p.in.ldi + col, i);
+float w[kVec], a[kVec], q[kVec];
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    float a, b;
-                    gate(x[j], r[j], i[j], rate[j], a, b);
-                    h[j] = fmaf(a, h[j], b);
-                }
-                store_row<BF>((char*)p.y + tok * p.dim * Io<BF>::kBytes, 0, 0, col, h);
+                for (int j = 0; j < kVec; ++j) w[j] = rate[j] * sigmoid(r[j]);
+                decay(w, false, a, q);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) h[j] = fmaf(a[j], h[j], __builtin_amdgcn_sqrtf(q[j]) * sigmoid(i[j]) * x[j]);
+                put<BF>(p.y, tok * p.dim + col, h);
             }
         if (following >= p.B) break;
         row = following;
