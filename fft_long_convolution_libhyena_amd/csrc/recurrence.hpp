@@ -22,13 +22,13 @@
 namespace hy {
 namespace rec {
 
-constexpr int kWaves = 8;                // of a workgroup
-constexpr int kThreads = 64 * kWaves;
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
-// Tokens a wave, forward and backward (which holds twice as much of each)
-constexpr int kForwardSpan = 16, kBackwardSpan = 8;
-constexpr int kForwardChunk = kWaves * kForwardSpan, kBackwardChunk = kWaves * kBackwardSpan;
+// Tokens of a chunk, forward and backward, and of a wave (the backward holds twice as much of each token)
+constexpr int kForwardChunk = 128, kBackwardChunk = 64;
+constexpr int forward_span(bool) { return 16; }
+constexpr int backward_span(bool) { return 8; }
+constexpr int kMaxThreads = 512;
 static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY && kForwardChunk % kBackwardChunk == 0, "states kept for the backward");
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - kForwardChunk;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -189,12 +189,12 @@ __device__ __forceinline__ bool near_rates(const float (&rate)[kVec]) { return _
 // run, so every wait ends; a bound on the polls ends it whatever a caller does to the workspace
 // (states are NaN then). A word of 64 bits holds both values of a channel and that they are
 // there, so no fences are needed: 0 until then, with bit 63 set (A >= 0), and A = 2 for a
-// chunk in which a sequence begins (its H is a state). The last of every 32 chunks publishes, as such
-// a word, the state behind it; so a chunk folds at most 32 words, always in the same order, and states run
-// through long sequences at a hop for 32 chunks. A wave polls four words at once.
-constexpr int kGroup = 32;
+// chunk in which a sequence begins (its H is a state). The last of every 16 chunks publishes, as such
+// a word, the state behind it; so a chunk folds at most 16 words, always in the same order, and states run
+// through long sequences at a hop for 16 chunks. A wave polls its share of them at once; the words of
+// even and of odd channels lie apart, so that it reads whole lines.
+constexpr int kGroup = 16;
 constexpr int kPolls = 1 << 20;  // about a second
-static_assert(kGroup == 4 * kWaves, "four words a wave");
 
 using Word = unsigned long long;
 constexpr uint32_t kResetWord = 0xc0000000u;  // the high half: A = -2
@@ -212,57 +212,71 @@ __device__ __forceinline__ void publish(Word* words, int order, int dim, int col
     for (int j = 0; j < kVec; ++j) {
         const float a = A[j] == A[j] ? A[j] : 0.f;  // H is NaN where A is
         const uint32_t hi = reset ? kResetWord : __float_as_uint(a) | 0x80000000u;
-        __hip_atomic_store(words + (int64_t)order * dim + col + j, (Word)hi << 32 | __float_as_uint(H[j]), __ATOMIC_RELAXED,
+        __hip_atomic_store(words + (int64_t)order * dim + (uint32_t)(j * (dim / 2) + col / 2), (Word)hi << 32 | __float_as_uint(H[j]), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
-// (A, H) of this wave's words: 4 wave .. of those in front of chunk `order` in its group, the first of
-// which is the last of the group before. Returns whether a sequence begins among them.
-__device__ __forceinline__ bool look_back(const Word* words, int order, int dim, int col, int wave, Link& link) {
-    const int base = (order & ~(kGroup - 1)) - 1 + 4 * wave;
-    Word v[4][kVec];
-    for (int polls = 0;; ++polls) {
-        Word there = ~(Word)0;
+// This wave's words: kPolled wave .. of those in front of chunk `order` in its group, the first of which is the
+// last of the group before. ask() sends for them, done() waits for all, gives (A, H) of the run and
+// returns whether a sequence begins in it.
+template <int W>
+struct LookBack {
+    static constexpr int kPolled = kGroup / W;
+    const Word* words;
+    int base, order, dim, col;
+    Word v[kPolled][kVec];
+
+    __device__ __forceinline__ LookBack(const Word* words_, int order_, int dim_, int col_, int wave)
+        : words(words_), base((order_ & ~(kGroup - 1)) - 1 + kPolled * wave), order(order_), dim(dim_), col(col_) {}
+    __device__ __forceinline__ void ask() {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kPolled; ++k) {
             const int at = base + k;
             if (at >= 0 && at < order) {
                 const Word* p = words + (int64_t)at * dim;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    v[k][j] = __hip_atomic_load(p + (uint32_t)(col + j), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    there &= v[k][j];
-                }
+                for (int j = 0; j < kVec; ++j)
+                    v[k][j] = __hip_atomic_load(p + (uint32_t)(j * (dim / 2) + col / 2), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             } else {
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) v[k][j] = (Word)0xbf800000u << 32;  // (1, 0): nothing happens
             }
         }
-        if (__all((int)(there >> 63))) break;
-        if (polls >= kPolls) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) v[3][j] = (Word)kResetWord << 32 | 0x7fc00000u;
-            break;
-        }
-        __builtin_amdgcn_s_sleep(1);
     }
-    bool any = false;
-    link = Link{1.f, 1.f, 0.f, 0.f};
+    __device__ __forceinline__ bool done(Link& link) {
+        for (int polls = 0;; ++polls) {
+            Word there = ~(Word)0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        // the same for all channels
-        const bool reset = __builtin_amdgcn_readfirstlane((int)(v[k][0] >> 32)) == (int)kResetWord;
-        any |= reset;
+            for (int k = 0; k < kPolled; ++k)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float a = fabsf(__uint_as_float((uint32_t)(v[k][j] >> 32))), h = __uint_as_float((uint32_t)v[k][j]);
-            link[2 + j] = reset ? h : fmaf(a, link[2 + j], h);
-            link[j] *= a;
+                for (int j = 0; j < kVec; ++j) there &= v[k][j];
+            if (__all((int)(there >> 63))) break;
+            if (polls >= kPolls) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[kPolled - 1][j] = (Word)kResetWord << 32 | 0x7fc00000u;
+                break;
+            }
+            __builtin_amdgcn_s_sleep(1);
+            ask();
         }
+        bool any = false;
+        link = Link{1.f, 1.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kPolled; ++k) {
+            // the same for all channels
+            const bool reset = __builtin_amdgcn_readfirstlane((int)(v[k][0] >> 32)) == (int)kResetWord;
+            any |= reset;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float a = fabsf(__uint_as_float((uint32_t)(v[k][j] >> 32))), h = __uint_as_float((uint32_t)v[k][j]);
+                link[2 + j] = reset ? h : fmaf(a, link[2 + j], h);
+                link[j] *= a;
+            }
+        }
+        return any;
     }
-    return any;
-}
+};
 
 // ------------------------------------------------------------------ host side
 

@@ -33,12 +33,12 @@ struct BackwardArgs {
 
 // One chunk and 128 channels, the chunks from the last to the first.
 template <bool BF>
-__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
+__global__ __launch_bounds__(64 * kBackwardChunk / backward_span(BF), BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    constexpr int S = kBackwardSpan;
-    __shared__ Link sOwn[kWaves][64], sBehind[kWaves][64];
-    __shared__ float2 sG[kWaves][64];
-    __shared__ int sFirst[kWaves], sLast[kWaves], sBehindReset[kWaves];
+    constexpr int S = backward_span(BF), W = kBackwardChunk / S;
+    __shared__ Link sG[W][64], sBehind[W][64];  // (A, G) of the waves and of the chunks behind
+    __shared__ float2 sH[W][64];
+    __shared__ int sFirst[W], sLast[W], sBehindReset[W];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ticket = blockIdx.x;
@@ -59,41 +59,38 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = from ? from[n * p.dim + col + j] : 0.f;
     };
-    Raw x[S], dy[S];
+    Raw x[S], dy[S], i[S];
     float w[S][kVec], si[S][kVec], a[S][kVec], b[S][kVec];  // w = -log a, sig(i), a, m sig(i) x
     float rate[kVec], A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
     const bool near = near_rates(rate);
     if (span.have) {
-        Raw r[S], i[S];
+        Raw r[S];
         const Rows<BF> xs(p.in.x, p.in.ldx, span.t0, rows, p.dim), rs(p.in.r, p.in.ldr, span.t0, rows, p.dim),
             is(p.in.i, p.in.ldi, span.t0, rows, p.dim), ds(p.dy, p.dim, span.t0, rows, p.dim);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int row = span.row(s);
             r[s] = rs.load(row, at);
-            i[s] = is.load(row, at);
-            x[s] = xs.load(row, at);
             dy[s] = ds.load(row, at);
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float rv[kVec], xv[kVec], iv[kVec], q[kVec];
+            const int row = span.row(s);
+            i[s] = is.load(row, at);
+            x[s] = xs.load(row, at);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float rv[kVec], q[kVec];
             Io<BF>::get(r[s], rv);
-            Io<BF>::get(x[s], xv);
-            Io<BF>::get(i[s], iv);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                w[s][j] = rate[j] * sigmoid(rv[j]);
-                si[s][j] = sigmoid(iv[j]);
-            }
+            for (int j = 0; j < kVec; ++j) w[s][j] = rate[j] * sigmoid(rv[j]);
             decay(w[s], near, a[s], q);
-            if (span.begins(s)) state(p.state_in, s, H);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                b[s][j] = __builtin_amdgcn_sqrtf(q[j]) * si[s][j] * xv[j];
-                H[j] = fmaf(a[s][j], H[j], b[s][j]);
+                b[s][j] = __builtin_amdgcn_sqrtf(q[j]);
                 A[j] *= a[s][j];
             }
         }
@@ -106,57 +103,75 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
             for (int j = 0; j < kVec; ++j) G[j] = a[s][j] * (d[j] + G[j]);
         }
     }
-    sOwn[wave][lane] = Link{A[0], A[1], H[0], H[1]};
-    sG[wave][lane] = float2{G[0], G[1]};
+    sG[wave][lane] = Link{A[0], A[1], G[0], G[1]};
     if (lane == 0) {
         sFirst[wave] = span.first != 0;
         sLast[wave] = span.last != 0;
     }
     __syncthreads();
-    auto behind = [&](int k) {  // (A, G) of wave k
-        const Link v = sOwn[k][lane];
-        const float2 u = sG[k][lane];
-        return Link{v[0], v[1], u.x, u.y};
-    };
-    float g[kVec] = {}, h[kVec] = {};
-    if (p.words) {
-        const bool publishes = wave == 0 && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
-        float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
-        bool reset = false;
-        if (publishes) {
+    // (A, G) goes out as soon as it is known; the words of the chunks behind travel while the waves
+    // work on what only this chunk needs
+    const bool publishes = p.words && wave == 0 && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
+    const bool looks = p.words && order;
+    float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
+    bool reset = false;
+    if (publishes) {
 #pragma unroll
-            for (int k = kWaves - 1; k >= 0; --k) {
-                const Link v = behind(k);
-                const bool rs = __builtin_amdgcn_readfirstlane(sLast[k]);
-                reset |= rs;
-                join_link(rs, v, cG);
-                cA[0] *= v[0];
-                cA[1] *= v[1];
+        for (int k = W - 1; k >= 0; --k) {
+            const Link v = sG[k][lane];
+            const bool rs = __builtin_amdgcn_readfirstlane(sLast[k]);
+            reset |= rs;
+            join_link(rs, v, cG);
+            cA[0] *= v[0];
+            cA[1] *= v[1];
+        }
+        if (!ends && ok) publish(p.words, order, p.dim, own, reset, cA, cG);
+    }
+    LookBack<W> look(p.words, order, p.dim, col, wave);
+    if (looks) look.ask();
+    if (span.have) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float xv[kVec], iv[kVec];
+            Io<BF>::get(x[s], xv);
+            Io<BF>::get(i[s], iv);
+            if (span.begins(s)) state(p.state_in, s, H);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                si[s][j] = sigmoid(iv[j]);
+                b[s][j] *= si[s][j] * xv[j];
+                H[j] = fmaf(a[s][j], H[j], b[s][j]);
             }
-            if (!ends && ok) publish(p.words, order, p.dim, own, reset, cA, cG);
         }
-        if (order) {
-            Link back;
-            const bool rs = look_back(p.words, order, p.dim, col, wave, back);
-            sBehind[wave][lane] = back;
-            if (lane == 0) sBehindReset[wave] = rs;
-            __syncthreads();
+    }
+    sH[wave][lane] = float2{H[0], H[1]};
+    if (looks) {
+        Link back;
+        const bool rs = look.done(back);
+        sBehind[wave][lane] = back;
+        if (lane == 0) sBehindReset[wave] = rs;
+    }
+    __syncthreads();
+    float g[kVec] = {}, h[kVec] = {};
+    if (looks)
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) join_link(__builtin_amdgcn_readfirstlane(sBehindReset[k]), sBehind[k][lane], g);
-        }
-        if (publishes && ends) {
-            float e[kVec];
+        for (int k = 0; k < W; ++k) join_link(__builtin_amdgcn_readfirstlane(sBehindReset[k]), sBehind[k][lane], g);
+    if (publishes && ends) {
+        float e[kVec];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) e[j] = reset ? cG[j] : fmaf(cA[j], g[j], cG[j]);
-            if (ok) publish(p.words, order, p.dim, own, true, e, e);
-        }
+        for (int j = 0; j < kVec; ++j) e[j] = reset ? cG[j] : fmaf(cA[j], g[j], cG[j]);
+        if (ok) publish(p.words, order, p.dim, own, true, e, e);
     }
     float sum[kVec] = {};
     if (span.have) {
-        for (int k = kWaves - 1; k > wave; --k) join_link(__builtin_amdgcn_readfirstlane(sLast[k]), behind(k), g);
+        for (int k = W - 1; k > wave; --k) join_link(__builtin_amdgcn_readfirstlane(sLast[k]), sG[k][lane], g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
-        for (int k = 0; k < wave; ++k) join_link(__builtin_amdgcn_readfirstlane(sFirst[k]), sOwn[k][lane], h);
+        for (int k = 0; k < wave; ++k) {
+            const Link v = sG[k][lane];
+            const float2 u = sH[k][lane];
+            join_link(__builtin_amdgcn_readfirstlane(sFirst[k]), Link{v[0], v[1], u.x, u.y}, h);
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) {  // b becomes the states in front of the tokens
             if (span.begins(s)) state(p.state_in, s, h);
@@ -187,9 +202,9 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
                 const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si[s][j] * xv[j], aw = a[s][j] * w[s][j];
                 ox[j] = dh * (q[j] * rs) * si[s][j];
                 oi[j] = ox[j] * fmaf(-si[s][j], xv[j], xv[j]);
-                const float W = dh * aw * fmaf(a[s][j] * rs, sx, -b[s][j]);
-                orr[j] = fmaf(w[s][j], per_rate[j], 1.f) * W;
-                sum[j] += W;
+                const float share = dh * aw * fmaf(a[s][j] * rs, sx, -b[s][j]);
+                orr[j] = fmaf(w[s][j], per_rate[j], 1.f) * share;
+                sum[j] += share;
                 g[j] = a[s][j] * dh;
             }
             oxs.store(s, at, ox);
@@ -203,13 +218,13 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         }
     }
     __syncthreads();
-    sG[wave][lane] = float2{sum[0], sum[1]};
+    sH[wave][lane] = float2{sum[0], sum[1]};
     __syncthreads();
     if (wave == 0 && ok) {
         float2 t{0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
-            const float2 v = sG[k][lane];
+        for (int k = 0; k < W; ++k) {
+            const float2 v = sH[k][lane];
             t.x += v.x;
             t.y += v.y;
         }
@@ -217,23 +232,24 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     }
 }
 
-// drate: 32 channels x 32 rows of threads over the chunks' sums
+// drate: 32 channels x 32 rows of threads over the chunks' sums, 16 of each thread on their way
 __global__ __launch_bounds__(1024) void k_rec_drate(const float* part, const float* rate, float* drate, int64_t chunks,
                                                     int dim) {
+    constexpr int kAhead = 16;
     __shared__ double red[32][33];
     const int c = threadIdx.x & 31, r = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
     double s = 0;
-    if (e < dim) {
-        int64_t i = r;
-        for (; i + 224 < chunks; i += 256) {
-            float x[8];
+    if (e < dim)
+        for (int64_t i = r; i < chunks; i += 32 * kAhead) {
+            float x[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = part[(i + 32 * j) * dim + e];
+            for (int j = 0; j < kAhead; ++j) {  // rows behind the last are read again, without a branch
+                const int64_t row = i + 32 * j;
+                x[j] = part[(row < chunks ? row : chunks - 1) * dim + e];
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += (double)x[j];
+            for (int j = 0; j < kAhead; ++j) s += i + 32 * j < chunks ? (double)x[j] : 0.;
         }
-        for (; i < chunks; i += 32) s += (double)part[i * dim + e];
-    }
     red[r][c] = s;
     __syncthreads();
     for (int d = 16; d > 0; d >>= 1) {
@@ -308,11 +324,11 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
         rec::BackwardArgs a{c.seqs, c.in,      params->rate, state_in, dy,      dstate_out,
                             dx,     dr,        di,           dstate_in, carries ? carries : l.carry,
                             l.part, tickets,   c.back_chunks > 1 ? words : nullptr, dim, (int)c.back_chunks, (int)c.blocks};
-        const dim3 grid((unsigned)(c.back_chunks * c.blocks)), block(rec::kThreads);
+        const dim3 grid((unsigned)(c.back_chunks * c.blocks));
         if (c.bf)
-            hipLaunchKernelGGL(rec::k_rec_backward<true>, grid, block, 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<true>, grid, dim3(64 * rec::kBackwardChunk / rec::backward_span(true)), 0, stream, a);
         else
-            hipLaunchKernelGGL(rec::k_rec_backward<false>, grid, block, 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<false>, grid, dim3(64 * rec::kBackwardChunk / rec::backward_span(false)), 0, stream, a);
         e = hipGetLastError();
     }
     if (e == hipSuccess) {

@@ -21,11 +21,11 @@ struct ForwardArgs {
 
 // One chunk and 128 channels.
 template <bool BF>
-__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
+__global__ __launch_bounds__(64 * kForwardChunk / forward_span(BF), BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    constexpr int S = kForwardSpan;
-    __shared__ Link sOwn[kWaves][64], sBack[kWaves][64];
-    __shared__ int sOwnReset[kWaves], sBackReset[kWaves];
+    constexpr int S = forward_span(BF), W = kForwardChunk / S;
+    __shared__ Link sOwn[W][64], sBack[W][64];
+    __shared__ int sOwnReset[W], sBackReset[W];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int ticket = blockIdx.x;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
         bool reset = false;
         if (publishes) {
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
+            for (int k = 0; k < W; ++k) {
                 const Link v = sOwn[k][lane];
                 const bool rs = __builtin_amdgcn_readfirstlane(sOwnReset[k]);
                 reset |= rs;
@@ -106,12 +106,14 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
         }
         if (chunk) {
             Link back;
-            const bool rs = look_back(p.words, chunk, p.dim, col, wave, back);
+            LookBack<W> look(p.words, chunk, p.dim, col, wave);
+            look.ask();
+            const bool rs = look.done(back);
             sBack[wave][lane] = back;
             if (lane == 0) sBackReset[wave] = rs;
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) join_link(__builtin_amdgcn_readfirstlane(sBackReset[k]), sBack[k][lane], h);
+            for (int k = 0; k < W; ++k) join_link(__builtin_amdgcn_readfirstlane(sBackReset[k]), sBack[k][lane], h);
         }
         if (publishes && ends) {
             float e[kVec];
@@ -140,9 +142,13 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     }
 }
 
-// Clears what the chunks' words and tickets lie in; a sequence without tokens passes its state on.
+// Clears what the chunks' words and tickets lie in (n words, 16 bytes a thread and round); a sequence without
+// tokens passes its state on.
 __global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs q, const float* from, float* to, int dim) {
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) clear[e] = 0;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; 2 * e < n; e += step)
+        __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(clear) + e);
     if (to)
         for (int s = blockIdx.x; s < q.N; s += gridDim.x) {
             if (q.at(s + 1) > q.at(s)) continue;
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs 
 hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, hipStream_t st) {
     if (!(c.seqs.start || c.seqs.T == 0)) to = nullptr;  // every sequence has tokens
     if (!n && !to) return hipSuccess;
-    int64_t wgs = (n + 1023) / 1024;
+    int64_t wgs = (n + 511) / 512;  // n is even
     wgs = to && wgs < c.seqs.N ? c.seqs.N : wgs;
     hipLaunchKernelGGL(k_rec_start, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, st, (Word*)clear, n, c.seqs, from, to,
                        (int)c.p.dim);
@@ -171,9 +177,9 @@ hipError_t forward(const Call& c, const float* state_in, void* y, float* state_o
                   (int)c.p.dim, (int)c.chunks, (int)c.blocks};
     const dim3 grid((unsigned)(c.chunks * c.blocks));
     if (c.bf)
-        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(kThreads), 0, st, a);
+        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(64 * kForwardChunk / forward_span(true)), 0, st, a);
     else
-        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(kThreads), 0, st, a);
+        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(64 * kForwardChunk / forward_span(false)), 0, st, a);
     return hipGetLastError();
 }
 
@@ -190,7 +196,7 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
     c.chunks = (tokens + kForwardChunk - 1) / kForwardChunk;
     c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
     c.blocks = (p->dim + kCols - 1) / kCols;
-    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
+    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kMaxThreads) return HYENA_ERR_UNSUPPORTED;
     c.seqs = Seqs{seq_start, (int)N, (int)tokens, (int)(tokens / N)};
     if (!in) return HYENA_OK;
     c.in = *in;
