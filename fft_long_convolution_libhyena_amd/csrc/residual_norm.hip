@@ -7,10 +7,12 @@
 //   ds = inv w dy - s inv^3 mean(w dy s) + ds_out,   dw = sum over rows of dy s inv.
 //
 // Every value is read and written once: bound by memory. A row belongs to R threads (a
-// wave up to 2048 columns, then 256 or 1024 threads) and stays in their registers between the
+// wave up to 1024 columns, 256 threads up to 8192, then 512) and stays in their registers between the
 // sum and the result: K pieces of 4 neighbours a thread, piece k of thread t at columns
 // 4 (k R + t). So 128 columns are 32 lanes of one wave and a block's largest value needs
-// no LDS. Threads walk over rows with the next row's loads under way; the weights are loaded once.
+// no LDS. Threads walk over rows; the weights are loaded once. 65536 x 768 in bf16 take 70 us (5.7 TB/s), 16384 x
+// 2048 to 8 bits from an fp32 residual 66 (5.6; a wave a row, 32 values a lane: 82), the backward of
+// 65536 x 768 with the residual in fp32 146 (5.5).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -21,8 +23,6 @@ namespace hy {
 namespace {
 
 constexpr int64_t kRmsMaxDim = 16384;
-constexpr int kRmsBackWgs = 1024;  // at most, in the backward: partial sums of dw
-constexpr int kRmsForwardWgs = 4096;
 constexpr float kE4m3Most = 448.f;
 
 struct RmsArgs {
@@ -299,11 +299,22 @@ __global__ __launch_bounds__(1024) void k_residual_norm_dw(const float* part, in
     if (r == 0 && e < dim) dw[e] = (float)red[0][c];
 }
 
-int64_t rms_rows(int64_t dim) { return dim <= 2048 ? 4 : 1; }  // rows a workgroup
+int64_t rms_rows(int64_t dim) { return dim <= 1024 ? 4 : 1; }  // rows a workgroup
 
-int64_t rms_back_wgs(int64_t rows, int64_t dim) {
+// Workgroups of the forward: two rounds where there are enough rows, at most 8192 (65536 x 768: 2048, 4096, 8192
+// and 16384 workgroups 81, 76, 73 and 81 us; 8192 x 4096: 47, 47, 52 and 52).
+int64_t rms_forward_wgs(int64_t rows, int64_t dim) {
     const int64_t n = (rows + rms_rows(dim) - 1) / rms_rows(dim);
-    return n < kRmsBackWgs ? n : kRmsBackWgs;
+    return n <= 4096 ? n : n < 16384 ? (n + 1) / 2 : 8192;
+}
+
+// Workgroups of the backward, each with partial sums of dw. Two a CU read the longest runs that still
+// hide the latency; rows of one piece need more (us, 256, 512 and 1024 of them: 65536 x 768 of bf16 103, 78, 86,
+// with the residual in fp32 146, 153, 163; 16384 x 2048 119, 101, 110; 65536 x 128 55, 32, 25). Sending for
+// the next row early gains nothing on top (512: 84 and 158).
+int64_t rms_back_wgs(int64_t rows, int64_t dim) {
+    const int64_t n = (rows + rms_rows(dim) - 1) / rms_rows(dim), most = dim <= 256 ? 1024 : 512;
+    return n < most ? n : most;
 }
 
 // f.template go<R, K>() for the threads of a row and the pieces of one that dim needs
@@ -313,11 +324,10 @@ void by_dim(int dim, F f) {
     else if (dim <= 512) f.template go<64, 2>();
     else if (dim <= 768) f.template go<64, 3>();
     else if (dim <= 1024) f.template go<64, 4>();
-    else if (dim <= 1536) f.template go<64, 6>();
-    else if (dim <= 2048) f.template go<64, 8>();
+    else if (dim <= 2048) f.template go<256, 2>();
     else if (dim <= 4096) f.template go<256, 4>();
     else if (dim <= 8192) f.template go<256, 8>();
-    else f.template go<1024, 4>();
+    else f.template go<512, 8>();
 }
 
 template <bool XB, bool SB>
@@ -326,8 +336,7 @@ struct RmsForward {
     hipStream_t st;
     template <int R, int K>
     void go() const {
-        const int64_t n = (a.rows + rms_rows(a.dim) - 1) / rms_rows(a.dim);
-        const dim3 grid((unsigned)(n < kRmsForwardWgs ? n : kRmsForwardWgs)), block(R < 256 ? 256 : R);
+        const dim3 grid((unsigned)rms_forward_wgs(a.rows, a.dim)), block(R < 256 ? 256 : R);
         if (a.scales)
             hipLaunchKernelGGL((k_residual_norm<XB, SB, true, R, K>), grid, block, 0, st, a);
         else

@@ -1,7 +1,7 @@
 """Residual norm on the GPU against its plain form in 64 bits.
 
 Tolerances (relative 2-norm, E = 2^-24). fp32: the addition one rounding, which its square doubles; a sum of n squares at
-most n of them, halved by the root; root, reciprocal and two products 6: (n / 2 + 8) E. Sums run over 64 to 1024 threads of at most 32
+most n of them, halved by the root; root, reciprocal and two products 6: (n / 2 + 8) E. Sums run over 64 to 512 threads of at most 32
 values and ten exchanges each, so n is held at 48, whatever dim. The backward has a second such sum and 10 more operations:
 (48 + 24 + 24) E. The weight's gradient sums rows in chains of at most 512 here: 512 E more. bf16 adds half a
 step, 2^-8, and e4m3 half a step 2^-4 of each value, or, below its smallest normal 2^-6, half of 2^-9 (in
