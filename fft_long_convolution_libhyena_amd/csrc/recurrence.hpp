@@ -9,7 +9,7 @@
 // begins a sequence takes its initial state in and lets nothing of what lies in front through
 // (not as a factor 0: an infinity there must not become NaN here).
 //
-// A workgroup has one chunk and 128 channels: a wave 16 (backward: 8) tokens, a lane two channels. All
+// A workgroup has one chunk and 128 channels: a wave 20 (backward: 8) tokens, a lane two channels. All
 // tokens of a lane are loaded at once and stay in registers from the first pass (which gives
 // the wave's A and H) to the second (which gives the outputs).
 #pragma once
@@ -24,13 +24,14 @@ namespace rec {
 
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
-// Tokens of a chunk, forward and backward, and of a wave (the backward holds twice as much of each token)
-constexpr int kForwardChunk = 128, kBackwardChunk = 64;
-constexpr int forward_span(bool) { return 16; }
-constexpr int backward_span(bool) { return 8; }
-constexpr int kMaxThreads = 512;
-static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY && kForwardChunk % kBackwardChunk == 0, "states kept for the backward");
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - kForwardChunk;
+// Tokens of a wave and of a chunk: as many as 128 registers hold, which leaves two workgroups a CU (the
+// backward holds twice as much of each). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22 tokens a wave: 134,
+// 112, 107, 104, 102 and 103 us; with 32 tokens in waves at two or three a SIMD 114 and 125.
+constexpr int kForwardSpan = 20, kBackwardSpan = 8;
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kForwardChunk = kWaves * kForwardSpan, kBackwardChunk = kWaves * kBackwardSpan;
+static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY && kForwardSpan <= 32, "states kept for the backward; bits of a span");
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ sequences
@@ -220,9 +221,8 @@ __device__ __forceinline__ void publish(Word* words, int order, int dim, int col
 // This wave's words: kPolled wave .. of those in front of chunk `order` in its group, the first of which is the
 // last of the group before. ask() sends for them, done() waits for all, gives (A, H) of the run and
 // returns whether a sequence begins in it.
-template <int W>
 struct LookBack {
-    static constexpr int kPolled = kGroup / W;
+    static constexpr int kPolled = kGroup / kWaves;
     const Word* words;
     int base, order, dim, col;
     Word v[kPolled][kVec];

@@ -33,9 +33,9 @@ struct BackwardArgs {
 
 // One chunk and 128 channels, the chunks from the last to the first.
 template <bool BF>
-__global__ __launch_bounds__(64 * kBackwardChunk / backward_span(BF), BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
+__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    constexpr int S = backward_span(BF), W = kBackwardChunk / S;
+    constexpr int S = kBackwardSpan, W = kWaves;
     __shared__ Link sG[W][64], sBehind[W][64];  // (A, G) of the waves and of the chunks behind
     __shared__ float2 sH[W][64];
     __shared__ int sFirst[W], sLast[W], sBehindReset[W];
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(64 * kBackwardChunk / backward_span(BF), BF ? 4 : 2
         }
         if (!ends && ok) publish(p.words, order, p.dim, own, reset, cA, cG);
     }
-    LookBack<W> look(p.words, order, p.dim, col, wave);
+    LookBack look(p.words, order, p.dim, col, wave);
     if (looks) look.ask();
     if (span.have) {
 #pragma unroll
@@ -326,9 +326,9 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
                             l.part, tickets,   c.back_chunks > 1 ? words : nullptr, dim, (int)c.back_chunks, (int)c.blocks};
         const dim3 grid((unsigned)(c.back_chunks * c.blocks));
         if (c.bf)
-            hipLaunchKernelGGL(rec::k_rec_backward<true>, grid, dim3(64 * rec::kBackwardChunk / rec::backward_span(true)), 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<true>, grid, dim3(rec::kThreads), 0, stream, a);
         else
-            hipLaunchKernelGGL(rec::k_rec_backward<false>, grid, dim3(64 * rec::kBackwardChunk / rec::backward_span(false)), 0, stream, a);
+            hipLaunchKernelGGL(rec::k_rec_backward<false>, grid, dim3(rec::kThreads), 0, stream, a);
         e = hipGetLastError();
     }
     if (e == hipSuccess) {

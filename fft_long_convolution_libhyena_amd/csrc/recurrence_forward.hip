@@ -21,9 +21,9 @@ struct ForwardArgs {
 
 // One chunk and 128 channels.
 template <bool BF>
-__global__ __launch_bounds__(64 * kForwardChunk / forward_span(BF), BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
+__global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    constexpr int S = forward_span(BF), W = kForwardChunk / S;
+    constexpr int S = kForwardSpan, W = kWaves;
     __shared__ Link sOwn[W][64], sBack[W][64];
     __shared__ int sOwnReset[W], sBackReset[W];
     __shared__ uint32_t sTicket;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(64 * kForwardChunk / forward_span(BF), BF ? 4 : 2) 
         }
         if (chunk) {
             Link back;
-            LookBack<W> look(p.words, chunk, p.dim, col, wave);
+            LookBack look(p.words, chunk, p.dim, col, wave);
             look.ask();
             const bool rs = look.done(back);
             sBack[wave][lane] = back;
@@ -123,13 +123,15 @@ __global__ __launch_bounds__(64 * kForwardChunk / forward_span(BF), BF ? 4 : 2) 
         }
     }
     for (int k = 0; k < wave; ++k) join_link(__builtin_amdgcn_readfirstlane(sOwnReset[k]), sOwn[k][lane], h);
-    if (p.carry && span.t0 % kBackwardChunk == 0 && span.t0 < p.seqs.tokens && ok)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) p.carry[(int64_t)(span.t0 / kBackwardChunk) * p.dim + own + j] = h[j];
-    if (!p.y || !span.have) return;
-    const Rows<BF> ys(p.y, p.dim, span.t0, rows, p.dim);
+    if (!span.have) return;
+    // the state in front of one of these tokens may be one that the backward asks for
+    const int kept = p.carry ? -span.t0 & (kBackwardChunk - 1) : S;
+    const Rows<BF> ys(p.y, p.dim, span.t0, p.y ? rows : 0, p.dim);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
+        if (s == kept && s < rows && ok)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) p.carry[(int64_t)((span.t0 + s) / kBackwardChunk) * p.dim + own + j] = h[j];
         if (span.begins(s)) h[0] = h[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = fmaf(a[s][j], h[j], b[s][j]);
@@ -177,9 +179,9 @@ hipError_t forward(const Call& c, const float* state_in, void* y, float* state_o
                   (int)c.p.dim, (int)c.chunks, (int)c.blocks};
     const dim3 grid((unsigned)(c.chunks * c.blocks));
     if (c.bf)
-        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(64 * kForwardChunk / forward_span(true)), 0, st, a);
+        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(kThreads), 0, st, a);
     else
-        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(64 * kForwardChunk / forward_span(false)), 0, st, a);
+        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -196,7 +198,7 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
     c.chunks = (tokens + kForwardChunk - 1) / kForwardChunk;
     c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
     c.blocks = (p->dim + kCols - 1) / kCols;
-    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kMaxThreads) return HYENA_ERR_UNSUPPORTED;
+    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
     c.seqs = Seqs{seq_start, (int)N, (int)tokens, (int)(tokens / N)};
     if (!in) return HYENA_OK;
     c.in = *in;

@@ -883,7 +883,7 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  * reproducible; where a sequence lies among the rows may change their rounding. Outputs must not alias
  * inputs, but for state_out. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
- * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 128, or 2^23 or
+ * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 256, or 2^23 or
  * more pairs of 64 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
 hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                         const int64_t* seq_start, const hyena_recurrence_inputs_t* in,
