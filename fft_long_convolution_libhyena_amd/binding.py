@@ -1080,7 +1080,7 @@ class GatedRecurrence:
     [dim] fp32 on the device, above 0, dtype "f32" or "bf16". Tensors must be on one device and
     calls run there, on its current stream; rate is used by every call."""
 
-    CARRY = 64  # HYENA_RECURRENCE_CARRY
+    CARRY = 80  # HYENA_RECURRENCE_CARRY
 
     def __init__(self, dim: int, rate, dtype: str = "bf16"):
         import torch

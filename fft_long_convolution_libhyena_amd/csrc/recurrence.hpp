@@ -9,7 +9,7 @@
 // begins a sequence takes its initial state in and lets nothing of what lies in front through
 // (not as a factor 0: an infinity there must not become NaN here).
 //
-// A workgroup has one chunk and 128 channels: a wave 20 (backward: 8) tokens, a lane two channels. All
+// A workgroup has one chunk and 128 channels: a wave 20 (backward: 10) tokens, a lane two channels. All
 // tokens of a lane are loaded at once and stay in registers from the first pass (which gives
 // the wave's A and H) to the second (which gives the outputs).
 #pragma once
@@ -25,12 +25,14 @@ namespace rec {
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
 // Tokens of a wave and of a chunk: as many as 128 registers hold, which leaves two workgroups a CU (the
-// backward holds twice as much of each). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22 tokens a wave: 134,
-// 112, 107, 104, 102 and 103 us; with 32 tokens in waves at two or three a SIMD 114 and 125.
-constexpr int kForwardSpan = 20, kBackwardSpan = 8;
+// backward holds twice as much of each, sig(i) in LDS). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22
+// tokens a wave: 134, 112, 107, 104, 102 and 103 us; with 32 in waves at two or three a SIMD 114 and 125. Training step
+// of 8 x 8192 with 6, 8 and 10 in the backward: 334, 297 and 285 us (8 without LDS the same, 10 without it spills: 375).
+constexpr int kForwardSpan = 20, kBackwardSpan = 10;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kForwardChunk = kWaves * kForwardSpan, kBackwardChunk = kWaves * kBackwardSpan;
-static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY && kForwardSpan <= 32, "states kept for the backward; bits of a span");
+static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY, "states kept for the backward");
+static_assert(kForwardSpan <= 32 && kForwardSpan <= kBackwardChunk, "bits of a span; one kept state at most in it");
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -157,8 +159,8 @@ __device__ __forceinline__ float sigmoid(float x) {
 // w times a polynomial (a fit of degree 5 at Chebyshev points, 5e-9 off) with half a step of error and no
 // bias, and q = e (1 + a) keeps e's digits. (With the exponential instruction, a step off to one
 // side, states of 2000 tokens with a around 0.999 were 2.7e-6 off in place of 5e-7.)
-// near (of the wave): all w are known to be below 1/2, as rates below 1/2 make them.
-__device__ __forceinline__ void decay(const float (&w)[kVec], bool near, float (&a)[kVec], float (&q)[kVec]) {
+// least: added to e, so that q is not 0. near (of the wave): all w are known to be below 1/2, as rates below 1/2 make them.
+__device__ __forceinline__ void decay(const float (&w)[kVec], bool near, float (&a)[kVec], float (&q)[kVec], float least = 0.f) {
     float e[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
@@ -167,7 +169,7 @@ __device__ __forceinline__ void decay(const float (&w)[kVec], bool near, float (
         p = fmaf(w[j], p, 0.16666245460510254f);
         p = fmaf(w[j], p, -0.4999998211860657f);
         p = fmaf(w[j], p, 1.f);
-        e[j] = w[j] * p;
+        e[j] = fmaf(w[j], p, least);
         a[j] = 1.f - e[j];
     }
     if (!near)
@@ -205,6 +207,25 @@ typedef float Link __attribute__((ext_vector_type(4)));  // A, A, H, H
 __device__ __forceinline__ void join_link(bool reset, const Link& v, float (&h)[kVec]) {
     h[0] = reset ? v[2] : fmaf(v[0], h[0], v[2]);
     h[1] = reset ? v[3] : fmaf(v[1], h[1], v[3]);
+}
+// bit k: flag k of the workgroup's waves is set
+__device__ __forceinline__ uint32_t flag_bits(const int (&flags)[kWaves], int lane) {
+    return (uint32_t)__ballot(lane < kWaves && flags[lane & (kWaves - 1)] != 0);
+}
+// h through the links of waves k, k + step, ... n of them; mostly no sequence begins in any
+template <class F>
+__device__ __forceinline__ void join_links(uint32_t resets, int k, int step, int n, F link, float (&h)[kVec]) {
+    if (!resets) {
+#pragma unroll 2
+        for (; n > 0; --n, k += step) {
+            const Link v = link(k);
+            h[0] = fmaf(v[0], h[0], v[2]);
+            h[1] = fmaf(v[1], h[1], v[3]);
+        }
+    } else {
+#pragma unroll 1
+        for (; n > 0; --n, k += step) join_link(resets >> k & 1, link(k), h);
+    }
 }
 
 __device__ __forceinline__ void publish(Word* words, int order, int dim, int col, bool reset, const float (&A)[kVec],

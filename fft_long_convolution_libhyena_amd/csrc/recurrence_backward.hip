@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     using Raw = typename Io<BF>::Raw;
     constexpr int S = kBackwardSpan, W = kWaves;
     __shared__ Link sG[W][64], sBehind[W][64];  // (A, G) of the waves and of the chunks behind
-    __shared__ float2 sH[W][64];
+    __shared__ float2 sH[W][64], sSi[W][S][64];  // sSi: a lane's own sig(i), kept for the last pass
     __shared__ int sFirst[W], sLast[W], sBehindReset[W];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         for (int j = 0; j < kVec; ++j) h[j] = from ? from[n * p.dim + col + j] : 0.f;
     };
     Raw x[S], dy[S], i[S];
-    float w[S][kVec], si[S][kVec], a[S][kVec], b[S][kVec];  // w = -log a, sig(i), a, m sig(i) x
+    float w[S][kVec], a[S][kVec], b[S][kVec];  // w = -log a, sig(i), a, m sig(i) x
     float rate[kVec], A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
@@ -115,13 +115,13 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     const bool looks = p.words && order;
     float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
     bool reset = false;
+    const uint32_t first_bits = flag_bits(sFirst, lane), last_bits = flag_bits(sLast, lane);
     if (publishes) {
+        reset = last_bits != 0;
 #pragma unroll
         for (int k = W - 1; k >= 0; --k) {
             const Link v = sG[k][lane];
-            const bool rs = __builtin_amdgcn_readfirstlane(sLast[k]);
-            reset |= rs;
-            join_link(rs, v, cG);
+            join_link(last_bits >> k & 1, v, cG);
             cA[0] *= v[0];
             cA[1] *= v[1];
         }
@@ -136,12 +136,14 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
             Io<BF>::get(x[s], xv);
             Io<BF>::get(i[s], iv);
             if (span.begins(s)) state(p.state_in, s, H);
+            float si[kVec];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                si[s][j] = sigmoid(iv[j]);
-                b[s][j] *= si[s][j] * xv[j];
+                si[j] = sigmoid(iv[j]);
+                b[s][j] *= si[j] * xv[j];
                 H[j] = fmaf(a[s][j], H[j], b[s][j]);
             }
+            sSi[wave][s][lane] = float2{si[0], si[1]};
         }
     }
     sH[wave][lane] = float2{H[0], H[1]};
@@ -154,8 +156,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     __syncthreads();
     float g[kVec] = {}, h[kVec] = {};
     if (looks)
-#pragma unroll
-        for (int k = 0; k < W; ++k) join_link(__builtin_amdgcn_readfirstlane(sBehindReset[k]), sBehind[k][lane], g);
+        join_links(flag_bits(sBehindReset, lane), 0, 1, W, [&](int k) { return sBehind[k][lane]; }, g);
     if (publishes && ends) {
         float e[kVec];
 #pragma unroll
@@ -164,14 +165,17 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     }
     float sum[kVec] = {};
     if (span.have) {
-        for (int k = W - 1; k > wave; --k) join_link(__builtin_amdgcn_readfirstlane(sLast[k]), sG[k][lane], g);
+        join_links(last_bits, W - 1, -1, W - 1 - wave, [&](int k) { return sG[k][lane]; }, g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = p.carry[(int64_t)chunk * p.dim + col + j];
-        for (int k = 0; k < wave; ++k) {
-            const Link v = sG[k][lane];
-            const float2 u = sH[k][lane];
-            join_link(__builtin_amdgcn_readfirstlane(sFirst[k]), Link{v[0], v[1], u.x, u.y}, h);
-        }
+        join_links(
+            first_bits, 0, 1, wave,
+            [&](int k) {
+                const Link v = sG[k][lane];
+                const float2 u = sH[k][lane];
+                return Link{v[0], v[1], u.x, u.y};
+            },
+            h);
 #pragma unroll
         for (int s = 0; s < S; ++s) {  // b becomes the states in front of the tokens
             if (span.begins(s)) state(p.state_in, s, h);
@@ -194,14 +198,15 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
             Io<BF>::get(x[s], xv);
             Io<BF>::get(dy[s], d);
             if (span.ends(s)) state(p.dstate_out, s, g);
-            decay(w[s], near, again, q);
+            const float2 kept = sSi[wave][s][lane];
+            const float si[kVec] = {kept.x, kept.y};
+            decay(w[s], near, again, q, 1e-37f);  // w / m is 0 where both are
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float dh = d[j] + g[j];
-                q[j] += 1e-37f;  // w / m is 0 where both are
-                const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si[s][j] * xv[j], aw = a[s][j] * w[s][j];
-                ox[j] = dh * (q[j] * rs) * si[s][j];
-                oi[j] = ox[j] * fmaf(-si[s][j], xv[j], xv[j]);
+                const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si[j] * xv[j], aw = a[s][j] * w[s][j];
+                ox[j] = dh * (q[j] * rs) * si[j];
+                oi[j] = ox[j] * fmaf(-si[j], xv[j], xv[j]);
                 const float share = dh * aw * fmaf(a[s][j] * rs, sx, -b[s][j]);
                 orr[j] = fmaf(w[s][j], per_rate[j], 1.f) * share;
                 sum[j] += share;

@@ -87,18 +87,19 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     sOwn[wave][lane] = Link{A[0], A[1], H[0], H[1]};
     if (lane == 0) sOwnReset[wave] = span.first != 0;
     __syncthreads();
+    const uint32_t resets = flag_bits(sOwnReset, lane);
+    auto own_link = [&](int k) { return sOwn[k][lane]; };
     float h[kVec] = {};
     if (p.words) {
         const bool publishes = wave == 0 && chunk + 1 < p.chunks, ends = (chunk & (kGroup - 1)) == kGroup - 1;
         float cA[kVec] = {1.f, 1.f}, cH[kVec] = {};
         bool reset = false;
         if (publishes) {
+            reset = resets != 0;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 const Link v = sOwn[k][lane];
-                const bool rs = __builtin_amdgcn_readfirstlane(sOwnReset[k]);
-                reset |= rs;
-                join_link(rs, v, cH);
+                join_link(resets >> k & 1, v, cH);
                 cA[0] *= v[0];
                 cA[1] *= v[1];
             }
@@ -112,8 +113,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
             sBack[wave][lane] = back;
             if (lane == 0) sBackReset[wave] = rs;
             __syncthreads();
-#pragma unroll
-            for (int k = 0; k < W; ++k) join_link(__builtin_amdgcn_readfirstlane(sBackReset[k]), sBack[k][lane], h);
+            join_links(flag_bits(sBackReset, lane), 0, 1, W, [&](int k) { return sBack[k][lane]; }, h);
         }
         if (publishes && ends) {
             float e[kVec];
@@ -122,10 +122,10 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
             if (ok) publish(p.words, chunk, p.dim, own, true, e, e);
         }
     }
-    for (int k = 0; k < wave; ++k) join_link(__builtin_amdgcn_readfirstlane(sOwnReset[k]), sOwn[k][lane], h);
+    join_links(resets, 0, 1, wave, own_link, h);
     if (!span.have) return;
     // the state in front of one of these tokens may be one that the backward asks for
-    const int kept = p.carry ? -span.t0 & (kBackwardChunk - 1) : S;
+    const int kept = p.carry ? (kBackwardChunk - span.t0 % kBackwardChunk) % kBackwardChunk : S;
     const Rows<BF> ys(p.y, p.dim, span.t0, p.y ? rows : 0, p.dim);
 #pragma unroll
     for (int s = 0; s < S; ++s) {

@@ -844,7 +844,7 @@ hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params,
  * sequences of tokens / N each (seq_start NULL), or packed with N + 1 offsets in device
  * memory under the same rules. Rows that belong to no sequence are neither read nor written.
  * ------------------------------------------------------------------------ */
-#define HYENA_RECURRENCE_CARRY 64 /* tokens between the states that the forward keeps for its backward */
+#define HYENA_RECURRENCE_CARRY 80 /* tokens between the states that the forward keeps for its backward */
 
 typedef struct hyena_recurrence_params_s {
     int64_t dim;         /* channels: a multiple of 8, at most 2^20 */
@@ -875,7 +875,7 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  *   state_out [N][dim] fp32, device (output), or NULL; may be state_in itself. An empty sequence
  *             passes its state on.
  *   carries   [ceil(tokens / HYENA_RECURRENCE_CARRY)][dim] fp32, device (output), or NULL: the states
- *             in front of rows 0, 64, 128, ..., which spare hyena_recurrence_backward a pass over
+ *             in front of rows 0, 80, 160, ..., which spare hyena_recurrence_backward a pass over
  *             the inputs
  *   workspace at least hyena_recurrence_workspace_bytes(...) bytes, 16-byte aligned
  * All arithmetic is fp32 and y is rounded once. A value that is not finite spoils its channel of its
@@ -884,7 +884,7 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  * inputs, but for state_out. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
  * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 256, or 2^23 or
- * more pairs of 64 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+ * more pairs of 80 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
 hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                         const int64_t* seq_start, const hyena_recurrence_inputs_t* in,
                                         const float* state_in, void* y, float* state_out, float* carries,

@@ -120,8 +120,8 @@ def test_binding(launches):
     start = torch.tensor([0, 300], dtype=torch.int64)
     for call in (lambda: m.forward(x[0], x[0], x[0]), lambda: m.forward(x, x, x, seq_start=start),
                  lambda: m.forward(x, x.bfloat16(), x), lambda: m.forward(x, x[:, :299], x), lambda: m.forward(x, None, x),
-                 lambda: m.forward(x, x, x, state=torch.zeros(3, 16)), lambda: m.forward(x, x, x, carries=torch.zeros(4, 16)),
-                 lambda: m.forward(x, x, x, carries=torch.zeros(10, 16).double()),
+                 lambda: m.forward(x, x, x, state=torch.zeros(3, 16)), lambda: m.forward(x, x, x, carries=torch.zeros(9, 16)),
+                 lambda: m.forward(x, x, x, carries=torch.zeros(8, 16).double()),
                  lambda: m.forward(x, x, torch.zeros(2, 300, 32)[..., ::2]), lambda: m.forward(x, x, torch.zeros(2, 300, 20)[..., 2:18]),
                  lambda: m.forward(x[0], x[0], x[0], seq_start=start.int()), lambda: m.forward(x[0], x[0], x[0], seq_start=start[:1]),
                  lambda: m.backward(x, x, x, x[0]), lambda: m.backward(x, x, x, x, dstate_out=torch.zeros(2, 8)),
