@@ -1057,15 +1057,22 @@ class DeltaRule:
 
 
 def _rows_of(t, name, shape, dtype, device):
-    """Address and row stride of t [*rows, dim] of this shape, as _token_rows."""
+    """Address and row stride of t [rows, dim] or [B, T, dim] of this shape, as _token_rows."""
     try:
-        if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
-            at, dim = t.data_ptr(), shape[-1]
-            if not (at | dim * dtype.itemsize) & 15:
-                return at, dim
-        return _token_rows(t.unsqueeze(-2), name, tuple(shape[:-1]), 1, shape[-1], dtype, device)
+        if t.shape != shape or t.dtype is not dtype or t.device != device:
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        ld, at = shape[-1], t.data_ptr()
+        if not t.is_contiguous():
+            st, dim, rows = t.stride(), ld, shape[-2]
+            ld = st[-2] if rows > 1 else st[0] if len(shape) == 3 and shape[0] > 1 else dim
+            if (dim > 1 and st[-1] != 1) or ld < dim or (len(shape) == 3 and shape[0] > 1 and st[0] != rows * ld):
+                raise ValueError(f"{name} must have dense rows and one stride between them")
     except AttributeError:
         raise ValueError(f"{name} must be a tensor, got {type(t).__name__}") from None
+    if (ld * dtype.itemsize | at) & 15 and t.numel():
+        raise ValueError(f"{name}'s rows must start on 16 bytes")
+    return at, ld
 
 
 def _like(torch, t, dtype, device):
