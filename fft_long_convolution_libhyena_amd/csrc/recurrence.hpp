@@ -25,7 +25,7 @@ namespace rec {
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
 // Tokens of a wave and of a chunk: as many as 128 registers hold, which leaves two workgroups a CU (the
-// backward holds twice as much of each, sig(i) in LDS). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22
+// backward holds twice as much of each, exp(-i) in LDS). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22
 // tokens a wave: 134, 112, 107, 104, 102 and 103 us; with 32 in waves at two or three a SIMD 114 and 125. Training step
 // of 8 x 8192 with 6, 8 and 10 in the backward: 334, 297 and 285 us (8 without LDS the same, 10 without it spills: 375).
 constexpr int kForwardSpan = 20, kBackwardSpan = 10;
@@ -151,9 +151,11 @@ struct Rows {
     }
 };
 
-__device__ __forceinline__ float sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
-}
+__device__ __forceinline__ float exp_minus(float x) { return __builtin_amdgcn_exp2f(-kLog2e * x); }
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + exp_minus(x)); }
+// 1 - sig(x) from e = exp(-x) and sig(x), without the difference, which would cancel where the gate is open;
+// 1 where e is infinite and sig(x) 0
+__device__ __forceinline__ float one_minus(float e, float sig) { return fminf(e * sig, 1.f); }
 // a = exp(-w) and q = 1 - a^2 for w = -log a >= 0. Near a = 1 the error of a counts once for every
 // token that a state outlives, and 1 - a^2 cancels: below w = 1/2 a comes from e = 1 - exp(-w) as
 // w times a polynomial (a fit of degree 5 at Chebyshev points, 5e-9 off) with half a step of error and no
@@ -197,7 +199,7 @@ __device__ __forceinline__ bool near_rates(const float (&rate)[kVec]) { return _
 // through long sequences at a hop for 16 chunks. A wave polls its share of them at once; the words of
 // even and of odd channels lie apart, so that it reads whole lines.
 constexpr int kGroup = 16;
-constexpr int kPolls = 1 << 20;  // about a second
+constexpr int kPolls = 1 << 22;  // some seconds
 
 using Word = unsigned long long;
 constexpr uint32_t kResetWord = 0xc0000000u;  // the high half: A = -2

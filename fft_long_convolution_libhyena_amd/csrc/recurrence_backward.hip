@@ -4,7 +4,9 @@
 //   dx = dh m sig(i),   di = dh m x sig(i) (1 - sig(i)),
 //   W  = dh (a log(a) h[t - 1] - a^2 (log(a) / m) sig(i) x),
 //   dr = (1 - sig(r)) W,   drate = sum W / c.
-// log(a) / m -> 0 as a -> 1, so nothing is divided by 0 where a gate is shut. g runs
+// log(a) / m -> 0 as a -> 1, so nothing is divided by 0 where a gate is shut; 1 - sig comes from exp(-r) and
+// exp(-i), which are kept, so that the gradients of gates wide open keep their digits (2% of the training
+// step's time against the difference). g runs
 // through the chunks from the last to the first as h does from the first: (A, G) of a chunk
 // need only its own tokens. h is computed again from the states in front of the chunks.
 #include <hip/hip_runtime.h>
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     using Raw = typename Io<BF>::Raw;
     constexpr int S = kBackwardSpan, W = kWaves;
     __shared__ Link sG[W][64], sBehind[W][64];  // (A, G) of the waves and of the chunks behind
-    __shared__ float2 sH[W][64], sSi[W][S][64];  // sSi: a lane's own sig(i), kept for the last pass
+    __shared__ float2 sH[W][64], sEi[W][S][64];  // sEi: a lane's own exp(-i), kept for the last pass
     __shared__ int sFirst[W], sLast[W], sBehindReset[W];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -60,7 +62,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         for (int j = 0; j < kVec; ++j) h[j] = from ? from[n * p.dim + col + j] : 0.f;
     };
     Raw x[S], dy[S], i[S];
-    float w[S][kVec], a[S][kVec], b[S][kVec];  // w = -log a, sig(i), a, m sig(i) x
+    float er[S][kVec], a[S][kVec], b[S][kVec];  // exp(-r), a, m sig(i) x
     float rate[kVec], A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
@@ -83,11 +85,14 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float rv[kVec], q[kVec];
+            float rv[kVec], q[kVec], w[kVec];
             Io<BF>::get(r[s], rv);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) w[s][j] = rate[j] * sigmoid(rv[j]);
-            decay(w[s], near, a[s], q);
+            for (int j = 0; j < kVec; ++j) {
+                er[s][j] = exp_minus(rv[j]);
+                w[j] = rate[j] * __builtin_amdgcn_rcpf(1.f + er[s][j]);
+            }
+            decay(w, near, a[s], q);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 b[s][j] = __builtin_amdgcn_sqrtf(q[j]);
@@ -136,14 +141,14 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
             Io<BF>::get(x[s], xv);
             Io<BF>::get(i[s], iv);
             if (span.begins(s)) state(p.state_in, s, H);
-            float si[kVec];
+            float ei[kVec];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                si[j] = sigmoid(iv[j]);
-                b[s][j] *= si[j] * xv[j];
+                ei[j] = exp_minus(iv[j]);
+                b[s][j] *= __builtin_amdgcn_rcpf(1.f + ei[j]) * xv[j];
                 H[j] = fmaf(a[s][j], H[j], b[s][j]);
             }
-            sSi[wave][s][lane] = float2{si[0], si[1]};
+            sEi[wave][s][lane] = float2{ei[0], ei[1]};
         }
     }
     sH[wave][lane] = float2{H[0], H[1]};
@@ -186,29 +191,33 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
                 b[s][j] = before;
             }
         }
-        float per_rate[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) per_rate[j] = -__builtin_amdgcn_rcpf(rate[j]);
         const Rows<BF> oxs(p.dx, p.dim, span.t0, rows, p.dim), ors(p.dr, p.dim, span.t0, rows, p.dim),
             ois(p.di, p.dim, span.t0, rows, p.dim);
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             if (!span.has(s)) continue;
-            float xv[kVec], d[kVec], ox[kVec], orr[kVec], oi[kVec], again[kVec], q[kVec];
+            float xv[kVec], d[kVec], ox[kVec], orr[kVec], oi[kVec], w[kVec], shut[kVec], again[kVec], q[kVec];
             Io<BF>::get(x[s], xv);
             Io<BF>::get(dy[s], d);
             if (span.ends(s)) state(p.dstate_out, s, g);
-            const float2 kept = sSi[wave][s][lane];
-            const float si[kVec] = {kept.x, kept.y};
-            decay(w[s], near, again, q, 1e-37f);  // w / m is 0 where both are
+            const float2 kept = sEi[wave][s][lane];
+            const float ei[kVec] = {kept.x, kept.y};
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float sr = __builtin_amdgcn_rcpf(1.f + er[s][j]);
+                w[j] = rate[j] * sr;
+                shut[j] = one_minus(er[s][j], sr);
+            }
+            decay(w, near, again, q, 1e-37f);  // w / m is 0 where both are
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float dh = d[j] + g[j];
-                const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si[j] * xv[j], aw = a[s][j] * w[s][j];
-                ox[j] = dh * (q[j] * rs) * si[j];
-                oi[j] = ox[j] * fmaf(-si[j], xv[j], xv[j]);
+                const float si = __builtin_amdgcn_rcpf(1.f + ei[j]);
+                const float rs = __builtin_amdgcn_rsqf(q[j]), sx = si * xv[j], aw = a[s][j] * w[j];
+                ox[j] = dh * (q[j] * rs) * si;
+                oi[j] = ox[j] * xv[j] * one_minus(ei[j], si);
                 const float share = dh * aw * fmaf(a[s][j] * rs, sx, -b[s][j]);
-                orr[j] = fmaf(w[s][j], per_rate[j], 1.f) * share;
+                orr[j] = shut[j] * share;
                 sum[j] += share;
                 g[j] = a[s][j] * dh;
             }

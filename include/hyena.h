@@ -849,7 +849,7 @@ hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params,
 typedef struct hyena_recurrence_params_s {
     int64_t dim;         /* channels: a multiple of 8, at most 2^20 */
     hyena_dtype_t dtype; /* of x, r, i, y and their gradients */
-    const float* rate;   /* [dim] fp32, device: c, above 0 and finite */
+    const float* rate;   /* [dim] fp32, device: c, a normal number above 0 */
 } hyena_recurrence_params_t;
 
 /* Token t's channels lie at x + t*ldx, r + t*ldr, i + t*ldi (elements; column ranges of one

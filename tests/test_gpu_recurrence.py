@@ -140,6 +140,22 @@ def test_gates_wide_open_and_shut(dtype):
         assert R.rel(g.cpu()[fine], w[fine]) <= (bwd(lens, dtype) if k < 3 else 2 * f32(lens)), k
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("z", [8.0, 14.0, 18.0])
+def test_gates_all_open_keep_the_digits_of_their_gradients(z, dtype):
+    """sig' = sig (1 - sig) where 1 - sig is 3e-4 .. 2e-8: relative to itself, not to 1. (z is exact in bf16; its
+    exponential's argument is off by at most z E, the rest as above.)"""
+    lens = [100]
+    d = R.make(lens, 16, dtype, seed=12)
+    d["r"].fill_(z)
+    d["i"].fill_(z)
+    m = rule(d, 16, dtype)
+    got = m.backward(*R.gpu(d, "x", "r", "i", "dy"), state=d["state"].cuda(), dstate_out=d["dstate"].cuda(), seq_start=R.starts(lens))
+    want = R.backward(d)
+    for k, (g, w) in enumerate(zip(got, want)):
+        assert R.rel(g, w) <= (bwd(lens, dtype) if k < 3 else 2 * f32(lens)) + 2 * z * 2.0 ** -24, k
+
+
 def test_gradients_against_differences():
     """Central differences of the kernels' own fp32 forward along random directions, in fp32 sums: a
     step of 1e-2 leaves curvature of about 1e-4 and rounding of 2^-24 * sqrt(n) / 1e-2, both under 1 percent of
@@ -226,6 +242,57 @@ def test_rows_of_no_sequence(dtype):
     m.forward(*x[:3], state=d["state"].cuda(), seq_start=start, y=given)
     assert bool((given[:front] == 7).all()) and bool((given[-back:] == 7).all())
     assert torch.equal(given[front:-back], y[front:-back])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_states_in_place(dtype):
+    """state_out may be the initial states: sequences within a wave, a chunk and over many, and empty ones."""
+    lens = [3, 0, 500, 1, 4000, 40, 0, 700]
+    d = R.make(lens, 72, dtype, seed=13)
+    m = rule(d, 72, dtype)
+    x, start = R.gpu(d, "x", "r", "i"), R.starts(lens)
+    y, s = m.forward(*x, state=d["state"].cuda(), seq_start=start)
+    for _ in range(3):
+        pool = d["state"].cuda()
+        y2, s2 = m.forward(*x, state=pool, seq_start=start, state_out=pool)
+        assert s2 is pool and torch.equal(s2, s) and torch.equal(y2, y)
+    rows = [v[:4200].unflatten(0, (6, 700)) for v in x]
+    y, s = m.forward(*rows, state=d["state"][:6].cuda())
+    pool = d["state"][:6].cuda()
+    assert torch.equal(m.forward(*rows, state=pool, state_out=pool)[0], y) and torch.equal(pool, s)
+
+
+def test_more_than_32_bits_of_elements():
+    """Two sequences of 2^20 rows of 2304 channels, 4.8e9 elements: constant gates and inputs reach b / (1 - a), and
+    the backward's sums their closed forms."""
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 110 GB of free memory")
+    from fft_long_convolution_libhyena_amd import GatedRecurrence
+
+    T, dim = 1 << 20, 2304
+    rate = torch.linspace(0.1, 0.4, dim).cuda()
+    m = GatedRecurrence(dim, rate)
+    x = torch.ones(2, T, dim, dtype=torch.bfloat16, device="cuda")
+    x[1] = -2
+    zero = torch.zeros_like(x)
+    y, s = m.forward(x, zero, zero)
+    a = torch.exp(-rate.double() / 2)
+    b = (1 - a * a).sqrt() / 2
+    full = b / (1 - a)
+    for n, v in ((0, 1.0), (1, -2.0)):
+        assert R.rel(s[n], v * full) <= 1e-5 and R.rel(y[n, 0], v * b) <= 2.0 ** -8
+        for t in (5000, T // 2 + 7, T - 1):
+            assert R.rel(y[n, t], v * full) <= 2.0 ** -8 + 1e-5
+    del y
+    dx, dr, di, drate, dstate = m.backward(x, zero, zero, x)
+    at = T // 2 + 3  # far from both ends: dh = v / (1 - a), h = v full
+    for n, v in ((0, 1.0), (1, -2.0)):
+        dh = v / (1 - a)
+        assert R.rel(dx[n, at], dh * b) <= 2.0 ** -8 + 1e-5 and R.rel(di[n, at], dh * b * v / 2) <= 2.0 ** -8 + 1e-5
+        assert R.rel(dx[n, T - 1], v * b) <= 2.0 ** -8 + 1e-5
+    assert bool(torch.isfinite(drate).all())
+    del x, zero, dx, dr, di
+    torch.cuda.empty_cache()
 
 
 def test_no_tokens():

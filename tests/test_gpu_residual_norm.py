@@ -142,6 +142,29 @@ def test_views_batches_and_in_place():
     assert torch.equal(a[0].flatten(0, 1), b[0]) and torch.equal(a[2], b[2])
 
 
+def test_single_outputs_of_the_backward():
+    """Any of the three may be left out, and dresidual may be dsum."""
+    dim, rows = 520, 70
+    d = make(rows, dim, "bf16", True, seed=6)
+    m = norm(d, dim, "bf16", True)
+    s, dy, ds = d["residual"].cuda(), d["dy"].cuda(), d["dsum"].cuda()
+    dx, dres, dw = m.backward(s, dy, ds)
+    ws = torch.empty(m.backward_workspace_bytes(rows), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(x=None, r=None, w=None):
+        p = [t.data_ptr() if t is not None else None for t in (x, r, w)]
+        assert m.lib.hyena_residual_norm_backward(m._params(), rows, s.data_ptr(), dim, dy.data_ptr(), ds.data_ptr(), *p,
+                                                  ws.data_ptr() if w is not None else None, ws.numel(), stream) == 0
+
+    for want, key in ((dx, "x"), (dres, "r"), (dw, "w")):
+        got = torch.full_like(want, 7)
+        call(**{key: got})
+        assert torch.equal(got, want)
+    call(r=ds)
+    assert torch.equal(ds, dres)
+
+
 def test_no_rows():
     d = make(1, 64, "bf16", False)
     e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
