@@ -161,7 +161,8 @@ __device__ __forceinline__ float one_minus(float e, float sig) { return fminf(e 
 // w times a polynomial (a fit of degree 5 at Chebyshev points, 5e-9 off) with half a step of error and no
 // bias, and q = e (1 + a) keeps e's digits. (With the exponential instruction, a step off to one
 // side, states of 2000 tokens with a around 0.999 were 2.7e-6 off in place of 5e-7.)
-// least: added to e, so that q is not 0. near (of the wave): all w are known to be below 1/2, as rates below 1/2 make them.
+// least: added to e, so that q is not 0. near (of the wave): all w are known to be below 1/2, as rates below
+// 1/2 make them.
 __device__ __forceinline__ void decay(const float (&w)[kVec], bool near, float (&a)[kVec], float (&q)[kVec], float least = 0.f) {
     float e[kVec];
 #pragma unroll
@@ -236,12 +237,12 @@ __device__ __forceinline__ void publish(Word* words, int order, int dim, int col
     for (int j = 0; j < kVec; ++j) {
         const float a = A[j] == A[j] ? A[j] : 0.f;  // H is NaN where A is
         const uint32_t hi = reset ? kResetWord : __float_as_uint(a) | 0x80000000u;
-        __hip_atomic_store(words + (int64_t)order * dim + (uint32_t)(j * (dim / 2) + col / 2), (Word)hi << 32 | __float_as_uint(H[j]), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(words + (int64_t)order * dim + (uint32_t)(j * (dim / 2) + col / 2),
+                           (Word)hi << 32 | __float_as_uint(H[j]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
-// This wave's words: kPolled wave .. of those in front of chunk `order` in its group, the first of which is the
+// This wave's words: kPolled of them from kPolled * wave on, of those in front of chunk `order` in its group, the first of which is the
 // last of the group before. ask() sends for them, done() waits for all, gives (A, H) of the run and
 // returns whether a sequence begins in it.
 struct LookBack {
@@ -312,7 +313,7 @@ struct Call {
 };
 
 hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
-                     const hyena_recurrence_inputs_t* in, Call& c);
+                     const hyena_recurrence_inputs_t* in, Call& c, int64_t most_ld = int64_t(1) << 22);
 // 64-bit values at the head of a workspace that start() clears: the tickets of up to two launches, then the words
 constexpr int kHead = 2;
 inline int64_t word_count(const Call& c, int64_t chunks) { return chunks > 1 ? chunks * c.p.dim : 0; }

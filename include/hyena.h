@@ -854,7 +854,7 @@ typedef struct hyena_recurrence_params_s {
 
 /* Token t's channels lie at x + t*ldx, r + t*ldr, i + t*ldi (elements; column ranges of one
  * projection's rows may be given as they lie); ld* at least dim, a multiple of 16 bytes and at
- * most 2^22. */
+ * most 2^22 (hyena_recurrence_step: 2^31). */
 typedef struct hyena_recurrence_inputs_s {
     const void* x;
     int64_t ldx;

@@ -369,6 +369,20 @@ def test_step_shared_slots_padding_and_continuing():
     assert R.rel(y3, y1[:, 6:]) <= 2 * f32([9]) and R.rel(s2, s1) <= 2 * f32([9])
 
 
+def test_step_on_the_last_tokens_of_long_rows():
+    """A view with one token of each of a few long rows: strides beyond what whole sequences take."""
+    B, T, dim = 3, 60000, 136
+    d = R.make([1] * B, dim, "bf16", seed=14)
+    m = rule(d, dim, "bf16")
+    long = torch.zeros(3, B, T, dim, dtype=torch.bfloat16, device="cuda")
+    for k, n in enumerate(("x", "r", "i")):
+        long[k, :, -1] = d[n].cuda()
+    states = [d["state"].cuda() for _ in range(2)]
+    y = m.step(*long[:, :, -1:], states[0])
+    assert T * dim > 1 << 22 and y.is_contiguous()
+    assert torch.equal(y, m.step(*(d[n].cuda()[:, None] for n in ("x", "r", "i")), states[1])) and torch.equal(*states)
+
+
 def test_capture_replays_and_streams():
     """A captured training step replayed on new inputs, with eager work between, and the same calls on two
     streams at once, against eager results."""

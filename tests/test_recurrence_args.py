@@ -56,10 +56,15 @@ def test_params(lib, kw, want):
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(r=None), dict(i=None), dict(x=P + 8), dict(ldx=248), dict(ldr=260),
-                                dict(ldi=(1 << 22) + 8)])
+                                dict(ldi=(1 << 31) + 8)])
 def test_inputs(lib, kw):
     assert forward(lib, i=inputs(**kw)) == INVALID and backward(lib, i=inputs(**kw)) == INVALID
     assert step(lib, i=inputs(**kw)) == INVALID
+
+
+def test_stride_of_whole_sequences(lib):
+    i = inputs(ldx=(1 << 22) + 8)
+    assert forward(lib, i=i) == INVALID and backward(lib, i=i) == INVALID
 
 
 def test_sizes(lib):
