@@ -20,7 +20,7 @@ SOURCES = ["hyena_api.hip", "hyena_backward.hip", "hyena_operator.hip", "fourste
            "recurrence_forward.hip", "recurrence_backward.hip", "recurrence_step.hip", "residual_norm.hip"]
 HEADERS = ["fft_core.hpp", "kernels.hpp", "pair.hpp", "plan.hpp", "tables.hpp", "conv_nd.hpp", "lds_path.hpp", "fourstep.hpp", "backward.hpp",
            "lds_backward.hpp", "outproj.hpp", "delta.hpp", "delta_prep.hpp", "delta_scan.hpp", "delta_rev.hpp",
-           "delta_grad.hpp", "recurrence.hpp"]
+           "delta_grad.hpp", "recurrence.hpp", "stream.hpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -20,6 +20,7 @@
 
 #include "../../include/hyena.h"
 #include "plan.hpp"
+#include "stream.hpp"
 
 namespace hy {
 namespace {
@@ -55,8 +56,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4n __attribute__((ext_vector_type(4)));
 
-// eight elements of a head: quads a and b (neighbours unless HALVES)
-template <bool BF, bool HALVES>
+// eight elements of a head: quads a and b (neighbours unless HALVES); ST: as accesses of a stream (stream.hpp)
+template <bool BF, bool HALVES, bool ST>
 struct Eight {
     u32x4 r[BF ? 1 : 2];
     __device__ __forceinline__ void load(const void* base, int a, int b, bool ok) {
@@ -68,14 +69,14 @@ struct Eight {
         if constexpr (BF) {
             const uint16_t* p = (const uint16_t*)base;
             if constexpr (HALVES) {
-                const u32x2 x = *(const u32x2*)(p + 4 * a), y = *(const u32x2*)(p + 4 * b);
+                const u32x2 x = load_once<ST>((const u32x2*)(p + 4 * a)), y = load_once<ST>((const u32x2*)(p + 4 * b));
                 r[0] = u32x4{x[0], x[1], y[0], y[1]};
             } else {
-                r[0] = *(const u32x4*)(p + 4 * a);
+                r[0] = load_once<ST>((const u32x4*)(p + 4 * a));
             }
         } else {
-            r[0] = *(const u32x4*)((const float*)base + 4 * a);
-            r[1] = *(const u32x4*)((const float*)base + 4 * b);
+            r[0] = load_once<ST>((const u32x4*)((const float*)base + 4 * a));
+            r[1] = load_once<ST>((const u32x4*)((const float*)base + 4 * b));
         }
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -99,14 +100,14 @@ struct Eight {
             const u32x4 w = __builtin_bit_cast(u32x4, h);
             uint16_t* p = (uint16_t*)base;
             if constexpr (HALVES) {
-                *(u32x2*)(p + 4 * a) = u32x2{w[0], w[1]};
-                *(u32x2*)(p + 4 * b) = u32x2{w[2], w[3]};
+                store_once<ST>(u32x2{w[0], w[1]}, (u32x2*)(p + 4 * a));
+                store_once<ST>(u32x2{w[2], w[3]}, (u32x2*)(p + 4 * b));
             } else {
-                *(u32x4*)(p + 4 * a) = w;
+                store_once<ST>(w, (u32x4*)(p + 4 * a));
             }
         } else {
-            *(f32x4n*)((float*)base + 4 * a) = f32x4n{x[0], x[1], x[2], x[3]};
-            *(f32x4n*)((float*)base + 4 * b) = f32x4n{x[4], x[5], x[6], x[7]};
+            store_once<ST>(f32x4n{x[0], x[1], x[2], x[3]}, (f32x4n*)((float*)base + 4 * a));
+            store_once<ST>(f32x4n{x[4], x[5], x[6], x[7]}, (f32x4n*)((float*)base + 4 * b));
         }
     }
 };
@@ -123,10 +124,10 @@ __device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const f
     }
 }
 
-template <bool BF, int G, bool HALVES, bool BACK, int AHEAD>
+template <bool BF, int G, bool HALVES, bool BACK, int AHEAD, bool ST>
 __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
     constexpr int GW = kNormThreads / G;  // groups per workgroup
-    using E8 = Eight<BF, HALVES>;
+    using E8 = Eight<BF, HALVES, ST>;
     constexpr int64_t E = BF ? 2 : 4;
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
     const int quads = a.dim / 4, rq = a.rot / 4;
@@ -316,10 +317,13 @@ NormGrid norm_grid(const hyena_qk_norm_params_t& p, int64_t tokens, bool back) {
 template <bool BF, int G, bool HALVES, bool BACK>
 void launch_norm_g(const NormArgs& a, const NormGrid& g, hipStream_t st) {
     const dim3 grid(g.x, g.y), block(kNormThreads);
-    if (g.per > 1)
-        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead>), grid, block, 0, st, a);
+    const int64_t bytes = a.tokens * (a.hq + a.hk) * a.dim * (BF ? 2 : 4) * (BACK ? 3 : 2);
+    if (bytes > kInfinityCache)  // with so many tokens a group takes several heads
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, true>), grid, block, 0, st, a);
+    else if (g.per > 1)
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, false>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1, false>), grid, block, 0, st, a);
 }
 
 template <bool BF, bool HALVES, bool BACK>

@@ -122,7 +122,8 @@ struct Io<false> {
 
 // Rows t0 .. of an array, read and written by buffer instructions: the row is a scalar offset and the
 // lane's channels a constant one, so an access costs no vector arithmetic; a lane behind the last channel
-// has the offset kNone outside of the range, loads 0 and stores nothing.
+// has the offset kNone outside of the range, loads 0 and stores nothing. Stores are marked as not read again soon
+// (1 x 65536 x 768: 102 to 98 us, training step of 8 x 8192: 292 to 281; loads so too: 98 and 279, but small calls 2 us longer).
 constexpr int kNone = (int)0x80000000u;
 template <bool BF>
 struct Rows {
@@ -143,10 +144,10 @@ struct Rows {
     }
     __device__ __forceinline__ void store(int row, int at, const float (&x)[kVec]) const {
         if constexpr (BF) {
-            __builtin_amdgcn_raw_buffer_store_b32(Io<BF>::put(x), buf, at, row * pitch, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(Io<BF>::put(x), buf, at, row * pitch, 2);
         } else {
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, Io<BF>::put(x)), buf, at, row * pitch, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, Io<BF>::put(x)), buf, at, row * pitch, 2);
         }
     }
 };

@@ -11,13 +11,14 @@
 // sum and the result: K pieces of 4 neighbours a thread, piece k of thread t at columns
 // 4 (k R + t). So 128 columns are 32 lanes of one wave and a block's largest value needs
 // no LDS. Threads walk over rows; the weights are loaded once. 65536 x 768 in bf16 take 70 us (5.7 TB/s), 16384 x
-// 2048 to 8 bits from an fp32 residual 66 (5.6; a wave a row, 32 values a lane: 82), the backward of
-// 65536 x 768 with the residual in fp32 146 (5.5).
+// 2048 to 8 bits from an fp32 residual 65 (5.7; a wave a row, 32 values a lane: 82), the backward of
+// 65536 x 768 with the residual in fp32 135 (5.9).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "../../include/hyena.h"
 #include "plan.hpp"
+#include "stream.hpp"
 
 namespace hy {
 namespace {
@@ -42,13 +43,13 @@ struct RmsArgs {
 typedef uint32_t u32x2r __attribute__((ext_vector_type(2)));
 typedef float f32x4r __attribute__((ext_vector_type(4)));
 
-// four neighbours of a row
-template <bool BF>
+// four neighbours of a row; ST: as accesses of a stream (stream.hpp)
+template <bool BF, bool ST>
 struct Four;
-template <>
-struct Four<true> {
+template <bool ST>
+struct Four<true, ST> {
     u32x2r r;
-    __device__ __forceinline__ void load(const void* row, int e) { r = *(const u32x2r*)((const uint16_t*)row + e); }
+    __device__ __forceinline__ void load(const void* row, int e) { r = load_once<ST>((const u32x2r*)((const uint16_t*)row + e)); }
     __device__ __forceinline__ void get(float (&x)[4]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -58,19 +59,19 @@ struct Four<true> {
     }
     static __device__ __forceinline__ void store(void* row, int e, const float (&x)[4]) {
         typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        *(bf16x4*)((uint16_t*)row + e) = bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        store_once<ST>(bf16x4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]}, (bf16x4*)((uint16_t*)row + e));
     }
 };
-template <>
-struct Four<false> {
+template <bool ST>
+struct Four<false, ST> {
     f32x4r r;
-    __device__ __forceinline__ void load(const void* row, int e) { r = *(const f32x4r*)((const float*)row + e); }
+    __device__ __forceinline__ void load(const void* row, int e) { r = load_once<ST>((const f32x4r*)((const float*)row + e)); }
     __device__ __forceinline__ void get(float (&x)[4]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = r[i];
     }
     static __device__ __forceinline__ void store(void* row, int e, const float (&x)[4]) {
-        *(f32x4r*)((float*)row + e) = f32x4r{x[0], x[1], x[2], x[3]};
+        store_once<ST>(f32x4r{x[0], x[1], x[2], x[3]}, (f32x4r*)((float*)row + e));
     }
 };
 
@@ -102,7 +103,7 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], float* lds) {
 }
 
 // XB, SB: x and y, the residual and the sum are bf16 (otherwise fp32); Q: output in 8 bits
-template <bool XB, bool SB, bool Q, int R, int K>
+template <bool XB, bool SB, bool Q, bool ST, int R, int K>
 __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) {
     constexpr int kPer = R < 256 ? 256 / R : 1;  // rows a workgroup
     constexpr int XE = XB ? 2 : 4, SE = SB ? 2 : 4;
@@ -120,8 +121,8 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
         for (int i = 0; i < 4; ++i) w[k][i] = p.w ? p.w[col[k] + i] : 1.f;
     }
     const int64_t step = (int64_t)gridDim.x * kPer;
-    Four<XB> x[K];
-    Four<SB> r[K];
+    Four<XB, ST> x[K];
+    Four<SB, ST> r[K];
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[k][i] += o[i];
             }
-            if (p.sum && in && ok[k]) Four<SB>::store((char*)p.sum + row * p.dim * SE, col[k], s[k]);
+            if (p.sum && in && ok[k]) Four<SB, ST>::store((char*)p.sum + row * p.dim * SE, col[k], s[k]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) ss[0] = ok[k] ? fmaf(s[k][i], s[k][i], ss[0]) : ss[0];
         }
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
             if (in)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (ok[k]) Four<XB>::store((char*)p.y + row * p.dim * XE, col[k], s[k]);
+                    if (ok[k]) Four<XB, ST>::store((char*)p.y + row * p.dim * XE, col[k], s[k]);
         } else {
             float most[K];
 #pragma unroll
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
                 if (in && ok[k]) {
                     int q = __builtin_amdgcn_cvt_pk_fp8_f32(s[k][0] * by, s[k][1] * by, 0, false);
                     q = __builtin_amdgcn_cvt_pk_fp8_f32(s[k][2] * by, s[k][3] * by, q, true);
-                    *(int*)((char*)p.y + row * p.dim + col[k]) = q;
+                    store_once<ST>(q, (int*)((char*)p.y + row * p.dim + col[k]));
                     if (p.block ? (t & 31) == 0 : k == 0 && t == 0)
                         p.scales[row * p.nscales + (p.block ? col[k] / 128 : 0)] = scale;
                 }
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
     }
 }
 
-template <bool XB, bool SB, int R, int K>
+template <bool XB, bool SB, bool ST, int R, int K>
 __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm_back(RmsArgs p) {
     constexpr int kPer = R < 256 ? 256 / R : 1;
     constexpr int XE = XB ? 2 : 4, SE = SB ? 2 : 4;
@@ -217,8 +218,8 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm_back(RmsArg
         const int64_t mine = r0 + threadIdx.x / R;
         const bool in = mine < p.rows;
         const int64_t row = in ? mine : p.rows - 1;
-        Four<SB> sr[K], dr[K];
-        Four<XB> yr[K];
+        Four<SB, ST> sr[K], dr[K];
+        Four<XB, ST> yr[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             sr[k].load((const char*)p.res + row * p.ldres * SE, col[k]);
@@ -249,8 +250,8 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm_back(RmsArg
                 o[i] = fmaf(inv, d[k][i] * w[k][i] - s[k][i] * along, e[i]);
             }
             if (in && ok[k]) {
-                if (p.dx) Four<XB>::store((char*)p.dx + row * p.dim * XE, col[k], o);
-                if (p.dres) Four<SB>::store((char*)p.dres + row * p.dim * SE, col[k], o);
+                if (p.dx) Four<XB, ST>::store((char*)p.dx + row * p.dim * XE, col[k], o);
+                if (p.dres) Four<SB, ST>::store((char*)p.dres + row * p.dim * SE, col[k], o);
             }
         }
     }
@@ -337,10 +338,17 @@ struct RmsForward {
     template <int R, int K>
     void go() const {
         const dim3 grid((unsigned)rms_forward_wgs(a.rows, a.dim)), block(R < 256 ? 256 : R);
-        if (a.scales)
-            hipLaunchKernelGGL((k_residual_norm<XB, SB, true, R, K>), grid, block, 0, st, a);
+        constexpr int XE = XB ? 2 : 4, SE = SB ? 2 : 4;
+        const int64_t bytes = a.rows * a.dim * (XE + (a.res ? SE : 0) + (a.sum ? SE : 0) + (a.scales ? 1 : XE));
+        const bool stream = bytes > kInfinityCache;
+        if (a.scales && stream)
+            hipLaunchKernelGGL((k_residual_norm<XB, SB, true, true, R, K>), grid, block, 0, st, a);
+        else if (a.scales)
+            hipLaunchKernelGGL((k_residual_norm<XB, SB, true, false, R, K>), grid, block, 0, st, a);
+        else if (stream)
+            hipLaunchKernelGGL((k_residual_norm<XB, SB, false, true, R, K>), grid, block, 0, st, a);
         else
-            hipLaunchKernelGGL((k_residual_norm<XB, SB, false, R, K>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((k_residual_norm<XB, SB, false, false, R, K>), grid, block, 0, st, a);
     }
 };
 template <bool XB, bool SB>
@@ -350,7 +358,12 @@ struct RmsBackward {
     template <int R, int K>
     void go() const {
         const dim3 grid((unsigned)rms_back_wgs(a.rows, a.dim)), block(R < 256 ? 256 : R);
-        hipLaunchKernelGGL((k_residual_norm_back<XB, SB, R, K>), grid, block, 0, st, a);
+        constexpr int XE = XB ? 2 : 4, SE = SB ? 2 : 4;
+        const int64_t bytes = a.rows * a.dim * (SE + XE + (a.ds ? SE : 0) + (a.dx ? XE : 0) + (a.dres ? SE : 0));
+        if (bytes > kInfinityCache)
+            hipLaunchKernelGGL((k_residual_norm_back<XB, SB, true, R, K>), grid, block, 0, st, a);
+        else
+            hipLaunchKernelGGL((k_residual_norm_back<XB, SB, false, R, K>), grid, block, 0, st, a);
     }
 };
 

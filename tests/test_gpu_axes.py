@@ -120,6 +120,23 @@ def test_batch_shape_no_tokens_and_capture():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,pairs", [(8, False), (64, True), (128, False), (256, True)])
+def test_calls_beyond_the_cache(dim, pairs, dtype):
+    """More than 256 MiB: the same bits for every token as in a call of few."""
+    few, hq, hk = 100, 2, 1
+    axis = [k % 3 for k in range(dim // 4 // 4 * 4)]
+    d = make(few, hq, hk, dim, axis, 3, dtype, dim, 1000, True)
+    m = norm(d, hq, hk, dim, dtype, "rms", pairs)
+    n = -(-(300 << 20) // ((hq + hk) * dim * 2 * (4 if dtype == "f32" else 2)) // few) + 1
+    small = [d[k].cuda() for k in ("q", "k", "dq_out", "dk_out", "pos")]
+    q, k, dq, dk, pos = (t.repeat(n, *[1] * (t.dim() - 1)) for t in small)
+    for a, b in zip(m.forward(q, k, pos), m.forward(small[0], small[1], small[4])):
+        assert torch.equal(a, b.repeat(n, 1, 1))
+    for a, b in zip(m.backward(q, k, dq, dk, pos)[:2], m.backward(*small)[:2]):
+        assert torch.equal(a, b.repeat(n, 1, 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_block_for_a_video(dtype):
     """A block as a layer runs it: residual norm, projection, head norm over time, height and width, gated delta rule,
     residual norm, projection, gated recurrence; then the gradients back through all of it, against 64 bits."""

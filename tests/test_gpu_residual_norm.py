@@ -126,6 +126,30 @@ def test_zeros_tiny_and_not_finite_rows(dim, block):
     assert bool(torch.isfinite(dx[[0, 1, 5]]).all())
 
 
+@pytest.mark.parametrize("dtype,wide", TYPES)
+@pytest.mark.parametrize("dim", [264, 768, 1544, 4104])
+def test_calls_beyond_the_cache(dim, dtype, wide):
+    """Calls of more than 256 MiB take other instructions for the same arithmetic: every row has the bits it has in a
+    small call, and the weight's gradient is the rows' sum (600 fp32 additions each way; signs cancel to the root of the rows)."""
+    rows = -(-(300 << 20) // (dim * 8))
+    few = 64
+    d = make(few, dim, dtype, wide, seed=dim)
+    small = [d[k].cuda() for k in ("x", "residual", "dy", "dsum")]
+    big = [t.repeat(-(-rows // few), 1)[:rows] for t in small]
+    for kw in (dict(), dict(bits8=True, block=128), dict(bits8=True)):
+        m = norm(d, dim, dtype, wide, **kw)
+        got, want = m.forward(big[0], big[1]), m.forward(small[0], small[1])
+        for a, b in zip(got, want):
+            a, b = (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for t in (a, b))
+            assert torch.equal(a, b.repeat(-(-rows // few), 1)[:rows])
+    dx, dres, dw = m.backward(*big[1:])
+    sx, sres, _ = m.backward(*small[1:])
+    assert torch.equal(dx, sx.repeat(-(-rows // few), 1)[:rows]) and torch.equal(dres, sres.repeat(-(-rows // few), 1)[:rows])
+    s = d["residual"].double()
+    each = (d["dy"].double() * s / (s.square().mean(-1, keepdim=True) + 1e-6).sqrt()).cuda()
+    assert rel(dw, each.repeat(-(-rows // few), 1)[:rows].sum(0)) <= (600 + 96) * E * few ** 0.5
+
+
 def test_views_batches_and_in_place():
     dim, B, T = 64, 2, 33
     d = make(B * T, dim, "bf16", False, seed=2)
