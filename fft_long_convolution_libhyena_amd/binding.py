@@ -85,8 +85,8 @@ class QKNormParamsStruct(ctypes.Structure):
 
 
 class RecurrenceParamsStruct(ctypes.Structure):
-    """hyena_recurrence_params_t: channels, dtype and the rates' device pointer."""
-    _fields_ = [("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("rate", ctypes.c_void_p)]
+    """hyena_recurrence_params_t: channels, dtype, whether rows of no sequence are cleared, the rates' device pointer."""
+    _fields_ = [("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("clear", ctypes.c_int), ("rate", ctypes.c_void_p)]
 
 
 class RecurrenceInputsStruct(ctypes.Structure):
@@ -1101,10 +1101,10 @@ class GatedRecurrence:
         if getattr(rate, "dtype", None) != torch.float32 or rate.shape != (self.dim,) or not rate.is_contiguous():
             raise ValueError(f"rate must be a contiguous fp32 vector of {self.dim}")
 
-    def _params(self, device=None):
+    def _params(self, device=None, clear=0):
         if device is not None and self.rate.device != device:
             raise ValueError("rate must be on the GPU that holds x")
-        return ctypes.byref(RecurrenceParamsStruct(self.dim, _DTYPES[self.dtype], self.rate.data_ptr()))
+        return ctypes.byref(RecurrenceParamsStruct(self.dim, _DTYPES[self.dtype], clear, self.rate.data_ptr()))
 
     def state_shape(self, N: int):
         return (int(N), self.dim)
@@ -1137,7 +1137,7 @@ class GatedRecurrence:
             return y, y.data_ptr()
         return y, _dense(y, "y", x.shape, self.io_dtype, device)
 
-    _out, _clear = DeltaRule._out, DeltaRule._clear
+    _out = DeltaRule._out
 
     def workspace_bytes(self, N: int, tokens: int, packed: bool = False) -> int:
         return int(self.lib.hyena_recurrence_workspace_bytes(self._params(), int(N), int(tokens), 16 if packed else None))
@@ -1154,17 +1154,15 @@ class GatedRecurrence:
         that belong to no sequence are zeros in y, but left as they were in a y that is given."""
         torch = self._torch
         dev, N, tokens, starts = self._sequences(x, seq_start)
-        inputs, params = self._inputs(x, r, i, dev), self._params(dev)
+        # rows of no sequence are zeros in a fresh y
+        inputs, params = self._inputs(x, r, i, dev), self._params(dev, 1 if y is None else 0)
         states = self.state_shape(N)
         sp = _dense(state, "state", states, torch.float32, dev) if state is not None else None
         cp = _dense(carries, "carries", self.carries_shape(tokens), torch.float32, dev) if carries is not None else None
-        fresh = y is None
         y, yp = self._y(y, x, dev)
         state_out, fp = self._out(state_out, "state_out", states, torch.float32, dev)
         need = self.lib.hyena_recurrence_workspace_bytes(params, N, tokens, starts)
         workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
-        if fresh and starts is not None:
-            self._clear(N, tokens, starts, dev, y)
         _launch(torch, "hyena_recurrence_forward", self.lib.hyena_recurrence_forward, dev, params, N, tokens, starts, inputs,
                 sp, yp, fp, cp, ws, ws_bytes)
         return y, state_out
@@ -1176,7 +1174,7 @@ class GatedRecurrence:
         same inputs filled, or None. Rows that belong to no sequence have gradients of zero."""
         torch = self._torch
         dev, N, tokens, starts = self._sequences(x, seq_start)
-        inputs, params = self._inputs(x, r, i, dev), self._params(dev)
+        inputs, params = self._inputs(x, r, i, dev), self._params(dev, 1)
         states = self.state_shape(N)
         dyp = _dense(dy, "dy", x.shape, self.io_dtype, dev)
         sp, dsp = (_dense(t, name, states, torch.float32, dev) if t is not None else None
@@ -1186,8 +1184,6 @@ class GatedRecurrence:
         out += [torch.empty(shape, dtype=torch.float32, device=dev) for shape in ((self.dim,), states)]
         need = self.lib.hyena_recurrence_backward_workspace_bytes(params, N, tokens, starts, cp)
         workspace, ws, ws_bytes = _workspace(torch, workspace, need, dev)
-        if starts is not None:
-            self._clear(N, tokens, starts, dev, *out[:3])
         _launch(torch, "hyena_recurrence_backward", self.lib.hyena_recurrence_backward, dev, params, N, tokens, starts, inputs,
                 sp, cp, dyp, dsp, *(t.data_ptr() for t in out), ws, ws_bytes)
         return tuple(out)

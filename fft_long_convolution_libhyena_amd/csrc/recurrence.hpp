@@ -318,8 +318,12 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
 // 64-bit values at the head of a workspace that start() clears: the tickets of up to two launches, then the words
 constexpr int kHead = 2;
 inline int64_t word_count(const Call& c, int64_t chunks) { return chunks > 1 ? chunks * c.p.dim : 0; }
-// Clears `n` values of 64 bits and passes the states of sequences without tokens on; no launch without either.
-hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, hipStream_t st);
+// Clears `n` values of 64 bits, passes the states of sequences without tokens on and clears the rows of no sequence
+// in `outs` (each may be null); no launch where there is nothing of it to do.
+struct Outs {
+    void* p[3];
+};
+hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, Outs outs, hipStream_t st);
 // y, state_out and carry may each be null
 hipError_t forward(const Call& c, const float* state_in, void* y, float* state_out, float* carry, uint32_t* ticket,
                    Word* words, hipStream_t st);

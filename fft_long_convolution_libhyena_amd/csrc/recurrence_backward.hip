@@ -328,7 +328,7 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
     if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return HYENA_ERR_WORKSPACE;
     if (l.bytes && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     const int dim = (int)params->dim;
-    hipError_t e = rec::start(c, l.head, l.clear, dstate_out, dstate_in, stream);
+    hipError_t e = rec::start(c, l.head, l.clear, dstate_out, dstate_in, {{dx, dr, di}}, stream);
     if (e == hipSuccess && tokens > 0) {
         rec::Word* const words = l.head + rec::kHead;
         uint32_t* const tickets = (uint32_t*)l.head;

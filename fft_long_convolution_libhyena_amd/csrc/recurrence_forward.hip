@@ -145,13 +145,13 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     }
 }
 
-// Clears what the chunks' words and tickets lie in (n words, 16 bytes a thread and round); a sequence without
-// tokens passes its state on.
-__global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs q, const float* from, float* to, int dim) {
+// Clears what the chunks' words and tickets lie in (n words, 16 bytes a thread and round), and rows of no sequence;
+// a sequence without tokens passes its state on.
+__global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs q, const float* from, float* to, int dim, Outs outs,
+                                                   int row_bytes) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; 2 * e < n; e += step)
-        __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(clear) + e);
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t e = first; 2 * e < n; e += step) __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(clear) + e);
     if (to)
         for (int s = blockIdx.x; s < q.N; s += gridDim.x) {
             if (q.at(s + 1) > q.at(s)) continue;
@@ -160,17 +160,28 @@ __global__ __launch_bounds__(256) void k_rec_start(Word* clear, int64_t n, Seqs 
                 to[e] = from ? from[e] : 0.f;
             }
         }
+    if (row_bytes) {  // a multiple of 16
+        const int64_t lo = q.at(0), end = q.at(q.N), hi = end > lo ? end : lo, per = row_bytes / 16;
+        for (int k = 0; k < 3; ++k) {
+            u32x4* const p = reinterpret_cast<u32x4*>(outs.p[k]);
+            if (!p) continue;
+            for (int64_t e = first; e < lo * per; e += step) p[e] = u32x4{};
+            for (int64_t e = hi * per + first; e < q.tokens * per; e += step) p[e] = u32x4{};
+        }
+    }
 }
 
 }  // namespace
 
-hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, hipStream_t st) {
+hipError_t start(const Call& c, void* clear, int64_t n, const float* from, float* to, Outs outs, hipStream_t st) {
     if (!(c.seqs.start || c.seqs.T == 0)) to = nullptr;  // every sequence has tokens
-    if (!n && !to) return hipSuccess;
+    const bool rows = c.p.clear && c.seqs.start && c.seqs.tokens > 0;
+    if (!n && !to && !rows) return hipSuccess;
     int64_t wgs = (n + 511) / 512;  // n is even
     wgs = to && wgs < c.seqs.N ? c.seqs.N : wgs;
+    wgs = rows && wgs < 256 ? 256 : wgs;
     hipLaunchKernelGGL(k_rec_start, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, st, (Word*)clear, n, c.seqs, from, to,
-                       (int)c.p.dim);
+                       (int)c.p.dim, outs, rows ? (int)c.p.dim * (c.bf ? 2 : 4) : 0);
     return hipGetLastError();
 }
 
@@ -240,7 +251,7 @@ hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params,
     if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     rec::Word* head = (rec::Word*)workspace;
-    hipError_t e = rec::start(c, head, (int64_t)(need / sizeof(rec::Word)), state_in, state_out, stream);
+    hipError_t e = rec::start(c, head, (int64_t)(need / sizeof(rec::Word)), state_in, state_out, {{y}}, stream);
     if (e == hipSuccess && tokens > 0)
         e = rec::forward(c, state_in, y, state_out, carries, (uint32_t*)head, head + rec::kHead, stream);
     return e == hipSuccess ? HYENA_OK : HYENA_ERR_DEVICE;

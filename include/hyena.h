@@ -842,13 +842,15 @@ hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params,
  * The calls take no plan: they run on the current device, which must be the one
  * that holds the buffers. Tokens lie behind each other as for the gated delta rule: N
  * sequences of tokens / N each (seq_start NULL), or packed with N + 1 offsets in device
- * memory under the same rules. Rows that belong to no sequence are neither read nor written.
+ * memory under the same rules. Rows that belong to no sequence are not read, and of outputs they are
+ * left as they were or, where `clear` asks for it, set to 0.
  * ------------------------------------------------------------------------ */
 #define HYENA_RECURRENCE_CARRY 80 /* tokens between the states that the forward keeps for its backward */
 
 typedef struct hyena_recurrence_params_s {
     int64_t dim;         /* channels: a multiple of 8, at most 2^20 */
     hyena_dtype_t dtype; /* of x, r, i, y and their gradients */
+    int clear;           /* not 0: rows of y, dx, dr and di that belong to no sequence become 0 */
     const float* rate;   /* [dim] fp32, device: c, a normal number above 0 */
 } hyena_recurrence_params_t;
 

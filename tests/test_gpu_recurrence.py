@@ -244,6 +244,37 @@ def test_rows_of_no_sequence(dtype):
     assert torch.equal(given[front:-back], y[front:-back])
 
 
+@pytest.mark.parametrize("clear", [0, 1])
+@pytest.mark.parametrize("tokens,start", [(300, [7, 7, 200]), (300, [300, 300, 300]), (300, [0, 100, 300]), (1, [0, 0, 0])])
+def test_rows_of_no_sequence_are_left_or_cleared(tokens, start, clear):
+    """Every output of rows, through the C calls, without state gradients and with the workspace's words or without."""
+    import ctypes
+
+    from fft_long_convolution_libhyena_amd.binding import RecurrenceInputsStruct
+
+    dim = 24
+    d = R.make([tokens], dim, "bf16", seed=14)
+    m = rule(d, dim, "bf16")
+    x, r, i, dy = R.gpu(d, "x", "r", "i", "dy")
+    at = torch.tensor(start, device="cuda")
+    p = m._params(None, clear)
+    need = m.lib.hyena_recurrence_backward_workspace_bytes(p, 2, tokens, at.data_ptr(), None)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    y, dx, dr, di = (torch.full_like(x, 7.0) for _ in range(4))
+    drate = torch.empty(dim, device="cuda")
+    ins = ctypes.byref(RecurrenceInputsStruct(x.data_ptr(), dim, r.data_ptr(), dim, i.data_ptr(), dim))
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert m.lib.hyena_recurrence_forward(p, 2, tokens, at.data_ptr(), ins, None, y.data_ptr(), None, None, ws.data_ptr(),
+                                          need, st) == 0
+    assert m.lib.hyena_recurrence_backward(p, 2, tokens, at.data_ptr(), ins, None, None, dy.data_ptr(), None, dx.data_ptr(),
+                                           dr.data_ptr(), di.data_ptr(), drate.data_ptr(), None, ws.data_ptr(), need, st) == 0
+    want = m.forward(x, r, i, seq_start=at)[0], *m.backward(x, r, i, dy, seq_start=at)[:3]
+    for t, w in zip((y, dx, dr, di), want):
+        assert torch.equal(t[start[0]:start[-1]], w[start[0]:start[-1]])
+        for rest in (t[:start[0]], t[start[-1]:]):
+            assert bool((rest == (0 if clear else 7)).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_states_in_place(dtype):
     """state_out may be the initial states: sequences within a wave, a chunk and over many, and empty ones."""

@@ -17,7 +17,7 @@ def lib():
 
 
 def params(**kw):
-    d = dict(dim=256, dtype=1, rate=P)
+    d = dict(dim=256, dtype=1, clear=0, rate=P)
     d.update(kw)
     return RecurrenceParamsStruct(*(d[n] for n, _ in RecurrenceParamsStruct._fields_))
 
