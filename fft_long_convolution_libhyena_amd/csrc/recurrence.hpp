@@ -9,7 +9,7 @@
 // begins a sequence takes its initial state in and lets nothing of what lies in front through
 // (not as a factor 0: an infinity there must not become NaN here).
 //
-// A workgroup has one chunk and 128 channels: a wave 20 (backward: 10) tokens, a lane two channels. All
+// A workgroup has one chunk and 128 channels: a wave 20 (backward: 10, short forward: 8) tokens, a lane two channels. All
 // tokens of a lane are loaded at once and stay in registers from the first pass (which gives
 // the wave's A and H) to the second (which gives the outputs).
 #pragma once
@@ -29,8 +29,13 @@ constexpr int kCols = 64 * kVec;         // channels a workgroup
 // tokens a wave: 134, 112, 107, 104, 102 and 103 us; with 32 in waves at two or three a SIMD 114 and 125. Training step
 // of 8 x 8192 with 6, 8 and 10 in the backward: 334, 297 and 285 us (8 without LDS the same, 10 without it spills: 375).
 constexpr int kForwardSpan = 20, kBackwardSpan = 10;
+// Tokens of a wave in a forward whose chunks then take no more workgroups than there are CUs: less to load and
+// to work through before the states pass on, while there are few chunks to pass through. 64, 512 and 2048 tokens
+// of 768 channels with 8 and 20: 5.4 and 7.2, 9.8 and 13.5, 12.8 and 14.7 us; 4096 tokens: 18.9 and 17.6.
+constexpr int kShortSpan = 8;
+constexpr int kShortGrid = 256;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kForwardChunk = kWaves * kForwardSpan, kBackwardChunk = kWaves * kBackwardSpan;
+constexpr int kBackwardChunk = kWaves * kBackwardSpan;
 static_assert(kBackwardChunk == HYENA_RECURRENCE_CARRY, "states kept for the backward");
 static_assert(kForwardSpan <= 32 && kForwardSpan <= kBackwardChunk, "bits of a span; one kept state at most in it");
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 256;
@@ -310,6 +315,7 @@ struct Call {
     hyena_recurrence_inputs_t in;
     Seqs seqs;
     bool bf;
+    int span;                             // tokens of a wave in the forward
     int64_t chunks, back_chunks, blocks;  // chunks of tokens (forward, backward), blocks of channels
 };
 

@@ -19,13 +19,13 @@ struct ForwardArgs {
     int dim, chunks, blocks;
 };
 
-// One chunk and 128 channels. 1 x 65536 x 768 in bf16 take 102 us: 425 MB, words and kept states among them, at 4.2
-// TB/s; vector work fills half of the cycles. Without the look-back it would be 78: words are read past the caches,
+// One chunk and 128 channels, S tokens a wave. 1 x 65536 x 768 in bf16 take 97 us, the start among them: 425 MB with words
+// and kept states, at 4.6 TB/s; vector work fills half of the cycles. Without the look-back it would be 78: words are read past the caches,
 // and chunks wait for others that started at about the same time.
-template <bool BF>
+template <bool BF, int S>
 __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;
-    constexpr int S = kForwardSpan, W = kWaves;
+    constexpr int W = kWaves;
     __shared__ Link sOwn[W][64], sBack[W][64];
     __shared__ int sOwnReset[W], sBackReset[W];
     __shared__ uint32_t sTicket;
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     const int own = (ticket - chunk * p.blocks) * kCols + kVec * lane;
     const bool ok = own < p.dim;
     const int col = ok ? own : p.dim - kVec, at = ok ? own * Io<BF>::kBytes : kNone;
-    const Span<S> span(p.seqs, chunk * kForwardChunk + wave * S);
+    const Span<S> span(p.seqs, chunk * (W * S) + wave * S);
     const int rows = p.seqs.tokens - span.t0 < S ? p.seqs.tokens - span.t0 : S;
     float a[S][kVec], b[S][kVec];
     float A[kVec] = {1.f, 1.f}, H[kVec] = {};
@@ -190,10 +190,9 @@ hipError_t forward(const Call& c, const float* state_in, void* y, float* state_o
     ForwardArgs a{c.seqs, c.in,   c.p.rate, state_in, y, state_out, carry, ticket, c.chunks > 1 ? words : nullptr,
                   (int)c.p.dim, (int)c.chunks, (int)c.blocks};
     const dim3 grid((unsigned)(c.chunks * c.blocks));
-    if (c.bf)
-        hipLaunchKernelGGL(k_rec_forward<true>, grid, dim3(kThreads), 0, st, a);
-    else
-        hipLaunchKernelGGL(k_rec_forward<false>, grid, dim3(kThreads), 0, st, a);
+    auto* const kernel = c.span == kShortSpan ? (c.bf ? k_rec_forward<true, kShortSpan> : k_rec_forward<false, kShortSpan>)
+                                              : (c.bf ? k_rec_forward<true, kForwardSpan> : k_rec_forward<false, kForwardSpan>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -207,9 +206,11 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
         return HYENA_ERR_UNSUPPORTED;
     c.p = *p;
     c.bf = p->dtype == HYENA_BF16;
-    c.chunks = (tokens + kForwardChunk - 1) / kForwardChunk;
-    c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
     c.blocks = (p->dim + kCols - 1) / kCols;
+    auto chunks = [&](int span) { return (tokens + kWaves * span - 1) / (kWaves * span); };
+    c.span = chunks(kShortSpan) * c.blocks <= kShortGrid ? kShortSpan : kForwardSpan;
+    c.chunks = chunks(c.span);
+    c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
     if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
     c.seqs = Seqs{seq_start, (int)N, (int)tokens, (int)(tokens / N)};
     if (!in) return HYENA_OK;

@@ -882,7 +882,7 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  *   workspace at least hyena_recurrence_workspace_bytes(...) bytes, 16-byte aligned
  * All arithmetic is fp32 and y is rounded once. A value that is not finite spoils its channel of its
  * sequence from its token on and nothing else. Every sum has a fixed order: results are bitwise
- * reproducible; where a sequence lies among the rows may change their rounding. Outputs must not alias
+ * reproducible; where a sequence lies among the rows, and how many there are, may change their rounding. Outputs must not alias
  * inputs, but for state_out. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
  * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 256, or 2^23 or

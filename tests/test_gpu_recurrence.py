@@ -62,6 +62,17 @@ def test_packed(lens, dim, dtype):
                 assert R.rel(g, w) <= (bwd(lens, dtype) if k < 3 else 2 * f32(lens)), (use, k)
 
 
+def over_one_grid(tokens):
+    """Columns with which the forward's chunks of 64 tokens would take more than 256 workgroups: then they have 160."""
+    return 128 * (256 // ((tokens + 63) // 64)) + 8
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", LENS + [[159], [160], [161], [19, 1, 140, 20, 0, 21], [320, 1]], ids=str)
+def test_packed_of_many_columns(lens, dtype):
+    test_packed(lens, over_one_grid(sum(lens)), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,T,dim", [(1, 1, 768), (3, 5, 136), (2, 333, 96), (5, 128, 128), (4, 16, 264), (1, 520, 1000)])
 def test_batched(N, T, dim, dtype):
@@ -79,10 +90,10 @@ def test_batched(N, T, dim, dtype):
     assert torch.equal(packed[0], y.flatten(0, 1)) and torch.equal(packed[1], s)
 
 
+@pytest.mark.parametrize("dim", [16, 264])
 @pytest.mark.parametrize("lens", [[9001], [4096, 100, 5000]], ids=str)
-def test_many_chunks(lens):
+def test_many_chunks(lens, dim):
     """Long enough that states pass through groups of chunks; slow decays carry them all the way."""
-    dim = 16
     d = R.make(lens, dim, "f32", seed=3, slow=1e-5, fast=1e-2)
     m = rule(d, dim, "f32")
     x = R.gpu(d, "x", "r", "i")
@@ -184,9 +195,10 @@ def test_gradients_against_differences():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("name", ["x", "r", "i", "state"])
-def test_where_a_value_that_is_not_finite_shows(name, bad, dtype):
+@pytest.mark.parametrize("dim", [16, over_one_grid(370)])
+def test_where_a_value_that_is_not_finite_shows(name, bad, dtype, dim):
     """In its channel of its sequence from its token on; everything else keeps its bits."""
-    lens, dim = [150, 0, 20, 200], 16
+    lens = [150, 0, 20, 200]
     d = R.make(lens, dim, dtype, seed=7)
     m = rule(d, dim, dtype)
 
@@ -214,11 +226,12 @@ def test_where_a_value_that_is_not_finite_shows(name, bad, dtype):
     assert bool(torch.isfinite(got[3][[c for c in range(dim) if c != 5]]).all()) and bool(torch.isfinite(got[4][kept]).all())
 
 
+@pytest.mark.parametrize("dim", [40, over_one_grid(368)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_rows_of_no_sequence(dtype):
+def test_rows_of_no_sequence(dtype, dim):
     """A padded packed batch: the rows around the sequences hold NaN, have no results and no gradients,
     and given outputs keep what they hold there."""
-    lens, front, back, dim = [70, 0, 33], 5, 260, 40
+    lens, front, back = [70, 0, 33], 5, 260
     d = R.make(lens, dim, dtype, seed=8)
     m = rule(d, dim, dtype)
     x = []
@@ -275,12 +288,13 @@ def test_rows_of_no_sequence_are_left_or_cleared(tokens, start, clear):
             assert bool((rest == (0 if clear else 7)).all())
 
 
+@pytest.mark.parametrize("dim", [72, 520])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_states_in_place(dtype):
+def test_states_in_place(dtype, dim):
     """state_out may be the initial states: sequences within a wave, a chunk and over many, and empty ones."""
     lens = [3, 0, 500, 1, 4000, 40, 0, 700]
-    d = R.make(lens, 72, dtype, seed=13)
-    m = rule(d, 72, dtype)
+    d = R.make(lens, dim, dtype, seed=13)
+    m = rule(d, dim, dtype)
     x, start = R.gpu(d, "x", "r", "i"), R.starts(lens)
     y, s = m.forward(*x, state=d["state"].cuda(), seq_start=start)
     for _ in range(3):
@@ -338,9 +352,10 @@ def test_no_tokens():
     assert not bool(packed[1].any())
 
 
-def test_offsets_that_break_the_rules_stay_inside():
+@pytest.mark.parametrize("dim", [16, over_one_grid(300)])
+def test_offsets_that_break_the_rules_stay_inside(dim):
     """Offsets below 0, beyond the rows or decreasing: any result, but nothing outside the arrays."""
-    dim, tokens, N = 16, 300, 4
+    tokens, N = 300, 4
     d = R.make([tokens], dim, "f32", seed=2)
     m = rule(d, dim, "f32")
     room = torch.full((3, tokens + 20, dim), 7.0, device="cuda")
