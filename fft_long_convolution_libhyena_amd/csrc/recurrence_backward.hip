@@ -33,8 +33,8 @@ struct BackwardArgs {
     int dim, chunks, blocks;
 };
 
-// One chunk and 128 channels, the chunks from the last to the first. 8 x 8192 x 768 in bf16 take 172 to 183 us: 753 MB
-// at 4.2 TB/s, vector work 63% of the cycles (an instruction an element is worth 1.1 us).
+// One chunk and 128 channels, the chunks from the last to the first. 8 x 8192 x 768 in bf16 take 172 to 177 us: 752 MB
+// at 4.3 TB/s, vector work 65% of the cycles (without the last pass's polynomial, with 1 - a kept in place of a: 1 us less).
 template <bool BF>
 __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardArgs p) {
     using Raw = typename Io<BF>::Raw;
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         ticket = __builtin_amdgcn_readfirstlane(sTicket);
     }
     const int order = (uint32_t)ticket / (uint32_t)p.blocks, chunk = p.chunks - 1 - order;
-    if (chunk < 0) return;  // only where a caller's workspace is not this call's alone
+    if ((uint32_t)order >= (uint32_t)p.chunks) return;  // only where a caller's workspace is not this call's alone
     const int own = (ticket - order * p.blocks) * kCols + kVec * lane;
     const bool ok = own < p.dim;
     const int col = ok ? own : p.dim - kVec, at = ok ? own * Io<BF>::kBytes : kNone;

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
         ticket = __builtin_amdgcn_readfirstlane(sTicket);
     }
     const int chunk = (uint32_t)ticket / (uint32_t)p.blocks;
-    if (chunk >= p.chunks) return;  // only where a caller's workspace is not this call's alone
+    if ((uint32_t)chunk >= (uint32_t)p.chunks) return;  // only where a caller's workspace is not this call's alone
     const int own = (ticket - chunk * p.blocks) * kCols + kVec * lane;
     const bool ok = own < p.dim;
     const int col = ok ? own : p.dim - kVec, at = ok ? own * Io<BF>::kBytes : kNone;

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kStepThreads) void k_rec_step(StepArgs p) {
                 take<BF>(p.in.x, tok * p.in.ldx + col, x);
                 take<BF>(p.in.r, tok * p.in.ldr + col, r);
                 take<BF>(p.in.i, tok * p.in.ldi + col, i);
-float w[kVec], a[kVec], q[kVec];
+                float w[kVec], a[kVec], q[kVec];
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) w[j] = rate[j] * sigmoid(r[j]);
                 decay(w, false, a, q);

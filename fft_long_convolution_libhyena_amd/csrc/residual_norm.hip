@@ -310,9 +310,9 @@ int64_t rms_forward_wgs(int64_t rows, int64_t dim) {
 }
 
 // Workgroups of the backward, each with partial sums of dw. Two a CU read the longest runs that still
-// hide the latency; rows of one piece need more (us, 256, 512 and 1024 of them: 65536 x 768 of bf16 103, 78, 86,
-// with the residual in fp32 146, 153, 163; 16384 x 2048 119, 101, 110; 65536 x 128 55, 32, 25). Sending for
-// the next row early gains nothing on top (512: 84 and 158).
+// hide the latency; rows of one piece need more (us, 256, 384, 512 and 768 of them: 65536 x 768 of bf16 100, 77, 70, 74,
+// with the residual in fp32 135, 151, 140, 151; 16384 x 2048 118, 94, 93, 96; 65536 x 128 with 256, 512 and 1024 55,
+// 32, 25). Sending for the next row early gains nothing on top.
 int64_t rms_back_wgs(int64_t rows, int64_t dim) {
     const int64_t n = (rows + rms_rows(dim) - 1) / rms_rows(dim), most = dim <= 256 ? 1024 : 512;
     return n < most ? n : most;
