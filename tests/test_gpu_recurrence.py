@@ -467,3 +467,71 @@ def test_capture_replays_and_streams():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_widest_rows_and_many_sequences():
+    """2^20 channels; 70000 sequences of no token, one or two, packed and in a batch."""
+    d = R.make([3, 0, 2], 1 << 20, "bf16", seed=15)
+    m = rule(d, 1 << 20, "bf16")
+    y, s = m.forward(*R.gpu(d, "x", "r", "i"), state=d["state"].cuda(), seq_start=R.starts(d["lens"]))
+    y0, s0 = R.forward(d)
+    assert R.rel(y, y0) <= fwd([3], "bf16") and R.rel(s, s0) <= f32([3])
+    got = m.backward(*R.gpu(d, "x", "r", "i", "dy"), state=d["state"].cuda(), dstate_out=d["dstate"].cuda(), seq_start=R.starts(d["lens"]))
+    for k, (g, w) in enumerate(zip(got, R.backward(d))):
+        assert R.rel(g, w) <= (bwd([3], "bf16") if k < 3 else 2 * f32([3])), k
+
+    N, dim = 70000, 8
+    d = R.make([1] * N, dim, "f32", seed=16)
+    m = rule(d, dim, "f32")
+    x, dy, state = R.gpu(d, "x", "r", "i"), d["dy"].cuda(), d["state"].cuda()
+    lens = torch.randint(0, 3, (N,), generator=torch.Generator().manual_seed(16))
+    lens = lens[lens.cumsum(0) <= N]
+    start = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    # every sequence in 64 bits at once: its first token, then its second
+    x64, r64, i64 = (d[k].double() for k in ("x", "r", "i"))
+    la = -d["rate"].double() * torch.sigmoid(r64)
+    a, b = la.exp(), (-torch.expm1(2 * la)).sqrt() * torch.sigmoid(i64) * x64
+    h = d["state"][:len(lens)].double()
+    y0 = torch.zeros(N, dim, dtype=torch.float64)
+    for t in range(2):
+        some = lens > t
+        at = start[:-1][some] + t
+        h[some] = a[at] * h[some] + b[at]
+        y0[at] = h[some]
+    y, s = m.forward(*x, state=state[:len(lens)], seq_start=start.cuda())
+    assert R.rel(y, y0) <= f32([2]) and R.rel(s, h) <= f32([2])
+    grads = m.backward(*x, dy, state=state[:len(lens)], seq_start=start.cuda())
+    dx = d["dy"].double().clone()  # of a sequence's last token dh = dy, of the one in front dy + a dh
+    before = (start[1:] - 2)[lens > 1]
+    dx[before] += a[before + 1] * d["dy"][before + 1].double()
+    dx[int(start[-1]):] = 0
+    assert R.rel(grads[0], dx * (-torch.expm1(2 * la)).sqrt() * torch.sigmoid(i64)) <= 2 * f32([2])
+    y, s = m.forward(*(v[:, None] for v in x), state=state)
+    want = a * d["state"].double() + b
+    assert R.rel(y[:, 0], want) <= f32([1]) and R.rel(s, want) <= f32([1])
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls of different sizes with one workspace, replayed in turn and between eager calls with it."""
+    d = [R.make([n], 136, "bf16", seed=n) for n in (3000, 700)]
+    m = [rule(v, 136, "bf16") for v in d]
+    x = [[v[k].cuda()[None] for k in ("x", "r", "i", "dy")] for v in d]
+    ws = torch.empty(max(m[0].backward_workspace_bytes(1, 3000), m[0].workspace_bytes(1, 3000)), dtype=torch.uint8, device="cuda")
+
+    def step(k):
+        return m[k].forward(*x[k][:3], workspace=ws) + m[k].backward(*x[k], workspace=ws)
+
+    want, graphs, outs = [step(k) for k in range(2)], [], []
+    torch.cuda.synchronize()
+    for k in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[k]):
+            outs.append(step(k))
+    for k in (0, 1, 1, 0, 0, 1):
+        for t in outs[k]:
+            t.zero_()
+        graphs[k].replay()
+        eager = step(1 - k)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k])), k
+        assert all(torch.equal(a, b) for a, b in zip(eager, want[1 - k])), k
