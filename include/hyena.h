@@ -842,7 +842,7 @@ hyena_status_t hyena_qk_norm_axes_backward(const hyena_qk_norm_params_t* params,
  * The calls take no plan: they run on the current device, which must be the one
  * that holds the buffers. Tokens lie behind each other as for the gated delta rule: N
  * sequences of tokens / N each (seq_start NULL), or packed with N + 1 offsets in device
- * memory under the same rules. Rows that belong to no sequence are not read, and of outputs they are
+ * memory under the same rules. Rows that belong to no sequence are not read; in outputs they are
  * left as they were or, where `clear` asks for it, set to 0.
  * ------------------------------------------------------------------------ */
 #define HYENA_RECURRENCE_CARRY 80 /* tokens between the states that the forward keeps for its backward */
@@ -882,8 +882,9 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  *   workspace at least hyena_recurrence_workspace_bytes(...) bytes, 16-byte aligned
  * All arithmetic is fp32 and y is rounded once. A value that is not finite spoils its channel of its
  * sequence from its token on and nothing else. Every sum has a fixed order: results are bitwise
- * reproducible; where a sequence lies among the rows, and how many there are, may change their rounding. Outputs must not alias
- * inputs, but for state_out. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned
+ * reproducible; where a sequence lies among the rows, and how many there are, may change their
+ * rounding. Outputs must not alias inputs, but for state_out. Enqueued on `stream`. Errors:
+ * HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
  * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 256, or 2^23 or
  * more pairs of 80 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
@@ -919,8 +920,8 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
  * [B] int32 or NULL, both exactly as for hyena_delta_step: rows that name the same slot are
  * successive tokens of it, a slot outside [0, num_states) gives zeros. Enqueued on `stream`; no
  * workspace. Errors as hyena_recurrence_forward, of N = B and tokens = B*T (HYENA_ERR_UNSUPPORTED where
- * 2^24 pairs of a row and 512 channels are reached), and HYENA_ERR_INVALID_ARG for B, T or num_states below 1 and for NULL slots with
- * num_states < B. */
+ * 2^24 pairs of a row and 512 channels are reached), and HYENA_ERR_INVALID_ARG for B, T or num_states
+ * below 1 and for NULL slots with num_states < B. */
 hyena_status_t hyena_recurrence_step(const hyena_recurrence_params_t* params, int64_t B, int64_t T,
                                      const hyena_recurrence_inputs_t* in, float* states, int64_t num_states,
                                      const int32_t* slots, void* y, hipStream_t stream);
@@ -948,8 +949,9 @@ typedef struct hyena_residual_norm_params_s {
  * residual likewise, or NULL (s = x); y [rows][dim], dense: of the dtype, or where scales is not NULL in 8
  * bits, with scales [rows][1 or ceil(dim / 128)] fp32; sum [rows][dim], dense: s, or NULL. Runs on
  * the current device, no plan. y, scales and sum must not alias the inputs, but sum may be the
- * residual itself where that is dense. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or misaligned pointers, bad sizes,
- * ld, eps, block or types), HYENA_ERR_UNSUPPORTED (dim outside the range above, a bf16 residual of fp32
+ * residual itself where that is dense. Enqueued on `stream`. Errors: HYENA_ERR_INVALID_ARG (NULL or
+ * misaligned pointers, bad sizes, ld, eps, block or types), HYENA_ERR_UNSUPPORTED (dim outside the
+ * range above, a bf16 residual of fp32
  * rows, rows > 2^31), HYENA_ERR_DEVICE. */
 hyena_status_t hyena_residual_norm_forward(const hyena_residual_norm_params_t* params, int64_t rows, const void* x,
                                            int64_t ldx, const void* residual, int64_t ldr, void* y, float* scales,
@@ -962,7 +964,8 @@ size_t hyena_residual_norm_backward_workspace_bytes(const hyena_residual_norm_pa
 /* Backward: for the stored sums s [rows][dim] (with lds elements between rows, as ldx) and the gradients dy (of the
  * dtype, dense) of y and dsum (of the residual's type, dense; NULL: zeros) of s, the gradient of x and of the
  * residual, which is one and the same, rounded to either type: dx [rows][dim] of the dtype and
- * dresidual of the residual's, dense (outputs; NULL where not wanted, not all three), and dw [dim] fp32 (output, or
+ * dresidual of the residual's, dense (outputs; NULL where not wanted, not all three), and dw [dim]
+ * fp32 (output, or
  * NULL), a complete sum in a fixed order. An output in 8 bits has the gradients of the values before
  * they were rounded. workspace: as above, 16-byte aligned; ignored without dw. Errors as the forward's, and
  * HYENA_ERR_WORKSPACE. Outputs must not alias inputs, but dresidual may be dsum. */
