@@ -102,6 +102,14 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], float* lds) {
     }
 }
 
+// a / b, from r = 1 / b rounded to nearest: the quotient's error is found exactly and taken off, so what lies
+// halfway between two 8-bit values is met as in a division, at 4 operations in place of some 10 (16384 x 2048
+// to 8 bits 64.7 us, with the product alone 64.5; 8192 x 8192 96.1 and 94.7)
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+    const float q = a * r;
+    return copysignf(fmaf(fmaf(-q, b, a), r, q), a);
+}
+
 // XB, SB: x and y, the residual and the sum are bf16 (otherwise fp32); Q: output in 8 bits
 template <bool XB, bool SB, bool Q, bool ST, int R, int K>
 __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) {
@@ -185,8 +193,11 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void k_residual_norm(RmsArgs p) 
                 const float scale = most[k] > 0.f ? fmaxf(most[k] / kE4m3Most, 1.17549435e-38f) : 1.f;
                 const float by = 1.f / scale;
                 if (in && ok[k]) {
-                    int q = __builtin_amdgcn_cvt_pk_fp8_f32(s[k][0] * by, s[k][1] * by, 0, false);
-                    q = __builtin_amdgcn_cvt_pk_fp8_f32(s[k][2] * by, s[k][3] * by, q, true);
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = quotient(s[k][i], scale, by);
+                    int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+                    q = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], q, true);
                     store_once<ST>(q, (int*)((char*)p.y + row * p.dim + col[k]));
                     if (p.block ? (t & 31) == 0 : k == 0 && t == 0)
                         p.scales[row * p.nscales + (p.block ? col[k] / 128 : 0)] = scale;
