@@ -324,6 +324,13 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
 // 64-bit values at the head of a workspace that start() clears: the tickets of up to two launches, then the words
 constexpr int kHead = 2;
 inline int64_t word_count(const Call& c, int64_t chunks) { return chunks > 1 ? chunks * c.p.dim : 0; }
+// Words of the forward that cover this call and every one of fewer tokens or channels: a short span's chunks are
+// many, but take at most kShortGrid workgroups
+inline int64_t covering_words(const Call& c) {
+    const int64_t own = word_count(c, c.chunks), brief = word_count(c, (c.seqs.tokens + kWaves * kShortSpan - 1) / (kWaves * kShortSpan));
+    const int64_t most = brief < kShortGrid * kCols ? brief : kShortGrid * kCols;
+    return own > most ? own : most;
+}
 // Clears `n` values of 64 bits, passes the states of sequences without tokens on and clears the rows of no sequence
 // in `outs` (each may be null); no launch where there is nothing of it to do.
 struct Outs {

@@ -282,8 +282,9 @@ struct Layout {
     float *part, *carry;
     size_t bytes;
 };
-Layout layout(const Call& c, bool carries, void* base) {
-    const int64_t n = word_count(c, c.back_chunks) + (carries ? 0 : word_count(c, c.chunks)), kept = c.back_chunks * c.p.dim;
+// forward_words: of the forward that makes the states again
+Layout layout(const Call& c, bool carries, int64_t forward_words, void* base) {
+    const int64_t n = word_count(c, c.back_chunks) + (carries ? 0 : forward_words), kept = c.back_chunks * c.p.dim;
     Layout l;
     l.head = (Word*)base;
     l.clear = n ? kHead + n : 0;
@@ -303,7 +304,7 @@ size_t hyena_recurrence_backward_workspace_bytes(const hyena_recurrence_params_t
                                                  const int64_t* seq_start, const float* carries) {
     hy::rec::Call c;
     if (hy::rec::check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
-    return hy::rec::layout(c, carries != nullptr, nullptr).bytes;
+    return hy::rec::layout(c, carries != nullptr, hy::rec::covering_words(c), nullptr).bytes;
 }
 
 hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
@@ -324,7 +325,7 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
     for (const void* q : states)
         if (!aligned16(q)) return HYENA_ERR_INVALID_ARG;
     if (!drate || ((uintptr_t)drate & 3u)) return HYENA_ERR_INVALID_ARG;
-    const rec::Layout l = rec::layout(c, carries != nullptr, workspace);
+    const rec::Layout l = rec::layout(c, carries != nullptr, rec::word_count(c, c.chunks), workspace);
     if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return HYENA_ERR_WORKSPACE;
     if (l.bytes && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     const int dim = (int)params->dim;

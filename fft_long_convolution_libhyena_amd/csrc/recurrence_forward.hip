@@ -229,12 +229,13 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
 
 extern "C" {
 
+static size_t words_bytes(int64_t n) { return n ? (size_t)(hy::rec::kHead + n) * sizeof(hy::rec::Word) : 0; }
+
 size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                         const int64_t* seq_start) {
     hy::rec::Call c;
     if (hy::rec::check(params, N, tokens, seq_start, nullptr, c) != HYENA_OK) return 0;
-    const int64_t n = hy::rec::word_count(c, c.chunks);
-    return n ? (size_t)(hy::rec::kHead + n) * sizeof(hy::rec::Word) : 0;
+    return words_bytes(hy::rec::covering_words(c));
 }
 
 hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
@@ -248,7 +249,7 @@ hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params,
     if (st != HYENA_OK) return st;
     if ((tokens > 0 && !y) || !aligned16(y) || !aligned16(state_in) || !aligned16(state_out) || !aligned16(carries))
         return HYENA_ERR_INVALID_ARG;
-    const size_t need = hyena_recurrence_workspace_bytes(params, N, tokens, seq_start);
+    const size_t need = words_bytes(rec::word_count(c, c.chunks));
     if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
     rec::Word* head = (rec::Word*)workspace;

@@ -866,8 +866,9 @@ typedef struct hyena_recurrence_inputs_s {
     int64_t ldi;
 } hyena_recurrence_inputs_t;
 
-/* Bytes of workspace hyena_recurrence_forward needs. Returns 0 for arguments that the call
- * would refuse, and where there are no tokens. seq_start is not read. */
+/* Bytes of workspace that hold for hyena_recurrence_forward and for its calls of fewer tokens or
+ * channels, so that one workspace, sized for the largest call, serves them all. Returns 0 for arguments
+ * that the call would refuse, and where there are no tokens. seq_start is not read. */
 size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                         const int64_t* seq_start);
 
@@ -893,8 +894,9 @@ hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params,
                                         const float* state_in, void* y, float* state_out, float* carries,
                                         void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace hyena_recurrence_backward needs, with carries or (NULL) without; the
- * pointers are not followed. Returns 0 as hyena_recurrence_workspace_bytes. */
+/* Bytes of workspace that hold for hyena_recurrence_backward, with carries or (NULL) without, and for
+ * its calls of fewer tokens or channels; the pointers are not followed. Returns 0 as
+ * hyena_recurrence_workspace_bytes. */
 size_t hyena_recurrence_backward_workspace_bytes(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                                  const int64_t* seq_start, const float* carries);
 
