@@ -314,6 +314,15 @@ NormGrid norm_grid(const hyena_qk_norm_params_t& p, int64_t tokens, bool back) {
     return g;
 }
 
+// No fewer workgroups than the backward of so many tokens or fewer has: with more tokens a group takes more heads, so
+// their number falls now and then.
+int64_t norm_covering_wgs(const hyena_qk_norm_params_t& p, int64_t tokens) {
+    const int64_t heads = p.heads_q + p.heads_k, gw = kNormThreads / group_lanes(p.dim);
+    const int64_t all = (tokens + gw - 1) / gw * heads, most = heads > kNormBackWgs ? heads : kNormBackWgs;
+    return all < most ? all : most;
+}
+size_t norm_part_bytes(int64_t wgs, int64_t dim) { return (size_t)wgs * 2 * (size_t)dim * sizeof(float); }
+
 template <bool BF, int G, bool HALVES, bool BACK>
 void launch_norm_g(const NormArgs& a, const NormGrid& g, hipStream_t st) {
     const dim3 grid(g.x, g.y), block(kNormThreads);
@@ -422,10 +431,10 @@ hyena_status_t norm_backward(const hyena_qk_norm_params_t* params, const int32_t
         if ((tokens > 0 && !p) || !aligned16(p)) return HYENA_ERR_INVALID_ARG;
     if (((uintptr_t)dw_q | (uintptr_t)dw_k) & 3u) return HYENA_ERR_INVALID_ARG;
     const bool sums = dw_q || dw_k;
-    const size_t need = sums ? hyena_qk_norm_backward_workspace_bytes(params, tokens) : 0;
+    const NormGrid g = norm_grid(*params, tokens, true);
+    const size_t need = sums && tokens > 0 ? norm_part_bytes((int64_t)g.x * g.y, params->dim) : 0;
     if (need && (!workspace || workspace_bytes < need)) return HYENA_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return HYENA_ERR_INVALID_ARG;
-    const NormGrid g = norm_grid(*params, tokens, true);
     hipError_t e = hipSuccess;
     if (tokens > 0) {
         a.axis = axis;
@@ -475,8 +484,7 @@ hyena_status_t hyena_qk_norm_axes_forward(const hyena_qk_norm_params_t* params, 
 
 size_t hyena_qk_norm_backward_workspace_bytes(const hyena_qk_norm_params_t* params, int64_t tokens) {
     if (hy::norm_check_params(params, tokens) != HYENA_OK || tokens == 0) return 0;
-    const hy::NormGrid g = hy::norm_grid(*params, tokens, true);
-    return (size_t)g.x * g.y * 2 * (size_t)params->dim * sizeof(float);
+    return hy::norm_part_bytes(hy::norm_covering_wgs(*params, tokens), params->dim);
 }
 
 hyena_status_t hyena_qk_norm_backward(const hyena_qk_norm_params_t* params, int64_t tokens, const void* q, int64_t ldq,

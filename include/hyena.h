@@ -801,9 +801,9 @@ hyena_status_t hyena_qk_norm_forward(const hyena_qk_norm_params_t* params, int64
                                      const void* k, int64_t ldk, const int64_t* positions, void* q_out, void* k_out,
                                      hipStream_t stream);
 
-/* Bytes of workspace hyena_qk_norm_backward needs where it sums weight gradients
- * (partial sums of at most 1024 workgroups, or one a head where there are more).
- * Returns 0 for arguments that the call would refuse and for tokens = 0. */
+/* Bytes of workspace that hold for hyena_qk_norm_backward of so many tokens or fewer where it
+ * sums weight gradients (partial sums of at most 1024 workgroups, or one a head where there
+ * are more). Returns 0 for arguments that the call would refuse and for tokens = 0. */
 size_t hyena_qk_norm_backward_workspace_bytes(const hyena_qk_norm_params_t* params, int64_t tokens);
 
 /* Backward: the gradients dq, dk (dense, outputs) of q and k, and dw_q, dw_k [dim] fp32
