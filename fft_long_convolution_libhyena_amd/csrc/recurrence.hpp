@@ -319,8 +319,9 @@ struct Call {
     int64_t chunks, back_chunks, blocks;  // chunks of tokens (forward, backward), blocks of channels
 };
 
+// whole: of whole sequences, whose strides and grids of chunks are bounded; the step's are its own
 hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
-                     const hyena_recurrence_inputs_t* in, Call& c, int64_t most_ld = int64_t(1) << 22);
+                     const hyena_recurrence_inputs_t* in, Call& c, bool whole = true);
 // 64-bit values at the head of a workspace that start() clears: the tickets of up to two launches, then the words
 constexpr int kHead = 2;
 inline int64_t word_count(const Call& c, int64_t chunks) { return chunks > 1 ? chunks * c.p.dim : 0; }

@@ -197,7 +197,7 @@ hipError_t forward(const Call& c, const float* state_in, void* y, float* state_o
 }
 
 hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t tokens, const int64_t* seq_start,
-                     const hyena_recurrence_inputs_t* in, Call& c, int64_t most_ld) {
+                     const hyena_recurrence_inputs_t* in, Call& c, bool whole) {
     if (!p || p->dim < 1 || (p->dtype != HYENA_F32 && p->dtype != HYENA_BF16) || N < 1 || tokens < 0)
         return HYENA_ERR_INVALID_ARG;
     if (!p->rate || ((uintptr_t)p->rate & 3u) || ((uintptr_t)seq_start & 7u)) return HYENA_ERR_INVALID_ARG;
@@ -211,7 +211,7 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
     c.span = chunks(kShortSpan) * c.blocks <= kShortGrid ? kShortSpan : kForwardSpan;
     c.chunks = chunks(c.span);
     c.back_chunks = (tokens + kBackwardChunk - 1) / kBackwardChunk;
-    if (c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
+    if (whole && c.back_chunks * c.blocks >= (int64_t(1) << 32) / kThreads) return HYENA_ERR_UNSUPPORTED;
     c.seqs = Seqs{seq_start, (int)N, (int)tokens, (int)(tokens / N)};
     if (!in) return HYENA_OK;
     c.in = *in;
@@ -219,7 +219,8 @@ hyena_status_t check(const hyena_recurrence_params_t* p, int64_t N, int64_t toke
     const int64_t lds[] = {in->ldx, in->ldr, in->ldi};
     for (int k = 0; k < 3; ++k) {
         if ((tokens > 0 && !rows[k]) || !aligned16(rows[k])) return HYENA_ERR_INVALID_ARG;
-        if (lds[k] < p->dim || lds[k] % (c.bf ? 8 : 4) || lds[k] > most_ld) return HYENA_ERR_INVALID_ARG;
+        // whole sequences: see Rows; the step's offsets are of 64 bits
+        if (lds[k] < p->dim || lds[k] % (c.bf ? 8 : 4) || lds[k] > int64_t(1) << (whole ? 22 : 31)) return HYENA_ERR_INVALID_ARG;
     }
     return HYENA_OK;
 }

@@ -113,7 +113,7 @@ hyena_status_t hyena_recurrence_step(const hyena_recurrence_params_t* params, in
     rec::Call c;
     if (!in || !states || !y || B < 1 || T < 1 || num_states < 1) return HYENA_ERR_INVALID_ARG;
     if (B > (int64_t(1) << 24) || T > (int64_t(1) << 24) || num_states > 0x7fffffff) return HYENA_ERR_UNSUPPORTED;
-    const hyena_status_t st = rec::check(params, B, B * T, nullptr, in, c, int64_t(1) << 31);  // 64-bit offsets
+    const hyena_status_t st = rec::check(params, B, B * T, nullptr, in, c, false);
     if (st != HYENA_OK) return st;
     if (!aligned16(states) || !aligned16(y) || ((uintptr_t)slots & 3u)) return HYENA_ERR_INVALID_ARG;
     if (!slots && num_states < B) return HYENA_ERR_INVALID_ARG;

@@ -887,8 +887,9 @@ size_t hyena_recurrence_workspace_bytes(const hyena_recurrence_params_t* params,
  * rounding. Outputs must not alias inputs, but for state_out. Enqueued on `stream`. Errors:
  * HYENA_ERR_INVALID_ARG (NULL or misaligned
  * pointers, sizes below 1, tokens not a multiple of N without seq_start, bad ld),
- * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, tokens > 2^31 - 256, or 2^23 or
- * more pairs of 80 tokens and 128 channels), HYENA_ERR_WORKSPACE, HYENA_ERR_DEVICE. */
+ * HYENA_ERR_UNSUPPORTED (dim not a multiple of 8 or above 2^20, N > 2^24, or 2^23 or more pairs of 80
+ * tokens and 128 channels: above 671088560 tokens, of more than 128 channels fewer), HYENA_ERR_WORKSPACE,
+ * HYENA_ERR_DEVICE. */
 hyena_status_t hyena_recurrence_forward(const hyena_recurrence_params_t* params, int64_t N, int64_t tokens,
                                         const int64_t* seq_start, const hyena_recurrence_inputs_t* in,
                                         const float* state_in, void* y, float* state_out, float* carries,
@@ -921,9 +922,9 @@ hyena_status_t hyena_recurrence_backward(const hyena_recurrence_params_t* params
  * inputs and of y [B*T][dim]; states [num_states][dim] fp32, read and updated in place once each; slots
  * [B] int32 or NULL, both exactly as for hyena_delta_step: rows that name the same slot are
  * successive tokens of it, a slot outside [0, num_states) gives zeros. Enqueued on `stream`; no
- * workspace. Errors as hyena_recurrence_forward, of N = B and tokens = B*T (HYENA_ERR_UNSUPPORTED where
- * 2^24 pairs of a row and 512 channels are reached), and HYENA_ERR_INVALID_ARG for B, T or num_states
- * below 1 and for NULL slots with num_states < B. */
+ * workspace. Errors as hyena_recurrence_forward, but for its limit of pairs: HYENA_ERR_UNSUPPORTED where
+ * 2^24 pairs of a row and 512 channels are reached, and for B or T > 2^24 or B*T > 2^31 - 256; and
+ * HYENA_ERR_INVALID_ARG for B, T or num_states below 1 and for NULL slots with num_states < B. */
 hyena_status_t hyena_recurrence_step(const hyena_recurrence_params_t* params, int64_t B, int64_t T,
                                      const hyena_recurrence_inputs_t* in, float* states, int64_t num_states,
                                      const int32_t* slots, void* y, hipStream_t stream);
