@@ -323,13 +323,28 @@ int64_t norm_covering_wgs(const hyena_qk_norm_params_t& p, int64_t tokens) {
 }
 size_t norm_part_bytes(int64_t wgs, int64_t dim) { return (size_t)wgs * 2 * (size_t)dim * sizeof(float); }
 
+// Whether a call's accesses are marked as a stream's (stream.hpp): it moves more than the Infinity Cache holds, and
+// what the lanes of a head reach with one instruction, `run` bytes behind each other, is whole lines. Of neighbours in
+// fp32 an instruction reaches 16 bytes of every 32, of halves with a rest that is not rotated as well.
+template <bool BF, bool HALVES, bool BACK>
+bool norm_streams(const NormArgs& a) {
+    constexpr int64_t E = BF ? 2 : 4;
+    if (a.tokens * (a.hq + a.hk) * a.dim * E * (BACK ? 3 : 2) <= kInfinityCache) return false;
+    const int64_t run = HALVES ? (2 * a.rot == a.dim ? a.rot * E : 0) : BF ? a.dim * E : 0;
+    if (!run || (run | a.ldq * E | a.ldk * E) % kLine) return false;
+    return whole_lines(a.q) && whole_lines(a.k) && whole_lines(a.qo) && whole_lines(a.ko) &&
+           (!BACK || (whole_lines(a.dqo) && whole_lines(a.dko)));
+}
+
 template <bool BF, int G, bool HALVES, bool BACK>
 void launch_norm_g(const NormArgs& a, const NormGrid& g, hipStream_t st) {
     const dim3 grid(g.x, g.y), block(kNormThreads);
-    const int64_t bytes = a.tokens * (a.hq + a.hk) * a.dim * (BF ? 2 : 4) * (BACK ? 3 : 2);
-    if (bytes > kInfinityCache)  // with so many tokens a group takes several heads
-        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, true>), grid, block, 0, st, a);
-    else if (g.per > 1)
+    if constexpr (8 * G * (BF ? 2 : 4) / (HALVES ? 2 : 1) >= kLine && (BF || HALVES))  // heads of G lanes fill lines
+        if (g.per > 1 && norm_streams<BF, HALVES, BACK>(a)) {
+            hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, true>), grid, block, 0, st, a);
+            return;
+        }
+    if (g.per > 1)
         hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, false>), grid, block, 0, st, a);
     else
         hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1, false>), grid, block, 0, st, a);
