@@ -124,7 +124,9 @@ __device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const f
     }
 }
 
-template <bool BF, int G, bool HALVES, bool BACK, int AHEAD, bool ST>
+// AXES: a position for each of several axes. One position keeps code of its own: with a choice a token the calls of 5 to
+// 16384 tokens of 12 heads of 128 were 1 to 5% slower, 8192 tokens of 5 fp32 heads of 256 19.8 us in place of 17.4.
+template <bool BF, int G, bool HALVES, bool BACK, int AHEAD, bool ST, bool AXES>
 __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
     constexpr int GW = kNormThreads / G;  // groups per workgroup
     using E8 = Eight<BF, HALVES, ST>;
@@ -146,12 +148,12 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
         for (int i = 0; i < 8; ++i) w[t][i] = wp ? wp[4 * (i < 4 ? qa : qb) + (i & 3)] : 1.f;
     }
     float fr[4] = {};
-    int ax[4] = {};
+    int ax[AXES ? 4 : 1] = {};
     if (turns)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             fr[p] = a.freq[4 * lane + p];
-            if (a.axis) {
+            if constexpr (AXES) {
                 const int i = a.axis[4 * lane + p];
                 ax[p] = i < 0 ? 0 : i < a.axes ? i : a.axes - 1;
             }
@@ -179,16 +181,16 @@ __global__ __launch_bounds__(kNormThreads) void k_qk_norm(NormArgs a) {
         fetch(h0);
         float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
         if (turns && tok) {
-            double pos[4];
-            if (a.axis) {
+            double pos[AXES ? 4 : 1];
+            if constexpr (AXES) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p) pos[p] = (double)a.pos[t * a.axes + ax[p]];
             } else {
-                pos[0] = pos[1] = pos[2] = pos[3] = (double)a.pos[t];
+                pos[0] = (double)a.pos[t];
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                const double u = pos[p] * (double)fr[p] * 0.15915494309189533577;  // turns
+                const double u = pos[AXES ? p : 0] * (double)fr[p] * 0.15915494309189533577;  // turns
                 sincospif((float)(2.0 * (u - rint(u))), &s[p], &c[p]);
             }
         }
@@ -336,37 +338,41 @@ bool norm_streams(const NormArgs& a) {
            (!BACK || (whole_lines(a.dqo) && whole_lines(a.dko)));
 }
 
-template <bool BF, int G, bool HALVES, bool BACK>
+template <bool BF, int G, bool HALVES, bool BACK, bool AXES>
 void launch_norm_g(const NormArgs& a, const NormGrid& g, hipStream_t st) {
     const dim3 grid(g.x, g.y), block(kNormThreads);
     if constexpr (8 * G * (BF ? 2 : 4) / (HALVES ? 2 : 1) >= kLine && (BF || HALVES))  // heads of G lanes fill lines
         if (g.per > 1 && norm_streams<BF, HALVES, BACK>(a)) {
-            hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, true>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, true, AXES>), grid, block, 0, st, a);
             return;
         }
     if (g.per > 1)
-        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, kNormAhead, false, AXES>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((k_qk_norm<BF, G, HALVES, BACK, 1, false, AXES>), grid, block, 0, st, a);
 }
 
-template <bool BF, bool HALVES, bool BACK>
+template <bool BF, bool HALVES, bool BACK, bool AXES>
 hipError_t launch_norm_t(const NormArgs& a, const NormGrid& g, hipStream_t st) {
     switch (group_lanes(a.dim)) {
-        case 1: launch_norm_g<BF, 1, HALVES, BACK>(a, g, st); break;
-        case 2: launch_norm_g<BF, 2, HALVES, BACK>(a, g, st); break;
-        case 4: launch_norm_g<BF, 4, HALVES, BACK>(a, g, st); break;
-        case 8: launch_norm_g<BF, 8, HALVES, BACK>(a, g, st); break;
-        case 16: launch_norm_g<BF, 16, HALVES, BACK>(a, g, st); break;
-        default: launch_norm_g<BF, 32, HALVES, BACK>(a, g, st); break;
+        case 1: launch_norm_g<BF, 1, HALVES, BACK, AXES>(a, g, st); break;
+        case 2: launch_norm_g<BF, 2, HALVES, BACK, AXES>(a, g, st); break;
+        case 4: launch_norm_g<BF, 4, HALVES, BACK, AXES>(a, g, st); break;
+        case 8: launch_norm_g<BF, 8, HALVES, BACK, AXES>(a, g, st); break;
+        case 16: launch_norm_g<BF, 16, HALVES, BACK, AXES>(a, g, st); break;
+        default: launch_norm_g<BF, 32, HALVES, BACK, AXES>(a, g, st); break;
     }
     return hipGetLastError();
 }
 
+template <bool BACK, bool AXES>
+hipError_t launch_norm_a(bool bf, bool halves, const NormArgs& a, const NormGrid& g, hipStream_t st) {
+    if (bf) return halves ? launch_norm_t<true, true, BACK, AXES>(a, g, st) : launch_norm_t<true, false, BACK, AXES>(a, g, st);
+    return halves ? launch_norm_t<false, true, BACK, AXES>(a, g, st) : launch_norm_t<false, false, BACK, AXES>(a, g, st);
+}
 template <bool BACK>
 hipError_t launch_norm(bool bf, bool halves, const NormArgs& a, const NormGrid& g, hipStream_t st) {
-    if (bf) return halves ? launch_norm_t<true, true, BACK>(a, g, st) : launch_norm_t<true, false, BACK>(a, g, st);
-    return halves ? launch_norm_t<false, true, BACK>(a, g, st) : launch_norm_t<false, false, BACK>(a, g, st);
+    return a.axis ? launch_norm_a<BACK, true>(bf, halves, a, g, st) : launch_norm_a<BACK, false>(bf, halves, a, g, st);
 }
 
 hyena_status_t norm_check_params(const hyena_qk_norm_params_t* p, int64_t tokens) {
