@@ -127,7 +127,8 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     if (!span.have) return;
     // the state in front of one of these tokens may be one that the backward asks for
     const int kept = p.carry ? (kBackwardChunk - span.t0 % kBackwardChunk) % kBackwardChunk : S;
-    const Rows<BF> ys(p.y, p.dim, span.t0, p.y ? rows : 0, p.dim);
+    const Rows<BF> ys(p.y, p.dim, span.t0, rows, p.dim);
+    const uint32_t wanted = p.y ? span.have : 0;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         if (s == kept && s < rows && ok)
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
         if (span.begins(s)) h[0] = h[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < kVec; ++j) h[j] = fmaf(a[s][j], h[j], b[s][j]);
-        if (span.has(s)) ys.store(s, at, h);
+        if (wanted >> s & 1) ys.store(s, at, h);
         if (span.ends(s) && p.state_out && ok) {
             const int64_t n = span.sequence(s);
 #pragma unroll
