@@ -40,6 +40,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     using Raw = typename Io<BF>::Raw;
     constexpr int S = kBackwardSpan, W = kWaves;
     __shared__ Link sG[W][64], sBehind[W][64];  // (A, G) of the waves and of the chunks behind
+    __shared__ float2 sSum[W][64];               // of the waves' w
     __shared__ float2 sH[W][64], sEi[W][S][64];  // sEi: a lane's own exp(-i), kept for the last pass
     __shared__ int sFirst[W], sLast[W], sBehindReset[W];
     __shared__ uint32_t sTicket;
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     };
     Raw x[S], dy[S], i[S];
     float er[S][kVec], a[S][kVec], b[S][kVec];  // exp(-r), a, m sig(i) x
-    float rate[kVec], A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
+    float rate[kVec], w_sum[kVec] = {}, A[kVec] = {1.f, 1.f}, H[kVec] = {}, G[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) rate[j] = p.rate[col + j];
     const bool near = near_rates(rate);
@@ -97,9 +98,10 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 b[s][j] = __builtin_amdgcn_sqrtf(q[j]);
-                A[j] *= a[s][j];
+                w_sum[j] += w[j];
             }
         }
+        run_decay(w_sum, A);
 #pragma unroll
         for (int s = S - 1; s >= 0; --s) {
             float d[kVec];
@@ -110,6 +112,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
         }
     }
     sG[wave][lane] = Link{A[0], A[1], G[0], G[1]};
+    sSum[wave][lane] = float2{w_sum[0], w_sum[1]};
     if (lane == 0) {
         sFirst[wave] = span.first != 0;
         sLast[wave] = span.last != 0;
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
     // work on what only this chunk needs
     const bool publishes = p.words && wave == 0 && order + 1 < p.chunks, ends = (order & (kGroup - 1)) == kGroup - 1;
     const bool looks = p.words && order;
-    float cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
+    float cw[kVec] = {}, cA[kVec] = {1.f, 1.f}, cG[kVec] = {};
     bool reset = false;
     const uint32_t first_bits = flag_bits(sFirst, lane), last_bits = flag_bits(sLast, lane);
     if (publishes) {
@@ -127,10 +130,12 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_backward(BackwardA
 #pragma unroll
         for (int k = W - 1; k >= 0; --k) {
             const Link v = sG[k][lane];
+            const float2 u = sSum[k][lane];
             join_link(last_bits >> k & 1, v, cG);
-            cA[0] *= v[0];
-            cA[1] *= v[1];
+            cw[0] += u.x;
+            cw[1] += u.y;
         }
+        run_decay(cw, cA);
         if (!ends && ok) publish(p.words, order, p.dim, own, reset, cA, cG);
     }
     LookBack look(p.words, order, p.dim, col, wave);

@@ -27,6 +27,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     using Raw = typename Io<BF>::Raw;
     constexpr int W = kWaves;
     __shared__ Link sOwn[W][64], sBack[W][64];
+    __shared__ float2 sSum[W][64];  // of the waves' w
     __shared__ int sOwnReset[W], sBackReset[W];
     __shared__ uint32_t sTicket;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
     const Span<S> span(p.seqs, chunk * (W * S) + wave * S);
     const int rows = p.seqs.tokens - span.t0 < S ? p.seqs.tokens - span.t0 : S;
     float a[S][kVec], b[S][kVec];
-    float A[kVec] = {1.f, 1.f}, H[kVec] = {};
+    float w_sum[kVec] = {}, A[kVec] = {1.f, 1.f}, H[kVec] = {};
     if (span.have) {
         Raw x[S], r[S], i[S];
         const Rows<BF> xs(p.in.x, p.in.ldx, span.t0, rows, p.dim), rs(p.in.r, p.in.ldr, span.t0, rows, p.dim),
@@ -67,7 +68,11 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
             Io<BF>::get(r[s], rv);
             Io<BF>::get(i[s], iv);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) w[j] = rate[j] * sigmoid(rv[j]);
+            for (int j = 0; j < kVec; ++j) {
+                w[j] = rate[j] * sigmoid(rv[j]);
+                w_sum[j] += w[j];
+            }
+            asm volatile("" : "+v"(w_sum[0]), "+v"(w_sum[1]));  // added here, or all w are kept for later and 8 values spill
             decay(w, near, a[s], q);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) b[s][j] = __builtin_amdgcn_sqrtf(q[j]) * sigmoid(iv[j]) * xv[j];
@@ -80,30 +85,31 @@ __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArg
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                H[j] = fmaf(a[s][j], H[j], b[s][j]);
-                A[j] *= a[s][j];
-            }
+            for (int j = 0; j < kVec; ++j) H[j] = fmaf(a[s][j], H[j], b[s][j]);
         }
+        run_decay(w_sum, A);
     }
     sOwn[wave][lane] = Link{A[0], A[1], H[0], H[1]};
+    sSum[wave][lane] = float2{w_sum[0], w_sum[1]};
     if (lane == 0) sOwnReset[wave] = span.first != 0;
     __syncthreads();
     const uint32_t resets = flag_bits(sOwnReset, lane);
     float h[kVec] = {};
     if (p.words) {
         const bool publishes = wave == 0 && chunk + 1 < p.chunks, ends = (chunk & (kGroup - 1)) == kGroup - 1;
-        float cA[kVec] = {1.f, 1.f}, cH[kVec] = {};
+        float cw[kVec] = {}, cA[kVec] = {1.f, 1.f}, cH[kVec] = {};
         bool reset = false;
         if (publishes) {
             reset = resets != 0;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 const Link v = sOwn[k][lane];
+                const float2 u = sSum[k][lane];
                 join_link(resets >> k & 1, v, cH);
-                cA[0] *= v[0];
-                cA[1] *= v[1];
+                cw[0] += u.x;
+                cw[1] += u.y;
             }
+            run_decay(cw, cA);
             if (!ends && ok) publish(p.words, chunk, p.dim, own, reset, cA, cH);
         }
         if (chunk) {
