@@ -24,8 +24,10 @@ namespace rec {
 
 constexpr int kVec = 2;                  // channels a lane
 constexpr int kCols = 64 * kVec;         // channels a workgroup
-// Tokens of a wave and of a chunk: as many as 128 registers hold, which leaves two workgroups a CU (the
-// backward holds twice as much of each, exp(-i) in LDS). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22
+// Tokens of a wave and of a chunk: in bf16 as many as 128 registers hold, which leaves two workgroups a CU (the
+// backward holds twice as much of each, exp(-i) in LDS). In fp32 the same spans take 138 and 158 registers, one workgroup a
+// CU; twice the bytes are in flight for it (1 x 65536 x 768: 178 us forward, 334 backward, 91% and 85% of a copy's rate by
+// inputs and outputs; other spans were measured in bf16 only). Forward of 1 x 65536 x 768 with 8, 12, 16, 18, 20 and 22
 // tokens a wave: 134, 112, 107, 104, 102 and 103 us; with 32 in waves at two or three a SIMD 114 and 125. Training step
 // of 8 x 8192 with 6, 8 and 10 in the backward: 334, 297 and 285 us (8 without LDS the same, 10 without it spills: 375).
 constexpr int kForwardSpan = 20, kBackwardSpan = 10;
@@ -129,6 +131,9 @@ struct Io<false> {
 // lane's channels a constant one, so an access costs no vector arithmetic; a lane behind the last channel
 // has the offset kNone outside of the range, loads 0 and stores nothing. Stores are marked as not read again soon
 // (1 x 65536 x 768: 102 to 98 us, training step of 8 x 8192: 292 to 281; loads so too: 98 and 279, but small calls 2 us longer).
+// Unlike the norms' (stream.hpp) this goes for small calls and lines covered in part too: no width from 8 to 2048 channels lost more
+// than 1%, and forward and residual norm of its output together take, marked and not, for 4936 tokens of 768 channels 26.4 and
+// 26.3 us, 16384 64.6 and 63.8, 32768 101 and 106, 65536 165 and 172.
 constexpr int kNone = (int)0x80000000u;
 template <bool BF>
 struct Rows {

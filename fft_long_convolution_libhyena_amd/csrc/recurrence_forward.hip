@@ -19,9 +19,9 @@ struct ForwardArgs {
     int dim, chunks, blocks;
 };
 
-// One chunk and 128 channels, S tokens a wave. 1 x 65536 x 768 in bf16 take 97 us, the start among them: 425 MB with words
-// and kept states, at 4.6 TB/s; vector work fills half of the cycles. Without the look-back it would be 78: words are read past the caches,
-// and chunks wait for others that started at about the same time.
+// One chunk and 128 channels, S tokens a wave. 1 x 65536 x 768 in bf16 take 98 us, the start among them: 425 MB with words
+// and kept states, at 4.3 TB/s (in fp32 178 us, 828 MB, 4.7); vector work fills half of the cycles. Without the look-back bf16
+// would take 78: words are read past the caches, and chunks wait for others that started at about the same time.
 template <bool BF, int S>
 __global__ __launch_bounds__(kThreads, BF ? 4 : 2) void k_rec_forward(ForwardArgs p) {
     using Raw = typename Io<BF>::Raw;

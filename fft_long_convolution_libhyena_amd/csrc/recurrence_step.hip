@@ -1,6 +1,8 @@
 // Gated linear recurrence, recurrent form: a few tokens of every row against states that
 // stay in a pool in device memory (see recurrence.hpp). A workgroup has one row and 512
-// channels, two a lane; all of it is fp32.
+// channels, two a lane; all of it is fp32. With slots every workgroup looks through all of them for rows that share its
+// own: work that grows with the square of the rows. One token of 2048 channels, with slots and with the rows in order (captured):
+// 256 rows 4.2 and 3.6 us, 1024 9.1 and 6.7, 4096 44 and 18, 16384 411 and 60.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
